@@ -175,6 +175,70 @@ OKV_API okv_status okv_predict(okv_ctx* ctx, int32_t layer, const void* query, i
 OKV_API okv_status okv_attend_lookahead(okv_ctx* ctx, int32_t layer, const void* q, const void* draft_q,
                                         void* out, void* draft_out, void* stream);
 
+/* ---- drafted trees and rows of a projection ----
+ *
+ * A drafter proposes a tree of tokens per request; the model's next pass verifies it: the tree's
+ * queries attend over the resident set and over the drafted tokens they descend from, and the
+ * accepted path is then appended. The calls below take one layer of that pass (and the plain decode
+ * step's row) from the projection onwards:
+ *   okv_norm_rope -> okv_attend_tree -> (the caller accepts a path) -> okv_append_tree
+ *   okv_append_qkv -> okv_attend
+ */
+
+/* Per-head norms and the position rotation of a row of q_heads query, kv_heads key and kv_heads
+ * value heads. For a query or key head x at position p:
+ *   y = x / sqrt(mean(x^2) + eps) * weight                    (left out where the weight is NULL)
+ *   (y_a, y_b) <- (y_a cos t_i - y_b sin t_i, y_b cos t_i + y_a sin t_i),  t_i = p * inv_freq[i]
+ * for i < rotary_dim / 2, with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) if `interleaved`.
+ * The other dims and the value heads pass unchanged. Computed in binary32 (the angles from the exact
+ * product, whatever the position) and rounded once. */
+typedef struct {
+  const float* inv_freq; /* device [rotary_dim / 2], radians per position; NULL if rotary_dim is 0 */
+  const void* q_weight;  /* device [head_dim] storage dtype, 16-byte aligned, or NULL */
+  const void* k_weight;  /* the same for keys */
+  float eps;             /* not negative */
+  int32_t rotary_dim;    /* a multiple of 16, from 0 to head_dim */
+  int32_t interleaved;   /* 0 or 1 */
+} okv_rotary;
+
+/* One token per active request from its row of the projection: norms and rotates the row's queries
+ * and keys at the request's length (the new token's position), writes the queries to q and appends
+ * the key and value to `layer` as okv_append does (same waits, same refusals).
+ * qkv: device, request r's row at element r * row_stride, (q_heads + 2 kv_heads) * head_dim elements
+ * (queries, keys, values), row_stride at least that and a multiple of 16 bytes; q: device
+ * [max_requests][q_heads][head_dim]. Both 16-byte aligned, not overlapping. Rows of inactive requests
+ * are not read or written. EINVAL also if the context's device is not current; ESTATE if `stream` is
+ * being captured (the lengths advance once per call, on the host too). */
+OKV_API okv_status okv_append_qkv(okv_ctx* ctx, int32_t layer, const void* qkv, int64_t row_stride,
+                                  const okv_rotary* rotary, void* q, void* stream);
+
+/* Attention of each request's drafted tokens over the resident set and over one another. n_draft (1
+ * to 64) is the stride of the inputs; counts: device [max_requests] int32, each request's drafted
+ * tokens (values outside 0..n_draft are clamped), or NULL for n_draft each. q, out: device
+ * [max_requests][n_draft][q_heads][head_dim]; k_draft, v_draft: device [max_requests][n_draft]
+ * [kv_heads][head_dim]; all of the storage dtype, 16-byte aligned; mask: device
+ * [max_requests][n_draft] uint64, bit j of token i set if i attends drafted token j (itself among
+ * them, as a rule; bits from the request's count on are ignored).
+ * For every active request and drafted token: softmax(q.k / sqrt(d)) v over every valid token of
+ * every occupied slot of its unit and the drafted tokens of its mask, zeros if there are none. A
+ * drafted token that a row does not attend has no part in it, whatever its values (infinite and NaN
+ * among them). Rows from a request's count on and rows of inactive requests are not written. Waits on
+ * `stream` for the layer's last staging. EINVAL as okv_append_qkv; ESTATE if `stream` is being
+ * captured and the layer has been staged (a captured wait on the staging is not possible). */
+OKV_API okv_status okv_attend_tree(okv_ctx* ctx, int32_t layer, int32_t n_draft, const int32_t* counts,
+                                   const void* q, const void* k_draft, const void* v_draft,
+                                   const uint64_t* mask, void* out, void* stream);
+
+/* Append accepted drafted tokens to `layer`, any number per request. k_draft, v_draft: as in
+ * okv_attend_tree. counts: HOST [max_requests], the tokens to append to each active request (0 to
+ * n_draft); index: HOST [max_requests][n_draft], the first counts[r] entries of row r the drafted
+ * tokens to append, in order. Both are read before the call returns; entries of inactive requests are
+ * ignored. The result is that of okv_append for one token after another. Waits and refusals as
+ * okv_append, for the requests that append; EINVAL also on a count or index out of range. */
+OKV_API okv_status okv_append_tree(okv_ctx* ctx, int32_t layer, int32_t n_draft, const void* k_draft,
+                                   const void* v_draft, const int32_t* counts, const int32_t* index,
+                                   void* stream);
+
 /* One decode step over every layer, in layer order ("4 System Design": the foreground waits
  * only for each layer's transfer; the background chain of layer l overlaps the attention of the
  * later layers). The result is that of: for l = 0 .. layers-1: okv_append(l) if k_new is not NULL,
@@ -294,6 +358,50 @@ OKV_API okv_status okv_attend_static(int32_t n_requests, int32_t q_heads, int32_
                                      int32_t head_dim, int32_t block_size, int32_t slots,
                                      int32_t dtype, const void* pool, const int32_t* slot_block,
                                      const int32_t* lengths, const void* q, void* out, void* stream);
+
+/* ---- rows, append and drafted trees without a context ----
+ *
+ * For callers that keep their own pool, as okv_attend_static's do. The three calls allocate nothing
+ * and have no workspace, so calls on different streams are independent, and each can be captured into
+ * a graph. They enqueue one launch on `stream`, which must belong to the current device (else
+ * OKV_EINVAL). Shapes okv_create refuses, NULL and misaligned pointers return OKV_EINVAL without
+ * launching. Device pointers are 16-byte aligned except those of 32- and 64-bit integers and
+ * inv_freq. Failures the kernels record are not reported: a slot whose block id is outside its
+ * request's length counts as empty. */
+
+/* Norms and rotates n_rows rows of a projection (okv_rotary) at positions: device [n_rows] int32. qkv
+ * and row_stride as in okv_append_qkv. q [n_rows][q_heads][head_dim], k and v [n_rows][kv_heads]
+ * [head_dim]: device outputs, any of them NULL to leave it out; they may not overlap qkv or one
+ * another. A row with a negative position is not written. n_rows = 0 is a no-op. */
+OKV_API okv_status okv_norm_rope(int32_t n_rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                 int32_t dtype, const void* qkv, int64_t row_stride,
+                                 const int32_t* positions, const okv_rotary* rotary, void* q, void* k,
+                                 void* v, void* stream);
+
+/* Append to a pool of okv_attend_static's layout. Row r * n_new + t of qkv is token t of request r, at
+ * position lengths[r] + t, for t < counts[r] (device [n_requests] int32, clamped to 0..n_new; NULL for
+ * n_new each). Its normed and rotated queries go to q [n_requests][n_new][q_heads][head_dim] (NULL to
+ * leave them out), its keys and values into the slot of each unit that holds the token's block (the
+ * lowest such slot), or nowhere where none does. lengths: device [n_requests] int32, the tokens
+ * before the call; the caller advances it, and assigns blocks to slots. Rows from a request's count
+ * on are not written; a request with a negative length, or with lengths[r] + n_new past 2^31 - 1, is
+ * left out. */
+OKV_API okv_status okv_append_qkv_static(int32_t n_requests, int32_t n_new, int32_t q_heads,
+                                         int32_t kv_heads, int32_t head_dim, int32_t block_size,
+                                         int32_t slots, int32_t dtype, const void* qkv,
+                                         int64_t row_stride, const int32_t* lengths,
+                                         const int32_t* counts, const okv_rotary* rotary, void* pool,
+                                         const int32_t* slot_block, void* q, void* stream);
+
+/* okv_attend_tree over a pool of okv_attend_static's layout (pool, slot_block, lengths), every request
+ * 0 .. n_requests-1. counts may be NULL. */
+OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, int32_t q_heads,
+                                          int32_t kv_heads, int32_t head_dim, int32_t block_size,
+                                          int32_t slots, int32_t dtype, const void* pool,
+                                          const int32_t* slot_block, const int32_t* lengths,
+                                          const int32_t* counts, const void* q, const void* k_draft,
+                                          const void* v_draft, const uint64_t* mask, void* out,
+                                          void* stream);
 
 #ifdef __cplusplus
 }

@@ -47,6 +47,11 @@ class _Timing(ctypes.Structure):
                 ("local_hits", ctypes.c_int64), ("local_fills", ctypes.c_int64), ("full_reads", ctypes.c_int64)]
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 def load_library():
     """Load libokv.so (raises ImportError if it has not been built)."""
     global _lib
@@ -88,6 +93,12 @@ def load_library():
             "okv_set_timing": ([vp, i32], st),
             "okv_read_timing": ([vp, ctypes.POINTER(_Timing)], st),
             "okv_launch_count": ([vp], i64),
+            "okv_append_qkv": ([vp, i32, vp, i64, vp, vp, vp], st),
+            "okv_attend_tree": ([vp, i32, i32, vp, vp, vp, vp, vp, vp, vp], st),
+            "okv_append_tree": ([vp, i32, i32, vp, vp, vp, vp, vp], st),
+            "okv_norm_rope": ([i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp], st),
+            "okv_append_qkv_static": ([i32] * 8 + [vp, i64, vp, vp, vp, vp, vp, vp, vp], st),
+            "okv_attend_tree_static": ([i32] * 8 + [vp] * 10, st),
             "okv_attend_static": ([i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp], st),
         }
         for name, (args, res) in sig.items():
@@ -272,6 +283,52 @@ class Context:
                                     self._tensor_ptr(out, qs, "out"), kp, vp, step, fetch_cap,
                                     ctypes.c_void_p(_stream_handle(stream))), "okv_step")
 
+    def append_qkv(self, layer: int, qkv, q, rotary: "Rotary", stream=None):
+        """One token per active request from its projection row: qkv [R][(Hq + 2 Hkv) d] (rows may be
+        strided) -> q [R][Hq][d], the key and value appended."""
+        c = self.cfg
+        dt, _ = _storage(qkv, "qkv")
+        if dt != c.dtype or qkv.dim() != 2 or qkv.shape[0] != c.max_requests:
+            raise ValueError(f"qkv: expected [{c.max_requests}][{(c.q_heads + 2 * c.kv_heads) * c.head_dim}] of the "
+                             f"context's dtype, got {qkv.dtype} {tuple(qkv.shape)}")
+        stride = _row_stride(qkv, (c.q_heads + 2 * c.kv_heads) * c.head_dim)
+        rotary._check(qkv, c.head_dim)
+        self._check(self.L.okv_append_qkv(self.h, layer, qkv.data_ptr(), stride, rotary._ref,
+                                          self._tensor_ptr(q, self._qshape, "q"), _stream_handle(stream)),
+                    "okv_append_qkv")
+
+    def attend_tree(self, layer: int, q, k, v, mask, out, counts=None, stream=None):
+        """Drafted tokens' attention: q, out [R][T][Hq][d], k, v [R][T][Hkv][d], mask [R][T] int64 or uint64
+        (bit j: drafted token j is attended), counts [R] int32 or None."""
+        import torch
+        c = self.cfg
+        T = q.shape[1] if q.dim() == 4 else 0
+        if counts is not None:
+            _expect(counts, "counts", (c.max_requests,), (torch.int32,), q.device)
+        _expect(mask, "mask", (c.max_requests, T), (torch.int64, torch.uint64), q.device)
+        qs, ks = (c.max_requests, T, c.q_heads, c.head_dim), (c.max_requests, T, c.kv_heads, c.head_dim)
+        self._check(self.L.okv_attend_tree(self.h, layer, T, counts.data_ptr() if counts is not None else None,
+                                           self._tensor_ptr(q, qs, "q"), self._tensor_ptr(k, ks, "k"),
+                                           self._tensor_ptr(v, ks, "v"), mask.data_ptr(),
+                                           self._tensor_ptr(out, qs, "out"), _stream_handle(stream)),
+                    "okv_attend_tree")
+
+    def append_tree(self, layer: int, k, v, accepted, stream=None):
+        """Append accepted drafted tokens: `accepted` maps a request id to its drafted tokens, in order
+        (requests left out append none); k, v [R][T][Hkv][d]."""
+        c = self.cfg
+        T = k.shape[1] if k.dim() == 4 else 0
+        counts = np.zeros(c.max_requests, np.int32)
+        index = np.zeros((c.max_requests, max(T, 1)), np.int32)
+        for r, path in accepted.items():
+            if not 0 <= r < c.max_requests or len(path) > T:
+                raise ValueError(f"accepted: request {r} with {len(path)} tokens (at most {T})")
+            counts[r] = len(path)
+            index[r, :len(path)] = path
+        ks = (c.max_requests, T, c.kv_heads, c.head_dim)
+        self._check(self.L.okv_append_tree(self.h, layer, T, self._tensor_ptr(k, ks, "k"), self._tensor_ptr(v, ks, "v"),
+                                           _np_ptr(counts), _np_ptr(index), _stream_handle(stream)), "okv_append_tree")
+
     def join(self, stream=None):
         self._check(self.L.okv_join(self.h, ctypes.c_void_p(_stream_handle(stream))), "okv_join")
 
@@ -383,3 +440,153 @@ def attend_static(pool, slot_block, lengths, q, out, *, q_heads: int, kv_heads: 
                              ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(_stream_handle(stream)))
     if st != OK:
         raise OkvError(st, "okv_attend_static failed (shape or size outside its limits, or a CUDA error)")
+
+
+# ---- rows, append and drafted trees without a context ------------------------------------------------
+
+_DTYPE_OF = {}
+
+
+def _storage(t, name: str):
+    """(okv dtype, device) of a CUDA tensor of a storage dtype."""
+    if not _DTYPE_OF:
+        import torch
+        _DTYPE_OF.update({torch.float32: F32, torch.bfloat16: BF16})
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    dt = _DTYPE_OF.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return dt, t.device
+
+
+def _expect(t, name: str, shape, dtypes, device):
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _row_stride(t, width: int) -> int:
+    """Elements between the rows of t [...][width], whose leading dims are one run of rows."""
+    shape, stride = t.shape, t.stride()
+    if shape[-1] != width or (stride[-1] != 1 and width > 1):
+        raise ValueError(f"qkv: expected rows of {width} adjacent elements, got shape {tuple(shape)} strides {stride}")
+    step = None  # between rows, of the dims seen so far from the last one
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step, run = s, s * n
+        elif s != run:
+            raise ValueError(f"qkv: rows are not at one distance: shape {tuple(shape)} strides {stride}")
+        else:
+            run *= n
+    return width if step is None else step
+
+
+class Rotary:
+    """okv_rotary: inv_freq [rotary_dim / 2] float32 (None: no rotation), q_weight and k_weight [head_dim] of
+    the rows' dtype (None: no norm). Keeps the tensors; read at each call."""
+
+    def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False):
+        import torch
+        for name, t in (("inv_freq", inv_freq), ("q_weight", q_weight), ("k_weight", k_weight)):
+            if t is not None and (not t.is_cuda or t.dim() != 1 or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected a contiguous CUDA vector")
+        if inv_freq is not None and inv_freq.dtype != torch.float32:
+            raise ValueError(f"inv_freq: expected float32, got {inv_freq.dtype}")
+        self.tensors = (inv_freq, q_weight, k_weight)
+        ptr = [t.data_ptr() if t is not None else None for t in self.tensors]
+        self._c = _Rotary(ptr[0], ptr[1], ptr[2], eps, 2 * inv_freq.numel() if inv_freq is not None else 0,
+                          1 if interleaved else 0)
+        self._ref = ctypes.addressof(self._c)
+
+    def _check(self, rows, head_dim: int):
+        inv_freq, qw, kw = self.tensors
+        dev = rows.device
+        if inv_freq is not None and inv_freq.device != dev:
+            raise ValueError(f"inv_freq: on {inv_freq.device}, the rows on {dev}")
+        for w in (qw, kw):
+            if w is not None and (w.dtype != rows.dtype or w.device != dev or w.numel() != head_dim):
+                raise ValueError(f"weights: expected {rows.dtype} [{head_dim}] on {dev}, got {w.dtype} {tuple(w.shape)} on {w.device}")
+
+
+def _call(fn: str, device, stream, *args) -> None:
+    """A context-free call with `device` current and its stream as the last argument."""
+    import torch
+    L = _lib or load_library()
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            st = getattr(L, fn)(*args, _stream_handle(stream))
+    else:
+        st = getattr(L, fn)(*args, _stream_handle(stream))
+    if st != OK:
+        raise OkvError(st, f"{fn} failed (shape, alignment or size outside its limits, or a CUDA error)")
+
+
+def norm_rope(qkv, positions, q=None, k=None, v=None, *, q_heads: int, kv_heads: int, head_dim: int, rotary: Rotary,
+              stream=None) -> None:
+    """okv_norm_rope: norms and rotates rows qkv [n][(q_heads + 2 kv_heads) head_dim] (rows may be strided) at
+    positions [n] int32 into q [n][q_heads][head_dim], k and v [n][kv_heads][head_dim] (any may be None).
+    Rows with a negative position are not written."""
+    import torch
+    dt, dev = _storage(qkv, "qkv")
+    if qkv.dim() != 2:
+        raise ValueError(f"qkv: expected rows [n][...], got {tuple(qkv.shape)}")
+    n = qkv.shape[0]
+    stride = _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim)
+    _expect(positions, "positions", (n,), (torch.int32,), dev)
+    for name, t, h in (("q", q, q_heads), ("k", k, kv_heads), ("v", v, kv_heads)):
+        if t is not None:
+            _expect(t, name, (n, h, head_dim), (qkv.dtype,), dev)
+    rotary._check(qkv, head_dim)
+    _call("okv_norm_rope", dev, stream, n, q_heads, kv_heads, head_dim, dt, qkv.data_ptr(), stride, positions.data_ptr(),
+          rotary._ref, q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
+          v.data_ptr() if v is not None else None)
+
+
+def append_qkv_static(qkv, lengths, counts, pool, slot_block, q=None, *, q_heads: int, kv_heads: int, head_dim: int,
+                      block_size: int, slots: int, rotary: Rotary, stream=None) -> None:
+    """okv_append_qkv_static: rows qkv [R][T][(q_heads + 2 kv_heads) head_dim] at positions lengths[r] + t, normed
+    and rotated; queries into q [R][T][q_heads][head_dim] (or None), keys and values into the resident slots of
+    pool [R][kv_heads][slots][2][block_size][head_dim]; counts [R] int32 or None."""
+    import torch
+    dt, dev = _storage(qkv, "qkv")
+    if qkv.dim() != 3:
+        raise ValueError(f"qkv: expected rows [R][T][...], got {tuple(qkv.shape)}")
+    R, T = qkv.shape[0], qkv.shape[1]
+    stride = _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim)
+    i32 = (torch.int32,)
+    _expect(lengths, "lengths", (R,), i32, dev)
+    if counts is not None:
+        _expect(counts, "counts", (R,), i32, dev)
+    _expect(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), (qkv.dtype,), dev)
+    _expect(slot_block, "slot_block", (R, kv_heads, slots), i32, dev)
+    if q is not None:
+        _expect(q, "q", (R, T, q_heads, head_dim), (qkv.dtype,), dev)
+    rotary._check(qkv, head_dim)
+    _call("okv_append_qkv_static", dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, qkv.data_ptr(),
+          stride, lengths.data_ptr(), counts.data_ptr() if counts is not None else None, rotary._ref, pool.data_ptr(),
+          slot_block.data_ptr(), q.data_ptr() if q is not None else None)
+
+
+def attend_tree_static(pool, slot_block, lengths, counts, q, k, v, mask, out, *, q_heads: int, kv_heads: int,
+                       head_dim: int, block_size: int, slots: int, stream=None) -> None:
+    """okv_attend_tree_static: drafted tokens q, out [R][T][q_heads][head_dim], k, v [R][T][kv_heads][head_dim], mask
+    [R][T] int64 or uint64 (bit j: drafted token j is attended), counts [R] int32 or None, over a pool of
+    attend_static's layout."""
+    import torch
+    dt, dev = _storage(pool, "pool")
+    R, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (0, 0)
+    i32, st = (torch.int32,), (pool.dtype,)
+    _expect(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev)
+    _expect(slot_block, "slot_block", (R, kv_heads, slots), i32, dev)
+    _expect(lengths, "lengths", (R,), i32, dev)
+    if counts is not None:
+        _expect(counts, "counts", (R,), i32, dev)
+    for name, t, h in (("q", q, q_heads), ("k", k, kv_heads), ("v", v, kv_heads), ("out", out, q_heads)):
+        _expect(t, name, (R, T, h, head_dim), st, dev)
+    _expect(mask, "mask", (R, T), (torch.int64, torch.uint64), dev)
+    _call("okv_attend_tree_static", dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, pool.data_ptr(),
+          slot_block.data_ptr(), lengths.data_ptr(), counts.data_ptr() if counts is not None else None, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), mask.data_ptr(), out.data_ptr())

@@ -1,0 +1,472 @@
+// Attention of a tree of drafted tokens over the resident slot pool.
+//
+// T <= 64 drafted tokens per request, token i seeing every valid token of the request's occupied
+// slots and the drafted tokens whose bit is set in its 64-bit mask. For query head h of KV head k:
+//   o_ih = sum_j softmax_j(q_ih . k_j / sqrt(d)) v_j
+// over those tokens, zero where there are none. The g T rows of a unit (request, KV head) share its
+// keys and values, so a unit's pool is read once for a group of rows.
+//
+// The tokens of a unit are taken in tiles of whole slots (at most 64 tokens); tiles without a valid
+// token are left out, the rest are dealt to the CTAs of a thread-block cluster, with the drafted
+// tokens as one more tile of the last CTA. Each CTA keeps a running maximum, sum and output per
+// row; the cluster merges them through distributed shared memory in rank order, so results do not
+// depend on timing and a launch needs no workspace.
+#include <cuda_bf16.h>
+
+#include <utility>
+
+#include "okv_tree.h"
+#include "tc5.cuh"
+
+namespace okv {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 64;         // tokens of a tile, at most
+constexpr int kMaxSplit = 8;      // CTAs of a cluster (the portable limit)
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// Four outputs, one rounding each.
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+// One CTA's share of the work: a request, a KV head, a group of rows and a part of the tokens.
+struct Site {
+  int32_t a, r, h, part, cnt, len;  // cnt: drafted tokens of the request
+  int32_t row0, rows;               // rows [row0, row0 + rows) of the unit's g * cnt
+};
+
+__device__ __forceinline__ Site make_site(const TreeArgs& A, int32_t split, int32_t group_rows) {
+  Site s;
+  const int32_t ua = blockIdx.x / split;
+  s.part = blockIdx.x % split;
+  s.a = ua / A.G.Hkv;
+  s.h = ua % A.G.Hkv;
+  s.r = A.active ? A.active[s.a] : s.a;
+  s.cnt = A.counts ? min(max(A.counts[s.r], 0), A.T) : A.T;
+  s.len = A.len[s.r];
+  s.row0 = blockIdx.y * group_rows;
+  s.rows = min(group_rows, s.cnt * A.G.g - s.row0);
+  return s;
+}
+__device__ __forceinline__ uint64_t low_bits(int32_t n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// Element offset of row m's vector in q and out, [R][T][Hq][d]; row m is drafted token m / g, head m % g.
+__device__ __forceinline__ int64_t row_offset(const TreeArgs& A, const Site& s, int32_t m) {
+  const int32_t t = m / A.G.g, j = m - t * A.G.g;
+  return (((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j) * A.G.d;
+}
+// ... and of drafted token t's key and value, [R][T][Hkv][d].
+__device__ __forceinline__ int64_t draft_offset(const TreeArgs& A, const Site& s, int32_t t) {
+  return (((int64_t)s.r * A.T + t) * A.G.Hkv + s.h) * A.G.d;
+}
+
+// Valid tokens of every slot of the unit (0: empty) into nv, by all threads of the CTA. A block id
+// outside the request's length counts as an empty slot and is recorded.
+__device__ __forceinline__ void read_slots(const TreeArgs& A, const Site& s, uint8_t* nv) {
+  const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  for (int32_t i = threadIdx.x; i < A.G.kb; i += blockDim.x) {
+    const int32_t b = sb[i];
+    int32_t n = 0;
+    if (b >= 0) {
+      const int64_t rem = (int64_t)s.len - (int64_t)b * A.G.bs;
+      if (rem <= 0 || b >= A.G.nb_max) {
+        if (A.err) record_error(A.err, kErrBlockRange, -2, s.r, b);
+      } else {
+        n = (int32_t)(rem < A.G.bs ? rem : A.G.bs);
+      }
+    }
+    nv[i] = (uint8_t)n;
+  }
+}
+// The tiles (spt slots each) that hold a valid token, in order, into `tiles`; their number. One warp.
+__device__ __forceinline__ int32_t list_tiles(const uint8_t* nv, int32_t kb, int32_t spt, uint16_t* tiles) {
+  const int lane = threadIdx.x & 31;
+  int32_t n = 0;
+  for (int32_t t0 = 0; t0 * spt < kb; t0 += 32) {
+    bool any = false;
+    for (int32_t s = (t0 + lane) * spt, e = min(s + spt, kb); s < e; ++s) any = any || nv[s];
+    const unsigned have = __ballot_sync(0xffffffffu, any);
+    if (any) tiles[n + __popc(have & ((1u << lane) - 1u))] = (uint16_t)(t0 + lane);
+    n += __popc(have);
+  }
+  return n;
+}
+
+// Adds what the drafted values that are not finite give to four outputs (dims c .. c + 3) of a row
+// that sees them. Those elements are zero in the products, where a weight of zero times them would
+// reach rows that do not see them.
+template <typename T>
+__device__ __forceinline__ void add_not_finite(const TreeArgs& A, const Site& s, uint64_t seen, int32_t c, float4& o) {
+  while (seen) {
+    const int32_t t = __ffsll((long long)seen) - 1;
+    seen &= seen - 1;
+    const T* v = (const T*)A.v + draft_offset(A, s, t) + c;
+    const float x = to_f(v[0]), y = to_f(v[1]), z = to_f(v[2]), w = to_f(v[3]);
+    if (!is_finite(x)) o.x += x;
+    if (!is_finite(y)) o.y += y;
+    if (!is_finite(z)) o.z += z;
+    if (!is_finite(w)) o.w += w;
+  }
+}
+
+// What a CTA hands to its cluster: per row of the group the running maximum (log2 units), sum and
+// output (binary32, rows of d with 16-byte chunks at chunk ^ (row & mask)).
+struct Partial {
+  uint32_t o, m, l, bad;  // shared-memory addresses; bad: the drafted values that are not finite
+};
+__device__ __forceinline__ uint32_t part_chunk(int32_t row, int32_t chunk, int32_t d, int32_t xor_mask) {
+  return (uint32_t)(row * d * 4 + ((chunk ^ (row & xor_mask)) << 4));
+}
+
+// Merges the cluster's partials, each CTA a share of the outputs, and writes them. Every thread of
+// every CTA of the cluster calls it.
+template <typename T>
+__device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, int32_t split, const Partial& P, int32_t xor_mask) {
+  cluster_sync();
+  const int32_t d4 = A.G.d / 4, total = s.rows * d4;
+  const uint64_t bad = ld_cluster_u64(cluster_map(P.bad, split - 1));
+  for (int32_t i = s.part * blockDim.x + threadIdx.x; i < total; i += split * blockDim.x) {
+    const int32_t row = i / d4, c = i - row * d4;
+    float m[kMaxSplit], M = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < kMaxSplit; ++p) {
+      m[p] = p < split ? ld_cluster(cluster_map(P.m + row * 4, p)) : -INFINITY;
+      M = fmaxf(M, m[p]);
+    }
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kMaxSplit; ++p) {
+      if (p >= split || m[p] == -INFINITY) continue;  // nothing seen there: its outputs were not written
+      const float f = ex2(m[p] - M);
+      const float4 x = ld_cluster4(cluster_map(P.o + part_chunk(row, c, A.G.d, xor_mask), p));
+      l = fmaf(f, ld_cluster(cluster_map(P.l + row * 4, p)), l);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const int32_t mrow = s.row0 + row;
+    if (bad) add_not_finite<T>(A, s, bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, o);
+    store4((T*)A.out + row_offset(A, s, mrow) + c * 4, o);
+  }
+  cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+// ---- CUDA cores: binary32, and bf16 shapes the tensor-core kernel does not take ---------------------
+//
+// 128 threads, 32 rows x 64 tokens. S = Q K^T as 4 x 4 per thread (rows tr*4+i, tokens tc+16j), the
+// softmax of a row over the 16 threads that hold it, then O += P V as 4 rows x 2 DV dims per thread.
+// Operands are binary32 in shared memory; rows of d + 4 floats keep the 16-byte loads of eight
+// different rows on different banks.
+constexpr int kCudaThreads = 128, kCudaRows = 32;
+
+__host__ __device__ constexpr int cuda_pitch(int d) { return d + 4; }
+__host__ __device__ constexpr size_t cuda_smem(int d, int kb, int tiles) {
+  return (size_t)(kCudaRows + 2 * kTile) * cuda_pitch(d) * 4 + (size_t)kCudaRows * (kTile + 4) * 4 + kCudaRows * 8 + 64 +
+         ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+template <typename T, int DV>
+__global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs A, const int32_t split) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int d = DV * 32, pitch = cuda_pitch(d);
+  float* qs = reinterpret_cast<float*>(smem);      // [32][pitch]
+  float* ks = qs + kCudaRows * pitch;              // [64][pitch]
+  float* vs = ks + kTile * pitch;                  // [64][pitch]
+  float* ps = vs + kTile * pitch;                  // [32][64 + 4]
+  float* ms = ps + kCudaRows * (kTile + 4);        // [32]
+  float* ls = ms + kCudaRows;                      // [32]
+  uint64_t* bad = reinterpret_cast<uint64_t*>(ls + kCudaRows);
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(bad + 1);
+  uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 2);
+  uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
+
+  const Site s = make_site(A, split, kCudaRows);
+  if (s.rows <= 0) return;
+  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
+  const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
+  if (tid == 0) *bad = 0;
+  read_slots(A, s, nv);
+  for (int i = tid; i < kCudaRows * (d / 4); i += kCudaThreads) {
+    const int row = i / (d / 4), c = i % (d / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < s.rows) x = load4((const T*)A.q + row_offset(A, s, s.row0 + row) + c * 4);
+    *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = x;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int32_t n = list_tiles(nv, A.G.kb, spt, tiles);
+    if (tid == 0) {
+      *n_tiles = n;
+      if (A.ctr && s.part == 0 && blockIdx.y == 0) {
+        int32_t slots = 0;
+        for (int32_t i = 0; i < A.G.kb; ++i) slots += nv[i] != 0;
+        atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
+      }
+    }
+  }
+  __syncthreads();
+  const bool draft = s.part == split - 1;
+  const int32_t mine = (*n_tiles - s.part + split - 1) / split + (draft ? 1 : 0);
+  const float scale = kLog2e / sqrtf((float)d);
+
+  uint64_t sees[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t row = tr * 4 + i;
+    sees[i] = row < s.rows ? A.mask[(int64_t)s.r * A.T + (s.row0 + row) / A.G.g] & low_bits(s.cnt) : 0;
+  }
+  float o[4][2 * DV], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2 * DV; ++c) o[i][c] = 0.f;
+  }
+  const uint8_t* unit = A.pool + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb * A.G.block_bytes;
+
+  for (int32_t it = 0; it < mine; ++it) {
+    const bool is_draft = draft && it == 0;
+    const int32_t slot0 = is_draft ? 0 : tiles[s.part + (it - (draft ? 1 : 0)) * split] * spt;
+    __syncthreads();  // the tile before has been read
+    for (int i = tid; i < kTile * (d / 4); i += kCudaThreads) {
+      const int j = i / (d / 4), c = i % (d / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (is_draft) {
+        if (j < s.cnt) {
+          const int64_t at = draft_offset(A, s, j) + c * 4;
+          x = load4((const T*)A.k + at);
+          y = load4((const T*)A.v + at);
+          if (!(is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w))) {
+            atomicOr(reinterpret_cast<unsigned long long*>(bad), 1ull << j);
+            if (!is_finite(y.x)) y.x = 0.f;
+            if (!is_finite(y.y)) y.y = 0.f;
+            if (!is_finite(y.z)) y.z = 0.f;
+            if (!is_finite(y.w)) y.w = 0.f;
+          }
+        }
+      } else {
+        const int32_t slot = slot0 + j / bs, off = j % bs;
+        if (j < tt && slot < A.G.kb && off < nv[slot]) {
+          const T* kp = reinterpret_cast<const T*>(unit + slot * A.G.block_bytes) + (int64_t)off * d + c * 4;
+          x = load4(kp);
+          y = load4(kp + (int64_t)bs * d);
+        }
+      }
+      *reinterpret_cast<float4*>(ks + j * pitch + c * 4) = x;
+      *reinterpret_cast<float4*>(vs + j * pitch + c * 4) = y;
+    }
+    __syncthreads();
+    float sc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < d; c += 4) {
+      float4 qv[4], kv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (tr * 4 + i) * pitch + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (tc + 16 * j) * pitch + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sc[i][j] = fmaf(qv[i].w, kv[j].w, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].x, kv[j].x, sc[i][j]))));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = tc + 16 * j;
+      const int32_t slot = slot0 + tok / bs;
+      const bool valid = !is_draft && tok < tt && slot < A.G.kb && tok % bs < nv[slot];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sc[i][j] = (is_draft ? (sees[i] >> tok & 1) != 0 : valid) ? sc[i][j] * scale : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = fmaxf(fmaxf(sc[i][0], sc[i][1]), fmaxf(sc[i][2], sc[i][3]));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - ref);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(sc[i][j] - ref);
+        sum += p;
+        ps[(tr * 4 + i) * (kTile + 4) + tc + 16 * j] = p;
+      }
+      m[i] = mn;
+      l[i] = l[i] * f + sum;  // of this thread's tokens; summed over the 16 threads at the end
+#pragma unroll
+      for (int c = 0; c < 2 * DV; ++c) o[i][c] *= f;
+    }
+    __syncwarp();  // the rows of ps are read by the half-warp that wrote them
+#pragma unroll 2
+    for (int t = 0; t < kTile; t += 4) {
+      float4 pv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (tr * 4 + i) * (kTile + 4) + t);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int c = 0; c < DV; ++c) {
+          const float2 x = *reinterpret_cast<const float2*>(vs + (t + u) * pitch + 32 * c + 2 * tc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = u == 0 ? pv[i].x : u == 1 ? pv[i].y : u == 2 ? pv[i].z : pv[i].w;
+            o[i][2 * c] = fmaf(p, x.x, o[i][2 * c]);
+            o[i][2 * c + 1] = fmaf(p, x.y, o[i][2 * c + 1]);
+          }
+        }
+    }
+  }
+  __syncthreads();  // every tile read: the key tile becomes the partial outputs
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+    const int row = tr * 4 + i;
+#pragma unroll
+    for (int c = 0; c < DV; ++c) *reinterpret_cast<float2*>(ks + row * d + 32 * c + 2 * tc) = make_float2(o[i][2 * c], o[i][2 * c + 1]);
+    if (tc == 0) {
+      ms[row] = m[i];
+      ls[row] = l[i];
+    }
+  }
+  const Partial P{smem_u32(ks), smem_u32(ms), smem_u32(ls), smem_u32(bad)};
+  if (split > 1) {
+    merge_cluster<T>(A, s, split, P, 0);
+    return;
+  }
+  __syncthreads();
+  for (int i = tid; i < s.rows * (d / 4); i += kCudaThreads) {
+    const int row = i / (d / 4), c = i % (d / 4);
+    float4 x = *reinterpret_cast<const float4*>(ks + row * d + c * 4);
+    const float inv = ls[row] == 0.f ? 0.f : 1.f / ls[row];
+    x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    const int32_t mrow = s.row0 + row;
+    if (*bad) add_not_finite<T>(A, s, *bad & low_bits(s.cnt) & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, x);
+    store4((T*)A.out + row_offset(A, s, mrow) + c * 4, x);
+  }
+}
+
+// CTAs per cluster: as many as fill `slots` CTA places once, a tile of the pool each at least.
+int32_t pick_split(int64_t clusters, int64_t slots, int32_t tiles) {
+  int64_t s = slots / clusters;
+  if (s > tiles) s = tiles;
+  return (int32_t)(s < 1 ? 1 : s > kMaxSplit ? kMaxSplit : s);
+}
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+template <typename... P, typename... Q>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int32_t split, cudaStream_t s, Q&&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
+}
+
+template <typename T, int DV>
+cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
+  const int32_t groups = (A.T * A.G.g + kCudaRows - 1) / kCudaRows;
+  const size_t smem = cuda_smem(DV * 32, A.G.kb, tiles);
+  const int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
+  const int64_t units = (int64_t)n_active * A.G.Hkv;
+  const int32_t split = pick_split(units * groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles);
+  return launch_cluster(tree_cuda_kernel<T, DV>, dim3((unsigned)(units * split), groups), kCudaThreads, smem, split, s, A, split);
+}
+
+template <typename T>
+cudaError_t run_cuda_dv(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  switch (A.G.d / 32) {
+    case 1: return run_cuda<T, 1>(A, n_active, s);
+    case 2: return run_cuda<T, 2>(A, n_active, s);
+    case 3: return run_cuda<T, 3>(A, n_active, s);
+    case 4: return run_cuda<T, 4>(A, n_active, s);
+    case 5: return run_cuda<T, 5>(A, n_active, s);
+    case 6: return run_cuda<T, 6>(A, n_active, s);
+    case 7: return run_cuda<T, 7>(A, n_active, s);
+    default: return run_cuda<T, 8>(A, n_active, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tree(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  if (n_active <= 0) return cudaSuccess;
+  return A.G.dtype == OKV_F32 ? run_cuda_dv<float>(A, n_active, s) : run_cuda_dv<__nv_bfloat16>(A, n_active, s);
+}
+
+}  // namespace okv
+
+extern "C" okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, int32_t q_heads, int32_t kv_heads,
+                                             int32_t head_dim, int32_t block_size, int32_t slots, int32_t dtype,
+                                             const void* pool, const int32_t* slot_block, const int32_t* lengths,
+                                             const int32_t* counts, const void* q, const void* k_draft,
+                                             const void* v_draft, const uint64_t* mask, void* out, void* stream) {
+  using namespace okv;
+  Geom G{};
+  if (!tree_geom(n_requests, q_heads, kv_heads, head_dim, block_size, slots, dtype, &G)) return OKV_EINVAL;
+  if (n_draft <= 0 || n_draft > 64) return OKV_EINVAL;
+  if (!pool || !slot_block || !lengths || !q || !k_draft || !v_draft || !mask || !out) return OKV_EINVAL;
+  if (!aligned16(pool) || !aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out)) return OKV_EINVAL;
+  if (okv_status st = check_stream(stream)) return st;
+  TreeArgs A{};
+  A.G = G;
+  A.T = n_draft;
+  A.pool = (const uint8_t*)pool;
+  A.slot_block = slot_block;
+  A.len = lengths;
+  A.counts = counts;
+  A.q = q;
+  A.k = k_draft;
+  A.v = v_draft;
+  A.mask = mask;
+  A.out = out;
+  A.pool_rows = (int64_t)n_requests * kv_heads * slots;
+  return launch_attend_tree(A, n_requests, (cudaStream_t)stream) == cudaSuccess ? OKV_OK : OKV_ECUDA;
+}

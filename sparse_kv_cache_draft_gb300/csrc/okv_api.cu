@@ -21,12 +21,14 @@
 #include <chrono>
 #include <thread>
 
-#include "okv_internal.h"
+#include "okv_tree.h"
 
 using okv::Counters;
 using okv::Geom;
 using okv::LayerState;
 using okv::ReqTables;
+
+constexpr int32_t kMaxDraft = 64;  // drafted tokens of a request: the bits of a mask
 
 struct TimedLaunch {
   int kind;
@@ -71,6 +73,7 @@ struct okv_ctx {
   uint32_t* scores2 = nullptr;
   int32_t* stage_arrivals2 = nullptr;
   int32_t* attend_arrivals = nullptr;  // [R * Hkv]: attention split CTAs finished per unit
+  int32_t* accept_dev = nullptr;       // [layers][R][1 + 64]: okv_append_tree's counts [R], then its indices
   int32_t* append_arrivals = nullptr;  // [layers][R]: append CTAs finished per request (kept at zero)
   int32_t* gather_work = nullptr;      // [layers][2]: gather work and exit counters (kept at zero)
   float* step_coef = nullptr;          // [2][layers][R][Hkv][2d]: okv_step's coefficients of its drafts
@@ -91,6 +94,7 @@ struct okv_ctx {
   std::vector<int32_t> local_cap;      // [R] its entries per unit (-1: full-KV request)
   std::vector<int32_t> len_host;       // [L][R]
   std::vector<int> shared_buf;         // [R] host buffer shared with another active request
+  std::vector<int32_t> accept_host;    // [R][1 + 64]: source of okv_append_tree's copy
 
   // streams and events
   cudaStream_t sel_stream = nullptr, copy_stream = nullptr;
@@ -327,7 +331,7 @@ void okv_destroy(okv_ctx* c) {
                   c->err_dev, c->ctr_dev, c->partials, c->coef_buf, c->pred_coef, c->scores, c->stage_arrivals, c->attend_arrivals,
                   c->scores2, c->stage_arrivals2,
                   c->local_of, c->local_used, c->route, c->local_kv_dev, c->local_cap_dev,
-                  c->append_arrivals, c->step_coef, c->gather_work};
+                  c->append_arrivals, c->step_coef, c->gather_work, c->accept_dev};
   for (void* p : bufs)
     if (p) cudaFree(p);
   delete c;
@@ -421,7 +425,8 @@ okv_status okv_create(const okv_config* cfg, okv_ctx** out) {
             alloc((void**)&c->route, (size_t)L * U * G.kb * 4) && alloc((void**)&c->local_kv_dev, G.R * 8) &&
             alloc((void**)&c->local_cap_dev, G.R * 4) && alloc((void**)&c->append_arrivals, (size_t)L * G.R * 4) &&
             alloc((void**)&c->step_coef, (size_t)2 * L * U * 2 * G.d * sizeof(float)) &&
-            alloc((void**)&c->gather_work, (size_t)L * 2 * 4);
+            alloc((void**)&c->gather_work, (size_t)L * 2 * 4) &&
+            alloc((void**)&c->accept_dev, (size_t)L * G.R * (1 + kMaxDraft) * 4);
   // Staging lanes: odd layers stage on a second stream with a workspace of its own, so one layer's
   // per-unit selection tails overlap the next layer's scoring (measured on GB300: +3% decode
   // tok/s at the 32B-class shapes, the same at Qwen3-8B batch 128). OKV_STAGE_LANES=1 keeps one.
@@ -517,6 +522,7 @@ okv_status okv_create(const okv_config* cfg, okv_ctx** out) {
   c->local_cap.assign(G.R, -1);
   c->len_host.assign((size_t)G.L * G.R, 0);
   c->shared_buf.assign(G.R, 0);
+  c->accept_host.assign((size_t)G.R * (1 + kMaxDraft), 0);
 
   if (st == OKV_OK && okv::attend_uses_tensor_cores(G)) {
     // pool as rows of 256 bytes: dims {64 elements, 2 halves, rows}, box = one slot (32 rows)
@@ -718,16 +724,30 @@ okv_status okv_remove_request(okv_ctx* c, int32_t req) {
 
 namespace {
 
-okv_status append_check(okv_ctx* c, int32_t layer) {
+// `counts`: tokens to append per request, or NULL for one each.
+okv_status append_check(okv_ctx* c, int32_t layer, const char* who = "okv_append", const int32_t* counts = nullptr) {
   const Geom& G = c->G;
-  if (layer < 0 || layer >= G.L) return fail(c, OKV_EINVAL, "okv_append: layer %d out of range", layer);
+  if (layer < 0 || layer >= G.L) return fail(c, OKV_EINVAL, "%s: layer %d out of range", who, layer);
   for (int32_t r : c->active_list) {
+    const int32_t add = counts ? counts[r] : 1;
+    if (add == 0) continue;
     if (c->shared_buf[r])
-      return fail(c, OKV_EINVAL, "okv_append: request %d shares its host buffer with another active request", r);
+      return fail(c, OKV_EINVAL, "%s: request %d shares its host buffer with another active request", who, r);
     const int32_t n = c->len_host[(size_t)layer * G.R + r];
-    if ((int64_t)n >= (int64_t)c->cap_blocks[r] * G.bs)
-      return fail(c, OKV_EINVAL, "okv_append: request %d is full at layer %d", r, layer);
+    if ((int64_t)n + add > (int64_t)c->cap_blocks[r] * G.bs)
+      return fail(c, OKV_EINVAL, "%s: request %d is full at layer %d", who, r, layer);
   }
+  return OKV_OK;
+}
+
+// The calls on rows and drafted trees launch on the current device, and may refuse a capture.
+okv_status device_check(okv_ctx* c, const char* who, cudaStream_t s, bool* capturing) {
+  int dev = 0;
+  OKV_CUDA(c, cudaGetDevice(&dev));
+  if (dev != c->device) return fail(c, OKV_EINVAL, "%s: the context's device %d is not current", who, c->device);
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  OKV_CUDA(c, cudaStreamIsCapturing(s, &cs));
+  *capturing = cs != cudaStreamCaptureStatusNone;
   return OKV_OK;
 }
 
@@ -757,6 +777,70 @@ okv_status okv_append(okv_ctx* c, int32_t layer, const void* k_new, const void* 
   if (!k_new || !v_new) return fail(c, OKV_EINVAL, "okv_append: NULL input");
   if (okv_status st = append_check(c, layer)) return st;
   return append_enqueue(c, layer, k_new, v_new, (cudaStream_t)stream);
+}
+
+okv_status okv_append_qkv(okv_ctx* c, int32_t layer, const void* qkv, int64_t row_stride, const okv_rotary* rotary, void* q,
+                          void* stream) {
+  if (!c) return OKV_EINVAL;
+  const Geom& G = c->G;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!qkv || !rotary || !q) return fail(c, OKV_EINVAL, "okv_append_qkv: NULL pointer");
+  okv::RowArgs A;
+  if (!okv::row_args(rotary, G.Hq, G.Hkv, G.d, G.dtype, qkv, row_stride, q, &A))
+    return fail(c, OKV_EINVAL, "okv_append_qkv: row_stride, alignment or rotary outside its limits");
+  if (okv_status st = append_check(c, layer, "okv_append_qkv")) return st;
+  bool capturing = false;
+  if (okv_status st = device_check(c, "okv_append_qkv", s, &capturing)) return st;
+  if (capturing) return fail(c, OKV_ESTATE, "okv_append_qkv: stream is being captured");
+  const int32_t n_active = (int32_t)c->active_list.size();
+  if (n_active == 0) return OKV_OK;
+  if (c->staged_once[layer]) OKV_CUDA(c, cudaStreamWaitEvent(s, c->ev_staged[layer], 0));
+  Timer t(c, OKV_K_APPEND, s);
+  OKV_CUDA(c, okv::launch_append_qkv(A, G, layer_state(c, layer), req_tables(c), n_active, layer, c->err_dev, s));
+  t.stop(1);
+  for (int32_t r : c->active_list) c->len_host[(size_t)layer * G.R + r] += 1;
+  return OKV_OK;
+}
+
+okv_status okv_append_tree(okv_ctx* c, int32_t layer, int32_t n_draft, const void* k_draft, const void* v_draft, const int32_t* counts,
+                           const int32_t* index, void* stream) {
+  if (!c) return OKV_EINVAL;
+  const Geom& G = c->G;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!k_draft || !v_draft || !counts || !index) return fail(c, OKV_EINVAL, "okv_append_tree: NULL pointer");
+  if (n_draft <= 0 || n_draft > kMaxDraft) return fail(c, OKV_EINVAL, "okv_append_tree: n_draft %d not in 1..%d", n_draft, kMaxDraft);
+  if (!okv::aligned16(k_draft) || !okv::aligned16(v_draft))
+    return fail(c, OKV_EINVAL, "okv_append_tree: k_draft and v_draft must be 16-byte aligned");
+  bool any = false;
+  for (int32_t r : c->active_list) {
+    if (counts[r] < 0 || counts[r] > n_draft)
+      return fail(c, OKV_EINVAL, "okv_append_tree: request %d: count %d not in 0..%d", r, counts[r], n_draft);
+    any = any || counts[r] > 0;
+    for (int32_t i = 0; i < counts[r]; ++i) {
+      const int32_t j = index[(size_t)r * n_draft + i];
+      if (j < 0 || j >= n_draft) return fail(c, OKV_EINVAL, "okv_append_tree: request %d: index %d not in 0..%d", r, j, n_draft - 1);
+    }
+  }
+  if (okv_status st = append_check(c, layer, "okv_append_tree", counts)) return st;
+  bool capturing = false;
+  if (okv_status st = device_check(c, "okv_append_tree", s, &capturing)) return st;
+  if (capturing) return fail(c, OKV_ESTATE, "okv_append_tree: stream is being captured");
+  if (!any) return OKV_OK;
+  if (c->staged_once[layer]) OKV_CUDA(c, cudaStreamWaitEvent(s, c->ev_staged[layer], 0));
+  // A layer's counts and indices stay in its own part of accept_dev: the copy follows the work on
+  // `stream`, the layer's last append among it. The copy's source is pageable, so it has been read
+  // when the copy call returns (the caller's arrays may be page-locked).
+  memcpy(c->accept_host.data(), counts, (size_t)G.R * 4);
+  memcpy(c->accept_host.data() + G.R, index, (size_t)G.R * n_draft * 4);
+  int32_t* dcounts = c->accept_dev + (size_t)layer * G.R * (1 + kMaxDraft);
+  int32_t* dindex = dcounts + G.R;
+  OKV_CUDA(c, cudaMemcpyAsync(dcounts, c->accept_host.data(), (size_t)G.R * (1 + n_draft) * 4, cudaMemcpyHostToDevice, s));
+  Timer t(c, OKV_K_APPEND, s);
+  OKV_CUDA(c, okv::launch_append_tree(G, layer_state(c, layer), req_tables(c), (int32_t)c->active_list.size(), layer, n_draft, k_draft,
+                                      v_draft, dcounts, dindex, c->append_arrivals + (size_t)layer * G.R, c->err_dev, s));
+  t.stop(1);
+  for (int32_t r : c->active_list) c->len_host[(size_t)layer * G.R + r] += counts[r];
+  return OKV_OK;
 }
 
 }  // extern "C"
@@ -905,6 +989,46 @@ okv_status okv_attend_lookahead(okv_ctx* c, int32_t layer, const void* q, const 
                                 void* draft_out, void* stream) {
   if (c && (!draft_q || !draft_out)) return fail(c, OKV_EINVAL, "okv_attend_lookahead: NULL draft pointer");
   return attend_impl(c, "okv_attend_lookahead", layer, q, out, draft_q, draft_out, stream);
+}
+
+okv_status okv_attend_tree(okv_ctx* c, int32_t layer, int32_t n_draft, const int32_t* counts, const void* q, const void* k_draft,
+                           const void* v_draft, const uint64_t* mask, void* out, void* stream) {
+  if (!c) return OKV_EINVAL;
+  const Geom& G = c->G;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (layer < 0 || layer >= G.L) return fail(c, OKV_EINVAL, "okv_attend_tree: layer %d out of range", layer);
+  if (n_draft <= 0 || n_draft > kMaxDraft) return fail(c, OKV_EINVAL, "okv_attend_tree: n_draft %d not in 1..%d", n_draft, kMaxDraft);
+  if (!q || !k_draft || !v_draft || !mask || !out) return fail(c, OKV_EINVAL, "okv_attend_tree: NULL pointer");
+  for (const void* p : {q, k_draft, v_draft, (const void*)out})
+    if (!okv::aligned16(p)) return fail(c, OKV_EINVAL, "okv_attend_tree: queries, keys, values and outputs must be 16-byte aligned");
+  bool capturing = false;
+  if (okv_status st = device_check(c, "okv_attend_tree", s, &capturing)) return st;
+  if (capturing && c->staged_once[layer])
+    return fail(c, OKV_ESTATE, "okv_attend_tree: stream is being captured and cannot wait for the layer's staging");
+  const int32_t n_active = (int32_t)c->active_list.size();
+  if (n_active == 0) return OKV_OK;
+  if (c->staged_once[layer]) OKV_CUDA(c, cudaStreamWaitEvent(s, c->ev_staged[layer], 0));
+  const LayerState S = layer_state(c, layer);
+  okv::TreeArgs A{};
+  A.G = G;
+  A.T = n_draft;
+  A.pool = S.pool;
+  A.slot_block = S.slot_block;
+  A.len = S.len;
+  A.active = c->active_dev;
+  A.counts = counts;
+  A.q = q;
+  A.k = k_draft;
+  A.v = v_draft;
+  A.mask = mask;
+  A.out = out;
+  A.pool_rows = c->per_layer_units * G.kb;
+  A.ctr = c->ctr_dev;
+  A.err = c->err_dev;
+  Timer t(c, OKV_K_ATTEND, s);
+  OKV_CUDA(c, okv::launch_attend_tree(A, n_active, s));
+  t.stop(1);
+  return OKV_OK;
 }
 
 okv_status okv_step(okv_ctx* c, const void* q, const void* draft_q, void* out, const void* k_new,
