@@ -162,7 +162,7 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
-// ---- CUDA cores: binary32, and bf16 shapes the tensor-core kernel does not take ---------------------
+// ---- CUDA cores: binary32 ---------------------------------------------------------------------------
 //
 // 128 threads, 32 rows x 64 tokens. S = Q K^T as 4 x 4 per thread (rows tr*4+i, tokens tc+16j), the
 // softmax of a row over the 16 threads that hold it, then O += P V as 4 rows x 2 DV dims per thread.
@@ -377,6 +377,434 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   }
 }
 
+// ---- tensor cores: bf16 ------------------------------------------------------------------------------
+//
+// A CTA holds NW groups of 128 rows (one softmax warpgroup each) over the same tiles of 64 tokens.
+// One warp copies K and V tiles by TMA into a ring of buffers, one thread issues the MMAs:
+//   S = Q K^T   128 x 64, Q and K in shared memory, S in TMEM (two buffers)
+//   O += P V    128 x d,  P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
+// S of the next tile is computed while the warpgroup works on this one's softmax, a thread to a row.
+// The running maximum moves only when a row grows past it by 2^8 (the weights then stay below 2^8,
+// exact in binary32 sums and as exact in bf16 as any other); only then is O read back and scaled.
+// Weights are rounded to bf16 for the second product, as the tensor cores take them; their sum is of
+// the unrounded weights.
+//
+// Rows past the group's are whatever the shared memory behind Q holds: they reach only outputs that
+// are not stored, and warps of such rows skip the softmax.
+//
+// Operand tiles are lines of 64 (or, for d not a multiple of 64, 32) elements: chunk c of a tile is
+// [rows][line] under the 128-byte (64-byte) swizzle, Q and K K-major, V MN-major. A K or V tile is d / line
+// TMA copies of whole slots, straight from the pool's layout.
+
+template <int D>
+struct Lines {
+  static constexpr int kElems = D % 64 == 0 ? 64 : 32;
+  static constexpr int kBytes = kElems * 2;
+  static constexpr int kChunks = D / kElems;
+  static constexpr uint32_t kSwizzle = kElems == 64 ? 2 : 4;  // of the operand descriptors
+  static constexpr uint32_t kGroup = 8 * kBytes;              // 8 rows
+  static constexpr int kBuf = kTile * D * 2;                  // a tile of K or V
+  // byte offset of 16-byte piece c (0 .. kBytes / 16 - 1) of line `row` of a chunk
+  __device__ static __forceinline__ uint32_t at(int row, int c) {
+    return kElems == 64 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+  }
+};
+
+// S, P and O have a barrier each for even and for odd tiles: a barrier's parity tells a phase from the
+// next one only, and the softmax may be done with tile i + 1 before the issuing thread has looked at
+// tile i, as that thread may be done with O of tile i - 1 before the softmax has looked at tile i - 2.
+constexpr int kMaxRing = 12;
+struct MmaBars {
+  uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][2], p_full[2][2], pv_done[2][2], drain;
+  uint64_t bad;
+  uint32_t tmem;
+  int32_t n_tiles, failed;
+};
+
+__host__ __device__ constexpr size_t mma_misc(int kb, int tiles) {
+  return sizeof(MmaBars) + ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// A 16-byte piece of bf16 values with those that are not finite as zero; whether there were any.
+__device__ __forceinline__ bool clean(uint4& u) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u, any = true;
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu, any = true;
+  }
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 128 + 64, D <= 128 && NW == 1 ? 2 : 1)
+tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const int32_t split, const int32_t ring, const int32_t q_rows) {
+  using L = Lines<D>;
+  constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S, S, O
+  constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem;                                                        // [NW][chunks][q_rows][line]
+  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][64][line]
+  MmaBars& B = *reinterpret_cast<MmaBars*>(rs + (size_t)ring * L::kBuf);
+  uint8_t* nv = reinterpret_cast<uint8_t*>(&B + 1);                          // [kb]
+  uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
+
+  const Site s = make_site(A, split, NW * 128);
+  if (s.rows <= 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1;
+  const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
+  const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
+  const uint32_t ring0 = smem_u32(rs);
+
+  if (is_mma) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+  if (tid == 0) {
+    for (int i = 0; i < ring; ++i) {
+      mbar_init(smem_u32(&B.full[i]), 1);
+      mbar_init(smem_u32(&B.empty[i]), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&B.s_full[w][0]), 1);
+      mbar_init(smem_u32(&B.s_full[w][1]), 1);
+      mbar_init(smem_u32(&B.p_full[w][0]), 128);
+      mbar_init(smem_u32(&B.p_full[w][1]), 128);
+      mbar_init(smem_u32(&B.pv_done[w][0]), 1);
+      mbar_init(smem_u32(&B.pv_done[w][1]), 1);
+    }
+    mbar_init(smem_u32(&B.drain), 1);
+    fence_mbar_init();
+    if (draft) {  // buffers 0 and 2 are filled below, once
+      mbar_arrive(smem_u32(&B.full[0]));
+      mbar_arrive(smem_u32(&B.full[2]));
+    }
+    B.failed = 0;
+    B.bad = 0;
+  }
+  read_slots(A, s, nv);
+  if (warp < NW * 4) {
+    constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
+    for (int i = tid; i < s.rows * kPieces; i += NW * 128) {
+      const int row = i / kPieces, c = i % kPieces;
+      const uint4 x = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.q + row_offset(A, s, s.row0 + row) + c * 8);
+      uint8_t* chunk = qs + ((size_t)(row >> 7) * L::kChunks + c / kLine) * q_rows * L::kBytes;
+      *reinterpret_cast<uint4*>(chunk + L::at(row & 127, c % kLine)) = x;
+    }
+    if (tt < kTile)  // the copies leave these lines alone; as V they meet weights of zero
+      for (int i = tid; i < ring * (kTile - tt) * kPieces; i += NW * 128) {
+        const int c = i % kPieces, rest = i / kPieces, row = tt + rest % (kTile - tt), b = rest / (kTile - tt);
+        *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(row, c % kLine)) = make_uint4(0, 0, 0, 0);
+      }
+  }
+  __syncthreads();
+  if (warp < NW * 4 && draft) {
+    constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
+    for (int i = tid; i < kTile * kPieces; i += NW * 128) {
+      const int j = i / kPieces, c = i % kPieces;
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (j < s.cnt) {
+        const int64_t at = draft_offset(A, s, j) + c * 8;
+        x = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.k + at);
+        y = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + at);
+        if (clean(y)) atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
+      }
+      const size_t to = (size_t)(c / kLine) * kTile * L::kBytes + L::at(j, c % kLine);
+      *reinterpret_cast<uint4*>(rs + to) = x;
+      *reinterpret_cast<uint4*>(rs + (size_t)2 * L::kBuf + to) = y;
+    }
+  }
+  if (warp < NW * 4) fence_proxy_async();
+  if (is_copy) {
+    const int32_t n = list_tiles(nv, A.G.kb, spt, tiles);
+    if (lane == 0) B.n_tiles = n;
+    if (A.ctr && s.part == 0 && blockIdx.y == 0) {
+      int32_t slots = 0;
+      for (int32_t i = lane; i < A.G.kb; i += 32) slots += nv[i] != 0;
+      slots = __reduce_add_sync(0xffffffffu, slots);
+      if (lane == 0) atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B.tmem;
+  const int32_t lead = draft ? 1 : 0;
+  const int32_t n = (B.n_tiles - s.part + split - 1) / split + lead;  // this CTA's tiles
+  // Tile i's K is the (2i - 1)-th use of the ring (the first: use 0), its V the (2i + 2)-th: the order
+  // in which the MMAs take them, S of tile i + 1 before O of tile i.
+  auto k_use = [](int32_t i) { return i == 0 ? 0 : 2 * i - 1; };
+  auto v_use = [](int32_t i) { return 2 * i + 2; };
+  auto full = [&](int32_t use) { return mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1)); };
+  // ... by all lanes of a warp: the TMEM loads and stores that follow are by whole warps
+  auto warp_wait = [&](uint64_t& bar, int32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
+  };
+  auto fail = [&](int32_t site) {
+    *(volatile int32_t*)&B.failed = 1;
+    if (A.err) record_error(A.err, kErrTimeout, -3, s.r, site);
+  };
+  float m_run = -INFINITY, l_run = 0.f;
+
+  if (is_copy) {
+    if (lane == 0) {
+      const int64_t slot_base = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+      int32_t last = -1;  // the last use filled
+      auto fill = [&](int32_t i, bool v) {
+        if (i < lead) return true;
+        const int32_t use = v ? v_use(i) : k_use(i), b = use % ring;
+        if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)((use / ring - 1) & 1))) return false;
+        const uint32_t bar = smem_u32(&B.full[b]);
+        const int32_t slot = (int32_t)(slot_base + (int64_t)tiles[s.part + (i - lead) * split] * spt);
+        mbar_expect_tx(bar, (uint32_t)(tt * D * 2));
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_5d(ring0 + b * L::kBuf + c * kTile * L::kBytes, &map, bar, 0, c, 0, v ? 1 : 0, slot);
+        last = use;
+        return true;
+      };
+      bool ok = true;
+      if (n > 0) ok = fill(0, false);
+      for (int32_t i = 0; i < n && ok; ++i) {
+        if (i + 1 < n) ok = fill(i + 1, false);
+        if (ok) ok = fill(i, true);
+      }
+      if (!ok) {
+        fail(0);
+        // the copies still in flight land before the shared memory is given up (bounded)
+        for (int32_t use = last > ring ? last - ring : 0; use <= last; ++use) full(use);
+      }
+    }
+  } else if (is_mma) {
+    if (lane == 0) {
+      const uint32_t q0 = smem_u32(qs);
+      auto qk = [&](int32_t i) {
+        const int32_t use = k_use(i);
+        if (!full(use)) return false;
+        tc_fence_after();
+        const uint32_t k0 = ring0 + (use % ring) * L::kBuf;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            constexpr int kSteps = L::kElems / 16;
+            const uint32_t qa = q0 + (w * L::kChunks + c / kSteps) * q_rows * L::kBytes + (c % kSteps) * 32;
+            const uint32_t ka = k0 + (c / kSteps) * kTile * L::kBytes + (c % kSteps) * 32;
+            mma_ss(tmem + w * kCols + (i & 1) * kTile, smem_desc(qa, 16, L::kGroup, L::kSwizzle), smem_desc(ka, 16, L::kGroup, L::kSwizzle),
+                   kDescQK, c > 0);
+          }
+          mma_commit(smem_u32(&B.s_full[w][i & 1]));
+        }
+        mma_commit(smem_u32(&B.empty[use % ring]));
+        return true;
+      };
+      bool ok = n > 0 ? qk(0) : true;
+      for (int32_t i = 0; i < n && ok; ++i) {
+        if (i + 1 < n && !qk(i + 1)) ok = false;
+        if (!ok || !full(v_use(i))) {
+          ok = false;
+          break;
+        }
+        const uint32_t v0 = ring0 + (v_use(i) % ring) * L::kBuf;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          if (!mbar_wait_timed(smem_u32(&B.p_full[w][i & 1]), (uint32_t)((i >> 1) & 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kTile / 16; ++c)
+            mma_ts(tmem + w * kCols + 2 * kTile, tmem + w * kCols + (i & 1) * kTile + c * 8,
+                   smem_desc(v0 + c * 2 * L::kGroup, kTile * L::kBytes, L::kGroup, L::kSwizzle), kDescPV, i > 0 || c > 0);
+          mma_commit(smem_u32(&B.pv_done[w][i & 1]));
+        }
+        mma_commit(smem_u32(&B.empty[v_use(i) % ring]));
+      }
+      if (!ok) {
+        fail(1);
+        mma_commit(smem_u32(&B.drain));
+        mbar_wait_timed(smem_u32(&B.drain), 0);
+      }
+    }
+  } else {
+    const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
+    const uint32_t my = tmem + w * kCols + lanes;
+    const bool active = w * 128 + (warp & 3) * 32 < s.rows;
+    const float scale = kLog2e * rsqrtf((float)D);
+    uint64_t sees = 0;
+    if (draft && wrow < s.rows) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
+    const int32_t so0 = lane / bs, to0 = lane % bs, so1 = (lane + 32) / bs, to1 = (lane + 32) % bs;
+    for (int32_t i = 0; i < n; ++i) {
+      uint64_t vis = sees;
+      bool gaps = false;
+      if (i >= lead) {
+        const int32_t slot0 = tiles[s.part + (i - lead) * split] * spt;
+        const bool v0 = lane < tt && slot0 + so0 < A.G.kb && to0 < nv[slot0 + so0];
+        const bool v1 = lane + 32 < tt && slot0 + so1 < A.G.kb && to1 < nv[slot0 + so1];
+        vis = (uint64_t)__ballot_sync(0xffffffffu, v0) | (uint64_t)__ballot_sync(0xffffffffu, v1) << 32;
+        gaps = vis != low_bits(tt);
+      }
+      if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
+        fail(2);
+        break;
+      }
+      // S of tile i follows O of tile i - 2, so this passes at once; it keeps each barrier's waits in step
+      // with its phases, where tile i - 1's below is waited for only now and then
+      if (i > 1 && !warp_wait(B.pv_done[w][i & 1], ((i - 2) >> 1) & 1)) {
+        fail(6);
+        break;
+      }
+      tc_fence_after();
+      if (active) {
+        uint32_t a[32], b[32];
+        tmem_ld32(a, my + (i & 1) * kTile);
+        tmem_ld32(b, my + (i & 1) * kTile + 32);
+        tmem_wait_ld(a);
+        tmem_wait_ld(b);
+        if (vis != ~0ull) {
+          const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (!(lo >> e & 1)) a[e] = 0xFF800000u;
+            if (!(hi >> e & 1)) b[e] = 0xFF800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        const bool grow = top > m_run + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? top : m_run;
+          const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mn);
+          m_run = mn;
+          l_run *= f;
+          if (i > 0) {
+            if (!warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1)) {
+              fail(3);
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, my + 2 * kTile + c);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(my + 2 * kTile + c, o);
+            }
+          }
+        }
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = ex2(fmaf(__uint_as_float(a[2 * e]), scale, neg)), y = ex2(fmaf(__uint_as_float(a[2 * e + 1]), scale, neg));
+          const float z = ex2(fmaf(__uint_as_float(b[2 * e]), scale, neg)), u = ex2(fmaf(__uint_as_float(b[2 * e + 1]), scale, neg));
+          sum[0] += x;
+          sum[1] += y;
+          sum[2] += z;
+          sum[3] += u;
+          p[e] = pack2(x, y);
+          p[16 + e] = pack2(z, u);
+        }
+        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st32(my + (i & 1) * kTile, p);
+        tmem_wait_st();
+      }
+      if (gaps && w == 0) {
+        // lines of the V tile that hold no valid token may hold anything: zero them before the product
+        if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
+          fail(4);
+          break;
+        }
+        constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
+        uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
+        for (int e = row; e < tt * kPieces; e += 128) {
+          const int j = e / kPieces, c = e % kPieces;
+          if (!(vis >> j & 1)) *reinterpret_cast<uint4*>(v + (size_t)(c / kLine) * kTile * L::kBytes + j * L::kBytes + (c % kLine) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&B.p_full[w][i & 1]));
+    }
+    if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail(5);
+    tc_fence_after();
+  }
+  __syncthreads();  // every product done: the ring and Q become the cluster's partials
+  const bool failed = *(volatile int32_t*)&B.failed != 0;
+  if (warp < NW * 4) {
+    const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row, mrow = s.row0 + wrow;
+    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + 2 * kTile;
+    if (w * 128 + (warp & 3) * 32 < s.rows) {
+      if (split == 1) {
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const uint64_t bad = B.bad && wrow < s.rows ? B.bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g] : 0;
+        __nv_bfloat16* to = (__nv_bfloat16*)A.out + (wrow < s.rows ? row_offset(A, s, mrow) : 0);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(o, my + c);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (wrow >= s.rows || failed) break;
+            float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv, __uint_as_float(o[e + 2]) * inv,
+                                   __uint_as_float(o[e + 3]) * inv);
+            float4 y = make_float4(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv, __uint_as_float(o[e + 6]) * inv,
+                                   __uint_as_float(o[e + 7]) * inv);
+            if (bad) {
+              add_not_finite<__nv_bfloat16>(A, s, bad, c + e, x);
+              add_not_finite<__nv_bfloat16>(A, s, bad, c + e + 4, y);
+            }
+            *reinterpret_cast<uint4*>(to + c + e) = make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+          }
+        }
+      } else {
+        float* ml = reinterpret_cast<float*>(qs);
+        if (wrow < s.rows) {
+          ml[wrow] = failed ? -INFINITY : m_run;
+          ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
+        }
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(o, my + c);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (wrow < s.rows)
+                *reinterpret_cast<uint4*>(rs + part_chunk(wrow, (c + e) / 4, D, 7)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+    }
+  }
+  if (split > 1) {
+    const Partial P{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4), smem_u32(&B.bad)};
+    merge_cluster<__nv_bfloat16>(A, s, split, P, 7);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (is_mma) {
+    tc_fence_after();
+    tmem_free(tmem, kCols * NW);
+  }
+}
+
 // CTAs per cluster: as many as fill `slots` CTA places once, a tile of the pool each at least.
 int32_t pick_split(int64_t clusters, int64_t slots, int32_t tiles) {
   int64_t s = slots / clusters;
@@ -434,11 +862,80 @@ cudaError_t run_cuda_dv(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   }
 }
 
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// The pool as [slots][K, V][tokens][chunks][line], a box of one chunk of the tokens of a tile's slots.
+template <int D>
+cudaError_t pool_map(const TreeArgs& A, int32_t spt, CUtensorMap* map) {
+  using L = Lines<D>;
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const uint64_t token = (uint64_t)D * 2, half = token * A.G.bs;
+  const cuuint64_t dims[5] = {(cuuint64_t)L::kElems, (cuuint64_t)L::kChunks, (cuuint64_t)A.G.bs, 2, (cuuint64_t)A.pool_rows};
+  const cuuint64_t strides[4] = {(cuuint64_t)L::kBytes, token, half, 2 * half};
+  const cuuint32_t box[5] = {(cuuint32_t)L::kElems, 1, (cuuint32_t)A.G.bs, 1, (cuuint32_t)spt};
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(A.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            L::kElems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int D, int NW>
+cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  using L = Lines<D>;
+  const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
+  const int32_t rows = A.T * A.G.g, groups = (rows + NW * 128 - 1) / (NW * 128);
+  const int32_t q_rows = NW > 1 || rows >= 128 ? 128 : (rows + 7) / 8 * 8;
+  // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
+  // that share of the shared memory. It is never so small that a third CTA could come to wait for TMEM.
+  const bool two = D <= 128 && NW == 1;
+  const size_t share = two ? 115712 : 232448, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb, tiles);
+  int32_t ring = (int32_t)((share - rest) / L::kBuf);
+  if (ring > kMaxRing) ring = kMaxRing;
+  size_t smem = rest + (size_t)ring * L::kBuf;
+  const size_t least = (two ? 233472 / 3 : 233472 / 2);
+  if (smem < least) smem = least;
+  const int64_t units = (int64_t)n_active * A.G.Hkv;
+  const int32_t split = pick_split(units * groups, (int64_t)sm_count() * (two ? 2 : 1), tiles);
+  CUtensorMap map;
+  if (cudaError_t e = pool_map<D>(A, spt, &map)) return e;
+  return launch_cluster(tree_mma_kernel<D, NW>, dim3((unsigned)(units * split), groups), NW * 128 + 64, smem, split, s, A, map, split, ring,
+                        q_rows);
+}
+
+cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  const bool wide = A.T * A.G.g > 128;
+  switch (A.G.d) {
+    case 32: return wide ? run_mma<32, 2>(A, n_active, s) : run_mma<32, 1>(A, n_active, s);
+    case 64: return wide ? run_mma<64, 2>(A, n_active, s) : run_mma<64, 1>(A, n_active, s);
+    case 96: return wide ? run_mma<96, 2>(A, n_active, s) : run_mma<96, 1>(A, n_active, s);
+    case 128: return wide ? run_mma<128, 2>(A, n_active, s) : run_mma<128, 1>(A, n_active, s);
+    case 160: return run_mma<160, 1>(A, n_active, s);
+    case 192: return run_mma<192, 1>(A, n_active, s);
+    case 224: return run_mma<224, 1>(A, n_active, s);
+    default: return run_mma<256, 1>(A, n_active, s);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_attend_tree(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   if (n_active <= 0) return cudaSuccess;
-  return A.G.dtype == OKV_F32 ? run_cuda_dv<float>(A, n_active, s) : run_cuda_dv<__nv_bfloat16>(A, n_active, s);
+  return A.G.dtype == OKV_F32 ? run_cuda_dv<float>(A, n_active, s) : run_mma_d(A, n_active, s);
 }
 
 }  // namespace okv
