@@ -9,12 +9,13 @@
 // and the value heads pass. Everything is binary32 with one rounding at the store.
 //
 // Angles: p inv_freq is reduced to less than a turn before anything is rounded to binary32.
-// inv_freq / 2 pi, as a 64-bit fraction of a turn, times the integer p modulo 2^64 is the phase with
-// an error of p 2^-54 turns at most (6e-8 turns at position 2^31 and one radian per position).
+// inv_freq / 2 pi as a 64-bit fraction of a turn, times the integer p modulo 2^64, is the phase, off by
+// p 2^-63 turns at most (2^-32 turns at position 2^31).
 //
-// The rows move once in and once out. A head row is 8 elements on each of d / 8 lanes (a subgroup of
-// the next power of two of lanes); a CTA takes the heads of a few tokens, four head rows in flight
-// per subgroup, and computes the tokens' angles once, while the first loads are on their way.
+// The rows move once in and once out. A head row is 8 elements on each of d / 8 lanes (a subgroup of the
+// next power of two of lanes). A warp takes a row, or a part of its heads where rows are few: it computes
+// the row's angles once, folds weights, cosines and sines into two factors per element that stay in
+// registers for all of its query (then key) heads, and keeps four head rows per subgroup in flight.
 #include <cuda_bf16.h>
 
 #include "okv_tree.h"
@@ -24,7 +25,7 @@ namespace okv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;  // head rows each subgroup loads before it computes
+constexpr int kInFlight = 4;  // head rows of each subgroup in flight
 
 // 8 elements of a head row.
 template <typename T>
@@ -32,6 +33,7 @@ struct Eight;
 template <>
 struct Eight<float> {
   float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + 4);
@@ -51,6 +53,7 @@ struct Eight<float> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 u;
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -72,11 +75,26 @@ struct Eight<__nv_bfloat16> {
   }
 };
 
-// cos and sin of pos * f radians.
-__device__ __forceinline__ void angle(float f, int32_t pos, float* c, float* s) {
-  double turns = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  turns -= floor(turns);
-  const uint64_t per = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
+// The fraction of a turn that one position adds, in units of 2^-64: f / 2 pi modulo 1, from the 24 bits of
+// f's mantissa times 2^66 / 2 pi, shifted to f's exponent. Off by less than 2^-64 and 2^-64 of itself.
+__device__ __forceinline__ uint64_t turn_per_position(float f) {
+  const uint32_t bits = __float_as_uint(f), ex = bits >> 23 & 255;
+  const uint64_t m = (bits & 0x7FFFFFu) | (ex ? 0x800000u : 0u), k = 11743562013128004906ull;  // round(2^66 / 2 pi)
+  const uint64_t hi = __umul64hi(m, k), lo = m * k;
+  const int sh = 2 - ((int)(ex ? ex : 1) - 150);  // f = m 2^(ex - 150)
+  uint64_t t;
+  if (sh >= 128)
+    t = 0;
+  else if (sh >= 64)
+    t = hi >> (sh - 64);
+  else if (sh > 0)
+    t = hi << (64 - sh) | lo >> sh;
+  else
+    t = sh > -64 ? lo << -sh : 0;
+  return bits >> 31 ? 0 - t : t;
+}
+// cos and sin of pos * f radians, `per` being f's turn_per_position.
+__device__ __forceinline__ void angle(uint64_t per, float f, int32_t pos, float* c, float* s) {
   const uint64_t phase = per * (uint64_t)(int64_t)pos;
   // the nearest quarter turn, and the rest in half turns, within +-1/4
   const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
@@ -89,61 +107,129 @@ __device__ __forceinline__ void angle(float f, int32_t pos, float* c, float* s) 
   if (!isfinite(f)) *c = *s = __int_as_float(0x7FC00000);
 }
 
-// Norm and rotation of one head row over the LPG lanes of a subgroup; `sub` is the lane within it.
-// Every lane of the warp calls it. cos / sin: the token's tables of `half` entries.
-template <int LPG, typename T>
-__device__ __forceinline__ void norm_turn(const RowArgs& A, float (&x)[8], const T* w, const float* cs, const float* sn, int sub, bool turn) {
-  // the subgroups of a warp hold heads of different kinds: all of them reduce, the normed ones scale
-  float ss = 0.f;
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// The turn of one kind of head (queries or keys) at one position, for the 8 dims of a lane: element e of a
+// head row x becomes r (x_e wc_e + x'_e ws_e), x' being the other element of its pair, r the norm's root,
+// wc the weight times the cosine and ws the other element's weight times the signed sine.
+struct Turn {
+  float2 wc[4], ws[4];
+  int other;       // the lane that holds the pairs' other elements
+  bool pair, norm; // this lane's dims are rotated; there is a norm
+};
+
+// Every lane calls it; `cs`, `sn`: the token's tables of `half` entries.
+template <typename T>
+__device__ __forceinline__ Turn make_turn(const RowArgs& A, const T* w, const float* cs, const float* sn, int sub) {
+  Turn t;
+  const int lane = threadIdx.x & 31, step = A.half / 8;  // lanes between the two halves
+  const bool low = sub < step;
+  t.pair = sub < 2 * step;
+  t.norm = w != nullptr;
+  t.other = A.interleaved || !t.pair ? lane : low ? lane + step : lane - step;
+  float c[8], s[8], a[8], b[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+  for (int e = 0; e < 8; ++e) c[e] = a[e] = b[e] = 1.f, s[e] = 0.f;
+  if (t.pair) {
 #pragma unroll
-  for (int off = LPG / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    for (int e = 0; e < 8; ++e) {
+      const int i = A.interleaved ? sub * 4 + e / 2 : (low ? sub : sub - step) * 8 + e;
+      c[e] = cs[i];
+      s[e] = (A.interleaved ? (e & 1) == 0 : low) ? -sn[i] : sn[i];
+    }
+  }
   if (w && sub * 8 < A.d) {
-    const float r = 1.f / sqrtf(ss / (float)A.d + A.eps);
-    Eight<T> wv;
-    float wf[8];
-    wv.load(w + sub * 8);
-    wv.get(wf);
+    Eight<T> v;
+    v.load(w + sub * 8);
+    v.get(a);
+    v.load(w + (sub + t.other - lane) * 8);
+    v.get(b);
+    if (A.interleaved) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wf[e];
-  }
-  const int step = A.half / 8;  // lanes between the two halves
-  const bool low = sub < step, in = sub < 2 * step;
-  if (A.interleaved) {
-    if (turn && in) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float c = cs[sub * 4 + e], s = sn[sub * 4 + e];
-        const float a = x[2 * e], b = x[2 * e + 1];
-        x[2 * e] = a * c - b * s;
-        x[2 * e + 1] = b * c + a * s;
-      }
-    }
-  } else {
-    const int lane = threadIdx.x & 31, other = in ? (low ? lane + step : lane - step) : lane;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], other);
-    if (turn && in) {
-      const int at = (low ? sub : sub - step) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = cs[at + e], s = low ? -sn[at + e] : sn[at + e];
-        x[e] = x[e] * c + y[e] * s;
-      }
+      for (int e = 0; e < 8; ++e) b[e] = a[e ^ 1];
     }
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    t.wc[e] = make_float2(a[2 * e] * c[2 * e], a[2 * e + 1] * c[2 * e + 1]);
+    t.ws[e] = make_float2(b[2 * e] * s[2 * e], b[2 * e + 1] * s[2 * e + 1]);
+  }
+  return t;
+}
+
+// x' of a lane: from the lane that holds it, or the neighbour within the lane.
+__device__ __forceinline__ void others(Eight<__nv_bfloat16>& x, const Turn& t, int interleaved) {
+  uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = interleaved ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(0xffffffffu, w[i], t.other);
+    if (!t.pair) w[i] = 0;
+  }
+  x.u = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void others(Eight<float>& x, const Turn& t, int interleaved) {
+  float v[8];
+  x.get(v);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float a = v[i], b = v[i + 1];
+    v[i] = interleaved ? b : __shfl_sync(0xffffffffu, a, t.other);
+    v[i + 1] = interleaved ? a : __shfl_sync(0xffffffffu, b, t.other);
+    if (!t.pair) v[i] = v[i + 1] = 0.f;
+  }
+  x.set(v);
+}
+
+// Norm and rotation of a head row held by the LPG lanes of a subgroup (zeros in lanes past d). Every lane of
+// the warp calls it.
+template <int LPG, typename T>
+__device__ __forceinline__ void norm_turn(const RowArgs& A, Eight<T>& raw, const Turn& t) {
+  Eight<T> mate = raw;
+  others(mate, t, A.interleaved);
+  float x[8], y[8];
+  raw.get(x);
+  mate.get(y);
+  float2 r = make_float2(1.f, 1.f);
+  if (t.norm) {
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s2 = fma2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(x[2 * e], x[2 * e + 1]), s2);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int off = LPG / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    r.x = r.y = rsqrtf(fmaf(ss, 1.f / (float)A.d, A.eps));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 v = mul2(make_float2(x[2 * e], x[2 * e + 1]), t.wc[e]);
+    v = mul2(fma2(make_float2(y[2 * e], y[2 * e + 1]), t.ws[e], v), r);
+    x[2 * e] = v.x;
+    x[2 * e + 1] = v.y;
+  }
+  raw.set(x);
 }
 
 // Where the rows of one launch come from and go to.
 struct RowsTo {
   int32_t n_rows;              // norm_rope: rows; append: requests
-  int32_t tok;                 // tokens of a CTA
+  int32_t parts;               // warps of a row
   const int32_t* positions;    // norm_rope
   void *k, *v;                 // norm_rope: [rows][Hkv][d] or NULL
   // append
-  int32_t n_new, bs, kb;
+  int32_t n_new, ctas, span;   // ctas of a request; blocks a CTA's tokens may touch
+  int32_t bs, kb;
   const int32_t *counts, *len, *slot_block;
   void* pool;                  // [R][Hkv][kb][2][bs][d]
 };
@@ -151,114 +237,127 @@ struct RowsTo {
 template <typename T, int LPG, bool APPEND>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs A, const RowsTo R) {
   extern __shared__ __align__(16) uint8_t smem[];
-  float* cs = reinterpret_cast<float*>(smem);          // [tok][half]
-  float* sn = cs + R.tok * A.half;                     // [tok][half]
-  int32_t* slot_of = reinterpret_cast<int32_t*>(sn + R.tok * A.half);  // append: [Hkv][tok + 1]
-  const int tid = threadIdx.x, sub = tid % LPG, group = tid / LPG;
-  constexpr int kGroups = kThreads / LPG;
-  const int32_t H = A.Hq + 2 * A.Hkv;
-
-  int64_t row0;       // first row of the CTA
-  int32_t n_tok;      // its rows
-  int32_t r = 0, pos0 = 0, blk0 = 0;
-  if (APPEND) {
-    const int32_t per = (R.n_new + R.tok - 1) / R.tok;
-    r = blockIdx.x / per;
-    const int32_t t0 = (blockIdx.x - r * per) * R.tok;
-    const int32_t cnt = R.counts ? min(max(R.counts[r], 0), R.n_new) : R.n_new;
-    row0 = (int64_t)r * R.n_new + t0;
-    n_tok = min(R.tok, cnt - t0);
-    const int32_t len = R.len[r];
-    if (n_tok <= 0 || len < 0 || len > INT32_MAX - R.n_new) return;  // positions stay within 31 bits
-    pos0 = len + t0;
-    blk0 = pos0 / R.bs;
-  } else {
-    row0 = (int64_t)blockIdx.x * R.tok;
-    n_tok = min((int64_t)R.tok, R.n_rows - row0);
-  }
-  const int32_t items = n_tok * H;
+  constexpr int kWarps = kThreads / 32, kSub = 32 / LPG;  // head rows of a warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPG, sg = lane / LPG;
+  float* cs = reinterpret_cast<float*>(smem) + warp * 2 * A.half;       // [warps][cos, sin][half]
+  float* sn = cs + A.half;
+  int32_t* slot_of = reinterpret_cast<int32_t*>(smem) + kWarps * 2 * A.half;  // append: [Hkv][span]
   const bool on = sub * 8 < A.d;
 
-  for (int32_t base = 0; base < items; base += kGroups * kInFlight) {
-    Eight<T> raw[kInFlight];
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const int32_t i = base + u * kGroups + group;
-      if (i < items && on) {
-        const int32_t tk = i / H, h = i - tk * H;
-        raw[u].load((const T*)A.qkv + (row0 + tk) * A.row_stride + (int64_t)h * A.d + sub * 8);
-      }
+  int64_t row;
+  int32_t pos, part, r = 0, blk0 = 0;
+  bool mine;
+  if (APPEND) {
+    r = blockIdx.x / R.ctas;
+    const int32_t w0 = (blockIdx.x - r * R.ctas) * kWarps, t0 = w0 / R.parts, t = (w0 + warp) / R.parts;
+    part = (w0 + warp) % R.parts;
+    const int32_t cnt = R.counts ? min(max(R.counts[r], 0), R.n_new) : R.n_new, len = R.len[r];
+    if (t0 >= cnt || len < 0 || len > INT32_MAX - R.n_new) return;  // positions stay within 31 bits
+    mine = t < cnt;
+    row = (int64_t)r * R.n_new + t;
+    pos = len + t;
+    blk0 = (len + t0) / R.bs;
+    const int32_t last = (len + min(cnt - 1, (w0 + kWarps - 1) / R.parts)) / R.bs;
+    for (int32_t i = threadIdx.x; i < A.Hkv * R.span; i += kThreads) slot_of[i] = INT32_MAX;
+    __syncthreads();
+    const int32_t* sb = R.slot_block + (int64_t)r * A.Hkv * R.kb;
+    for (int32_t i = threadIdx.x; i < A.Hkv * R.kb; i += kThreads) {
+      const int32_t b = sb[i];
+      if (b >= blk0 && b <= last) atomicMin(&slot_of[i / R.kb * R.span + (b - blk0)], i % R.kb);
     }
-    if (base == 0) {
-      const int32_t span = R.tok + 1;
-      if (APPEND) {
-        for (int32_t i = tid; i < A.Hkv * span; i += kThreads) slot_of[i] = INT32_MAX;
-        __syncthreads();
-        const int32_t last = (pos0 + n_tok - 1) / R.bs;
-        const int32_t* sb = R.slot_block + (int64_t)r * A.Hkv * R.kb;
-        for (int32_t i = tid; i < A.Hkv * R.kb; i += kThreads) {
-          const int32_t b = sb[i];
-          if (b >= blk0 && b <= last) atomicMin(&slot_of[i / R.kb * span + (b - blk0)], i % R.kb);
+    __syncthreads();
+  } else {
+    const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+    row = w / R.parts;
+    part = (int32_t)(w - row * R.parts);
+    mine = row < R.n_rows;
+    pos = mine ? R.positions[row] : -1;
+    mine = mine && pos >= 0;
+  }
+  if (!mine) return;
+  for (int32_t f = lane; f < A.half; f += 32) {
+    const float inv = A.inv_freq[f];
+    angle(turn_per_position(inv), inv, pos, &cs[f], &sn[f]);
+  }
+  __syncwarp();
+
+  // The row's head rows in groups of a warp: queries, keys, values. A warp takes every `parts`-th group,
+  // a batch of loads ahead of the work on them.
+  const int32_t gq = (A.Hq + kSub - 1) / kSub, gk = (A.Hkv + kSub - 1) / kSub;
+  const T* from = (const T*)A.qkv + row * A.row_stride + sub * 8;
+  int32_t g = part;
+  for (int kind = 0; kind < 3; ++kind) {
+    const int32_t heads = kind == 0 ? A.Hq : A.Hkv, first = kind == 0 ? 0 : kind == 1 ? gq : gq + gk, end = kind == 0 ? gq : first + gk;
+    if (g >= end) continue;
+    const T* in = from + (int64_t)(kind == 0 ? 0 : kind == 1 ? A.Hq : A.Hq + A.Hkv) * A.d;
+    T* out = nullptr;
+    if (kind == 0) {
+      if (A.q) out = (T*)A.q + row * A.Hq * A.d + sub * 8;
+    } else if (APPEND) {
+      out = (T*)R.pool + ((int64_t)r * A.Hkv * R.kb * 2 + kind - 1) * R.bs * A.d + (int64_t)(pos % R.bs) * A.d + sub * 8;
+    } else {
+      T* to = (T*)(kind == 1 ? R.k : R.v);
+      if (to) out = to + row * A.Hkv * A.d + sub * 8;
+    }
+    if (!out) {
+      g += (end - g + R.parts - 1) / R.parts * R.parts;
+      continue;
+    }
+    Turn t;
+    if (kind < 2) t = make_turn<T>(A, (const T*)(kind == 0 ? A.q_weight : A.k_weight), cs, sn, sub);
+    for (; g < end; g += kInFlight * R.parts) {
+      Eight<T> raw[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int32_t h = (g + u * R.parts - first) * kSub + sg;
+        raw[u].zero();
+        if (h < heads && on) raw[u].load(in + (int64_t)h * A.d);
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        if (g + u * R.parts >= end) break;
+        if (kind < 2) norm_turn<LPG, T>(A, raw[u], t);
+        const int32_t h = (g + u * R.parts - first) * kSub + sg;
+        if (h >= heads || !on) continue;
+        int64_t at = (int64_t)h * A.d;
+        if (APPEND && kind > 0) {
+          const int32_t slot = slot_of[h * R.span + (pos / R.bs - blk0)];
+          if (slot == INT32_MAX) continue;
+          at = ((int64_t)h * R.kb + slot) * 2 * R.bs * A.d;
         }
+        raw[u].store(out + at);
       }
-      for (int32_t i = tid; i < n_tok * A.half; i += kThreads) {
-        const int32_t tk = i / A.half, f = i - tk * A.half;
-        angle(A.inv_freq[f], APPEND ? pos0 + tk : R.positions[row0 + tk], &cs[i], &sn[i]);
-      }
-      __syncthreads();
     }
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const int32_t i = base + u * kGroups + group;
-      const bool real = i < items;
-      const int32_t tk = real ? i / H : 0, h = real ? i - tk * H : 0;
-      const bool is_q = h < A.Hq, is_k = !is_q && h < A.Hq + A.Hkv;
-      float x[8];
-      if (real && on)
-        raw[u].get(x);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      const T* w = (const T*)(is_q ? A.q_weight : is_k ? A.k_weight : nullptr);
-      norm_turn<LPG, T>(A, x, w, cs + tk * A.half, sn + tk * A.half, sub, is_q || is_k);
-      if (!real || !on) continue;
-      if (is_q || is_k) raw[u].set(x);  // values pass as they are
-      const int64_t row = row0 + tk;
-      T* to = nullptr;
-      if (is_q) {
-        if (A.q) to = (T*)A.q + (row * A.Hq + h) * A.d;
-      } else {
-        const int32_t hk = is_k ? h - A.Hq : h - A.Hq - A.Hkv;
-        if (APPEND) {
-          const int32_t pos = pos0 + tk, b = pos / R.bs;
-          const int32_t slot = slot_of[hk * (R.tok + 1) + (b - blk0)];
-          if (slot != INT32_MAX)
-            to = (T*)R.pool + (((((int64_t)r * A.Hkv + hk) * R.kb + slot) * 2 + (is_k ? 0 : 1)) * R.bs + (pos - b * R.bs)) * A.d;
-        } else if (is_k ? R.k != nullptr : R.v != nullptr) {
-          to = (T*)(is_k ? R.k : R.v) + (row * A.Hkv + hk) * A.d;
-        }
-      }
-      if (!APPEND && R.positions[row] < 0) to = nullptr;
-      if (to) raw[u].store(to + sub * 8);
-    }
+    // the last batch may have stepped past groups of the next kind
+    while (g - R.parts >= end) g -= R.parts;
   }
 }
 
 template <typename T, bool APPEND>
 cudaError_t run_rows(const RowArgs& A, RowsTo R, cudaStream_t s) {
-  const int d8 = A.d / 8, lpg = d8 <= 4 ? 4 : d8 <= 8 ? 8 : d8 <= 16 ? 16 : 32;
-  const int32_t H = A.Hq + 2 * A.Hkv, per_cta = kThreads / lpg * kInFlight;
+  const int d8 = A.d / 8, lpg = d8 <= 4 ? 4 : d8 <= 8 ? 8 : d8 <= 16 ? 16 : 32, heads = 32 / lpg, warps = kThreads / 32;
+  const int32_t groups = (A.Hq + heads - 1) / heads + 2 * ((A.Hkv + heads - 1) / heads);
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // tokens of a CTA: enough head rows for one full batch of loads, but no fewer CTAs than two per SM
-  const int64_t tokens = APPEND ? (int64_t)R.n_rows * R.n_new : R.n_rows;
-  int64_t tok = per_cta / H;
-  if (tok > tokens / (2 * sms)) tok = tokens / (2 * sms);
-  R.tok = (int32_t)(tok < 1 ? 1 : tok > 16 ? 16 : tok);
-  const int64_t ctas = APPEND ? (int64_t)R.n_rows * ((R.n_new + R.tok - 1) / R.tok) : ((int64_t)R.n_rows + R.tok - 1) / R.tok;
-  const size_t smem = (size_t)R.tok * A.half * 8 + (APPEND ? (size_t)A.Hkv * (R.tok + 1) * 4 : 0);
-  if (ctas > INT32_MAX || smem > 48 * 1024) return cudaErrorInvalidValue;
+  // warps of a row: one where there are rows enough for 16 warps on every SM, else as many as reach that
+  const int64_t rows = APPEND ? (int64_t)R.n_rows * R.n_new : R.n_rows;
+  int64_t parts = ((int64_t)sms * 16 + rows - 1) / rows;
+  R.parts = (int32_t)(parts > groups ? groups : parts);
+  int64_t ctas;
+  if (APPEND) {
+    const int64_t per = ((int64_t)R.n_new * R.parts + warps - 1) / warps;
+    ctas = per * R.n_rows;
+    R.ctas = (int32_t)per;
+    R.span = (warps + R.parts - 1) / R.parts + 1;  // blocks of a CTA's tokens, one token a block at worst
+  } else {
+    ctas = ((int64_t)R.n_rows * R.parts + warps - 1) / warps;
+  }
+  const size_t smem = (size_t)warps * A.half * 8 + (APPEND ? (size_t)A.Hkv * R.span * 4 : 0);
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
+    if (smem > 48 * 1024) {
+      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    }
     kernel<<<(unsigned)ctas, kThreads, smem, s>>>(A, R);
     return cudaGetLastError();
   };
@@ -351,28 +450,29 @@ __global__ void __launch_bounds__(kThreads) append_qkv_kernel(const RowArgs A, c
   const int32_t* sb = S.slot_block + (int64_t)r * G.Hkv * G.kb;
   for (int32_t i = tid; i < G.Hkv * G.kb; i += kThreads)
     if (sb[i] == pos / G.bs) atomicMin(&slot_of[i / G.kb], i % G.kb);
-  for (int32_t f = tid; f < A.half; f += kThreads) angle(A.inv_freq[f], pos, &cs[f], &sn[f]);
+  for (int32_t f = tid; f < A.half; f += kThreads) {
+    const float inv = A.inv_freq[f];
+    angle(turn_per_position(inv), inv, pos, &cs[f], &sn[f]);
+  }
   __syncthreads();
-  const int32_t H = A.Hq + 2 * A.Hkv;
   const T* from = (const T*)A.qkv + (int64_t)r * A.row_stride;
   const bool on = sub * 8 < A.d;
-  for (int32_t base = 0; base < H; base += kGroups) {
-    const int32_t h = base + group;
-    const bool real = h < H && on, is_q = h < A.Hq, is_k = !is_q && h < A.Hq + A.Hkv;
-    Eight<T> raw;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (real) {
-      raw.load(from + (int64_t)h * A.d + sub * 8);
-      raw.get(x);
-    }
-    norm_turn<LPG, T>(A, x, (const T*)(is_q ? A.q_weight : is_k ? A.k_weight : nullptr), cs, sn, sub, is_q || is_k);
-    if (!real) continue;
-    if (is_q || is_k) raw.set(x);
-    if (is_q) {
-      raw.store((T*)A.q + ((int64_t)r * A.Hq + h) * A.d + sub * 8);
-    } else {
-      const int32_t hk = is_k ? h - A.Hq : h - A.Hq - A.Hkv;
-      put(G, places<T>(G, S, RT, layer, r, hk, pos, slot_of[hk], err), is_k ? 0 : 1, sub * 8, raw);
+  for (int kind = 0; kind < 3; ++kind) {
+    const int32_t heads = kind == 0 ? A.Hq : A.Hkv;
+    const T* in = from + (int64_t)(kind == 0 ? 0 : kind == 1 ? A.Hq : A.Hq + A.Hkv) * A.d;
+    Turn t;
+    if (kind < 2) t = make_turn<T>(A, (const T*)(kind == 0 ? A.q_weight : A.k_weight), cs, sn, sub);
+    for (int32_t base = 0; base < heads; base += kGroups) {
+      const int32_t h = base + group;
+      Eight<T> raw;
+      raw.zero();
+      if (h < heads && on) raw.load(in + (int64_t)h * A.d + sub * 8);
+      if (kind < 2) norm_turn<LPG, T>(A, raw, t);
+      if (h >= heads || !on) continue;
+      if (kind == 0)
+        raw.store((T*)A.q + ((int64_t)r * A.Hq + h) * A.d + sub * 8);
+      else
+        put(G, places<T>(G, S, RT, layer, r, h, pos, slot_of[h], err), kind - 1, sub * 8, raw);
     }
   }
   __syncthreads();

@@ -176,21 +176,11 @@ __host__ __device__ constexpr size_t cuda_smem(int d, int kb, int tiles) {
          ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <typename T, int DV>
+template <int DV>
 __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs A, const int32_t split) {
+  using T = float;
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int d = DV * 32, pitch = cuda_pitch(d);
   float* qs = reinterpret_cast<float*>(smem);      // [32][pitch]
@@ -837,7 +827,7 @@ cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
-template <typename T, int DV>
+template <int DV>
 cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
   const int32_t groups = (A.T * A.G.g + kCudaRows - 1) / kCudaRows;
@@ -845,20 +835,19 @@ cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
   const int64_t units = (int64_t)n_active * A.G.Hkv;
   const int32_t split = pick_split(units * groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles);
-  return launch_cluster(tree_cuda_kernel<T, DV>, dim3((unsigned)(units * split), groups), kCudaThreads, smem, split, s, A, split);
+  return launch_cluster(tree_cuda_kernel<DV>, dim3((unsigned)(units * split), groups), kCudaThreads, smem, split, s, A, split);
 }
 
-template <typename T>
-cudaError_t run_cuda_dv(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+cudaError_t run_cuda_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   switch (A.G.d / 32) {
-    case 1: return run_cuda<T, 1>(A, n_active, s);
-    case 2: return run_cuda<T, 2>(A, n_active, s);
-    case 3: return run_cuda<T, 3>(A, n_active, s);
-    case 4: return run_cuda<T, 4>(A, n_active, s);
-    case 5: return run_cuda<T, 5>(A, n_active, s);
-    case 6: return run_cuda<T, 6>(A, n_active, s);
-    case 7: return run_cuda<T, 7>(A, n_active, s);
-    default: return run_cuda<T, 8>(A, n_active, s);
+    case 1: return run_cuda<1>(A, n_active, s);
+    case 2: return run_cuda<2>(A, n_active, s);
+    case 3: return run_cuda<3>(A, n_active, s);
+    case 4: return run_cuda<4>(A, n_active, s);
+    case 5: return run_cuda<5>(A, n_active, s);
+    case 6: return run_cuda<6>(A, n_active, s);
+    case 7: return run_cuda<7>(A, n_active, s);
+    default: return run_cuda<8>(A, n_active, s);
   }
 }
 
@@ -935,7 +924,7 @@ cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
 
 cudaError_t launch_attend_tree(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   if (n_active <= 0) return cudaSuccess;
-  return A.G.dtype == OKV_F32 ? run_cuda_dv<float>(A, n_active, s) : run_mma_d(A, n_active, s);
+  return A.G.dtype == OKV_F32 ? run_cuda_d(A, n_active, s) : run_mma_d(A, n_active, s);
 }
 
 }  // namespace okv
