@@ -67,37 +67,55 @@ __device__ __forceinline__ int64_t draft_offset(const TreeArgs& A, const Site& s
   return (((int64_t)s.r * A.T + t) * A.G.Hkv + s.h) * A.G.d;
 }
 
-// Valid tokens of every slot of the unit (0: empty) into nv, by all threads of the CTA. A block id
+// The valid tokens of every slot of the unit (0: empty) into nv, and the tiles of spt slots that hold any,
+// in order, into `tiles`, with kWhole set where all their places do; their number. One warp. A block id
 // outside the request's length counts as an empty slot and is recorded.
-__device__ __forceinline__ void read_slots(const TreeArgs& A, const Site& s, uint8_t* nv) {
+constexpr uint32_t kWhole = 0x8000;
+__device__ __forceinline__ int32_t list_tiles(const TreeArgs& A, const Site& s, int32_t spt, uint8_t* nv, uint16_t* tiles) {
   const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-  for (int32_t i = threadIdx.x; i < A.G.kb; i += blockDim.x) {
-    const int32_t b = sb[i];
-    int32_t n = 0;
-    if (b >= 0) {
-      const int64_t rem = (int64_t)s.len - (int64_t)b * A.G.bs;
-      if (rem <= 0 || b >= A.G.nb_max) {
-        if (A.err) record_error(A.err, kErrBlockRange, -2, s.r, b);
-      } else {
-        n = (int32_t)(rem < A.G.bs ? rem : A.G.bs);
-      }
-    }
-    nv[i] = (uint8_t)n;
-  }
-}
-// The tiles (spt slots each) that hold a valid token, in order, into `tiles`; their number. One warp.
-__device__ __forceinline__ int32_t list_tiles(const uint8_t* nv, int32_t kb, int32_t spt, uint16_t* tiles) {
   const int lane = threadIdx.x & 31;
+  int32_t used = 0;
+  for (int32_t i0 = lane; i0 < A.G.kb; i0 += 128) {
+    int32_t b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) b[u] = i0 + 32 * u < A.G.kb ? sb[i0 + 32 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int32_t i = i0 + 32 * u;
+      if (i >= A.G.kb) break;
+      int32_t n = 0;
+      if (b[u] >= 0) {
+        const int64_t rem = (int64_t)s.len - (int64_t)b[u] * A.G.bs;
+        if (rem <= 0 || b[u] >= A.G.nb_max) {
+          if (A.err) record_error(A.err, kErrBlockRange, -2, s.r, b[u]);
+        } else {
+          n = (int32_t)(rem < A.G.bs ? rem : A.G.bs);
+          ++used;
+        }
+      }
+      nv[i] = (uint8_t)n;
+    }
+  }
+  __syncwarp();
+  if (A.ctr && s.part == 0 && blockIdx.y == 0) {
+    const int32_t slots = __reduce_add_sync(0xffffffffu, used);
+    if (lane == 0) atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
+  }
   int32_t n = 0;
-  for (int32_t t0 = 0; t0 * spt < kb; t0 += 32) {
-    bool any = false;
-    for (int32_t s = (t0 + lane) * spt, e = min(s + spt, kb); s < e; ++s) any = any || nv[s];
+  for (int32_t t0 = 0; t0 * spt < A.G.kb; t0 += 32) {
+    const int32_t first = (t0 + lane) * spt;
+    bool any = false, whole = first + spt <= A.G.kb;
+    for (int32_t i = first, e = min(first + spt, A.G.kb); i < e; ++i) {
+      any = any || nv[i];
+      whole = whole && nv[i] == A.G.bs;
+    }
     const unsigned have = __ballot_sync(0xffffffffu, any);
-    if (any) tiles[n + __popc(have & ((1u << lane) - 1u))] = (uint16_t)(t0 + lane);
+    if (any) tiles[n + __popc(have & ((1u << lane) - 1u))] = (uint16_t)(t0 + lane | (whole ? kWhole : 0u));
     n += __popc(have);
   }
   return n;
 }
+__device__ __forceinline__ int32_t tile_of(uint16_t t) { return t & (kWhole - 1); }
 
 // Adds what the drafted values that are not finite give to four outputs (dims c .. c + 3) of a row
 // that sees them. Those elements are zero in the products, where a weight of zero times them would
@@ -134,24 +152,30 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
   const uint64_t bad = ld_cluster_u64(cluster_map(P.bad, split - 1));
   for (int32_t i = s.part * blockDim.x + threadIdx.x; i < total; i += split * blockDim.x) {
     const int32_t row = i / d4, c = i - row * d4;
-    float m[kMaxSplit], M = -INFINITY;
+    float m[kMaxSplit], ls[kMaxSplit], M = -INFINITY;
+    float4 x[kMaxSplit];
 #pragma unroll
-    for (int p = 0; p < kMaxSplit; ++p) {
-      m[p] = p < split ? ld_cluster(cluster_map(P.m + row * 4, p)) : -INFINITY;
-      M = fmaxf(M, m[p]);
+    for (int p = 0; p < kMaxSplit; ++p) {  // every load on its way before the first is used
+      m[p] = -INFINITY;
+      if (p < split) {
+        m[p] = ld_cluster(cluster_map(P.m + row * 4, p));
+        ls[p] = ld_cluster(cluster_map(P.l + row * 4, p));
+        x[p] = ld_cluster4(cluster_map(P.o + part_chunk(row, c, A.G.d, xor_mask), p));
+      }
     }
+#pragma unroll
+    for (int p = 0; p < kMaxSplit; ++p) M = fmaxf(M, m[p]);
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int p = 0; p < kMaxSplit; ++p) {
       if (p >= split || m[p] == -INFINITY) continue;  // nothing seen there: its outputs were not written
       const float f = ex2(m[p] - M);
-      const float4 x = ld_cluster4(cluster_map(P.o + part_chunk(row, c, A.G.d, xor_mask), p));
-      l = fmaf(f, ld_cluster(cluster_map(P.l + row * 4, p)), l);
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+      l = fmaf(f, ls[p], l);
+      o.x = fmaf(f, x[p].x, o.x);
+      o.y = fmaf(f, x[p].y, o.y);
+      o.z = fmaf(f, x[p].z, o.z);
+      o.w = fmaf(f, x[p].w, o.w);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -199,24 +223,15 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   if (tid == 0) *bad = 0;
-  read_slots(A, s, nv);
   for (int i = tid; i < kCudaRows * (d / 4); i += kCudaThreads) {
     const int row = i / (d / 4), c = i % (d / 4);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < s.rows) x = load4((const T*)A.q + row_offset(A, s, s.row0 + row) + c * 4);
     *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = x;
   }
-  __syncthreads();
   if (tid < 32) {
-    const int32_t n = list_tiles(nv, A.G.kb, spt, tiles);
-    if (tid == 0) {
-      *n_tiles = n;
-      if (A.ctr && s.part == 0 && blockIdx.y == 0) {
-        int32_t slots = 0;
-        for (int32_t i = 0; i < A.G.kb; ++i) slots += nv[i] != 0;
-        atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
-      }
-    }
+    const int32_t n = list_tiles(A, s, spt, nv, tiles);
+    if (tid == 0) *n_tiles = n;
   }
   __syncthreads();
   const bool draft = s.part == split - 1;
@@ -241,7 +256,7 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 
   for (int32_t it = 0; it < mine; ++it) {
     const bool is_draft = draft && it == 0;
-    const int32_t slot0 = is_draft ? 0 : tiles[s.part + (it - (draft ? 1 : 0)) * split] * spt;
+    const int32_t slot0 = is_draft ? 0 : tile_of(tiles[s.part + (it - (draft ? 1 : 0)) * split]) * spt;
     __syncthreads();  // the tile before has been read
     for (int i = tid; i < kTile * (d / 4); i += kCudaThreads) {
       const int j = i / (d / 4), c = i % (d / 4);
@@ -406,7 +421,7 @@ struct Lines {
 constexpr int kMaxRing = 12;
 struct MmaBars {
   uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][2], p_full[2][2], pv_done[2][2], drain;
-  uint64_t bad;
+  uint64_t bad, bad_of[8];  // drafted tokens with values that are not finite: all, found by each warp
   uint32_t tmem;
   int32_t n_tiles, failed;
 };
@@ -448,90 +463,17 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
 
   const Site s = make_site(A, split, NW * 128);
   if (s.rows <= 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1;
   const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   const uint32_t ring0 = smem_u32(rs);
 
-  if (is_mma) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
-  if (tid == 0) {
-    for (int i = 0; i < ring; ++i) {
-      mbar_init(smem_u32(&B.full[i]), 1);
-      mbar_init(smem_u32(&B.empty[i]), 1);
-    }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(smem_u32(&B.s_full[w][0]), 1);
-      mbar_init(smem_u32(&B.s_full[w][1]), 1);
-      mbar_init(smem_u32(&B.p_full[w][0]), 128);
-      mbar_init(smem_u32(&B.p_full[w][1]), 128);
-      mbar_init(smem_u32(&B.pv_done[w][0]), 1);
-      mbar_init(smem_u32(&B.pv_done[w][1]), 1);
-    }
-    mbar_init(smem_u32(&B.drain), 1);
-    fence_mbar_init();
-    if (draft) {  // buffers 0 and 2 are filled below, once
-      mbar_arrive(smem_u32(&B.full[0]));
-      mbar_arrive(smem_u32(&B.full[2]));
-    }
-    B.failed = 0;
-    B.bad = 0;
-  }
-  read_slots(A, s, nv);
-  if (warp < NW * 4) {
-    constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
-    for (int i = tid; i < s.rows * kPieces; i += NW * 128) {
-      const int row = i / kPieces, c = i % kPieces;
-      const uint4 x = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.q + row_offset(A, s, s.row0 + row) + c * 8);
-      uint8_t* chunk = qs + ((size_t)(row >> 7) * L::kChunks + c / kLine) * q_rows * L::kBytes;
-      *reinterpret_cast<uint4*>(chunk + L::at(row & 127, c % kLine)) = x;
-    }
-    if (tt < kTile)  // the copies leave these lines alone; as V they meet weights of zero
-      for (int i = tid; i < ring * (kTile - tt) * kPieces; i += NW * 128) {
-        const int c = i % kPieces, rest = i / kPieces, row = tt + rest % (kTile - tt), b = rest / (kTile - tt);
-        *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(row, c % kLine)) = make_uint4(0, 0, 0, 0);
-      }
-  }
-  __syncthreads();
-  if (warp < NW * 4 && draft) {
-    constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
-    for (int i = tid; i < kTile * kPieces; i += NW * 128) {
-      const int j = i / kPieces, c = i % kPieces;
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
-      if (j < s.cnt) {
-        const int64_t at = draft_offset(A, s, j) + c * 8;
-        x = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.k + at);
-        y = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + at);
-        if (clean(y)) atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
-      }
-      const size_t to = (size_t)(c / kLine) * kTile * L::kBytes + L::at(j, c % kLine);
-      *reinterpret_cast<uint4*>(rs + to) = x;
-      *reinterpret_cast<uint4*>(rs + (size_t)2 * L::kBuf + to) = y;
-    }
-  }
-  if (warp < NW * 4) fence_proxy_async();
-  if (is_copy) {
-    const int32_t n = list_tiles(nv, A.G.kb, spt, tiles);
-    if (lane == 0) B.n_tiles = n;
-    if (A.ctr && s.part == 0 && blockIdx.y == 0) {
-      int32_t slots = 0;
-      for (int32_t i = lane; i < A.G.kb; i += 32) slots += nv[i] != 0;
-      slots = __reduce_add_sync(0xffffffffu, slots);
-      if (lane == 0) atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = B.tmem;
-  const int32_t lead = draft ? 1 : 0;
-  const int32_t n = (B.n_tiles - s.part + split - 1) / split + lead;  // this CTA's tiles
   // Tile i's K is the (2i - 1)-th use of the ring (the first: use 0), its V the (2i + 2)-th: the order
   // in which the MMAs take them, S of tile i + 1 before O of tile i.
-  auto k_use = [](int32_t i) { return i == 0 ? 0 : 2 * i - 1; };
   auto v_use = [](int32_t i) { return 2 * i + 2; };
   auto full = [&](int32_t use) { return mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1)); };
-  // ... by all lanes of a warp: the TMEM loads and stores that follow are by whole warps
+  // ... by all lanes of a warp: what follows is by whole warps
   auto warp_wait = [&](uint64_t& bar, int32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
   };
@@ -539,88 +481,171 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     *(volatile int32_t*)&B.failed = 1;
     if (A.err) record_error(A.err, kErrTimeout, -3, s.r, site);
   };
+  const int32_t lead = draft ? 1 : 0;
+  int32_t n = 0;          // this CTA's tiles
+  int32_t next = 0;       // copy warp: the next use to fill
+  int32_t last_use = -1;  // copy warp: the last use filled
+  const int32_t unit_slot = (int32_t)(((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb);
+  auto fill = [&](int32_t use) {
+    const bool v = use > 0 && use % 2 == 0;
+    const int32_t i = v ? use / 2 - 1 : (use + 1) / 2, b = use % ring;
+    if (i < lead || i >= n) return true;  // the drafted tokens, or the use that a further K would have
+    if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)((use / ring - 1) & 1))) return false;
+    const uint32_t bar = smem_u32(&B.full[b]);
+    const int32_t slot = unit_slot + tile_of(tiles[s.part + (i - lead) * split]) * spt;
+    mbar_expect_tx(bar, (uint32_t)(tt * D * 2));
+#pragma unroll
+    for (int c = 0; c < L::kChunks; ++c) tma_load_5d(ring0 + b * L::kBuf + c * kTile * L::kBytes, &map, bar, 0, c, 0, v ? 1 : 0, slot);
+    last_use = use;
+    return true;
+  };
+
+  // Setup: the copy warp reads the slot table and starts the copies that need no free buffer, while the
+  // softmax warps bring in the queries and the drafted tokens.
+  if (is_copy) {
+    if (lane == 0) {
+      for (int i = 0; i < ring; ++i) {
+        mbar_init(smem_u32(&B.full[i]), 1);
+        mbar_init(smem_u32(&B.empty[i]), 1);
+      }
+      for (int w = 0; w < 2; ++w)
+        for (int e = 0; e < 2; ++e) {
+          mbar_init(smem_u32(&B.s_full[w][e]), 1);
+          mbar_init(smem_u32(&B.p_full[w][e]), 128);
+          mbar_init(smem_u32(&B.pv_done[w][e]), 1);
+        }
+      mbar_init(smem_u32(&B.drain), 1);
+      fence_mbar_init();
+      fence_proxy_async();
+      if (draft) {  // buffers 0 and 2 are filled by the softmax warps, once
+        mbar_arrive(smem_u32(&B.full[0]));
+        mbar_arrive(smem_u32(&B.full[2]));
+      }
+      B.failed = 0;
+    }
+    const int32_t all = list_tiles(A, s, spt, nv, tiles);
+    __syncwarp();
+    n = (all - s.part + split - 1) / split + lead;
+    if (lane == 0) {
+      B.n_tiles = n;
+      for (; next < ring && next <= 2 * n; ++next) fill(next);
+    }
+  } else if (is_mma) {
+    tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+  } else {
+    constexpr int kPieces = D / 8, kLine = L::kBytes / 16, kThreads = NW * 128;
+    const uint32_t q0 = smem_u32(qs);
+    uint64_t any_bad = 0;
+    for (int i = tid; i < s.rows * kPieces; i += kThreads) {
+      const int row = i / kPieces, c = i % kPieces;
+      copy16(q0 + ((row >> 7) * L::kChunks + c / kLine) * q_rows * L::kBytes + L::at(row & 127, c % kLine),
+             (const __nv_bfloat16*)A.q + row_offset(A, s, s.row0 + row) + c * 8);
+    }
+    if (draft) {
+      uint64_t bad = 0;
+      uint4 y[kTile * kPieces / kThreads];
+#pragma unroll
+      for (int u = 0; u < kTile * kPieces / kThreads; ++u) {
+        const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
+        const uint32_t to = ring0 + (c / kLine) * kTile * L::kBytes + L::at(j, c % kLine);
+        y[u] = make_uint4(0, 0, 0, 0);
+        if (j < s.cnt) {
+          const int64_t at = draft_offset(A, s, j) + c * 8;
+          copy16(to, (const __nv_bfloat16*)A.k + at);
+          y[u] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + at);
+        } else {
+          *reinterpret_cast<uint4*>(rs + (to - ring0)) = make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kTile * kPieces / kThreads; ++u) {
+        const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
+        if (clean(y[u])) bad |= 1ull << j;
+        *reinterpret_cast<uint4*>(rs + (size_t)2 * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(j, c % kLine)) = y[u];
+      }
+      any_bad = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)bad);
+    }
+    if (lane == 0) B.bad_of[warp] = any_bad;
+    if (tt < kTile)  // the copies leave these lines alone; as V they meet weights of zero
+      for (int i = tid; i < ring * (kTile - tt) * kPieces; i += kThreads) {
+        const int c = i % kPieces, rest = i / kPieces, row = tt + rest % (kTile - tt), b = rest / (kTile - tt);
+        if (!draft || (b != 0 && b != 2))
+          *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(row, c % kLine)) = make_uint4(0, 0, 0, 0);
+      }
+    copy16_wait();
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  n = __shfl_sync(0xffffffffu, B.n_tiles, 0);
+  if (tid == 0) {
+    uint64_t bad = 0;
+    for (int i = 0; i < NW * 4; ++i) bad |= B.bad_of[i];
+    B.bad = bad;  // read after the loops
+  }
   float m_run = -INFINITY, l_run = 0.f;
 
   if (is_copy) {
     if (lane == 0) {
-      const int64_t slot_base = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-      int32_t last = -1;  // the last use filled
-      auto fill = [&](int32_t i, bool v) {
-        if (i < lead) return true;
-        const int32_t use = v ? v_use(i) : k_use(i), b = use % ring;
-        if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)((use / ring - 1) & 1))) return false;
-        const uint32_t bar = smem_u32(&B.full[b]);
-        const int32_t slot = (int32_t)(slot_base + (int64_t)tiles[s.part + (i - lead) * split] * spt);
-        mbar_expect_tx(bar, (uint32_t)(tt * D * 2));
-#pragma unroll
-        for (int c = 0; c < L::kChunks; ++c)
-          tma_load_5d(ring0 + b * L::kBuf + c * kTile * L::kBytes, &map, bar, 0, c, 0, v ? 1 : 0, slot);
-        last = use;
-        return true;
-      };
       bool ok = true;
-      if (n > 0) ok = fill(0, false);
-      for (int32_t i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) ok = fill(i + 1, false);
-        if (ok) ok = fill(i, true);
-      }
+      for (; next <= 2 * n && ok; ++next) ok = fill(next);
       if (!ok) {
         fail(0);
         // the copies still in flight land before the shared memory is given up (bounded)
-        for (int32_t use = last > ring ? last - ring : 0; use <= last; ++use) full(use);
+        for (int32_t use = last_use > ring ? last_use - ring : 0; use <= last_use; ++use) full(use);
       }
     }
   } else if (is_mma) {
-    if (lane == 0) {
-      const uint32_t q0 = smem_u32(qs);
-      auto qk = [&](int32_t i) {
-        const int32_t use = k_use(i);
-        if (!full(use)) return false;
+    const bool one = lane == 0;
+    constexpr int kSteps = L::kElems / 16;
+    const uint64_t q_desc = smem_desc(smem_u32(qs), 16, L::kGroup, L::kSwizzle), k_desc = smem_desc(ring0, 16, L::kGroup, L::kSwizzle);
+    const uint64_t v_desc = smem_desc(ring0, kTile * L::kBytes, L::kGroup, L::kSwizzle);  // + byte offsets / 16
+    const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
+    int32_t kb_ = 0, kp = 0, vb = 2 % ring, vp = 2 / ring & 1;  // buffers and parities of the next K and V
+    auto qk = [&](int32_t i) {
+      if (!warp_wait(B.full[kb_], kp)) return false;
+      tc_fence_after();
+      const uint64_t kd = k_desc + (uint32_t)(kb_ * (L::kBuf >> 4));
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          mma_ss(tmem + w * kCols + (i & 1) * kTile, q_desc + (w * L::kChunks + c / kSteps) * q_chunk + (c % kSteps) * 2,
+                 kd + (uint32_t)((c / kSteps) * (kTile * L::kBytes >> 4) + (c % kSteps) * 2), kDescQK, c > 0, one);
+        mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
+      }
+      mma_commit(smem_u32(&B.empty[kb_]), one);
+      kb_ += i == 0 ? 1 : 2;
+      if (kb_ >= ring) kb_ -= ring, kp ^= 1;
+      return true;
+    };
+    bool ok = n > 0 ? qk(0) : true;
+    for (int32_t i = 0; i < n && ok; ++i) {
+      if (i + 1 < n) ok = qk(i + 1);
+      ok = ok && warp_wait(B.full[vb], vp);
+      const uint64_t vd = v_desc + (uint32_t)(vb * (L::kBuf >> 4));
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        ok = ok && warp_wait(B.p_full[w][i & 1], (i >> 1) & 1);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t k0 = ring0 + (use % ring) * L::kBuf;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            constexpr int kSteps = L::kElems / 16;
-            const uint32_t qa = q0 + (w * L::kChunks + c / kSteps) * q_rows * L::kBytes + (c % kSteps) * 32;
-            const uint32_t ka = k0 + (c / kSteps) * kTile * L::kBytes + (c % kSteps) * 32;
-            mma_ss(tmem + w * kCols + (i & 1) * kTile, smem_desc(qa, 16, L::kGroup, L::kSwizzle), smem_desc(ka, 16, L::kGroup, L::kSwizzle),
-                   kDescQK, c > 0);
-          }
-          mma_commit(smem_u32(&B.s_full[w][i & 1]));
-        }
-        mma_commit(smem_u32(&B.empty[use % ring]));
-        return true;
-      };
-      bool ok = n > 0 ? qk(0) : true;
-      for (int32_t i = 0; i < n && ok; ++i) {
-        if (i + 1 < n && !qk(i + 1)) ok = false;
-        if (!ok || !full(v_use(i))) {
-          ok = false;
-          break;
-        }
-        const uint32_t v0 = ring0 + (v_use(i) % ring) * L::kBuf;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          if (!mbar_wait_timed(smem_u32(&B.p_full[w][i & 1]), (uint32_t)((i >> 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < kTile / 16; ++c)
-            mma_ts(tmem + w * kCols + 2 * kTile, tmem + w * kCols + (i & 1) * kTile + c * 8,
-                   smem_desc(v0 + c * 2 * L::kGroup, kTile * L::kBytes, L::kGroup, L::kSwizzle), kDescPV, i > 0 || c > 0);
-          mma_commit(smem_u32(&B.pv_done[w][i & 1]));
-        }
-        mma_commit(smem_u32(&B.empty[v_use(i) % ring]));
+        for (int c = 0; c < kTile / 16; ++c)
+          mma_ts(tmem + w * kCols + 2 * kTile, tmem + w * kCols + (i & 1) * kTile + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
+                 i > 0 || c > 0, one);
+        mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
       }
-      if (!ok) {
-        fail(1);
-        mma_commit(smem_u32(&B.drain));
-        mbar_wait_timed(smem_u32(&B.drain), 0);
-      }
+      if (!ok) break;
+      mma_commit(smem_u32(&B.empty[vb]), one);
+      vb += 2;
+      if (vb >= ring) vb -= ring, vp ^= 1;
+    }
+    if (!ok) {
+      fail(1);
+      mma_commit(smem_u32(&B.drain), one);
+      warp_wait(B.drain, 0);
     }
   } else {
     const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row;
@@ -635,11 +660,15 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       uint64_t vis = sees;
       bool gaps = false;
       if (i >= lead) {
-        const int32_t slot0 = tiles[s.part + (i - lead) * split] * spt;
-        const bool v0 = lane < tt && slot0 + so0 < A.G.kb && to0 < nv[slot0 + so0];
-        const bool v1 = lane + 32 < tt && slot0 + so1 < A.G.kb && to1 < nv[slot0 + so1];
-        vis = (uint64_t)__ballot_sync(0xffffffffu, v0) | (uint64_t)__ballot_sync(0xffffffffu, v1) << 32;
-        gaps = vis != low_bits(tt);
+        const uint16_t tile = tiles[s.part + (i - lead) * split];
+        vis = low_bits(tt);
+        gaps = !(tile & kWhole);
+        if (gaps) {
+          const int32_t slot0 = tile_of(tile) * spt;
+          const bool v0 = lane < tt && slot0 + so0 < A.G.kb && to0 < nv[slot0 + so0];
+          const bool v1 = lane + 32 < tt && slot0 + so1 < A.G.kb && to1 < nv[slot0 + so1];
+          vis = (uint64_t)__ballot_sync(0xffffffffu, v0) | (uint64_t)__ballot_sync(0xffffffffu, v1) << 32;
+        }
       }
       if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
         fail(2);
