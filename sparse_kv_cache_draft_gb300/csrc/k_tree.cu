@@ -384,11 +384,16 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 
 // ---- tensor cores: bf16 ------------------------------------------------------------------------------
 //
-// A CTA holds NW groups of 128 rows (one softmax warpgroup each) over the same tiles of 64 tokens.
-// One warp copies K and V tiles by TMA into a ring of buffers, one thread issues the MMAs:
-//   S = Q K^T   128 x 64, Q and K in shared memory, S in TMEM (two buffers)
-//   O += P V    128 x d,  P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
-// S of the next tile is computed while the warpgroup works on this one's softmax, a thread to a row.
+// A CTA holds NW groups of 128 rows (one softmax warpgroup each) over the same tiles of tokens. One warp
+// copies K and V tiles by TMA into a ring of buffers, one thread issues the MMAs:
+//   S = Q K^T   128 x tile, Q and K in shared memory, S in TMEM
+//   O += P V    128 x d,    P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
+// and a thread of the warpgroup takes a row's softmax.
+//
+// Up to 128 rows (NW = 1) HBM is the limit: tiles are 64 tokens, two CTAs share an SM, and S has two
+// buffers, so that S of the next tile is there before this one's softmax is done. Beyond (NW = 2) it is the
+// tensor cores: tiles are 128 tokens (an MMA of 64 columns takes no less time for its A than one of 128)
+// and one S buffer per warpgroup is enough, as each warpgroup's softmax runs beside the other's products.
 // The running maximum moves only when a row grows past it by 2^8 (the weights then stay below 2^8,
 // exact in binary32 sums and as exact in bf16 as any other); only then is O read back and scaled.
 // Weights are rounded to bf16 for the second product, as the tensor cores take them; their sum is of
@@ -401,17 +406,24 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 // [rows][line] under the 128-byte (64-byte) swizzle, Q and K K-major, V MN-major. A K or V tile is d / line
 // TMA copies of whole slots, straight from the pool's layout.
 
-template <int D>
+template <int D, int NW>
 struct Lines {
+  static constexpr int kTile = NW == 2 ? 128 : 64;            // tokens of a tile
+  static constexpr int kS = 128 / kTile;                      // S buffers
   static constexpr int kElems = D % 64 == 0 ? 64 : 32;
   static constexpr int kBytes = kElems * 2;
   static constexpr int kChunks = D / kElems;
   static constexpr uint32_t kSwizzle = kElems == 64 ? 2 : 4;  // of the operand descriptors
   static constexpr uint32_t kGroup = 8 * kBytes;              // 8 rows
+  static constexpr int kChunk = kTile * kBytes;               // a chunk of a tile
   static constexpr int kBuf = kTile * D * 2;                  // a tile of K or V
   // byte offset of 16-byte piece c (0 .. kBytes / 16 - 1) of line `row` of a chunk
   __device__ static __forceinline__ uint32_t at(int row, int c) {
     return kElems == 64 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+  }
+  // ... of 16-byte piece c of token j's line in a tile
+  __device__ static __forceinline__ uint32_t piece(int j, int c) {
+    return (c / (kBytes / 16)) * kChunk + at(j, c % (kBytes / 16));
   }
 };
 
@@ -450,13 +462,15 @@ __device__ __forceinline__ bool clean(uint4& u) {
 template <int D, int NW>
 __global__ void __launch_bounds__(NW * 128 + 64, D <= 128 && NW == 1 ? 2 : 1)
 tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const int32_t split, const int32_t ring, const int32_t q_rows) {
-  using L = Lines<D>;
-  constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S, S, O
+  using L = Lines<D, NW>;
+  constexpr int kTile = L::kTile, kS = L::kS;
+  constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
+  constexpr uint32_t kO = 128;
   constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem;                                                        // [NW][chunks][q_rows][line]
-  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][64][line]
+  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
   MmaBars& B = *reinterpret_cast<MmaBars*>(rs + (size_t)ring * L::kBuf);
   uint8_t* nv = reinterpret_cast<uint8_t*>(&B + 1);                          // [kb]
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
@@ -469,9 +483,10 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   const uint32_t ring0 = smem_u32(rs);
 
-  // Tile i's K is the (2i - 1)-th use of the ring (the first: use 0), its V the (2i + 2)-th: the order
-  // in which the MMAs take them, S of tile i + 1 before O of tile i.
-  auto v_use = [](int32_t i) { return 2 * i + 2; };
+  // The uses of the ring are in the order in which the MMAs take them. With two S buffers, S of tile i + 1
+  // comes before O of tile i: K of tile i is use 2i - 1 (the first: 0), V use 2i + 2. With one, K is 2i, V 2i + 1.
+  auto v_use = [](int32_t i) { return kS == 2 ? 2 * i + 2 : 2 * i + 1; };
+  auto uses = [](int32_t tiles_) { return kS == 2 ? 2 * tiles_ + 1 : 2 * tiles_; };
   auto full = [&](int32_t use) { return mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1)); };
   // ... by all lanes of a warp: what follows is by whole warps
   auto warp_wait = [&](uint64_t& bar, int32_t parity) {
@@ -487,15 +502,15 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   int32_t last_use = -1;  // copy warp: the last use filled
   const int32_t unit_slot = (int32_t)(((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb);
   auto fill = [&](int32_t use) {
-    const bool v = use > 0 && use % 2 == 0;
-    const int32_t i = v ? use / 2 - 1 : (use + 1) / 2, b = use % ring;
+    const bool v = kS == 2 ? use > 0 && use % 2 == 0 : use % 2 == 1;
+    const int32_t i = kS == 1 ? use / 2 : v ? use / 2 - 1 : (use + 1) / 2, b = use % ring;
     if (i < lead || i >= n) return true;  // the drafted tokens, or the use that a further K would have
     if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)((use / ring - 1) & 1))) return false;
     const uint32_t bar = smem_u32(&B.full[b]);
     const int32_t slot = unit_slot + tile_of(tiles[s.part + (i - lead) * split]) * spt;
     mbar_expect_tx(bar, (uint32_t)(tt * D * 2));
 #pragma unroll
-    for (int c = 0; c < L::kChunks; ++c) tma_load_5d(ring0 + b * L::kBuf + c * kTile * L::kBytes, &map, bar, 0, c, 0, v ? 1 : 0, slot);
+    for (int c = 0; c < L::kChunks; ++c) tma_load_5d(ring0 + b * L::kBuf + c * L::kChunk, &map, bar, 0, c, 0, v ? 1 : 0, slot);
     last_use = use;
     return true;
   };
@@ -517,9 +532,9 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       mbar_init(smem_u32(&B.drain), 1);
       fence_mbar_init();
       fence_proxy_async();
-      if (draft) {  // buffers 0 and 2 are filled by the softmax warps, once
+      if (draft) {  // the first K and V are filled by the softmax warps
         mbar_arrive(smem_u32(&B.full[0]));
-        mbar_arrive(smem_u32(&B.full[2]));
+        mbar_arrive(smem_u32(&B.full[v_use(0)]));
       }
       B.failed = 0;
     }
@@ -528,12 +543,12 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     n = (all - s.part + split - 1) / split + lead;
     if (lane == 0) {
       B.n_tiles = n;
-      for (; next < ring && next <= 2 * n; ++next) fill(next);
+      for (; next < ring && next < uses(n); ++next) fill(next);
     }
   } else if (is_mma) {
     tmem_alloc(smem_u32(&B.tmem), kCols * NW);
   } else {
-    constexpr int kPieces = D / 8, kLine = L::kBytes / 16, kThreads = NW * 128;
+    constexpr int kPieces = D / 8, kLine = L::kBytes / 16, kThreads = NW * 128, kEach = kTile * kPieces / kThreads;
     const uint32_t q0 = smem_u32(qs);
     uint64_t any_bad = 0;
     for (int i = tid; i < s.rows * kPieces; i += kThreads) {
@@ -543,25 +558,25 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     }
     if (draft) {
       uint64_t bad = 0;
-      uint4 y[kTile * kPieces / kThreads];
+      uint4 y[kEach];
 #pragma unroll
-      for (int u = 0; u < kTile * kPieces / kThreads; ++u) {
+      for (int u = 0; u < kEach; ++u) {
         const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
-        const uint32_t to = ring0 + (c / kLine) * kTile * L::kBytes + L::at(j, c % kLine);
+        const uint32_t to = L::piece(j, c);
         y[u] = make_uint4(0, 0, 0, 0);
         if (j < s.cnt) {
           const int64_t at = draft_offset(A, s, j) + c * 8;
-          copy16(to, (const __nv_bfloat16*)A.k + at);
+          copy16(ring0 + to, (const __nv_bfloat16*)A.k + at);
           y[u] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + at);
         } else {
-          *reinterpret_cast<uint4*>(rs + (to - ring0)) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(rs + to) = make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kTile * kPieces / kThreads; ++u) {
+      for (int u = 0; u < kEach; ++u) {
         const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
         if (clean(y[u])) bad |= 1ull << j;
-        *reinterpret_cast<uint4*>(rs + (size_t)2 * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(j, c % kLine)) = y[u];
+        *reinterpret_cast<uint4*>(rs + v_use(0) * L::kBuf + L::piece(j, c)) = y[u];
       }
       any_bad = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)bad);
     }
@@ -569,8 +584,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     if (tt < kTile)  // the copies leave these lines alone; as V they meet weights of zero
       for (int i = tid; i < ring * (kTile - tt) * kPieces; i += kThreads) {
         const int c = i % kPieces, rest = i / kPieces, row = tt + rest % (kTile - tt), b = rest / (kTile - tt);
-        if (!draft || (b != 0 && b != 2))
-          *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + (size_t)(c / kLine) * kTile * L::kBytes + L::at(row, c % kLine)) = make_uint4(0, 0, 0, 0);
+        if (!draft || (b != 0 && b != v_use(0))) *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + L::piece(row, c)) = make_uint4(0, 0, 0, 0);
       }
     copy16_wait();
     fence_proxy_async();
@@ -590,7 +604,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   if (is_copy) {
     if (lane == 0) {
       bool ok = true;
-      for (; next <= 2 * n && ok; ++next) ok = fill(next);
+      for (; next < uses(n) && ok; ++next) ok = fill(next);
       if (!ok) {
         fail(0);
         // the copies still in flight land before the shared memory is given up (bounded)
@@ -601,29 +615,42 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     const bool one = lane == 0;
     constexpr int kSteps = L::kElems / 16;
     const uint64_t q_desc = smem_desc(smem_u32(qs), 16, L::kGroup, L::kSwizzle), k_desc = smem_desc(ring0, 16, L::kGroup, L::kSwizzle);
-    const uint64_t v_desc = smem_desc(ring0, kTile * L::kBytes, L::kGroup, L::kSwizzle);  // + byte offsets / 16
+    const uint64_t v_desc = smem_desc(ring0, L::kChunk, L::kGroup, L::kSwizzle);  // + byte offsets / 16
     const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
-    int32_t kb_ = 0, kp = 0, vb = 2 % ring, vp = 2 / ring & 1;  // buffers and parities of the next K and V
-    auto qk = [&](int32_t i) {
-      if (!warp_wait(B.full[kb_], kp)) return false;
-      tc_fence_after();
-      const uint64_t kd = k_desc + (uint32_t)(kb_ * (L::kBuf >> 4));
+    int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
+    auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
+      b += by;
+      if (b >= ring) b -= ring, parity ^= 1;
+    };
+    auto qk = [&](int32_t i, int w) {  // S of tile i for warpgroup w
+      const uint64_t kd = k_desc + (uint32_t)(kb * (L::kBuf >> 4));
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          mma_ss(tmem + w * kCols + (i & 1) * kTile, q_desc + (w * L::kChunks + c / kSteps) * q_chunk + (c % kSteps) * 2,
-                 kd + (uint32_t)((c / kSteps) * (kTile * L::kBytes >> 4) + (c % kSteps) * 2), kDescQK, c > 0, one);
-        mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0), q_desc + (w * L::kChunks + c / kSteps) * q_chunk + (c % kSteps) * 2,
+               kd + (uint32_t)((c / kSteps) * (L::kChunk >> 4) + (c % kSteps) * 2), kDescQK, c > 0, one);
+      mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
+      if (w == NW - 1) {
+        mma_commit(smem_u32(&B.empty[kb]), one);
+        step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
       }
-      mma_commit(smem_u32(&B.empty[kb_]), one);
-      kb_ += i == 0 ? 1 : 2;
-      if (kb_ >= ring) kb_ -= ring, kp ^= 1;
+    };
+    auto k_ready = [&] {
+      if (!warp_wait(B.full[kb], kp)) return false;
+      tc_fence_after();
       return true;
     };
-    bool ok = n > 0 ? qk(0) : true;
+    bool ok = true;
+    if (n > 0) {
+      ok = k_ready();
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        if (ok) qk(0, w);
+    }
     for (int32_t i = 0; i < n && ok; ++i) {
-      if (i + 1 < n) ok = qk(i + 1);
+      if (kS == 2 && i + 1 < n) {
+        ok = k_ready();
+        if (ok) qk(i + 1, 0);
+      }
       ok = ok && warp_wait(B.full[vb], vp);
       const uint64_t vd = v_desc + (uint32_t)(vb * (L::kBuf >> 4));
 #pragma unroll
@@ -633,14 +660,18 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kTile / 16; ++c)
-          mma_ts(tmem + w * kCols + 2 * kTile, tmem + w * kCols + (i & 1) * kTile + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
+          mma_ts(tmem + w * kCols + kO, tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0) + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
                  i > 0 || c > 0, one);
         mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
+        if (kS == 1 && i + 1 < n) {  // S takes the place of the P just used: the products run in order
+          if (w == 0) ok = k_ready();
+          if (!ok) break;
+          qk(i + 1, w);
+        }
       }
       if (!ok) break;
       mma_commit(smem_u32(&B.empty[vb]), one);
-      vb += 2;
-      if (vb >= ring) vb -= ring, vp ^= 1;
+      step(vb, vp, 2);
     }
     if (!ok) {
       fail(1);
@@ -655,19 +686,21 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     const float scale = kLog2e * rsqrtf((float)D);
     uint64_t sees = 0;
     if (draft && wrow < s.rows) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
-    const int32_t so0 = lane / bs, to0 = lane % bs, so1 = (lane + 32) / bs, to1 = (lane + 32) % bs;
+    int32_t slot_at[kTile / 32], tok_at[kTile / 32];  // of token lane + 32 u of a tile
+#pragma unroll
+    for (int u = 0; u < kTile / 32; ++u) slot_at[u] = (lane + 32 * u) / bs, tok_at[u] = (lane + 32 * u) % bs;
     for (int32_t i = 0; i < n; ++i) {
-      uint64_t vis = sees;
-      bool gaps = false;
+      uint32_t vis[kTile / 32] = {(uint32_t)sees, (uint32_t)(sees >> 32)};  // who the row sees of the tile
+      bool gaps = false, masked = true;
       if (i >= lead) {
         const uint16_t tile = tiles[s.part + (i - lead) * split];
-        vis = low_bits(tt);
         gaps = !(tile & kWhole);
-        if (gaps) {
+        masked = gaps || tt < kTile;
+        if (masked) {
           const int32_t slot0 = tile_of(tile) * spt;
-          const bool v0 = lane < tt && slot0 + so0 < A.G.kb && to0 < nv[slot0 + so0];
-          const bool v1 = lane + 32 < tt && slot0 + so1 < A.G.kb && to1 < nv[slot0 + so1];
-          vis = (uint64_t)__ballot_sync(0xffffffffu, v0) | (uint64_t)__ballot_sync(0xffffffffu, v1) << 32;
+#pragma unroll
+          for (int u = 0; u < kTile / 32; ++u)
+            vis[u] = __ballot_sync(0xffffffffu, lane + 32 * u < tt && slot0 + slot_at[u] < A.G.kb && tok_at[u] < nv[slot0 + slot_at[u]]);
         }
       }
       if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
@@ -682,22 +715,30 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       }
       tc_fence_after();
       if (active) {
+        const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
         uint32_t a[32], b[32];
-        tmem_ld32(a, my + (i & 1) * kTile);
-        tmem_ld32(b, my + (i & 1) * kTile + 32);
-        tmem_wait_ld(a);
-        tmem_wait_ld(b);
-        if (vis != ~0ull) {
-          const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+        // 64 scores of the row from column c on; those it does not see as -infinity
+        auto scores = [&](int c) {
+          tmem_ld32(a, st + c);
+          tmem_ld32(b, st + c + 32);
+          tmem_wait_ld(a);
+          tmem_wait_ld(b);
+          if (masked) {
+            const uint32_t lo = vis[c / 32], hi = vis[c / 32 + 1];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(lo >> e & 1)) a[e] = 0xFF800000u;
-            if (!(hi >> e & 1)) b[e] = 0xFF800000u;
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo >> e & 1)) a[e] = 0xFF800000u;
+              if (!(hi >> e & 1)) b[e] = 0xFF800000u;
+            }
           }
-        }
+        };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
+        for (int c = 0; c < kTile; c += 64) {
+          scores(kTile - 64 - c);  // the first 64 last: they stay in registers for the weights
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         const bool grow = top > m_run + 8.f;
         if (__any_sync(0xffffffffu, grow)) {
@@ -714,30 +755,34 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
-              tmem_ld32(o, my + 2 * kTile + c);
+              tmem_ld32(o, my + kO + c);
               tmem_wait_ld(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(my + 2 * kTile + c, o);
+              tmem_st32(my + kO + c, o);
             }
           }
         }
         const float neg = m_run == -INFINITY ? 0.f : -m_run;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t p[32];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = ex2(fmaf(__uint_as_float(a[2 * e]), scale, neg)), y = ex2(fmaf(__uint_as_float(a[2 * e + 1]), scale, neg));
-          const float z = ex2(fmaf(__uint_as_float(b[2 * e]), scale, neg)), u = ex2(fmaf(__uint_as_float(b[2 * e + 1]), scale, neg));
-          sum[0] += x;
-          sum[1] += y;
-          sum[2] += z;
-          sum[3] += u;
-          p[e] = pack2(x, y);
-          p[16 + e] = pack2(z, u);
+        for (int c = 0; c < kTile; c += 64) {
+          if (c > 0) scores(c);
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = ex2(fmaf(__uint_as_float(a[2 * e]), scale, neg)), y = ex2(fmaf(__uint_as_float(a[2 * e + 1]), scale, neg));
+            const float z = ex2(fmaf(__uint_as_float(b[2 * e]), scale, neg)), u = ex2(fmaf(__uint_as_float(b[2 * e + 1]), scale, neg));
+            sum[0] += x;
+            sum[1] += y;
+            sum[2] += z;
+            sum[3] += u;
+            p[e] = pack2(x, y);
+            p[16 + e] = pack2(z, u);
+          }
+          tmem_st32(st + c / 2, p);  // over scores that have been read
         }
         l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(my + (i & 1) * kTile, p);
         tmem_wait_st();
       }
       if (gaps && w == 0) {
@@ -746,12 +791,14 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
           fail(4);
           break;
         }
-        constexpr int kPieces = D / 8, kLine = L::kBytes / 16;
+        constexpr int kPieces = D / 8;
         uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
-        for (int e = row; e < tt * kPieces; e += 128) {
-          const int j = e / kPieces, c = e % kPieces;
-          if (!(vis >> j & 1)) *reinterpret_cast<uint4*>(v + (size_t)(c / kLine) * kTile * L::kBytes + j * L::kBytes + (c % kLine) * 16) = make_uint4(0, 0, 0, 0);
-        }
+#pragma unroll
+        for (int u = 0; u < kTile / 32; ++u)
+          for (int e = row; e < 32 * kPieces; e += 128) {
+            const int j = e / kPieces, c = e % kPieces;
+            if (!(vis[u] >> j & 1)) *reinterpret_cast<uint4*>(v + L::piece(32 * u + j, c)) = make_uint4(0, 0, 0, 0);
+          }
         fence_proxy_async();
       }
       tc_fence_before();
@@ -764,7 +811,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   const bool failed = *(volatile int32_t*)&B.failed != 0;
   if (warp < NW * 4) {
     const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row, mrow = s.row0 + wrow;
-    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + 2 * kTile;
+    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + kO;
     if (w * 128 + (warp & 3) * 32 < s.rows) {
       if (split == 1) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
@@ -895,9 +942,9 @@ EncodeFn encode_fn() {
 }
 
 // The pool as [slots][K, V][tokens][chunks][line], a box of one chunk of the tokens of a tile's slots.
-template <int D>
+template <int D, int NW>
 cudaError_t pool_map(const TreeArgs& A, int32_t spt, CUtensorMap* map) {
-  using L = Lines<D>;
+  using L = Lines<D, NW>;
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const uint64_t token = (uint64_t)D * 2, half = token * A.G.bs;
@@ -914,8 +961,8 @@ cudaError_t pool_map(const TreeArgs& A, int32_t spt, CUtensorMap* map) {
 
 template <int D, int NW>
 cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
-  using L = Lines<D>;
-  const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
+  using L = Lines<D, NW>;
+  const int32_t spt = L::kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
   const int32_t rows = A.T * A.G.g, groups = (rows + NW * 128 - 1) / (NW * 128);
   const int32_t q_rows = NW > 1 || rows >= 128 ? 128 : (rows + 7) / 8 * 8;
   // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
@@ -930,7 +977,7 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int64_t units = (int64_t)n_active * A.G.Hkv;
   const int32_t split = pick_split(units * groups, (int64_t)sm_count() * (two ? 2 : 1), tiles);
   CUtensorMap map;
-  if (cudaError_t e = pool_map<D>(A, spt, &map)) return e;
+  if (cudaError_t e = pool_map<D, NW>(A, spt, &map)) return e;
   return launch_cluster(tree_mma_kernel<D, NW>, dim3((unsigned)(units * split), groups), NW * 128 + 64, smem, split, s, A, map, split, ring,
                         q_rows);
 }
