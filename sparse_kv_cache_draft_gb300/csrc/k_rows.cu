@@ -19,7 +19,7 @@
 #include <cuda_bf16.h>
 
 #include "okv_tree.h"
-#include "ptx.cuh"
+#include "tc5.cuh"
 
 namespace okv {
 namespace {
@@ -105,20 +105,6 @@ __device__ __forceinline__ void angle(uint64_t per, float f, int32_t pos, float*
   *c = (quarter == 1 || quarter == 2) ? -a : a;
   *s = quarter >= 2 ? -b : b;
   if (!isfinite(f)) *c = *s = __int_as_float(0x7FC00000);
-}
-
-// Two binary32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
 }
 
 // The turn of one kind of head (queries or keys) at one position, for the 8 dims of a lane: element e of a

@@ -432,8 +432,8 @@ struct Lines {
 // tile i, as that thread may be done with O of tile i - 1 before the softmax has looked at tile i - 2.
 constexpr int kMaxRing = 12;
 struct MmaBars {
-  uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][2], p_full[2][2], pv_done[2][2], drain;
-  uint64_t bad, bad_of[8];  // drafted tokens with values that are not finite: all, found by each warp
+  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2], pv_done[2][2], drain;
+  uint64_t bad;  // drafted tokens with values that are not finite
   uint32_t tmem;
   int32_t n_tiles, failed;
 };
@@ -459,9 +459,14 @@ __device__ __forceinline__ bool clean(uint4& u) {
   return any;
 }
 
+// The tensor maps of a launch: the pool, the queries and the drafted keys and values.
+struct MmaMaps {
+  CUtensorMap pool, q, k, v;
+};
+
 template <int D, int NW>
 __global__ void __launch_bounds__(NW * 128 + 64, D <= 128 && NW == 1 ? 2 : 1)
-tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const int32_t split, const int32_t ring, const int32_t q_rows) {
+tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32_t split, const int32_t ring, const int32_t q_tok, const int32_t q_rows) {
   using L = Lines<D, NW>;
   constexpr int kTile = L::kTile, kS = L::kS;
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
@@ -475,10 +480,12 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   uint8_t* nv = reinterpret_cast<uint8_t*>(&B + 1);                          // [kb]
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
-  const Site s = make_site(A, split, NW * 128);
-  if (s.rows <= 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1;
+  if (is_copy && lane < 4) tma_prefetch_map(&M.pool + lane);
+  const int32_t gr = q_tok * A.G.g;  // rows of a warpgroup: q_tok drafted tokens, all heads of the group
+  const Site s = make_site(A, split, NW * gr);
+  if (s.rows <= 0) return;
   const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   const uint32_t ring0 = smem_u32(rs);
@@ -498,32 +505,36 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   };
   const int32_t lead = draft ? 1 : 0;
   int32_t n = 0;          // this CTA's tiles
-  int32_t next = 0;       // copy warp: the next use to fill
-  int32_t last_use = -1;  // copy warp: the last use filled
+  // copy warp: the next use to fill, its buffer and the parity of its fill
+  int32_t next = 0, next_buf = 0, next_par = 0, issued = 0;
   const int32_t unit_slot = (int32_t)(((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb);
-  auto fill = [&](int32_t use) {
+  auto fill = [&] {
+    const int32_t use = next, b = next_buf, parity = next_par;
     const bool v = kS == 2 ? use > 0 && use % 2 == 0 : use % 2 == 1;
-    const int32_t i = kS == 1 ? use / 2 : v ? use / 2 - 1 : (use + 1) / 2, b = use % ring;
+    const int32_t i = kS == 1 ? use / 2 : v ? use / 2 - 1 : (use + 1) / 2;
+    ++next;
+    if (++next_buf == ring) next_buf = 0, next_par ^= 1;
     if (i < lead || i >= n) return true;  // the drafted tokens, or the use that a further K would have
-    if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)((use / ring - 1) & 1))) return false;
+    if (use >= ring && !mbar_wait_timed(smem_u32(&B.empty[b]), (uint32_t)(parity ^ 1))) return false;
     const uint32_t bar = smem_u32(&B.full[b]);
     const int32_t slot = unit_slot + tile_of(tiles[s.part + (i - lead) * split]) * spt;
     mbar_expect_tx(bar, (uint32_t)(tt * D * 2));
 #pragma unroll
-    for (int c = 0; c < L::kChunks; ++c) tma_load_5d(ring0 + b * L::kBuf + c * L::kChunk, &map, bar, 0, c, 0, v ? 1 : 0, slot);
-    last_use = use;
+    for (int c = 0; c < L::kChunks; ++c) tma_load_5d(ring0 + b * L::kBuf + c * L::kChunk, &M.pool, bar, 0, c, 0, v ? 1 : 0, slot);
+    issued = next;
     return true;
   };
 
-  // Setup: the copy warp reads the slot table and starts the copies that need no free buffer, while the
-  // softmax warps bring in the queries and the drafted tokens.
+  // Setup: the copy warp starts the copies of the queries and the drafted tokens, reads the slot table and
+  // starts the pool's copies that need no free buffer.
   if (is_copy) {
     if (lane == 0) {
       for (int i = 0; i < ring; ++i) {
         mbar_init(smem_u32(&B.full[i]), 1);
         mbar_init(smem_u32(&B.empty[i]), 1);
       }
-      for (int w = 0; w < 2; ++w)
+      mbar_init(smem_u32(&B.q_full), 1);
+      for (int w = 0; w < NW; ++w)
         for (int e = 0; e < 2; ++e) {
           mbar_init(smem_u32(&B.s_full[w][e]), 1);
           mbar_init(smem_u32(&B.p_full[w][e]), 128);
@@ -532,84 +543,56 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       mbar_init(smem_u32(&B.drain), 1);
       fence_mbar_init();
       fence_proxy_async();
-      if (draft) {  // the first K and V are filled by the softmax warps
-        mbar_arrive(smem_u32(&B.full[0]));
-        mbar_arrive(smem_u32(&B.full[v_use(0)]));
-      }
       B.failed = 0;
+      B.bad = 0;
+      // rows (t, head of the group) of a box follow one another as the group's rows do; a box past the last
+      // request's tokens is filled up with zeros
+      const uint32_t q_bar = smem_u32(&B.q_full);
+      const int32_t boxes = NW > 1 && s.rows > gr ? 2 : 1, tok0 = s.r * A.T;
+      mbar_expect_tx(q_bar, (uint32_t)(boxes * gr * D * 2));
+      for (int w = 0; w < boxes; ++w)
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_5d(smem_u32(qs) + (w * L::kChunks + c) * q_rows * L::kBytes, &M.q, q_bar, 0, c, 0, s.h, tok0 + s.row0 / A.G.g + w * q_tok);
+      if (draft)
+        for (int e = 0; e < 2; ++e) {
+          const int32_t b = e ? v_use(0) : 0;
+          const uint32_t bar = smem_u32(&B.full[b]);
+          mbar_expect_tx(bar, (uint32_t)(A.T * D * 2));
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_5d(ring0 + b * L::kBuf + c * L::kChunk, e ? &M.v : &M.k, bar, 0, c, s.h, tok0, 0);
+        }
     }
+    __syncwarp();
     const int32_t all = list_tiles(A, s, spt, nv, tiles);
     __syncwarp();
     n = (all - s.part + split - 1) / split + lead;
     if (lane == 0) {
       B.n_tiles = n;
-      for (; next < ring && next < uses(n); ++next) fill(next);
+      while (next < ring && next < uses(n)) fill();
     }
   } else if (is_mma) {
     tmem_alloc(smem_u32(&B.tmem), kCols * NW);
-  } else {
-    constexpr int kPieces = D / 8, kLine = L::kBytes / 16, kThreads = NW * 128, kEach = kTile * kPieces / kThreads;
-    const uint32_t q0 = smem_u32(qs);
-    uint64_t any_bad = 0;
-    for (int i = tid; i < s.rows * kPieces; i += kThreads) {
-      const int row = i / kPieces, c = i % kPieces;
-      copy16(q0 + ((row >> 7) * L::kChunks + c / kLine) * q_rows * L::kBytes + L::at(row & 127, c % kLine),
-             (const __nv_bfloat16*)A.q + row_offset(A, s, s.row0 + row) + c * 8);
-    }
-    if (draft) {
-      uint64_t bad = 0;
-      uint4 y[kEach];
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
-        const uint32_t to = L::piece(j, c);
-        y[u] = make_uint4(0, 0, 0, 0);
-        if (j < s.cnt) {
-          const int64_t at = draft_offset(A, s, j) + c * 8;
-          copy16(ring0 + to, (const __nv_bfloat16*)A.k + at);
-          y[u] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + at);
-        } else {
-          *reinterpret_cast<uint4*>(rs + to) = make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kThreads, j = i / kPieces, c = i % kPieces;
-        if (clean(y[u])) bad |= 1ull << j;
-        *reinterpret_cast<uint4*>(rs + v_use(0) * L::kBuf + L::piece(j, c)) = y[u];
-      }
-      any_bad = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)bad);
-    }
-    if (lane == 0) B.bad_of[warp] = any_bad;
-    if (tt < kTile)  // the copies leave these lines alone; as V they meet weights of zero
-      for (int i = tid; i < ring * (kTile - tt) * kPieces; i += kThreads) {
-        const int c = i % kPieces, rest = i / kPieces, row = tt + rest % (kTile - tt), b = rest / (kTile - tt);
-        if (!draft || (b != 0 && b != v_use(0))) *reinterpret_cast<uint4*>(rs + (size_t)b * L::kBuf + L::piece(row, c)) = make_uint4(0, 0, 0, 0);
-      }
-    copy16_wait();
-    fence_proxy_async();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
   n = __shfl_sync(0xffffffffu, B.n_tiles, 0);
-  if (tid == 0) {
-    uint64_t bad = 0;
-    for (int i = 0; i < NW * 4; ++i) bad |= B.bad_of[i];
-    B.bad = bad;  // read after the loops
-  }
   float m_run = -INFINITY, l_run = 0.f;
 
   if (is_copy) {
     if (lane == 0) {
       bool ok = true;
-      for (; next < uses(n) && ok; ++next) ok = fill(next);
+      while (next < uses(n) && ok) ok = fill();
       if (!ok) {
         fail(0);
         // the copies still in flight land before the shared memory is given up (bounded)
-        for (int32_t use = last_use > ring ? last_use - ring : 0; use <= last_use; ++use) full(use);
+        for (int32_t use = issued > ring ? issued - ring : 0; use < issued; ++use) full(use);
+        if (draft && issued <= ring) full(0), full(v_use(0));
       }
+      if (!ok || n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
     }
   } else if (is_mma) {
     const bool one = lane == 0;
@@ -641,7 +624,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
     };
     bool ok = true;
     if (n > 0) {
-      ok = k_ready();
+      ok = warp_wait(B.q_full, 0) && k_ready();
 #pragma unroll
       for (int w = 0; w < NW; ++w)
         if (ok) qk(0, w);
@@ -679,13 +662,12 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       warp_wait(B.drain, 0);
     }
   } else {
-    const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
-    const uint32_t my = tmem + w * kCols + lanes;
-    const bool active = w * 128 + (warp & 3) * 32 < s.rows;
+    const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
+    const bool real = row < gr && wrow < s.rows, active = (warp & 3) * 32 < min(gr, s.rows - w * gr);
+    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
     const float scale = kLog2e * rsqrtf((float)D);
     uint64_t sees = 0;
-    if (draft && wrow < s.rows) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
+    if (draft && real) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
     int32_t slot_at[kTile / 32], tok_at[kTile / 32];  // of token lane + 32 u of a tile
 #pragma unroll
     for (int u = 0; u < kTile / 32; ++u) slot_at[u] = (lane + 32 * u) / bs, tok_at[u] = (lane + 32 * u) % bs;
@@ -694,9 +676,8 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
       bool gaps = false, masked = true;
       if (i >= lead) {
         const uint16_t tile = tiles[s.part + (i - lead) * split];
-        gaps = !(tile & kWhole);
-        masked = gaps || tt < kTile;
-        if (masked) {
+        gaps = masked = !(tile & kWhole) || tt < kTile;
+        if (gaps) {
           const int32_t slot0 = tile_of(tile) * spt;
 #pragma unroll
           for (int u = 0; u < kTile / 32; ++u)
@@ -707,9 +688,9 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
         fail(2);
         break;
       }
-      // S of tile i follows O of tile i - 2, so this passes at once; it keeps each barrier's waits in step
-      // with its phases, where tile i - 1's below is waited for only now and then
-      if (i > 1 && !warp_wait(B.pv_done[w][i & 1], ((i - 2) >> 1) & 1)) {
+      // With two S buffers, S of tile i follows O of tile i - 2, so this passes at once; it keeps each barrier's
+      // waits in step with its phases, where tile i - 1's below is waited for only now and then
+      if (kS == 2 && i > 1 && !warp_wait(B.pv_done[w][i & 1], ((i - 2) >> 1) & 1)) {
         fail(6);
         break;
       }
@@ -747,7 +728,8 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
           m_run = mn;
           l_run *= f;
           if (i > 0) {
-            if (!warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1)) {
+            // with one, S of tile i follows O of tile i - 1: nothing to wait for
+            if (kS == 2 && !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1)) {
               fail(3);
               break;
             }
@@ -764,41 +746,59 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
           }
         }
         const float neg = m_run == -INFINITY ? 0.f : -m_run;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < kTile; c += 64) {
           if (c > 0) scores(c);
           uint32_t p[32];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x = ex2(fmaf(__uint_as_float(a[2 * e]), scale, neg)), y = ex2(fmaf(__uint_as_float(a[2 * e + 1]), scale, neg));
-            const float z = ex2(fmaf(__uint_as_float(b[2 * e]), scale, neg)), u = ex2(fmaf(__uint_as_float(b[2 * e + 1]), scale, neg));
-            sum[0] += x;
-            sum[1] += y;
-            sum[2] += z;
-            sum[3] += u;
-            p[e] = pack2(x, y);
-            p[16 + e] = pack2(z, u);
+            float2 x = fma2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), scale2, neg2);
+            float2 y = fma2(make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])), scale2, neg2);
+            x = make_float2(ex2(x.x), ex2(x.y));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum0 = add2(sum0, x);
+            sum1 = add2(sum1, y);
+            p[e] = pack2(x.x, x.y);
+            p[16 + e] = pack2(y.x, y.y);
           }
           tmem_st32(st + c / 2, p);  // over scores that have been read
         }
-        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum0 = add2(sum0, sum1);
+        l_run += sum0.x + sum0.y;
         tmem_wait_st();
       }
-      if (gaps && w == 0) {
-        // lines of the V tile that hold no valid token may hold anything: zero them before the product
+      if (w == 0 && (gaps || i < lead)) {
+        // Lines of the V tile that hold no valid token may hold anything: zero them before the product. So
+        // are drafted values that are not finite, and their tokens noted.
         if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
           fail(4);
           break;
         }
         constexpr int kPieces = D / 8;
         uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
-#pragma unroll
-        for (int u = 0; u < kTile / 32; ++u)
-          for (int e = row; e < 32 * kPieces; e += 128) {
-            const int j = e / kPieces, c = e % kPieces;
-            if (!(vis[u] >> j & 1)) *reinterpret_cast<uint4*>(v + L::piece(32 * u + j, c)) = make_uint4(0, 0, 0, 0);
+        if (i < lead) {
+          for (int e = row; e < kTile * kPieces; e += 128) {
+            const int j = e / kPieces;
+            uint4* x = reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces));
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (j < s.cnt) {
+              y = *x;
+              if (!clean(y)) continue;
+              atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
+            }
+            *x = y;
           }
+        } else {
+#pragma unroll
+          for (int u = 0; u < kTile / 32; ++u)
+            for (int e = row; e < 32 * kPieces; e += 128) {
+              const int j = e / kPieces, c = e % kPieces;
+              if (!(vis[u] >> j & 1)) *reinterpret_cast<uint4*>(v + L::piece(32 * u + j, c)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        __syncwarp();
         fence_proxy_async();
       }
       tc_fence_before();
@@ -810,51 +810,60 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map, const
   __syncthreads();  // every product done: the ring and Q become the cluster's partials
   const bool failed = *(volatile int32_t*)&B.failed != 0;
   if (warp < NW * 4) {
-    const int w = warp >> 2, row = tid & 127, wrow = w * 128 + row, mrow = s.row0 + wrow;
+    const int w = warp >> 2, row = tid & 127, wrow = w * gr + row, mrow = s.row0 + wrow;
+    const bool real = row < gr && wrow < s.rows;
+    const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32;  // of this warp
     const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + kO;
-    if (w * 128 + (warp & 3) * 32 < s.rows) {
-      if (split == 1) {
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const uint64_t bad = B.bad && wrow < s.rows ? B.bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g] : 0;
-        __nv_bfloat16* to = (__nv_bfloat16*)A.out + (wrow < s.rows ? row_offset(A, s, mrow) : 0);
+    if (rows > 0 && split == 1 && !failed) {
+      // through shared memory (this warp's rows in the place of its queries), to write whole lines
+      constexpr int kPieces = D / 8, kXor = kPieces % 8 ? 3 : 7;  // pieces of eight rows on different banks
+      uint8_t* mine = qs + ((size_t)w * q_rows + (warp & 3) * 32) * D * 2;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      const uint64_t bad = B.bad && real ? B.bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g] : 0;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(o, my + c);
+        tmem_wait_ld(o);
+        if (!real) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv, __uint_as_float(o[e + 2]) * inv,
+                                 __uint_as_float(o[e + 3]) * inv);
+          float4 y = make_float4(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv, __uint_as_float(o[e + 6]) * inv,
+                                 __uint_as_float(o[e + 7]) * inv);
+          if (bad) {
+            add_not_finite<__nv_bfloat16>(A, s, bad, c + e, x);
+            add_not_finite<__nv_bfloat16>(A, s, bad, c + e + 4, y);
+          }
+          *reinterpret_cast<uint4*>(mine + ((size_t)lane * kPieces + (((c + e) / 8) ^ (lane & kXor))) * 16) =
+              make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+        }
+      }
+      __syncwarp();
+      for (int e = lane; e < min(rows, 32) * kPieces; e += 32) {
+        const int r = e / kPieces, c = e - r * kPieces;
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + ((size_t)r * kPieces + (c ^ (r & kXor))) * 16);
+        *reinterpret_cast<uint4*>((__nv_bfloat16*)A.out + row_offset(A, s, s.row0 + w * gr + (warp & 3) * 32 + r) + c * 8) = x;
+      }
+    } else if (rows > 0 && split > 1) {
+      float* ml = reinterpret_cast<float*>(qs);
+      if (real) {
+        ml[wrow] = failed ? -INFINITY : m_run;
+        ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
+      }
+      if (n > 0) {
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(o, my + c);
           tmem_wait_ld(o);
+          if (!real) continue;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (wrow >= s.rows || failed) break;
-            float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv, __uint_as_float(o[e + 2]) * inv,
-                                   __uint_as_float(o[e + 3]) * inv);
-            float4 y = make_float4(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv, __uint_as_float(o[e + 6]) * inv,
-                                   __uint_as_float(o[e + 7]) * inv);
-            if (bad) {
-              add_not_finite<__nv_bfloat16>(A, s, bad, c + e, x);
-              add_not_finite<__nv_bfloat16>(A, s, bad, c + e + 4, y);
-            }
-            *reinterpret_cast<uint4*>(to + c + e) = make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
-          }
-        }
-      } else {
-        float* ml = reinterpret_cast<float*>(qs);
-        if (wrow < s.rows) {
-          ml[wrow] = failed ? -INFINITY : m_run;
-          ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
-        }
-        if (n > 0) {
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            __syncwarp();
-            tmem_ld32(o, my + c);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (wrow < s.rows)
-                *reinterpret_cast<uint4*>(rs + part_chunk(wrow, (c + e) / 4, D, 7)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(rs + part_chunk(wrow, (c + e) / 4, D, 7)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
     }
@@ -941,30 +950,38 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// The pool as [slots][K, V][tokens][chunks][line], a box of one chunk of the tokens of a tile's slots.
+// Maps of 5 dims over lines and chunks: the pool as [slots][K, V][tokens], a box of one chunk of the tokens of
+// a tile's slots; the queries as [tokens][KV heads][group], a box of q_tok tokens of a KV head; drafted keys
+// and values as [tokens][KV heads], a box of a request's T tokens of a head.
 template <int D, int NW>
-cudaError_t pool_map(const TreeArgs& A, int32_t spt, CUtensorMap* map) {
+cudaError_t make_maps(const TreeArgs& A, int32_t spt, int32_t q_tok, MmaMaps* m) {
   using L = Lines<D, NW>;
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const uint64_t token = (uint64_t)D * 2, half = token * A.G.bs;
-  const cuuint64_t dims[5] = {(cuuint64_t)L::kElems, (cuuint64_t)L::kChunks, (cuuint64_t)A.G.bs, 2, (cuuint64_t)A.pool_rows};
-  const cuuint64_t strides[4] = {(cuuint64_t)L::kBytes, token, half, 2 * half};
-  const cuuint32_t box[5] = {(cuuint32_t)L::kElems, 1, (cuuint32_t)A.G.bs, 1, (cuuint32_t)spt};
-  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(A.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            L::kElems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
+  auto encode = [&](CUtensorMap* map, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[3], const cuuint32_t (&box)[3]) {
+    const cuuint64_t d[5] = {(cuuint64_t)L::kElems, (cuuint64_t)L::kChunks, dims[0], dims[1], dims[2]};
+    const cuuint64_t st[4] = {(cuuint64_t)L::kBytes, strides[0], strides[1], strides[2]};
+    const cuuint32_t b[5] = {(cuuint32_t)L::kElems, 1, box[0], box[1], box[2]}, step[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), d, st, b, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              L::kElems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t token = (cuuint64_t)D * 2, half = token * A.G.bs, all = (cuuint64_t)A.G.R * A.T;
+  const cuuint64_t g = A.G.g, hkv = A.G.Hkv, bs = A.G.bs;
+  const bool ok = encode(&m->pool, A.pool, {bs, 2, (cuuint64_t)A.pool_rows}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, (cuuint32_t)spt}) &&
+                  encode(&m->q, A.q, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok}) &&
+                  encode(&m->k, A.k, {hkv, all, 1}, {token, token * hkv, token * hkv * all}, {1, (cuuint32_t)A.T, 1}) &&
+                  encode(&m->v, A.v, {hkv, all, 1}, {token, token * hkv, token * hkv * all}, {1, (cuuint32_t)A.T, 1});
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int D, int NW>
 cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   using L = Lines<D, NW>;
   const int32_t spt = L::kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
-  const int32_t rows = A.T * A.G.g, groups = (rows + NW * 128 - 1) / (NW * 128);
-  const int32_t q_rows = NW > 1 || rows >= 128 ? 128 : (rows + 7) / 8 * 8;
+  // a warpgroup's rows: all heads of as many drafted tokens as fit 128
+  const int32_t q_tok = A.T < 128 / A.G.g ? A.T : 128 / A.G.g, gr = q_tok * A.G.g, q_rows = (gr + 7) / 8 * 8;
+  const int32_t groups = (A.T * A.G.g + NW * gr - 1) / (NW * gr);
   // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
   // that share of the shared memory. It is never so small that a third CTA could come to wait for TMEM.
   const bool two = D <= 128 && NW == 1;
@@ -976,10 +993,10 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   if (smem < least) smem = least;
   const int64_t units = (int64_t)n_active * A.G.Hkv;
   const int32_t split = pick_split(units * groups, (int64_t)sm_count() * (two ? 2 : 1), tiles);
-  CUtensorMap map;
-  if (cudaError_t e = pool_map<D, NW>(A, spt, &map)) return e;
-  return launch_cluster(tree_mma_kernel<D, NW>, dim3((unsigned)(units * split), groups), NW * 128 + 64, smem, split, s, A, map, split, ring,
-                        q_rows);
+  MmaMaps maps;
+  if (cudaError_t e = make_maps<D, NW>(A, spt, q_tok, &maps)) return e;
+  return launch_cluster(tree_mma_kernel<D, NW>, dim3((unsigned)(units * split), groups), NW * 128 + 64, smem, split, s, A, maps, split, ring,
+                        q_tok, q_rows);
 }
 
 cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
@@ -1013,7 +1030,7 @@ extern "C" okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft
   using namespace okv;
   Geom G{};
   if (!tree_geom(n_requests, q_heads, kv_heads, head_dim, block_size, slots, dtype, &G)) return OKV_EINVAL;
-  if (n_draft <= 0 || n_draft > 64) return OKV_EINVAL;
+  if (n_draft <= 0 || n_draft > 64 || (int64_t)n_requests * n_draft > INT32_MAX) return OKV_EINVAL;
   if (!pool || !slot_block || !lengths || !q || !k_draft || !v_draft || !mask || !out) return OKV_EINVAL;
   if (!aligned16(pool) || !aligned16(q) || !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out)) return OKV_EINVAL;
   if (okv_status st = check_stream(stream)) return st;

@@ -998,6 +998,7 @@ okv_status okv_attend_tree(okv_ctx* c, int32_t layer, int32_t n_draft, const int
   cudaStream_t s = (cudaStream_t)stream;
   if (layer < 0 || layer >= G.L) return fail(c, OKV_EINVAL, "okv_attend_tree: layer %d out of range", layer);
   if (n_draft <= 0 || n_draft > kMaxDraft) return fail(c, OKV_EINVAL, "okv_attend_tree: n_draft %d not in 1..%d", n_draft, kMaxDraft);
+  if ((int64_t)G.R * n_draft > INT32_MAX) return fail(c, OKV_EINVAL, "okv_attend_tree: max_requests * n_draft must fit in 32 bits");
   if (!q || !k_draft || !v_draft || !mask || !out) return fail(c, OKV_EINVAL, "okv_attend_tree: NULL pointer");
   for (const void* p : {q, k_draft, v_draft, (const void*)out})
     if (!okv::aligned16(p)) return fail(c, OKV_EINVAL, "okv_attend_tree: queries, keys, values and outputs must be 16-byte aligned");
