@@ -13,6 +13,8 @@
 // depend on timing and a launch needs no workspace.
 #include <cuda_bf16.h>
 
+#include <stddef.h>
+
 #include <utility>
 
 #include "okv_tree.h"
@@ -36,22 +38,35 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
-// One CTA's share of the work: a request, a KV head, a group of rows and a part of the tokens.
-struct Site {
-  int32_t a, r, h, part, cnt, len;  // cnt: drafted tokens of the request
-  int32_t row0, rows;               // rows [row0, row0 + rows) of the unit's g * cnt
+// How a launch covers its items, (unit, group of rows) with the groups of a unit side by side: clusters of
+// `split` CTAs, of which the first take `whole` items, one for each CTA, and the others one item each, dealt
+// to their CTAs. So the last items, fewer than would fill the GPU, are shared out.
+struct Shape {
+  int32_t split, whole, groups;
 };
 
-__device__ __forceinline__ Site make_site(const TreeArgs& A, int32_t split, int32_t group_rows) {
+// One CTA's share of the work: a request, a KV head, a group of rows and a part of the tokens.
+struct Site {
+  int32_t a, r, h, part, parts, cnt, len;  // cnt: drafted tokens of the request
+  int32_t row0, rows;                      // rows [row0, row0 + rows) of the unit's g * cnt
+  bool first;                              // the first CTA of its unit
+};
+
+__device__ __forceinline__ Site make_site(const TreeArgs& A, const Shape& P, int32_t group_rows) {
   Site s;
-  const int32_t ua = blockIdx.x / split;
-  s.part = blockIdx.x % split;
+  const int32_t cluster = blockIdx.x / P.split, rank = blockIdx.x - cluster * P.split, wholes = P.whole / P.split;
+  const bool whole = cluster < wholes;
+  const int32_t item = whole ? (int32_t)blockIdx.x : P.whole + cluster - wholes;
+  const int32_t ua = item / P.groups, group = item - ua * P.groups;
+  s.part = whole ? 0 : rank;
+  s.parts = whole ? 1 : P.split;
+  s.first = group == 0 && s.part == 0;
   s.a = ua / A.G.Hkv;
-  s.h = ua % A.G.Hkv;
+  s.h = ua - s.a * A.G.Hkv;
   s.r = A.active ? A.active[s.a] : s.a;
   s.cnt = A.counts ? min(max(A.counts[s.r], 0), A.T) : A.T;
   s.len = A.len[s.r];
-  s.row0 = blockIdx.y * group_rows;
+  s.row0 = group * group_rows;
   s.rows = min(group_rows, s.cnt * A.G.g - s.row0);
   return s;
 }
@@ -97,7 +112,7 @@ __device__ __forceinline__ int32_t list_tiles(const TreeArgs& A, const Site& s, 
     }
   }
   __syncwarp();
-  if (A.ctr && s.part == 0 && blockIdx.y == 0) {
+  if (A.ctr && s.first) {
     const int32_t slots = __reduce_add_sync(0xffffffffu, used);
     if (lane == 0) atomicAdd(&A.ctr->attended_slots, (unsigned long long)slots);
   }
@@ -146,7 +161,8 @@ __device__ __forceinline__ uint32_t part_chunk(int32_t row, int32_t chunk, int32
 // Merges the cluster's partials, each CTA a share of the outputs, and writes them. Every thread of
 // every CTA of the cluster calls it.
 template <typename T>
-__device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, int32_t split, const Partial& P, int32_t xor_mask) {
+__device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, const Partial& P, int32_t xor_mask) {
+  const int32_t split = s.parts;
   cluster_sync();
   const int32_t d4 = A.G.d / 4, total = s.rows * d4;
   const uint64_t bad = ld_cluster_u64(cluster_map(P.bad, split - 1));
@@ -203,7 +219,7 @@ __host__ __device__ constexpr size_t cuda_smem(int d, int kb, int tiles) {
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 template <int DV>
-__global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs A, const int32_t split) {
+__global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs A, const Shape shape) {
   using T = float;
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int d = DV * 32, pitch = cuda_pitch(d);
@@ -218,8 +234,9 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 2);
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
-  const Site s = make_site(A, split, kCudaRows);
+  const Site s = make_site(A, shape, kCudaRows);
   if (s.rows <= 0) return;
+  const int32_t split = s.parts;
   const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   if (tid == 0) *bad = 0;
@@ -367,7 +384,7 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   }
   const Partial P{smem_u32(ks), smem_u32(ms), smem_u32(ls), smem_u32(bad)};
   if (split > 1) {
-    merge_cluster<T>(A, s, split, P, 0);
+    merge_cluster<T>(A, s, P, 0);
     return;
   }
   __syncthreads();
@@ -466,7 +483,7 @@ struct MmaMaps {
 
 template <int D, int NW>
 __global__ void __launch_bounds__(NW * 128 + 64, D <= 128 && NW == 1 ? 2 : 1)
-tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32_t split, const int32_t ring, const int32_t q_tok, const int32_t q_rows) {
+tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape shape, const int32_t ring, const int32_t q_tok, const int32_t q_rows) {
   using L = Lines<D, NW>;
   constexpr int kTile = L::kTile, kS = L::kS;
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
@@ -484,8 +501,9 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1;
   if (is_copy && lane < 4) tma_prefetch_map(&M.pool + lane);
   const int32_t gr = q_tok * A.G.g;  // rows of a warpgroup: q_tok drafted tokens, all heads of the group
-  const Site s = make_site(A, split, NW * gr);
+  const Site s = make_site(A, shape, NW * gr);
   if (s.rows <= 0) return;
+  const int32_t split = s.parts;
   const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   const uint32_t ring0 = smem_u32(rs);
@@ -528,21 +546,13 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
   // Setup: the copy warp starts the copies of the queries and the drafted tokens, reads the slot table and
   // starts the pool's copies that need no free buffer.
   if (is_copy) {
+    // the barriers, one to a lane: those that one thread arrives at, then P's
+    uint64_t* bars = B.full;
+    for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32) mbar_init(smem_u32(bars + i), bars + i >= &B.p_full[0][0] && bars + i < &B.p_full[2][0] ? 128 : 1);
+    fence_mbar_init();
+    fence_proxy_async();
+    __syncwarp();
     if (lane == 0) {
-      for (int i = 0; i < ring; ++i) {
-        mbar_init(smem_u32(&B.full[i]), 1);
-        mbar_init(smem_u32(&B.empty[i]), 1);
-      }
-      mbar_init(smem_u32(&B.q_full), 1);
-      for (int w = 0; w < NW; ++w)
-        for (int e = 0; e < 2; ++e) {
-          mbar_init(smem_u32(&B.s_full[w][e]), 1);
-          mbar_init(smem_u32(&B.p_full[w][e]), 128);
-          mbar_init(smem_u32(&B.pv_done[w][e]), 1);
-        }
-      mbar_init(smem_u32(&B.drain), 1);
-      fence_mbar_init();
-      fence_proxy_async();
       B.failed = 0;
       B.bad = 0;
       // rows (t, head of the group) of a box follow one another as the group's rows do; a box past the last
@@ -570,7 +580,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
     n = (all - s.part + split - 1) / split + lead;
     if (lane == 0) {
       B.n_tiles = n;
-      while (next < ring && next < uses(n)) fill();
+      while (next < 2 && next < uses(n)) fill();  // the others behind the barrier below
     }
   } else if (is_mma) {
     tmem_alloc(smem_u32(&B.tmem), kCols * NW);
@@ -668,9 +678,6 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
     const float scale = kLog2e * rsqrtf((float)D);
     uint64_t sees = 0;
     if (draft && real) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
-    int32_t slot_at[kTile / 32], tok_at[kTile / 32];  // of token lane + 32 u of a tile
-#pragma unroll
-    for (int u = 0; u < kTile / 32; ++u) slot_at[u] = (lane + 32 * u) / bs, tok_at[u] = (lane + 32 * u) % bs;
     for (int32_t i = 0; i < n; ++i) {
       uint32_t vis[kTile / 32] = {(uint32_t)sees, (uint32_t)(sees >> 32)};  // who the row sees of the tile
       bool gaps = false, masked = true;
@@ -680,8 +687,10 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
         if (gaps) {
           const int32_t slot0 = tile_of(tile) * spt;
 #pragma unroll
-          for (int u = 0; u < kTile / 32; ++u)
-            vis[u] = __ballot_sync(0xffffffffu, lane + 32 * u < tt && slot0 + slot_at[u] < A.G.kb && tok_at[u] < nv[slot0 + slot_at[u]]);
+          for (int u = 0; u < kTile / 32; ++u) {
+            const int32_t tok = lane + 32 * u, slot = slot0 + tok / bs;
+            vis[u] = __ballot_sync(0xffffffffu, tok < tt && slot < A.G.kb && tok % bs < nv[min(slot, A.G.kb - 1)]);
+          }
         }
       }
       if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
@@ -778,24 +787,39 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
         }
         constexpr int kPieces = D / 8;
         uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
+        auto vis_of = [&](int u) {
+          uint32_t x = vis[0];
+#pragma unroll
+          for (int k = 1; k < kTile / 32; ++k)
+            if (u == k) x = vis[k];
+          return x;
+        };
         if (i < lead) {
-          for (int e = row; e < kTile * kPieces; e += 128) {
-            const int j = e / kPieces;
-            uint4* x = reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces));
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (j < s.cnt) {
-              y = *x;
-              if (!clean(y)) continue;
-              atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
+          constexpr int kEach = kTile * kPieces / 128, kBatch = kEach < 4 ? kEach : 4;
+#pragma unroll 1
+          for (int u0 = 0; u0 < kEach; u0 += kBatch) {
+            uint4 y[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              const int e = row + (u0 + u) * 128, j = e / kPieces;
+              y[u] = make_uint4(0, 0, 0, 0);
+              if (u0 + u < kEach && j < s.cnt) y[u] = *reinterpret_cast<const uint4*>(v + L::piece(j, e % kPieces));
             }
-            *x = y;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              const int e = row + (u0 + u) * 128, j = e / kPieces;
+              if (u0 + u >= kEach) break;
+              if (clean(y[u])) atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
+              else if (j < s.cnt) continue;
+              *reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces)) = y[u];
+            }
           }
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int u = 0; u < kTile / 32; ++u)
             for (int e = row; e < 32 * kPieces; e += 128) {
               const int j = e / kPieces, c = e % kPieces;
-              if (!(vis[u] >> j & 1)) *reinterpret_cast<uint4*>(v + L::piece(32 * u + j, c)) = make_uint4(0, 0, 0, 0);
+              if (!(vis_of(u) >> j & 1)) *reinterpret_cast<uint4*>(v + L::piece(32 * u + j, c)) = make_uint4(0, 0, 0, 0);
             }
         }
         __syncwarp();
@@ -842,10 +866,15 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
         }
       }
       __syncwarp();
+      const uint32_t per_g = (65536 + A.G.g - 1) / A.G.g;  // m * per_g >> 16 is m / g for the rows there are
+      const int32_t m0 = s.row0 + w * gr + (warp & 3) * 32;
+      __nv_bfloat16* base = (__nv_bfloat16*)A.out + row_offset(A, s, 0);
+#pragma unroll 4
       for (int e = lane; e < min(rows, 32) * kPieces; e += 32) {
         const int r = e / kPieces, c = e - r * kPieces;
+        const uint32_t m = m0 + r, t = m * per_g >> 16;
         const uint4 x = *reinterpret_cast<const uint4*>(mine + ((size_t)r * kPieces + (c ^ (r & kXor))) * 16);
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)A.out + row_offset(A, s, s.row0 + w * gr + (warp & 3) * 32 + r) + c * 8) = x;
+        *reinterpret_cast<uint4*>(base + (t * A.G.Hq + (m - t * A.G.g)) * D + c * 8) = x;
       }
     } else if (rows > 0 && split > 1) {
       float* ml = reinterpret_cast<float*>(qs);
@@ -870,7 +899,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
   }
   if (split > 1) {
     const Partial P{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4), smem_u32(&B.bad)};
-    merge_cluster<__nv_bfloat16>(A, s, split, P, 7);
+    merge_cluster<__nv_bfloat16>(A, s, P, 7);
   }
   tc_fence_before();
   __syncthreads();
@@ -880,11 +909,18 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const int32
   }
 }
 
-// CTAs per cluster: as many as fill `slots` CTA places once, a tile of the pool each at least.
-int32_t pick_split(int64_t clusters, int64_t slots, int32_t tiles) {
-  int64_t s = slots / clusters;
-  if (s > tiles) s = tiles;
-  return (int32_t)(s < 1 ? 1 : s > kMaxSplit ? kMaxSplit : s);
+// The shape of least time by a count of tile times: an item takes its tiles and `fixed` more, and `join` more
+// where its CTAs merge; `slots` CTAs run at once. Items that fill the GPU go whole, the last ones split.
+Shape pick_shape(int64_t items, int32_t groups, int64_t slots, int32_t tiles, double fixed, double join) {
+  Shape best{1, (int32_t)items, groups};
+  double least = 1e30;
+  for (int32_t c = 1; c <= kMaxSplit && c <= tiles; ++c) {
+    const int64_t full = items / slots * slots / c * c, whole = c == 1 ? items : full, rest = items - whole;
+    const double t = (double)((whole + slots - 1) / slots) * (tiles + fixed) +
+                     (double)((rest * c + slots - 1) / slots) * ((double)tiles / c + fixed + join);
+    if (t < least) least = t, best = Shape{c, (int32_t)whole, groups};
+  }
+  return best;
 }
 
 int sm_count() {
@@ -894,21 +930,21 @@ int sm_count() {
 }
 
 template <typename... P, typename... Q>
-cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int32_t split, cudaStream_t s, Q&&... args) {
+cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& shape, int threads, size_t smem, cudaStream_t s, Q&&... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3((unsigned)(shape.whole + (items - shape.whole) * shape.split));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.x = shape.split;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  cfg.numAttrs = shape.split > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
@@ -918,9 +954,9 @@ cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t groups = (A.T * A.G.g + kCudaRows - 1) / kCudaRows;
   const size_t smem = cuda_smem(DV * 32, A.G.kb, tiles);
   const int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
-  const int64_t units = (int64_t)n_active * A.G.Hkv;
-  const int32_t split = pick_split(units * groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles);
-  return launch_cluster(tree_cuda_kernel<DV>, dim3((unsigned)(units * split), groups), kCudaThreads, smem, split, s, A, split);
+  const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
+  const Shape shape = pick_shape(items, groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles, 1, 1);
+  return launch_cluster(tree_cuda_kernel<DV>, items, shape, kCudaThreads, smem, s, A, shape);
 }
 
 cudaError_t run_cuda_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
@@ -991,12 +1027,11 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   size_t smem = rest + (size_t)ring * L::kBuf;
   const size_t least = (two ? 233472 / 3 : 233472 / 2);
   if (smem < least) smem = least;
-  const int64_t units = (int64_t)n_active * A.G.Hkv;
-  const int32_t split = pick_split(units * groups, (int64_t)sm_count() * (two ? 2 : 1), tiles);
+  const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
+  const Shape shape = pick_shape(items, groups, (int64_t)sm_count() * (two ? 2 : 1), tiles, 3, 2);
   MmaMaps maps;
   if (cudaError_t e = make_maps<D, NW>(A, spt, q_tok, &maps)) return e;
-  return launch_cluster(tree_mma_kernel<D, NW>, dim3((unsigned)(units * split), groups), NW * 128 + 64, smem, split, s, A, maps, split, ring,
-                        q_tok, q_rows);
+  return launch_cluster(tree_mma_kernel<D, NW>, items, shape, NW * 128 + 64, smem, s, A, maps, shape, ring, q_tok, q_rows);
 }
 
 cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
