@@ -444,12 +444,13 @@ struct Lines {
   }
 };
 
-// S, P and O have a barrier each for even and for odd tiles: a barrier's parity tells a phase from the
-// next one only, and the softmax may be done with tile i + 1 before the issuing thread has looked at
-// tile i, as that thread may be done with O of tile i - 1 before the softmax has looked at tile i - 2.
+// With two S buffers, S, P and O have a barrier each for even and for odd tiles: a barrier's parity tells a
+// phase from the next one only, and the softmax may be done with tile i + 1 before the issuing thread has
+// looked at tile i, as that thread may be done with O of tile i - 1 before the softmax has looked at tile
+// i - 2. With one S buffer, P has a barrier for each half of a tile, and O another behind the first half.
 constexpr int kMaxRing = 12;
 struct MmaBars {
-  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2], pv_done[2][2], drain;
+  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2], pv_done[2][2], pv_half[2], drain;
   uint64_t bad;  // drafted tokens with values that are not finite
   uint32_t tmem;
   int32_t n_tiles, failed;
@@ -584,6 +585,13 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
     }
   } else if (is_mma) {
     tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+  } else if (draft) {
+    // the lines behind the drafted tokens' values meet weights of zero
+    constexpr int kPieces = D / 8;
+#pragma unroll 1
+    for (int e = A.T * kPieces + tid; e < kTile * kPieces; e += NW * 128)
+      *reinterpret_cast<uint4*>(rs + v_use(0) * L::kBuf + L::piece(e / kPieces, e % kPieces)) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
   }
   tc_fence_before();
   __syncthreads();
@@ -644,23 +652,26 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         ok = k_ready();
         if (ok) qk(i + 1, 0);
       }
-      ok = ok && warp_wait(B.full[vb], vp);
+      // with one S buffer, everything is seen to be there before the warpgroups' weights are waited for, and a
+      // warpgroup's two products go out together
+      ok = ok && warp_wait(B.full[vb], vp) && (kS == 2 || i + 1 == n || k_ready());
       const uint64_t vd = v_desc + (uint32_t)(vb * (L::kBuf >> 4));
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        ok = ok && warp_wait(B.p_full[w][i & 1], (i >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < kTile / 16; ++c)
-          mma_ts(tmem + w * kCols + kO, tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0) + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
-                 i > 0 || c > 0, one);
-        mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
-        if (kS == 1 && i + 1 < n) {  // S takes the place of the P just used: the products run in order
-          if (w == 0) ok = k_ready();
+        for (int h = 0; h < kTile / 64; ++h) {
+          ok = ok && (kS == 2 ? warp_wait(B.p_full[w][i & 1], (i >> 1) & 1) : warp_wait(B.p_full[w][h], i & 1));
           if (!ok) break;
-          qk(i + 1, w);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 4 * h; c < 4 * h + 4; ++c)
+            mma_ts(tmem + w * kCols + kO, tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0) + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
+                   i > 0 || c > 0, one);
+          if (kS == 1 && h == 0) mma_commit(smem_u32(&B.pv_half[w]), one);
         }
+        if (!ok) break;
+        mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
+        if (kS == 1 && i + 1 < n) qk(i + 1, w);  // S takes the place of the P just used: the products run in order
       }
       if (!ok) break;
       mma_commit(smem_u32(&B.empty[vb]), one);
@@ -704,80 +715,6 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         break;
       }
       tc_fence_after();
-      if (active) {
-        const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
-        uint32_t a[32], b[32];
-        // 64 scores of the row from column c on; those it does not see as -infinity
-        auto scores = [&](int c) {
-          tmem_ld32(a, st + c);
-          tmem_ld32(b, st + c + 32);
-          tmem_wait_ld(a);
-          tmem_wait_ld(b);
-          if (masked) {
-            const uint32_t lo = vis[c / 32], hi = vis[c / 32 + 1];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(lo >> e & 1)) a[e] = 0xFF800000u;
-              if (!(hi >> e & 1)) b[e] = 0xFF800000u;
-            }
-          }
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kTile; c += 64) {
-          scores(kTile - 64 - c);  // the first 64 last: they stay in registers for the weights
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        const bool grow = top > m_run + 8.f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? top : m_run;
-          const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mn);
-          m_run = mn;
-          l_run *= f;
-          if (i > 0) {
-            // with one, S of tile i follows O of tile i - 1: nothing to wait for
-            if (kS == 2 && !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1)) {
-              fail(3);
-              break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o, my + kO + c);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(my + kO + c, o);
-            }
-          }
-        }
-        const float neg = m_run == -INFINITY ? 0.f : -m_run;
-        const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-        for (int c = 0; c < kTile; c += 64) {
-          if (c > 0) scores(c);
-          uint32_t p[32];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = fma2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), scale2, neg2);
-            float2 y = fma2(make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])), scale2, neg2);
-            x = make_float2(ex2(x.x), ex2(x.y));
-            y = make_float2(ex2(y.x), ex2(y.y));
-            sum0 = add2(sum0, x);
-            sum1 = add2(sum1, y);
-            p[e] = pack2(x.x, x.y);
-            p[16 + e] = pack2(y.x, y.y);
-          }
-          tmem_st32(st + c / 2, p);  // over scores that have been read
-        }
-        sum0 = add2(sum0, sum1);
-        l_run += sum0.x + sum0.y;
-        tmem_wait_st();
-      }
       if (w == 0 && (gaps || i < lead)) {
         // Lines of the V tile that hold no valid token may hold anything: zero them before the product. So
         // are drafted values that are not finite, and their tokens noted.
@@ -795,22 +732,20 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
           return x;
         };
         if (i < lead) {
-          constexpr int kEach = kTile * kPieces / 128, kBatch = kEach < 4 ? kEach : 4;
 #pragma unroll 1
-          for (int u0 = 0; u0 < kEach; u0 += kBatch) {
-            uint4 y[kBatch];
+          for (int e0 = row; e0 < A.T * kPieces; e0 += 4 * 128) {
+            uint4 y[4];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              const int e = row + (u0 + u) * 128, j = e / kPieces;
+            for (int u = 0; u < 4; ++u) {
+              const int e = e0 + u * 128, j = e / kPieces;
               y[u] = make_uint4(0, 0, 0, 0);
-              if (u0 + u < kEach && j < s.cnt) y[u] = *reinterpret_cast<const uint4*>(v + L::piece(j, e % kPieces));
+              if (j < s.cnt) y[u] = *reinterpret_cast<const uint4*>(v + L::piece(j, e % kPieces));
             }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              const int e = row + (u0 + u) * 128, j = e / kPieces;
-              if (u0 + u >= kEach) break;
+            for (int u = 0; u < 4; ++u) {
+              const int e = e0 + u * 128, j = e / kPieces;
               if (clean(y[u])) atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
-              else if (j < s.cnt) continue;
+              else if (j < s.cnt || j >= A.T) continue;
               *reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces)) = y[u];
             }
           }
@@ -825,8 +760,82 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         __syncwarp();
         fence_proxy_async();
       }
-      tc_fence_before();
-      mbar_arrive(smem_u32(&B.p_full[w][i & 1]));
+      // 64 tokens at a time: where a row grows past its running maximum by more than 2^8 (a vote of the warp),
+      // the maximum moves and O and the sum are scaled. With two halves, the weights of the first go to the
+      // tensor cores while the second is at work.
+      bool lost = false;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 64) {
+        if (active && !lost) {
+          const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
+          uint32_t a[32], b[32], p[32];
+          tmem_ld32(a, st + c);
+          tmem_ld32(b, st + c + 32);
+          tmem_wait_ld(a);
+          tmem_wait_ld(b);
+          if (masked) {
+            const uint32_t lo = vis[c / 32], hi = vis[c / 32 + 1];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(lo >> e & 1)) a[e] = 0xFF800000u;
+              if (!(hi >> e & 1)) b[e] = 0xFF800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          const bool grow = top > m_run + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
+            const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
+            m_run = mn;
+            l_run *= f;
+            if (i > 0 || c > 0) {
+              // O has every product issued before: those of tile i - 1, which with one S buffer came before S of
+              // this tile, and of the first half
+              if (kS == 2)
+                lost = !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1);
+              else if (c > 0)
+                lost = !warp_wait(B.pv_half[w], i & 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < D; k += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, my + kO + k);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(my + kO + k, o);
+              }
+            }
+          }
+          const float neg = m_run == -INFINITY ? 0.f : -m_run;
+          const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), scale2, neg2);
+            float2 y = fma2(make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])), scale2, neg2);
+            x = make_float2(ex2(x.x), ex2(x.y));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum0 = add2(sum0, x);
+            sum1 = add2(sum1, y);
+            p[e] = pack2(x.x, x.y);
+            p[16 + e] = pack2(y.x, y.y);
+          }
+          sum0 = add2(sum0, sum1);
+          l_run += sum0.x + sum0.y;
+          tmem_st32(st + c / 2, p);  // over scores that have been read
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&B.p_full[w][kS == 2 ? i & 1 : c / 64]));
+      }
+      if (lost) {
+        fail(3);
+        break;
+      }
     }
     if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail(5);
     tc_fence_after();
@@ -844,7 +853,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
       uint8_t* mine = qs + ((size_t)w * q_rows + (warp & 3) * 32) * D * 2;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       const uint64_t bad = B.bad && real ? B.bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g] : 0;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         __syncwarp();
@@ -883,7 +892,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
       }
       if (n > 0) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           __syncwarp();
