@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 // ---- tensor cores: bf16 ------------------------------------------------------------------------------
 //
 // A CTA holds NW groups of 128 rows (one softmax warpgroup each) over the same tiles of tokens. One warp
-// copies K and V tiles by TMA into a ring of buffers, one thread issues the MMAs:
+// copies K and V tiles by TMA into a ring of buffers, a warp for each group issues its MMAs:
 //   S = Q K^T   128 x tile, Q and K in shared memory, S in TMEM
 //   O += P V    128 x d,    P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
 // and a thread of the warpgroup takes a row's softmax.
@@ -444,14 +444,13 @@ struct Lines {
   }
 };
 
-// With two S buffers, S, P and O have a barrier each for even and for odd tiles: a barrier's parity tells a
-// phase from the next one only, and the softmax may be done with tile i + 1 before the issuing thread has
-// looked at tile i, as that thread may be done with O of tile i - 1 before the softmax has looked at tile
-// i - 2. With one S buffer, P has a barrier for each half of a tile, and O another behind the first half.
+// S, P and O have a barrier each for even and for odd tiles: a barrier's parity tells a phase from the next
+// one only, and with two S buffers the softmax may be done with tile i + 1 before the issuing warp has
+// looked at tile i, as that warp may be done with O of tile i - 1 before the softmax has looked at tile i - 2.
 constexpr int kMaxRing = 12;
 struct MmaBars {
-  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2], pv_done[2][2], pv_half[2], drain;
-  uint64_t bad;  // drafted tokens with values that are not finite
+  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2], pv_done[2][2], drain[2], turn[2];
+  uint64_t bad, bad_of[8];  // drafted tokens with values that are not finite: all, found by each warp
   uint32_t tmem;
   int32_t n_tiles, failed;
 };
@@ -483,7 +482,7 @@ struct MmaMaps {
 };
 
 template <int D, int NW>
-__global__ void __launch_bounds__(NW * 128 + 64, D <= 128 && NW == 1 ? 2 : 1)
+__global__ void __launch_bounds__(NW * 160 + 32, D <= 128 && NW == 1 ? 2 : 1)
 tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape shape, const int32_t ring, const int32_t q_tok, const int32_t q_rows) {
   using L = Lines<D, NW>;
   constexpr int kTile = L::kTile, kS = L::kS;
@@ -499,7 +498,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1;
+  const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4;
   if (is_copy && lane < 4) tma_prefetch_map(&M.pool + lane);
   const int32_t gr = q_tok * A.G.g;  // rows of a warpgroup: q_tok drafted tokens, all heads of the group
   const Site s = make_site(A, shape, NW * gr);
@@ -547,15 +546,15 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   // Setup: the copy warp starts the copies of the queries and the drafted tokens, reads the slot table and
   // starts the pool's copies that need no free buffer.
   if (is_copy) {
-    // the barriers, one to a lane: those that one thread arrives at, then P's
-    uint64_t* bars = B.full;
-    for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32) mbar_init(smem_u32(bars + i), bars + i >= &B.p_full[0][0] && bars + i < &B.p_full[2][0] ? 128 : 1);
+    // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
+    constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
+    for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32)
+      mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 4 ? 128 : 1);
     fence_mbar_init();
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
       B.failed = 0;
-      B.bad = 0;
       // rows (t, head of the group) of a box follow one another as the group's rows do; a box past the last
       // request's tokens is filled up with zeros
       const uint32_t q_bar = smem_u32(&B.q_full);
@@ -584,20 +583,44 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
       while (next < 2 && next < uses(n)) fill();  // the others behind the barrier below
     }
   } else if (is_mma) {
-    tmem_alloc(smem_u32(&B.tmem), kCols * NW);
-  } else if (draft) {
-    // the lines behind the drafted tokens' values meet weights of zero
-    constexpr int kPieces = D / 8;
+    if (warp == NW * 4 + 1) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+  } else {
+    uint64_t bad = 0;
+    if (draft) {
+      // the lines behind the drafted tokens' values meet weights of zero
+      constexpr int kPieces = D / 8;
 #pragma unroll 1
-    for (int e = A.T * kPieces + tid; e < kTile * kPieces; e += NW * 128)
-      *reinterpret_cast<uint4*>(rs + v_use(0) * L::kBuf + L::piece(e / kPieces, e % kPieces)) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async();
+      for (int e = A.T * kPieces + tid; e < kTile * kPieces; e += NW * 128)
+        *reinterpret_cast<uint4*>(rs + v_use(0) * L::kBuf + L::piece(e / kPieces, e % kPieces)) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      // are there values that are not finite?
+#pragma unroll 1
+      for (int e0 = tid; e0 < s.cnt * kPieces; e0 += 4 * NW * 128) {
+        uint4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * NW * 128;
+          y[u] = make_uint4(0, 0, 0, 0);
+          if (e < s.cnt * kPieces) y[u] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)A.v + draft_offset(A, s, e / kPieces) + e % kPieces * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (clean(y[u])) bad |= 1ull << (e0 + u * NW * 128) / kPieces;
+      }
+      bad = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)bad);
+    }
+    if (lane == 0) B.bad_of[warp] = bad;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
   n = __shfl_sync(0xffffffffu, B.n_tiles, 0);
+  if (tid == 0) {
+    uint64_t bad = 0;
+    for (int i = 0; i < NW * 4; ++i) bad |= B.bad_of[i];
+    B.bad = bad;  // read behind the loops
+  }
   float m_run = -INFINITY, l_run = 0.f;
 
   if (is_copy) {
@@ -615,79 +638,76 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   } else if (is_mma) {
     const bool one = lane == 0;
     constexpr int kSteps = L::kElems / 16;
-    const uint64_t q_desc = smem_desc(smem_u32(qs), 16, L::kGroup, L::kSwizzle), k_desc = smem_desc(ring0, 16, L::kGroup, L::kSwizzle);
-    const uint64_t v_desc = smem_desc(ring0, L::kChunk, L::kGroup, L::kSwizzle);  // + byte offsets / 16
+    constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+    const int w = warp - NW * 4 - 1;  // the warpgroup it works for
+    const uint32_t my = tmem + w * kCols;
     const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
+    const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16) + w * L::kChunks * q_chunk, k_desc = smem_desc_lo(ring0, 16);
+    const uint32_t v_desc = smem_desc_lo(ring0, L::kChunk);
     int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
     auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
       b += by;
       if (b >= ring) b -= ring, parity ^= 1;
-    };
-    auto qk = [&](int32_t i, int w) {  // S of tile i for warpgroup w
-      const uint64_t kd = k_desc + (uint32_t)(kb * (L::kBuf >> 4));
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        mma_ss(tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0), q_desc + (w * L::kChunks + c / kSteps) * q_chunk + (c % kSteps) * 2,
-               kd + (uint32_t)((c / kSteps) * (L::kChunk >> 4) + (c % kSteps) * 2), kDescQK, c > 0, one);
-      mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
-      if (w == NW - 1) {
-        mma_commit(smem_u32(&B.empty[kb]), one);
-        step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
-      }
     };
     auto k_ready = [&] {
       if (!warp_wait(B.full[kb], kp)) return false;
       tc_fence_after();
       return true;
     };
+    auto qk = [&](int32_t i) {
+      const uint32_t kd = k_desc + kb * (L::kBuf >> 4);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(my + (kS == 2 ? (i & 1) * kTile : 0), q_desc + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2,
+               kHi, kDescQK, c > 0, one);
+      mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
+      mma_commit(smem_u32(&B.empty[kb]), one);
+      step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
+    };
+    // Two warpgroups take turns at the tensor cores, O of a tile and S of the next at a time: while one has
+    // them, the other is at its softmax. Left to themselves they end up side by side, waiting for each other
+    // at both (measured at 64 tokens x 32 requests: 153 us against 1xx).
+    int32_t turns = 0;
+    auto my_turn = [&] { return NW == 1 || (w == 0 && turns == 0) || warp_wait(B.turn[w], (turns - (w == 0)) & 1); };
+    auto pass_on = [&] {
+      ++turns;
+      if (NW == 2 && one) mbar_arrive(smem_u32(&B.turn[w ^ 1]));
+    };
     bool ok = true;
     if (n > 0) {
-      ok = warp_wait(B.q_full, 0) && k_ready();
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-        if (ok) qk(0, w);
+      ok = warp_wait(B.q_full, 0) && k_ready() && my_turn();
+      if (ok) qk(0);
+      pass_on();
     }
     for (int32_t i = 0; i < n && ok; ++i) {
-      if (kS == 2 && i + 1 < n) {
-        ok = k_ready();
-        if (ok) qk(i + 1, 0);
-      }
-      // with one S buffer, everything is seen to be there before the warpgroups' weights are waited for, and a
-      // warpgroup's two products go out together
-      ok = ok && warp_wait(B.full[vb], vp) && (kS == 2 || i + 1 == n || k_ready());
-      const uint64_t vd = v_desc + (uint32_t)(vb * (L::kBuf >> 4));
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-#pragma unroll
-        for (int h = 0; h < kTile / 64; ++h) {
-          ok = ok && (kS == 2 ? warp_wait(B.p_full[w][i & 1], (i >> 1) & 1) : warp_wait(B.p_full[w][h], i & 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 4 * h; c < 4 * h + 4; ++c)
-            mma_ts(tmem + w * kCols + kO, tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0) + c * 8, vd + c * 2 * (L::kGroup >> 4), kDescPV,
-                   i > 0 || c > 0, one);
-          if (kS == 1 && h == 0) mma_commit(smem_u32(&B.pv_half[w]), one);
-        }
-        if (!ok) break;
-        mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
-        if (kS == 1 && i + 1 < n) qk(i + 1, w);  // S takes the place of the P just used: the products run in order
-      }
+      if (i + 1 < n) ok = k_ready();
+      if (kS == 2 && ok && i + 1 < n) qk(i + 1);
+      ok = ok && warp_wait(B.full[vb], vp) && my_turn() && warp_wait(B.p_full[w][i & 1], (i >> 1) & 1);
       if (!ok) break;
+      tc_fence_after();
+      const uint32_t vd = v_desc + vb * (L::kBuf >> 4);
+#pragma unroll
+      for (int c = 0; c < kTile / 16; ++c)
+        mma_ts(my + kO, my + (kS == 2 ? (i & 1) * kTile : 0) + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV,
+               i > 0 || c > 0, one);
+      mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
       mma_commit(smem_u32(&B.empty[vb]), one);
       step(vb, vp, 2);
+      if (kS == 1 && i + 1 < n) qk(i + 1);  // S takes the place of the P just used: the products run in order
+      pass_on();
     }
     if (!ok) {
       fail(1);
-      mma_commit(smem_u32(&B.drain), one);
-      warp_wait(B.drain, 0);
+      mma_commit(smem_u32(&B.drain[w]), one);
+      warp_wait(B.drain[w], 0);
     }
   } else {
     const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
     const bool real = row < gr && wrow < s.rows, active = (warp & 3) * 32 < min(gr, s.rows - w * gr);
     const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
     const float scale = kLog2e * rsqrtf((float)D);
-    uint64_t sees = 0;
+    uint64_t sees = 0, bad = 0;
+    for (int k = 0; k < NW * 4; ++k) bad |= B.bad_of[k];
     if (draft && real) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
     for (int32_t i = 0; i < n; ++i) {
       uint32_t vis[kTile / 32] = {(uint32_t)sees, (uint32_t)(sees >> 32)};  // who the row sees of the tile
@@ -715,9 +735,9 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         break;
       }
       tc_fence_after();
-      if (w == 0 && (gaps || i < lead)) {
-        // Lines of the V tile that hold no valid token may hold anything: zero them before the product. So
-        // are drafted values that are not finite, and their tokens noted.
+      if (gaps || (i < lead && (bad || s.cnt < A.T))) {
+        // Lines of the V tile that hold no valid token may hold anything: zero them before the product, and so
+        // the drafted values that are not finite. Each warpgroup does, whichever product comes first.
         if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
           fail(4);
           break;
@@ -733,21 +753,16 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         };
         if (i < lead) {
 #pragma unroll 1
-          for (int e0 = row; e0 < A.T * kPieces; e0 += 4 * 128) {
-            uint4 y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int e = e0 + u * 128, j = e / kPieces;
-              y[u] = make_uint4(0, 0, 0, 0);
-              if (j < s.cnt) y[u] = *reinterpret_cast<const uint4*>(v + L::piece(j, e % kPieces));
+          for (int e = row; e < A.T * kPieces; e += 128) {
+            const int j = e / kPieces;
+            if (j < s.cnt && !(bad >> j & 1)) continue;
+            uint4* x = reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces));
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (j < s.cnt) {
+              y = *x;
+              clean(y);
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int e = e0 + u * 128, j = e / kPieces;
-              if (clean(y[u])) atomicOr(reinterpret_cast<unsigned long long*>(&B.bad), 1ull << j);
-              else if (j < s.cnt || j >= A.T) continue;
-              *reinterpret_cast<uint4*>(v + L::piece(j, e % kPieces)) = y[u];
-            }
+            *x = y;
           }
         } else {
 #pragma unroll 1
@@ -760,15 +775,12 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         __syncwarp();
         fence_proxy_async();
       }
-      // 64 tokens at a time: where a row grows past its running maximum by more than 2^8 (a vote of the warp),
-      // the maximum moves and O and the sum are scaled. With two halves, the weights of the first go to the
-      // tensor cores while the second is at work.
       bool lost = false;
-#pragma unroll
-      for (int c = 0; c < kTile; c += 64) {
-        if (active && !lost) {
-          const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
-          uint32_t a[32], b[32], p[32];
+      if (active) {
+        const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
+        uint32_t a[32], b[32];
+        // 64 scores of the row from column c on; those it does not see as -infinity
+        auto scores = [&](int c) {
           tmem_ld32(a, st + c);
           tmem_ld32(b, st + c + 32);
           tmem_wait_ld(a);
@@ -781,38 +793,42 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
               if (!(hi >> e & 1)) b[e] = 0xFF800000u;
             }
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = kTile - 64; c >= 0; c -= 64) {  // the first 64 last: they stay in registers for the weights
+          scores(c);
 #pragma unroll
           for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-          const bool grow = top > m_run + 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
-            const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
-            m_run = mn;
-            l_run *= f;
-            if (i > 0 || c > 0) {
-              // O has every product issued before: those of tile i - 1, which with one S buffer came before S of
-              // this tile, and of the first half
-              if (kS == 2)
-                lost = !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1);
-              else if (c > 0)
-                lost = !warp_wait(B.pv_half[w], i & 1);
-              tc_fence_after();
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        if (__any_sync(0xffffffffu, top > m_run + 8.f)) {
+          const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
+          const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
+          m_run = mn;
+          l_run *= f;
+          if (i > 0) {
+            // O has the products of tile i - 1; with one S buffer those came before S of this tile
+            if (kS == 2) lost = !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1);
+            tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < D; k += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, my + kO + k);
-                tmem_wait_ld(o);
+            for (int k = 0; k < D; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, my + kO + k);
+              tmem_wait_ld(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(my + kO + k, o);
-              }
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(my + kO + k, o);
             }
           }
-          const float neg = m_run == -INFINITY ? 0.f : -m_run;
-          const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        }
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+        const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 64) {
+          if (c > 0) scores(c);
+          uint32_t p[32];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float2 x = fma2(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), scale2, neg2);
@@ -824,18 +840,18 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
             p[e] = pack2(x.x, x.y);
             p[16 + e] = pack2(y.x, y.y);
           }
-          sum0 = add2(sum0, sum1);
-          l_run += sum0.x + sum0.y;
           tmem_st32(st + c / 2, p);  // over scores that have been read
-          tmem_wait_st();
         }
-        tc_fence_before();
-        mbar_arrive(smem_u32(&B.p_full[w][kS == 2 ? i & 1 : c / 64]));
+        sum0 = add2(sum0, sum1);
+        l_run += sum0.x + sum0.y;
+        tmem_wait_st();
       }
       if (lost) {
         fail(3);
         break;
       }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&B.p_full[w][i & 1]));
     }
     if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail(5);
     tc_fence_after();
@@ -912,7 +928,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   }
   tc_fence_before();
   __syncthreads();
-  if (is_mma) {
+  if (warp == NW * 4 + 1) {
     tc_fence_after();
     tmem_free(tmem, kCols * NW);
   }
@@ -1040,7 +1056,7 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const Shape shape = pick_shape(items, groups, (int64_t)sm_count() * (two ? 2 : 1), tiles, 3, 2);
   MmaMaps maps;
   if (cudaError_t e = make_maps<D, NW>(A, spt, q_tok, &maps)) return e;
-  return launch_cluster(tree_mma_kernel<D, NW>, items, shape, NW * 128 + 64, smem, s, A, maps, shape, ring, q_tok, q_rows);
+  return launch_cluster(tree_mma_kernel<D, NW>, items, shape, NW * 160 + 32, smem, s, A, maps, shape, ring, q_tok, q_rows);
 }
 
 cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {

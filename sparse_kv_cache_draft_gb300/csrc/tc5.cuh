@@ -56,28 +56,29 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 __host__ __device__ constexpr uint32_t mma_desc_bf16(uint32_t m, uint32_t n, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-// Shared-memory operand descriptor. `swizzle`: 2 = 128-byte, 4 = 64-byte lines. K-major operands:
-// `sbo` is the byte distance of 8-row groups. MN-major: `sbo` that of groups of 8 along K, `lbo`
-// that of groups of one line along MN.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | ((uint64_t)swizzle << 61);
-}
+// Shared-memory operand descriptor, in two halves: the lower holds the address (in 16-byte units, to which
+// offsets are added) and `lbo`, the upper `sbo` and the swizzle: 2 = 128-byte, 4 = 64-byte lines. K-major
+// operands: `sbo` is the byte distance of 8-row groups. MN-major: `sbo` that of groups of 8 along K, `lbo` that
+// of groups of one line along MN.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4 & 0x3FFF) | (lbo >> 4 & 0x3FFF) << 16; }
+__host__ __device__ constexpr uint32_t smem_desc_hi(uint32_t sbo, uint32_t swizzle) { return (sbo >> 4 & 0x3FFF) | 1u << 14 | swizzle << 29; }
 // D (TMEM) = A B (+ D): A and B in shared memory. A whole warp calls these with the same operands, which
 // then stay in uniform registers; the lane with `one` set issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, bool one) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool accumulate, bool one) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
       : "memory");
 }
 // The same with A in TMEM (a 32-bit column holds two consecutive elements along K).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, bool one) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool accumulate, bool one) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
       : "memory");
 }
 // The mbarrier is arrived at once every MMA the issuing thread issued before has completed.
