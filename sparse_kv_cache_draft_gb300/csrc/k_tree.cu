@@ -86,23 +86,35 @@ __device__ __forceinline__ int64_t draft_offset(const TreeArgs& A, const Site& s
 // in order, into `tiles`, with kWhole set where all their places do; their number. One warp. A block id
 // outside the request's length counts as an empty slot and is recorded.
 constexpr uint32_t kWhole = 0x8000;
-__device__ __forceinline__ int32_t list_tiles(const TreeArgs& A, const Site& s, int32_t spt, uint8_t* nv, uint16_t* tiles) {
+struct Slots {
+  int32_t b[4];  // of slots lane + 32 u from the first on
+};
+__device__ __forceinline__ Slots load_slots(const TreeArgs& A, const Site& s, int32_t first) {
   const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  Slots x;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int32_t i = first + (threadIdx.x & 31) + 32 * u;
+    x.b[u] = i < A.G.kb ? sb[i] : -1;
+  }
+  return x;
+}
+// `x`: the first slots, loaded ahead.
+__device__ __forceinline__ int32_t list_tiles(const TreeArgs& A, const Site& s, Slots x, int32_t spt, uint8_t* nv, uint16_t* tiles) {
   const int lane = threadIdx.x & 31;
   int32_t used = 0;
-  for (int32_t i0 = lane; i0 < A.G.kb; i0 += 128) {
-    int32_t b[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) b[u] = i0 + 32 * u < A.G.kb ? sb[i0 + 32 * u] : -1;
+#pragma unroll 1
+  for (int32_t i0 = 0; i0 < A.G.kb; i0 += 128) {
+    if (i0) x = load_slots(A, s, i0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int32_t i = i0 + 32 * u;
+      const int32_t i = i0 + lane + 32 * u, b = x.b[u];
       if (i >= A.G.kb) break;
       int32_t n = 0;
-      if (b[u] >= 0) {
-        const int64_t rem = (int64_t)s.len - (int64_t)b[u] * A.G.bs;
-        if (rem <= 0 || b[u] >= A.G.nb_max) {
-          if (A.err) record_error(A.err, kErrBlockRange, -2, s.r, b[u]);
+      if (b >= 0) {
+        const int64_t rem = (int64_t)s.len - (int64_t)b * A.G.bs;
+        if (rem <= 0 || b >= A.G.nb_max) {
+          if (A.err) record_error(A.err, kErrBlockRange, -2, s.r, b);
         } else {
           n = (int32_t)(rem < A.G.bs ? rem : A.G.bs);
           ++used;
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
     *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = x;
   }
   if (tid < 32) {
-    const int32_t n = list_tiles(A, s, spt, nv, tiles);
+    const int32_t n = list_tiles(A, s, load_slots(A, s, 0), spt, nv, tiles);
     if (tid == 0) *n_tiles = n;
   }
   __syncthreads();
@@ -499,9 +511,17 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4;
-  if (is_copy && lane < 4) tma_prefetch_map(&M.pool + lane);
   const int32_t gr = q_tok * A.G.g;  // rows of a warpgroup: q_tok drafted tokens, all heads of the group
   const Site s = make_site(A, shape, NW * gr);
+  Slots first_slots;
+  if (is_copy) {  // what needs no length yet, while that is on its way
+    if (lane < 4) tma_prefetch_map(&M.pool + lane);
+    first_slots = load_slots(A, s, 0);
+    // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
+    constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
+    for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32)
+      mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 4 ? 128 : 1);
+  }
   if (s.rows <= 0) return;
   const int32_t split = s.parts;
   const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
@@ -546,10 +566,6 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   // Setup: the copy warp starts the copies of the queries and the drafted tokens, reads the slot table and
   // starts the pool's copies that need no free buffer.
   if (is_copy) {
-    // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
-    constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
-    for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32)
-      mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 4 ? 128 : 1);
     fence_mbar_init();
     fence_proxy_async();
     __syncwarp();
@@ -575,7 +591,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         }
     }
     __syncwarp();
-    const int32_t all = list_tiles(A, s, spt, nv, tiles);
+    const int32_t all = list_tiles(A, s, first_slots, spt, nv, tiles);
     __syncwarp();
     n = (all - s.part + split - 1) / split + lead;
     if (lane == 0) {
