@@ -223,15 +223,14 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
 constexpr int kCudaThreads = 128, kCudaRows = 32;
 
 __host__ __device__ constexpr int cuda_pitch(int d) { return d + 4; }
+__host__ __device__ constexpr int cuda_ctas(int dv) { return dv <= 2 ? 3 : 2; }  // CTAs of an SM, by registers
 __host__ __device__ constexpr size_t cuda_smem(int d, int kb, int tiles) {
   return (size_t)(kCudaRows + 2 * kTile) * cuda_pitch(d) * 4 + (size_t)kCudaRows * (kTile + 4) * 4 + kCudaRows * 8 + 64 +
          ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
 }
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
 template <int DV>
-__global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs A, const Shape shape) {
+__global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(const TreeArgs A, const Shape shape) {
   using T = float;
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int d = DV * 32, pitch = cuda_pitch(d);
@@ -251,12 +250,12 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   const int32_t split = s.parts;
   const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
+  constexpr int kPieces = d / 4, kEach = kTile * kPieces / kCudaThreads;  // 16-byte pieces of a token, of a thread's share of a tile
   if (tid == 0) *bad = 0;
-  for (int i = tid; i < kCudaRows * (d / 4); i += kCudaThreads) {
-    const int row = i / (d / 4), c = i % (d / 4);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < s.rows) x = load4((const T*)A.q + row_offset(A, s, s.row0 + row) + c * 4);
-    *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = x;
+#pragma unroll 1
+  for (int u = 0; u < kCudaRows * kPieces / kCudaThreads; ++u) {
+    const int i = tid + u * kCudaThreads, row = i / kPieces, c = i % kPieces;
+    copy16(smem_u32(qs + row * pitch + c * 4), (const T*)A.q + row_offset(A, s, s.row0 + (row < s.rows ? row : 0)) + c * 4, row < s.rows);
   }
   if (tid < 32) {
     const int32_t n = list_tiles(A, s, load_slots(A, s, 0), spt, nv, tiles);
@@ -266,6 +265,35 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
   const bool draft = s.part == split - 1;
   const int32_t mine = (*n_tiles - s.part + split - 1) / split + (draft ? 1 : 0);
   const float scale = kLog2e / sqrtf((float)d);
+  const uint8_t* unit = A.pool + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb * A.G.block_bytes;
+  const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
+  auto first_slot = [&](int32_t it) { return draft && it == 0 ? 0 : tile_of(tiles[s.part + (it - (draft ? 1 : 0)) * split]) * spt; };
+  // Tile it's keys (which = 0) or values into shared memory, zeros for what holds no valid token.
+  auto load = [&](int32_t it, int which) {
+    if (it < mine) {
+      const int32_t slot0 = first_slot(it);
+      const bool is_draft = draft && it == 0;
+      const float* to = which ? vs : ks;
+#pragma unroll 1
+      for (int u = 0; u < kEach; ++u) {
+        const int i = tid + u * kCudaThreads, j = i / kPieces, c = i % kPieces;
+        const T* from = (const T*)A.pool;
+        bool real;
+        if (is_draft) {
+          real = j < s.cnt;
+          if (real) from = (const T*)(which ? A.v : A.k) + draft_offset(A, s, j) + c * 4;
+        } else {
+          const int32_t in = j * per_bs >> 16, slot = slot0 + in, off = j - in * bs;
+          real = j < tt && slot < A.G.kb && off < nv[slot];
+          if (real) from = reinterpret_cast<const T*>(unit + slot * A.G.block_bytes) + (int64_t)(which * bs + off) * d + c * 4;
+        }
+        copy16(smem_u32(to + j * pitch + c * 4), from, real);
+      }
+    }
+    copy_group();
+  };
+  load(0, 0);
+  load(0, 1);
 
   uint64_t sees[4];
 #pragma unroll
@@ -281,40 +309,12 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 #pragma unroll
     for (int c = 0; c < 2 * DV; ++c) o[i][c] = 0.f;
   }
-  const uint8_t* unit = A.pool + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb * A.G.block_bytes;
 
   for (int32_t it = 0; it < mine; ++it) {
     const bool is_draft = draft && it == 0;
-    const int32_t slot0 = is_draft ? 0 : tile_of(tiles[s.part + (it - (draft ? 1 : 0)) * split]) * spt;
-    __syncthreads();  // the tile before has been read
-    for (int i = tid; i < kTile * (d / 4); i += kCudaThreads) {
-      const int j = i / (d / 4), c = i % (d / 4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (is_draft) {
-        if (j < s.cnt) {
-          const int64_t at = draft_offset(A, s, j) + c * 4;
-          x = load4((const T*)A.k + at);
-          y = load4((const T*)A.v + at);
-          if (!(is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w))) {
-            atomicOr(reinterpret_cast<unsigned long long*>(bad), 1ull << j);
-            if (!is_finite(y.x)) y.x = 0.f;
-            if (!is_finite(y.y)) y.y = 0.f;
-            if (!is_finite(y.z)) y.z = 0.f;
-            if (!is_finite(y.w)) y.w = 0.f;
-          }
-        }
-      } else {
-        const int32_t slot = slot0 + j / bs, off = j % bs;
-        if (j < tt && slot < A.G.kb && off < nv[slot]) {
-          const T* kp = reinterpret_cast<const T*>(unit + slot * A.G.block_bytes) + (int64_t)off * d + c * 4;
-          x = load4(kp);
-          y = load4(kp + (int64_t)bs * d);
-        }
-      }
-      *reinterpret_cast<float4*>(ks + j * pitch + c * 4) = x;
-      *reinterpret_cast<float4*>(vs + j * pitch + c * 4) = y;
-    }
-    __syncthreads();
+    const int32_t slot0 = first_slot(it);
+    copy_wait<1>();
+    __syncthreads();  // the keys are there, the values may be on their way
     float sc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -361,7 +361,26 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
 #pragma unroll
       for (int c = 0; c < 2 * DV; ++c) o[i][c] *= f;
     }
-    __syncwarp();  // the rows of ps are read by the half-warp that wrote them
+    __syncthreads();
+    load(it + 1, 0);  // the keys have been read
+    copy_wait<1>();
+    if (is_draft) {
+      // values that are not finite are zero in the products (each thread looks at what it copied)
+#pragma unroll 1
+      for (int u = 0; u < kEach; ++u) {
+        const int i = tid + u * kCudaThreads, j = i / kPieces, c = i % kPieces;
+        float4* at = reinterpret_cast<float4*>(vs + j * pitch + c * 4);
+        float4 y = *at;
+        if (is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w)) continue;
+        atomicOr(reinterpret_cast<unsigned long long*>(bad), 1ull << j);
+        if (!is_finite(y.x)) y.x = 0.f;
+        if (!is_finite(y.y)) y.y = 0.f;
+        if (!is_finite(y.z)) y.z = 0.f;
+        if (!is_finite(y.w)) y.w = 0.f;
+        *at = y;
+      }
+    }
+    __syncthreads();  // the values are there
 #pragma unroll 2
     for (int t = 0; t < kTile; t += 4) {
       float4 pv[4];
@@ -380,7 +399,10 @@ __global__ void __launch_bounds__(kCudaThreads) tree_cuda_kernel(const TreeArgs 
           }
         }
     }
+    __syncthreads();
+    load(it + 1, 1);  // the values have been read
   }
+  copy_wait<0>();
   __syncthreads();  // every tile read: the key tile becomes the partial outputs
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -994,9 +1016,10 @@ cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
   const int32_t groups = (A.T * A.G.g + kCudaRows - 1) / kCudaRows;
   const size_t smem = cuda_smem(DV * 32, A.G.kb, tiles);
-  const int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
+  int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
+  if (per_sm > cuda_ctas(DV)) per_sm = cuda_ctas(DV);
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
-  const Shape shape = pick_shape(items, groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles, 1, 1);
+  const Shape shape = pick_shape(items, groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles, 3, 2);
   return launch_cluster(tree_cuda_kernel<DV>, items, shape, kCudaThreads, smem, s, A, shape);
 }
 
