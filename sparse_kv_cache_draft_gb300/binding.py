@@ -292,24 +292,21 @@ class Context:
             raise ValueError(f"qkv: expected [{c.max_requests}][{(c.q_heads + 2 * c.kv_heads) * c.head_dim}] of the "
                              f"context's dtype, got {qkv.dtype} {tuple(qkv.shape)}")
         stride = _row_stride(qkv, (c.q_heads + 2 * c.kv_heads) * c.head_dim)
-        rotary._check(qkv, c.head_dim)
-        self._check(self.L.okv_append_qkv(self.h, layer, qkv.data_ptr(), stride, rotary._ref,
+        self._check(self.L.okv_append_qkv(self.h, layer, qkv.data_ptr(), stride, rotary._check(qkv.dtype, qkv.get_device(), c.head_dim),
                                           self._tensor_ptr(q, self._qshape, "q"), _stream_handle(stream)),
                     "okv_append_qkv")
 
     def attend_tree(self, layer: int, q, k, v, mask, out, counts=None, stream=None):
         """Drafted tokens' attention: q, out [R][T][Hq][d], k, v [R][T][Hkv][d], mask [R][T] int64 or uint64
         (bit j: drafted token j is attended), counts [R] int32 or None."""
-        import torch
         c = self.cfg
         T = q.shape[1] if q.dim() == 4 else 0
-        if counts is not None:
-            _expect(counts, "counts", (c.max_requests,), (torch.int32,), q.device)
-        _expect(mask, "mask", (c.max_requests, T), (torch.int64, torch.uint64), q.device)
+        _, dev = _storage(q, "q")
         qs, ks = (c.max_requests, T, c.q_heads, c.head_dim), (c.max_requests, T, c.kv_heads, c.head_dim)
-        self._check(self.L.okv_attend_tree(self.h, layer, T, counts.data_ptr() if counts is not None else None,
+        self._check(self.L.okv_attend_tree(self.h, layer, T,
+                                           _ptr(counts, "counts", (c.max_requests,), _I32, dev) if counts is not None else None,
                                            self._tensor_ptr(q, qs, "q"), self._tensor_ptr(k, ks, "k"),
-                                           self._tensor_ptr(v, ks, "v"), mask.data_ptr(),
+                                           self._tensor_ptr(v, ks, "v"), _ptr(mask, "mask", (c.max_requests, T), _I64, dev),
                                            self._tensor_ptr(out, qs, "out"), _stream_handle(stream)),
                     "okv_attend_tree")
 
@@ -443,32 +440,51 @@ def attend_static(pool, slot_block, lengths, q, out, *, q_heads: int, kv_heads: 
 
 
 # ---- rows, append and drafted trees without a context ------------------------------------------------
+#
+# A small call's time is the host's, so the checks here are few and flat: a tensor's shape, type, device
+# and contiguity once each, pointers as plain integers.
 
+_torch = None      # the module, _DTYPE_OF and the index types once a call has needed them
 _DTYPE_OF = {}
+_I32 = _I64 = ()
+
+
+def _load_torch():
+    global _torch, _I32, _I64
+    import torch
+    _DTYPE_OF.update({torch.float32: F32, torch.bfloat16: BF16})
+    _I32, _I64 = (torch.int32,), (torch.int64, torch.uint64)
+    _torch = torch
+    load_library()
+    return torch
 
 
 def _storage(t, name: str):
-    """(okv dtype, device) of a CUDA tensor of a storage dtype."""
-    if not _DTYPE_OF:
-        import torch
-        _DTYPE_OF.update({torch.float32: F32, torch.bfloat16: BF16})
-    if not t.is_cuda:
+    """(okv dtype, device index) of a CUDA tensor of a storage dtype."""
+    _torch or _load_torch()
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError(f"{name}: expected a CUDA tensor")
     dt = _DTYPE_OF.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return dt, t.device
+    return dt, dev
 
 
-def _expect(t, name: str, shape, dtypes, device):
-    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}, "
+def _ptr(t, name: str, shape, dtypes, dev: int) -> int:
+    """The address of a contiguous tensor of this shape and one of these types on device `dev`."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on cuda:{dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _row_stride(t, width: int) -> int:
     """Elements between the rows of t [...][width], whose leading dims are one run of rows."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
+    if shape[-1] == width and t.is_contiguous():
+        return width
+    stride = t.stride()
     if shape[-1] != width or (stride[-1] != 1 and width > 1):
         raise ValueError(f"qkv: expected rows of {width} adjacent elements, got shape {tuple(shape)} strides {stride}")
     step = None  # between rows, of the dims seen so far from the last one
@@ -488,40 +504,51 @@ class Rotary:
     """okv_rotary: inv_freq [rotary_dim / 2] float32 (None: no rotation), q_weight and k_weight [head_dim] of
     the rows' dtype (None: no norm). Keeps the tensors; read at each call."""
 
+    __slots__ = ("tensors", "_c", "_ref")
+
     def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False):
-        import torch
-        for name, t in (("inv_freq", inv_freq), ("q_weight", q_weight), ("k_weight", k_weight)):
-            if t is not None and (not t.is_cuda or t.dim() != 1 or not t.is_contiguous()):
-                raise ValueError(f"{name}: expected a contiguous CUDA vector")
-        if inv_freq is not None and inv_freq.dtype != torch.float32:
-            raise ValueError(f"inv_freq: expected float32, got {inv_freq.dtype}")
+        torch = _torch or _load_torch()
+        ptr, rot = [None, None, None], 0
+        for i, t in enumerate((inv_freq, q_weight, k_weight)):
+            if t is None:
+                continue
+            if t.get_device() < 0 or t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{('inv_freq', 'q_weight', 'k_weight')[i]}: expected a contiguous CUDA vector")
+            ptr[i] = t.data_ptr()
+        if inv_freq is not None:
+            if inv_freq.dtype != torch.float32:
+                raise ValueError(f"inv_freq: expected float32, got {inv_freq.dtype}")
+            rot = 2 * inv_freq.numel()
         self.tensors = (inv_freq, q_weight, k_weight)
-        ptr = [t.data_ptr() if t is not None else None for t in self.tensors]
-        self._c = _Rotary(ptr[0], ptr[1], ptr[2], eps, 2 * inv_freq.numel() if inv_freq is not None else 0,
-                          1 if interleaved else 0)
+        self._c = _Rotary(ptr[0], ptr[1], ptr[2], eps, rot, 1 if interleaved else 0)
         self._ref = ctypes.addressof(self._c)
 
-    def _check(self, rows, head_dim: int):
+    def _check(self, dtype, dev: int, head_dim: int) -> int:
         inv_freq, qw, kw = self.tensors
-        dev = rows.device
-        if inv_freq is not None and inv_freq.device != dev:
-            raise ValueError(f"inv_freq: on {inv_freq.device}, the rows on {dev}")
+        if inv_freq is not None and inv_freq.get_device() != dev:
+            raise ValueError(f"inv_freq: on {inv_freq.device}, the rows on cuda:{dev}")
         for w in (qw, kw):
-            if w is not None and (w.dtype != rows.dtype or w.device != dev or w.numel() != head_dim):
-                raise ValueError(f"weights: expected {rows.dtype} [{head_dim}] on {dev}, got {w.dtype} {tuple(w.shape)} on {w.device}")
+            if w is not None and (w.dtype != dtype or w.get_device() != dev or w.numel() != head_dim):
+                raise ValueError(f"weights: expected {dtype} [{head_dim}] on cuda:{dev}, got {w.dtype} {tuple(w.shape)} on {w.device}")
+        return self._ref
 
 
-def _call(fn: str, device, stream, *args) -> None:
-    """A context-free call with `device` current and its stream as the last argument."""
-    import torch
-    L = _lib or load_library()
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            st = getattr(L, fn)(*args, _stream_handle(stream))
+def _current(dev: int, stream):
+    """The handle of `stream`, or of device `dev`'s current stream."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(fn, dev: int, stream, *args) -> None:
+    """A context-free call with device `dev` current and its stream as the last argument."""
+    if _torch._C._cuda_getDevice() == dev:
+        st = fn(*args, _current(dev, stream))
     else:
-        st = getattr(L, fn)(*args, _stream_handle(stream))
+        with _torch.cuda.device(dev):
+            st = fn(*args, _current(dev, stream))
     if st != OK:
-        raise OkvError(st, f"{fn} failed (shape, alignment or size outside its limits, or a CUDA error)")
+        raise OkvError(st, f"{fn.__name__} failed (shape, alignment or size outside its limits, or a CUDA error)")
 
 
 def norm_rope(qkv, positions, q=None, k=None, v=None, *, q_heads: int, kv_heads: int, head_dim: int, rotary: Rotary,
@@ -529,20 +556,16 @@ def norm_rope(qkv, positions, q=None, k=None, v=None, *, q_heads: int, kv_heads:
     """okv_norm_rope: norms and rotates rows qkv [n][(q_heads + 2 kv_heads) head_dim] (rows may be strided) at
     positions [n] int32 into q [n][q_heads][head_dim], k and v [n][kv_heads][head_dim] (any may be None).
     Rows with a negative position are not written."""
-    import torch
     dt, dev = _storage(qkv, "qkv")
     if qkv.dim() != 2:
         raise ValueError(f"qkv: expected rows [n][...], got {tuple(qkv.shape)}")
-    n = qkv.shape[0]
-    stride = _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim)
-    _expect(positions, "positions", (n,), (torch.int32,), dev)
-    for name, t, h in (("q", q, q_heads), ("k", k, kv_heads), ("v", v, kv_heads)):
-        if t is not None:
-            _expect(t, name, (n, h, head_dim), (qkv.dtype,), dev)
-    rotary._check(qkv, head_dim)
-    _call("okv_norm_rope", dev, stream, n, q_heads, kv_heads, head_dim, dt, qkv.data_ptr(), stride, positions.data_ptr(),
-          rotary._ref, q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
-          v.data_ptr() if v is not None else None)
+    n, dtype = qkv.shape[0], qkv.dtype
+    st, kv = (dtype,), (n, kv_heads, head_dim)
+    _call(_lib.okv_norm_rope, dev, stream, n, q_heads, kv_heads, head_dim, dt, qkv.data_ptr(),
+          _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim), _ptr(positions, "positions", (n,), _I32, dev),
+          rotary._check(dtype, dev, head_dim),
+          _ptr(q, "q", (n, q_heads, head_dim), st, dev) if q is not None else None,
+          _ptr(k, "k", kv, st, dev) if k is not None else None, _ptr(v, "v", kv, st, dev) if v is not None else None)
 
 
 def append_qkv_static(qkv, lengths, counts, pool, slot_block, q=None, *, q_heads: int, kv_heads: int, head_dim: int,
@@ -550,24 +573,17 @@ def append_qkv_static(qkv, lengths, counts, pool, slot_block, q=None, *, q_heads
     """okv_append_qkv_static: rows qkv [R][T][(q_heads + 2 kv_heads) head_dim] at positions lengths[r] + t, normed
     and rotated; queries into q [R][T][q_heads][head_dim] (or None), keys and values into the resident slots of
     pool [R][kv_heads][slots][2][block_size][head_dim]; counts [R] int32 or None."""
-    import torch
     dt, dev = _storage(qkv, "qkv")
     if qkv.dim() != 3:
         raise ValueError(f"qkv: expected rows [R][T][...], got {tuple(qkv.shape)}")
-    R, T = qkv.shape[0], qkv.shape[1]
-    stride = _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim)
-    i32 = (torch.int32,)
-    _expect(lengths, "lengths", (R,), i32, dev)
-    if counts is not None:
-        _expect(counts, "counts", (R,), i32, dev)
-    _expect(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), (qkv.dtype,), dev)
-    _expect(slot_block, "slot_block", (R, kv_heads, slots), i32, dev)
-    if q is not None:
-        _expect(q, "q", (R, T, q_heads, head_dim), (qkv.dtype,), dev)
-    rotary._check(qkv, head_dim)
-    _call("okv_append_qkv_static", dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, qkv.data_ptr(),
-          stride, lengths.data_ptr(), counts.data_ptr() if counts is not None else None, rotary._ref, pool.data_ptr(),
-          slot_block.data_ptr(), q.data_ptr() if q is not None else None)
+    R, T, dtype = qkv.shape[0], qkv.shape[1], qkv.dtype
+    st = (dtype,)
+    _call(_lib.okv_append_qkv_static, dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, qkv.data_ptr(),
+          _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim), _ptr(lengths, "lengths", (R,), _I32, dev),
+          _ptr(counts, "counts", (R,), _I32, dev) if counts is not None else None, rotary._check(dtype, dev, head_dim),
+          _ptr(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev),
+          _ptr(slot_block, "slot_block", (R, kv_heads, slots), _I32, dev),
+          _ptr(q, "q", (R, T, q_heads, head_dim), st, dev) if q is not None else None)
 
 
 def attend_tree_static(pool, slot_block, lengths, counts, q, k, v, mask, out, *, q_heads: int, kv_heads: int,
@@ -575,18 +591,12 @@ def attend_tree_static(pool, slot_block, lengths, counts, q, k, v, mask, out, *,
     """okv_attend_tree_static: drafted tokens q, out [R][T][q_heads][head_dim], k, v [R][T][kv_heads][head_dim], mask
     [R][T] int64 or uint64 (bit j: drafted token j is attended), counts [R] int32 or None, over a pool of
     attend_static's layout."""
-    import torch
     dt, dev = _storage(pool, "pool")
     R, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (0, 0)
-    i32, st = (torch.int32,), (pool.dtype,)
-    _expect(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev)
-    _expect(slot_block, "slot_block", (R, kv_heads, slots), i32, dev)
-    _expect(lengths, "lengths", (R,), i32, dev)
-    if counts is not None:
-        _expect(counts, "counts", (R,), i32, dev)
-    for name, t, h in (("q", q, q_heads), ("k", k, kv_heads), ("v", v, kv_heads), ("out", out, q_heads)):
-        _expect(t, name, (R, T, h, head_dim), st, dev)
-    _expect(mask, "mask", (R, T), (torch.int64, torch.uint64), dev)
-    _call("okv_attend_tree_static", dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, pool.data_ptr(),
-          slot_block.data_ptr(), lengths.data_ptr(), counts.data_ptr() if counts is not None else None, q.data_ptr(),
-          k.data_ptr(), v.data_ptr(), mask.data_ptr(), out.data_ptr())
+    st, qs, ks = (pool.dtype,), (R, T, q_heads, head_dim), (R, T, kv_heads, head_dim)
+    _call(_lib.okv_attend_tree_static, dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt,
+          _ptr(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev),
+          _ptr(slot_block, "slot_block", (R, kv_heads, slots), _I32, dev), _ptr(lengths, "lengths", (R,), _I32, dev),
+          _ptr(counts, "counts", (R,), _I32, dev) if counts is not None else None, _ptr(q, "q", qs, st, dev),
+          _ptr(k, "k", ks, st, dev), _ptr(v, "v", ks, st, dev), _ptr(mask, "mask", (R, T), _I64, dev),
+          _ptr(out, "out", qs, st, dev))
