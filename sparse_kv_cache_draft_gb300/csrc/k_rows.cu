@@ -221,7 +221,7 @@ struct RowsTo {
 };
 
 template <typename T, int LPG, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs A, const RowsTo R) {
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, const RowsTo R) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32, kSub = 32 / LPG;  // head rows of a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPG, sg = lane / LPG;
@@ -261,17 +261,27 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs A, const R
     mine = mine && pos >= 0;
   }
   if (!mine) return;
+  // The row's head rows in groups of a warp: queries, keys, values. A warp takes every `parts`-th group, a
+  // batch of loads ahead of the work on them; the first ones go out before the angles.
+  const int32_t gq = (A.Hq + kSub - 1) / kSub, gk = (A.Hkv + kSub - 1) / kSub;
+  const T* from = (const T*)A.qkv + row * A.row_stride + sub * 8;
+  auto load = [&](Eight<T>(&raw)[kInFlight], int32_t g, int32_t first, int32_t heads, const T* in) {
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int32_t h = (g + u * R.parts - first) * kSub + sg;
+      raw[u].zero();
+      if (h < heads && on) raw[u].load(in + (int64_t)h * A.d);
+    }
+  };
+  int32_t g = part;
+  Eight<T> raw[kInFlight];
+  bool ahead = g < gq && A.q;
+  if (ahead) load(raw, g, 0, A.Hq, from);
   for (int32_t f = lane; f < A.half; f += 32) {
     const float inv = A.inv_freq[f];
     angle(turn_per_position(inv), inv, pos, &cs[f], &sn[f]);
   }
   __syncwarp();
-
-  // The row's head rows in groups of a warp: queries, keys, values. A warp takes every `parts`-th group,
-  // a batch of loads ahead of the work on them.
-  const int32_t gq = (A.Hq + kSub - 1) / kSub, gk = (A.Hkv + kSub - 1) / kSub;
-  const T* from = (const T*)A.qkv + row * A.row_stride + sub * 8;
-  int32_t g = part;
   for (int kind = 0; kind < 3; ++kind) {
     const int32_t heads = kind == 0 ? A.Hq : A.Hkv, first = kind == 0 ? 0 : kind == 1 ? gq : gq + gk, end = kind == 0 ? gq : first + gk;
     if (g >= end) continue;
@@ -291,14 +301,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs A, const R
     }
     Turn t;
     if (kind < 2) t = make_turn<T>(A, (const T*)(kind == 0 ? A.q_weight : A.k_weight), cs, sn, sub);
-    for (; g < end; g += kInFlight * R.parts) {
-      Eight<T> raw[kInFlight];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int32_t h = (g + u * R.parts - first) * kSub + sg;
-        raw[u].zero();
-        if (h < heads && on) raw[u].load(in + (int64_t)h * A.d);
-      }
+    auto work = [&](Eight<T>(&raw)[kInFlight], int32_t g) {
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         if (g + u * R.parts >= end) break;
@@ -313,6 +316,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs A, const R
         }
         raw[u].store(out + at);
       }
+    };
+    for (; g < end; g += kInFlight * R.parts) {
+      if (!ahead) load(raw, g, first, heads, in);
+      ahead = false;
+      work(raw, g);
     }
     // the last batch may have stepped past groups of the next kind
     while (g - R.parts >= end) g -= R.parts;
