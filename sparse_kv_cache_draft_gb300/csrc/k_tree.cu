@@ -214,48 +214,81 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
-// ---- CUDA cores: binary32 ---------------------------------------------------------------------------
+// ---- binary32 ------------------------------------------------------------------------------------------
 //
-// 128 threads, 32 rows x 64 tokens. S = Q K^T as 4 x 4 per thread (rows tr*4+i, tokens tc+16j), the
-// softmax of a row over the 16 threads that hold it, then O += P V as 4 rows x 2 DV dims per thread.
-// Operands are binary32 in shared memory; rows of d + 4 floats keep the 16-byte loads of eight
-// different rows on different banks.
-constexpr int kCudaThreads = 128, kCudaRows = 32;
+// Products of binary32 numbers on the tensor cores, as three products of 11-bit parts: x = hi + lo + less
+// than 2^-21 x, hi the upper 11 bits and lo the next 11, and x y = hi hi + hi lo + lo hi within 2^-20 of
+// |x y|; sums in binary32. (On the CUDA cores the reads of shared memory bound both products: 25 TFLOP/s at
+// 64 tokens x 16 requests, 32 / 8 heads, d 128, 2048 tokens of context.) A product with an infinite factor may give NaN.
+//
+// 128 threads, 16 RG rows x 64 tokens; a warp takes 16 rows and 64 / TH of the tokens with a maximum, sum and
+// output of its own, merged at the end. m16n8k8: S's accumulators are P's operand as they stand, with the
+// tokens 2t and 2t + 1 of a lane as k = t and t + 4, and V's rows read in that order. Rows of d + 4 floats
+// keep all fragment reads free of bank conflicts.
+constexpr int kF32Threads = 128;
 
-__host__ __device__ constexpr int cuda_pitch(int d) { return d + 4; }
-__host__ __device__ constexpr int cuda_ctas(int dv) { return dv <= 2 ? 3 : 2; }  // CTAs of an SM, by registers
-__host__ __device__ constexpr size_t cuda_smem(int d, int kb, int tiles) {
-  return (size_t)(kCudaRows + 2 * kTile) * cuda_pitch(d) * 4 + (size_t)kCudaRows * (kTile + 4) * 4 + kCudaRows * 8 + 64 +
-         ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
+__host__ __device__ constexpr int f32_pitch(int d) { return d + 4; }
+__host__ __device__ constexpr size_t f32_smem(int d, int rg, int kb, int tiles) {
+  const int th = 4 / rg;
+  return (size_t)(16 * rg + 2 * kTile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 16 + ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
+}
+__host__ __device__ constexpr int f32_ctas(int dv) { return dv <= 4 ? 3 : 2; }  // CTAs of an SM, by registers
+
+struct Parts {
+  uint32_t hi, lo;
+};
+// The tensor cores take the upper 19 bits of an operand as they stand: hi is rounded here, lo is cut off, which
+// of a part of either sign leaves no bias.
+__device__ __forceinline__ Parts parts_of(float x) {
+  const uint32_t hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  return {hi, __float_as_uint(x - __uint_as_float(hi))};
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c += a b. The eight products of a step are summed on the tensor cores, which cut sums off (towards zero);
+// the steps are summed here, rounded to nearest.
+__device__ __forceinline__ void mma_f32(float (&c)[4], const Parts (&a)[4], const Parts& b0, const Parts& b1) {
+  float x[4];
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+      : "r"(a[0].lo), "r"(a[1].lo), "r"(a[2].lo), "r"(a[3].lo), "r"(b0.hi), "r"(b1.hi), "f"(0.f));
+  mma_tf32(x, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+  mma_tf32(x, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += x[i];
 }
 
-template <int DV>
-__global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(const TreeArgs A, const Shape shape) {
-  using T = float;
+template <int DV, int RG>
+__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(const TreeArgs A, const Shape shape) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int d = DV * 32, pitch = cuda_pitch(d);
-  float* qs = reinterpret_cast<float*>(smem);      // [32][pitch]
-  float* ks = qs + kCudaRows * pitch;              // [64][pitch]
+  constexpr int d = DV * 32, pitch = f32_pitch(d), kRows = 16 * RG, TH = 4 / RG, kTok = kTile / TH, NT = kTok / 8;
+  float* qs = reinterpret_cast<float*>(smem);      // [rows][pitch]
+  float* ks = qs + kRows * pitch;                  // [64][pitch]
   float* vs = ks + kTile * pitch;                  // [64][pitch]
-  float* ps = vs + kTile * pitch;                  // [32][64 + 4]
-  float* ms = ps + kCudaRows * (kTile + 4);        // [32]
-  float* ls = ms + kCudaRows;                      // [32]
-  uint64_t* bad = reinterpret_cast<uint64_t*>(ls + kCudaRows);
+  float* ms = vs + kTile * pitch;                  // [rows], then [TH][rows] of the warps
+  float* ls = ms + (TH + 1) * kRows;               // the same
+  uint64_t* bad = reinterpret_cast<uint64_t*>(ls + (TH + 1) * kRows);
   int32_t* n_tiles = reinterpret_cast<int32_t*>(bad + 1);
   uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 2);
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
-  const Site s = make_site(A, shape, kCudaRows);
+  const Site s = make_site(A, shape, kRows);
   if (s.rows <= 0) return;
   const int32_t split = s.parts;
-  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
+  const int rg = warp % RG, th = warp / RG, tok0 = th * kTok;
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
-  constexpr int kPieces = d / 4, kEach = kTile * kPieces / kCudaThreads;  // 16-byte pieces of a token, of a thread's share of a tile
+  constexpr int kPieces = d / 4, kEach = kTile * kPieces / kF32Threads;  // 16-byte pieces of a token, of a thread's share of a tile
   if (tid == 0) *bad = 0;
 #pragma unroll 1
-  for (int u = 0; u < kCudaRows * kPieces / kCudaThreads; ++u) {
-    const int i = tid + u * kCudaThreads, row = i / kPieces, c = i % kPieces;
-    copy16(smem_u32(qs + row * pitch + c * 4), (const T*)A.q + row_offset(A, s, s.row0 + (row < s.rows ? row : 0)) + c * 4, row < s.rows);
+  for (int u = 0; u < kRows * kPieces / kF32Threads; ++u) {
+    const int i = tid + u * kF32Threads, row = i / kPieces, c = i % kPieces;
+    copy16(smem_u32(qs + row * pitch + c * 4), (const float*)A.q + row_offset(A, s, s.row0 + (row < s.rows ? row : 0)) + c * 4, row < s.rows);
   }
   if (tid < 32) {
     const int32_t n = list_tiles(A, s, load_slots(A, s, 0), spt, nv, tiles);
@@ -267,25 +300,25 @@ __global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(
   const float scale = kLog2e / sqrtf((float)d);
   const uint8_t* unit = A.pool + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb * A.G.block_bytes;
   const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
-  auto first_slot = [&](int32_t it) { return draft && it == 0 ? 0 : tile_of(tiles[s.part + (it - (draft ? 1 : 0)) * split]) * spt; };
+  auto entry = [&](int32_t it) { return tiles[s.part + (it - (draft ? 1 : 0)) * split]; };
   // Tile it's keys (which = 0) or values into shared memory, zeros for what holds no valid token.
   auto load = [&](int32_t it, int which) {
     if (it < mine) {
-      const int32_t slot0 = first_slot(it);
       const bool is_draft = draft && it == 0;
+      const int32_t slot0 = is_draft ? 0 : tile_of(entry(it)) * spt;
       const float* to = which ? vs : ks;
-#pragma unroll 1
+#pragma unroll 2
       for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kCudaThreads, j = i / kPieces, c = i % kPieces;
-        const T* from = (const T*)A.pool;
+        const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
+        const float* from = (const float*)A.pool;
         bool real;
         if (is_draft) {
           real = j < s.cnt;
-          if (real) from = (const T*)(which ? A.v : A.k) + draft_offset(A, s, j) + c * 4;
+          if (real) from = (const float*)(which ? A.v : A.k) + draft_offset(A, s, j) + c * 4;
         } else {
           const int32_t in = j * per_bs >> 16, slot = slot0 + in, off = j - in * bs;
           real = j < tt && slot < A.G.kb && off < nv[slot];
-          if (real) from = reinterpret_cast<const T*>(unit + slot * A.G.block_bytes) + (int64_t)(which * bs + off) * d + c * 4;
+          if (real) from = reinterpret_cast<const float*>(unit + slot * A.G.block_bytes) + (int64_t)(which * bs + off) * d + c * 4;
         }
         copy16(smem_u32(to + j * pitch + c * 4), from, real);
       }
@@ -295,71 +328,69 @@ __global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(
   load(0, 0);
   load(0, 1);
 
-  uint64_t sees[4];
+  uint64_t sees[2];  // of rows gi and gi + 8 of the warp's 16
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t row = tr * 4 + i;
+  for (int i = 0; i < 2; ++i) {
+    const int32_t row = rg * 16 + gi + 8 * i;
     sees[i] = row < s.rows ? A.mask[(int64_t)s.r * A.T + (s.row0 + row) / A.G.g] & low_bits(s.cnt) : 0;
   }
-  float o[4][2 * DV], m[4], l[4];
+  float o[d / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < 2 * DV; ++c) o[i][c] = 0.f;
-  }
+  for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
   for (int32_t it = 0; it < mine; ++it) {
     const bool is_draft = draft && it == 0;
-    const int32_t slot0 = first_slot(it);
+    uint64_t vis[2] = {sees[0], sees[1]};
+    if (!is_draft) {
+      const uint16_t tile = entry(it);
+      uint32_t half[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int32_t j = lane + 32 * u, in = j * per_bs >> 16, slot = tile_of(tile) * spt + in;
+        half[u] = __ballot_sync(0xffffffffu, j < tt && slot < A.G.kb && j - in * bs < nv[min(slot, A.G.kb - 1)]);
+      }
+      vis[0] = vis[1] = (uint64_t)half[1] << 32 | half[0];
+    }
     copy_wait<1>();
     __syncthreads();  // the keys are there, the values may be on their way
-    float sc[4][4];
+    float sc[NT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    const float* qa = qs + (rg * 16 + gi) * pitch + ti;
+    const float* kr = ks + (tok0 + gi) * pitch + ti;
 #pragma unroll 4
-    for (int c = 0; c < d; c += 4) {
-      float4 qv[4], kv[4];
+    for (int k = 0; k < d; k += 8) {
+      const Parts a[4] = {parts_of(qa[k]), parts_of(qa[k + 8 * pitch]), parts_of(qa[k + 4]), parts_of(qa[k + 8 * pitch + 4])};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (tr * 4 + i) * pitch + c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (tc + 16 * j) * pitch + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[i][j] = fmaf(qv[i].w, kv[j].w, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].x, kv[j].x, sc[i][j]))));
+      for (int n = 0; n < NT; ++n) mma_f32(sc[n], a, parts_of(kr[n * 8 * pitch + k]), parts_of(kr[n * 8 * pitch + k + 4]));
     }
+    // rows gi: sc[.][0], sc[.][1]; gi + 8: sc[.][2], sc[.][3]; tokens tok0 + 8 n + 2 ti and the next
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int tok = tc + 16 * j;
-      const int32_t slot = slot0 + tok / bs;
-      const bool valid = !is_draft && tok < tt && slot < A.G.kb && tok % bs < nv[slot];
+    for (int i = 0; i < 2; ++i) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sc[i][j] = (is_draft ? (sees[i] >> tok & 1) != 0 : valid) ? sc[i][j] * scale : -INFINITY;
-    }
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float mx = fmaxf(fmaxf(sc[i][0], sc[i][1]), fmaxf(sc[i][2], sc[i][3]));
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m[i] - ref);
+        for (int e = 0; e < 2; ++e) {
+          float& x = sc[n][2 * i + e];
+          x = vis[i] >> (tok0 + 8 * n + 2 * ti + e) & 1 ? x * scale : -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
+      m[i] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(sc[i][j] - ref);
-        sum += p;
-        ps[(tr * 4 + i) * (kTile + 4) + tc + 16 * j] = p;
-      }
-      m[i] = mn;
-      l[i] = l[i] * f + sum;  // of this thread's tokens; summed over the 16 threads at the end
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 2 * DV; ++c) o[i][c] *= f;
+        for (int e = 0; e < 2; ++e) sum += sc[n][2 * i + e] = ex2(sc[n][2 * i + e] - ref);
+      l[i] = l[i] * f + sum;  // of this lane's tokens; summed over the four lanes at the end
+#pragma unroll
+      for (int n = 0; n < d / 8; ++n) {
+        o[n][2 * i] *= f;
+        o[n][2 * i + 1] *= f;
+      }
     }
     __syncthreads();
     load(it + 1, 0);  // the keys have been read
@@ -368,7 +399,7 @@ __global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(
       // values that are not finite are zero in the products (each thread looks at what it copied)
 #pragma unroll 1
       for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kCudaThreads, j = i / kPieces, c = i % kPieces;
+        const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
         float4* at = reinterpret_cast<float4*>(vs + j * pitch + c * 4);
         float4 y = *at;
         if (is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w)) continue;
@@ -381,56 +412,63 @@ __global__ void __launch_bounds__(kCudaThreads, cuda_ctas(DV)) tree_cuda_kernel(
       }
     }
     __syncthreads();  // the values are there
-#pragma unroll 2
-    for (int t = 0; t < kTile; t += 4) {
-      float4 pv[4];
+    const float* vr = vs + (tok0 + 2 * ti) * pitch + gi;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (tr * 4 + i) * (kTile + 4) + t);
+    for (int n = 0; n < NT; ++n) {
+      const Parts a[4] = {parts_of(sc[n][0]), parts_of(sc[n][2]), parts_of(sc[n][1]), parts_of(sc[n][3])};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int c = 0; c < DV; ++c) {
-          const float2 x = *reinterpret_cast<const float2*>(vs + (t + u) * pitch + 32 * c + 2 * tc);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = u == 0 ? pv[i].x : u == 1 ? pv[i].y : u == 2 ? pv[i].z : pv[i].w;
-            o[i][2 * c] = fmaf(p, x.x, o[i][2 * c]);
-            o[i][2 * c + 1] = fmaf(p, x.y, o[i][2 * c + 1]);
-          }
-        }
+      for (int c = 0; c < d / 8; ++c)
+        mma_f32(o[c], a, parts_of(vr[n * 8 * pitch + c * 8]), parts_of(vr[n * 8 * pitch + pitch + c * 8]));
     }
     __syncthreads();
     load(it + 1, 1);  // the values have been read
   }
   copy_wait<0>();
-  __syncthreads();  // every tile read: the key tile becomes the partial outputs
+  __syncthreads();  // every tile read: keys and values give way to the warps' outputs, [TH][rows][d]
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    const int row = rg * 16 + gi + 8 * i;
+    float* to = ks + (th * kRows + row) * d + 2 * ti;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-    const int row = tr * 4 + i;
-#pragma unroll
-    for (int c = 0; c < DV; ++c) *reinterpret_cast<float2*>(ks + row * d + 32 * c + 2 * tc) = make_float2(o[i][2 * c], o[i][2 * c + 1]);
-    if (tc == 0) {
-      ms[row] = m[i];
-      ls[row] = l[i];
+    for (int c = 0; c < d / 8; ++c) *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+    if (ti == 0) {
+      ms[(1 + th) * kRows + row] = m[i];
+      ls[(1 + th) * kRows + row] = l[i];
     }
   }
-  const Partial P{smem_u32(ks), smem_u32(ms), smem_u32(ls), smem_u32(bad)};
-  if (split > 1) {
-    merge_cluster<T>(A, s, P, 0);
-    return;
-  }
   __syncthreads();
-  for (int i = tid; i < s.rows * (d / 4); i += kCudaThreads) {
-    const int row = i / (d / 4), c = i % (d / 4);
-    float4 x = *reinterpret_cast<const float4*>(ks + row * d + c * 4);
-    const float inv = ls[row] == 0.f ? 0.f : 1.f / ls[row];
+#pragma unroll 1
+  for (int i = tid; i < s.rows * kPieces; i += kF32Threads) {
+    const int row = i / kPieces, c = i % kPieces;
+    float M = -INFINITY, sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 1; k <= TH; ++k) M = fmaxf(M, ms[k * kRows + row]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < TH; ++k) {
+      const float f = ex2(ms[(1 + k) * kRows + row] - ref);
+      const float4 y = *reinterpret_cast<const float4*>(ks + (k * kRows + row) * d + c * 4);
+      sum = fmaf(f, ls[(1 + k) * kRows + row], sum);
+      x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+    }
+    if (split > 1) {
+      *reinterpret_cast<float4*>(ks + row * d + c * 4) = x;  // read above by this thread alone
+      if (c == 0) {
+        ms[row] = M;
+        ls[row] = sum;
+      }
+      continue;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     const int32_t mrow = s.row0 + row;
-    if (*bad) add_not_finite<T>(A, s, *bad & low_bits(s.cnt) & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, x);
-    store4((T*)A.out + row_offset(A, s, mrow) + c * 4, x);
+    if (*bad) add_not_finite<float>(A, s, *bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, x);
+    store4((float*)A.out + row_offset(A, s, mrow) + c * 4, x);
   }
+  if (split > 1) merge_cluster<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls), smem_u32(bad)}, 0);
 }
 
 // ---- tensor cores: bf16 ------------------------------------------------------------------------------
@@ -973,14 +1011,16 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
 }
 
 // The shape of least time by a count of tile times: an item takes its tiles and `fixed` more, and `join` more
-// where its CTAs merge; `slots` CTAs run at once. Items that fill the GPU go whole, the last ones split.
+// where its CTAs merge; `slots` CTAs run at once, of clusters an eighth fewer (a cluster stays within a GPC,
+// whose SMs it seldom fills). Items that fill the GPU go whole, the last ones split.
 Shape pick_shape(int64_t items, int32_t groups, int64_t slots, int32_t tiles, double fixed, double join) {
   Shape best{1, (int32_t)items, groups};
   double least = 1e30;
   for (int32_t c = 1; c <= kMaxSplit && c <= tiles; ++c) {
-    const int64_t full = items / slots * slots / c * c, whole = c == 1 ? items : full, rest = items - whole;
+    const int64_t room = c == 1 ? slots : slots * 7 / 8;
+    const int64_t whole = c == 1 ? items : items / slots * slots / c * c, rest = items - whole;
     const double t = (double)((whole + slots - 1) / slots) * (tiles + fixed) +
-                     (double)((rest * c + slots - 1) / slots) * ((double)tiles / c + fixed + join);
+                     (double)((rest * c + room - 1) / room) * ((double)tiles / c + fixed + join);
     if (t < least) least = t, best = Shape{c, (int32_t)whole, groups};
   }
   return best;
@@ -1011,28 +1051,33 @@ cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& sha
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
-template <int DV>
-cudaError_t run_cuda(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+template <int DV, int RG>
+cudaError_t run_f32(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
-  const int32_t groups = (A.T * A.G.g + kCudaRows - 1) / kCudaRows;
-  const size_t smem = cuda_smem(DV * 32, A.G.kb, tiles);
+  const int32_t groups = (A.T * A.G.g + 16 * RG - 1) / (16 * RG);
+  const size_t smem = f32_smem(DV * 32, RG, A.G.kb, tiles);
   int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
-  if (per_sm > cuda_ctas(DV)) per_sm = cuda_ctas(DV);
+  if (per_sm > f32_ctas(DV)) per_sm = f32_ctas(DV);
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
   const Shape shape = pick_shape(items, groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles, 3, 2);
-  return launch_cluster(tree_cuda_kernel<DV>, items, shape, kCudaThreads, smem, s, A, shape);
+  return launch_cluster(tree_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape);
 }
 
-cudaError_t run_cuda_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+template <int DV>
+cudaError_t run_f32_rows(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
+  return A.T * A.G.g <= 16 ? run_f32<DV, 1>(A, n_active, s) : run_f32<DV, 2>(A, n_active, s);
+}
+
+cudaError_t run_f32_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   switch (A.G.d / 32) {
-    case 1: return run_cuda<1>(A, n_active, s);
-    case 2: return run_cuda<2>(A, n_active, s);
-    case 3: return run_cuda<3>(A, n_active, s);
-    case 4: return run_cuda<4>(A, n_active, s);
-    case 5: return run_cuda<5>(A, n_active, s);
-    case 6: return run_cuda<6>(A, n_active, s);
-    case 7: return run_cuda<7>(A, n_active, s);
-    default: return run_cuda<8>(A, n_active, s);
+    case 1: return run_f32_rows<1>(A, n_active, s);
+    case 2: return run_f32_rows<2>(A, n_active, s);
+    case 3: return run_f32_rows<3>(A, n_active, s);
+    case 4: return run_f32_rows<4>(A, n_active, s);
+    case 5: return run_f32_rows<5>(A, n_active, s);
+    case 6: return run_f32_rows<6>(A, n_active, s);
+    case 7: return run_f32_rows<7>(A, n_active, s);
+    default: return run_f32_rows<8>(A, n_active, s);
   }
 }
 
@@ -1116,7 +1161,7 @@ cudaError_t run_mma_d(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
 
 cudaError_t launch_attend_tree(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   if (n_active <= 0) return cudaSuccess;
-  return A.G.dtype == OKV_F32 ? run_cuda_d(A, n_active, s) : run_mma_d(A, n_active, s);
+  return A.G.dtype == OKV_F32 ? run_f32_d(A, n_active, s) : run_mma_d(A, n_active, s);
 }
 
 }  // namespace okv
