@@ -350,7 +350,7 @@ cudaError_t run_rows(const RowArgs& A, RowsTo R, cudaStream_t s) {
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
     if (smem > 48 * 1024) {
-      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448)) return e;
     }
     kernel<<<(unsigned)ctas, kThreads, smem, s>>>(A, R);
     return cudaGetLastError();

@@ -26,6 +26,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 64;         // tokens of a tile, at most
 constexpr int kMaxSplit = 8;      // CTAs of a cluster (the portable limit)
+constexpr int kMaxSmem = 232448;  // bytes of shared memory a CTA may have
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -1034,7 +1035,8 @@ int sm_count() {
 
 template <typename... P, typename... Q>
 cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& shape, int threads, size_t smem, cudaStream_t s, Q&&... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit is the same for every launch: another thread's may come between this and the launch
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(shape.whole + (items - shape.whole) * shape.split));
@@ -1130,7 +1132,7 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
   // that share of the shared memory. It is never so small that a third CTA could come to wait for TMEM.
   const bool two = D <= 128 && NW == 1;
-  const size_t share = two ? 115712 : 232448, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb, tiles);
+  const size_t share = two ? 115712 : kMaxSmem, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb, tiles);
   int32_t ring = (int32_t)((share - rest) / L::kBuf);
   if (ring > kMaxRing) ring = kMaxRing;
   size_t smem = rest + (size_t)ring * L::kBuf;

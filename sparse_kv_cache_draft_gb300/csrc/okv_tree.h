@@ -85,7 +85,7 @@ inline bool row_args(const okv_rotary* t, int32_t q_heads, int32_t kv_heads, int
                      void* q, RowArgs* out) {
   const int32_t elem = dtype == OKV_F32 ? 4 : 2;
   if (!t || !qkv || !aligned16(qkv) || !aligned16(q)) return false;
-  if (q_heads <= 0 || kv_heads <= 0 || q_heads > 8192 || kv_heads > 8192 || q_heads % kv_heads) return false;
+  if (q_heads <= 0 || kv_heads <= 0 || q_heads > 4096 || kv_heads > 4096 || q_heads % kv_heads) return false;
   if (head_dim <= 0 || head_dim % 32 || head_dim > 256 || (dtype != OKV_F32 && dtype != OKV_BF16)) return false;
   if (row_stride < (int64_t)(q_heads + 2 * kv_heads) * head_dim || row_stride > INT32_MAX || row_stride * elem % 16) return false;
   if (t->rotary_dim < 0 || t->rotary_dim > head_dim || t->rotary_dim % 16 || (t->rotary_dim && !t->inv_freq)) return false;

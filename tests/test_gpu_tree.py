@@ -81,12 +81,24 @@ SHAPES = [  # R, T, Hq, Hkv, d, bs, kb, dtype, holes
     (2, 9, 4, 2, 160, 16, 19, "bf16", True),
     (2, 17, 16, 2, 256, 16, 19, "bf16", True),
     (1, 4, 8, 2, 128, 64, 1024, "bf16", False),    # the longest resident set
+    (2, 64, 16, 2, 256, 16, 21, "bf16", True),
+    (2, 43, 18, 3, 128, 16, 19, "bf16", True),     # 6 heads: 126 rows to a warpgroup
+    (2, 64, 5, 1, 96, 8, 50, "bf16", True),
+    (3, 64, 8, 1, 32, 16, 30, "bf16", True),
+    (2, 64, 8, 1, 64, 33, 20, "bf16", True),       # drafted tokens past a block's lines of a tile
+    (2, 60, 8, 1, 128, 48, 20, "bf16", True),
+    (1, 2, 1, 1, 160, 7, 30, "bf16", True),
+    (60, 3, 8, 8, 128, 16, 9, "bf16", True),       # whole items and split ones
+    (90, 33, 32, 4, 64, 16, 6, "bf16", True),
     (2, 12, 8, 2, 64, 16, 32, "f32", False),
     (3, 1, 2, 1, 128, 16, 21, "f32", True),
     (2, 64, 8, 1, 128, 16, 33, "f32", True),
     (2, 5, 6, 2, 96, 5, 50, "f32", True),
     (2, 9, 8, 8, 32, 64, 7, "f32", True),
     (1, 3, 16, 2, 256, 16, 40, "f32", True),
+    (2, 2, 8, 1, 64, 16, 40, "f32", True),          # 16 rows
+    (2, 5, 8, 2, 192, 33, 9, "f32", True),
+    (70, 9, 8, 8, 32, 16, 5, "f32", True),
 ]
 
 
@@ -186,6 +198,33 @@ def test_same_bits_every_time_and_from_a_graph(R, T, kb):
     g1.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, b)
+
+
+def test_calls_from_several_threads():
+    """Calls of different shapes at once from several host threads, each on a stream of its own."""
+    import threading
+    import torch
+    shapes = [(1, 8, 32, 8, 128, 16, 40), (2, 64, 16, 2, 128, 16, 20), (3, 5, 8, 2, 64, 32, 9), (2, 9, 4, 2, 256, 16, 30)]
+    xs = [make(*sh, "bf16", seed=i) for i, sh in enumerate(shapes)]
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                got = call(xs[i])
+                st.synchronize()
+                if not torch.equal(got, want[i]):
+                    wrong.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong
 
 
 def test_mask_as_uint64_and_refusals():

@@ -42,7 +42,7 @@ ROWS_OK = dict(n_rows=4, q_heads=32, kv_heads=8, head_dim=128, dtype=1, qkv=P, r
 
 
 @pytest.mark.parametrize("bad", [
-    dict(n_rows=-1), dict(q_heads=0), dict(q_heads=30), dict(kv_heads=0), dict(kv_heads=-8), dict(q_heads=16384, kv_heads=8),
+    dict(n_rows=-1), dict(q_heads=0), dict(q_heads=30), dict(kv_heads=0), dict(kv_heads=-8), dict(q_heads=16384, kv_heads=8), dict(q_heads=4104, kv_heads=8, row_stride=4120 * 128),
     dict(head_dim=0), dict(head_dim=100), dict(head_dim=288), dict(dtype=2), dict(qkv=None), dict(qkv=P + 8),
     dict(row_stride=6143), dict(row_stride=6148), dict(row_stride=1 << 40), dict(positions=None),
     dict(q=None, k=None, v=None), dict(q=P + 4), dict(k=P + 2), dict(v=P + 8),
@@ -89,7 +89,7 @@ TREE_OK = dict(n_requests=2, n_draft=8, q_heads=32, kv_heads=8, head_dim=128, bl
 @pytest.mark.parametrize("bad", [
     dict(n_requests=0), dict(n_draft=0), dict(n_draft=65), dict(q_heads=36), dict(q_heads=72), dict(kv_heads=0), dict(head_dim=48),
     dict(head_dim=320), dict(block_size=0), dict(block_size=100), dict(slots=0), dict(slots=2000), dict(dtype=-1),
-    dict(n_requests=1 << 22), dict(pool=None), dict(pool=P + 4), dict(slot_block=None), dict(lengths=None), dict(q=None), dict(q=P + 8),
+    dict(n_requests=1 << 22), dict(n_requests=1 << 26, kv_heads=1, q_heads=4, slots=1, n_draft=64), dict(pool=None), dict(pool=P + 4), dict(slot_block=None), dict(lengths=None), dict(q=None), dict(q=P + 8),
     dict(k=None), dict(k=P + 2), dict(v=None), dict(v=P + 8), dict(mask=None), dict(out=None), dict(out=P + 8),
 ], ids=str)
 def test_attend_tree_static_refuses(lib, bad):
