@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -50,6 +51,9 @@ class _Timing(ctypes.Structure):
 class _Rotary(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+_ROTARY = struct.Struct("@PPPfii0P")  # the same, packed (a bytes object passes as a pointer)
 
 
 def load_library():
@@ -504,15 +508,15 @@ class Rotary:
     """okv_rotary: inv_freq [rotary_dim / 2] float32 (None: no rotation), q_weight and k_weight [head_dim] of
     the rows' dtype (None: no norm). Keeps the tensors; read at each call."""
 
-    __slots__ = ("tensors", "_c", "_ref")
+    __slots__ = ("tensors", "_ref")
 
     def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False):
         torch = _torch or _load_torch()
-        ptr, rot = [None, None, None], 0
+        ptr, rot = [0, 0, 0], 0
         for i, t in enumerate((inv_freq, q_weight, k_weight)):
             if t is None:
                 continue
-            if t.get_device() < 0 or t.dim() != 1 or not t.is_contiguous():
+            if t.get_device() < 0 or (t.stride() != (1,) and (t.dim() != 1 or not t.is_contiguous())):
                 raise ValueError(f"{('inv_freq', 'q_weight', 'k_weight')[i]}: expected a contiguous CUDA vector")
             ptr[i] = t.data_ptr()
         if inv_freq is not None:
@@ -520,10 +524,10 @@ class Rotary:
                 raise ValueError(f"inv_freq: expected float32, got {inv_freq.dtype}")
             rot = 2 * inv_freq.numel()
         self.tensors = (inv_freq, q_weight, k_weight)
-        self._c = _Rotary(ptr[0], ptr[1], ptr[2], eps, rot, 1 if interleaved else 0)
-        self._ref = ctypes.addressof(self._c)
+        self._ref = _ROTARY.pack(ptr[0], ptr[1], ptr[2], eps, rot, 1 if interleaved else 0)
 
-    def _check(self, dtype, dev: int, head_dim: int) -> int:
+    def _check(self, dtype, dev: int, head_dim: int) -> bytes:
+        """The okv_rotary, once the tensors are seen to fit rows of this type, device and head_dim."""
         inv_freq, qw, kw = self.tensors
         if inv_freq is not None and inv_freq.get_device() != dev:
             raise ValueError(f"inv_freq: on {inv_freq.device}, the rows on cuda:{dev}")

@@ -25,7 +25,8 @@ namespace okv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;  // head rows of each subgroup in flight
+template <typename T>
+constexpr int kInFlight = 16 / (int)sizeof(T) / 2;  // head rows of each subgroup in flight: 64 bytes a lane
 
 // 8 elements of a head row.
 template <typename T>
@@ -224,6 +225,7 @@ template <typename T, int LPG, bool APPEND>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, const RowsTo R) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32, kSub = 32 / LPG;  // head rows of a warp
+  constexpr int kFly = kInFlight<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPG, sg = lane / LPG;
   float* cs = reinterpret_cast<float*>(smem) + warp * 2 * A.half;       // [warps][cos, sin][half]
   float* sn = cs + A.half;
@@ -231,52 +233,63 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
   const bool on = sub * 8 < A.d;
 
   int64_t row;
-  int32_t pos, part, r = 0, blk0 = 0;
-  bool mine;
+  int32_t pos = 0, part, r = 0, blk0 = 0, last = 0;
+  bool mine;  // a row of this warp's own (its position may still leave it out)
+  constexpr int kAhead = 4;
+  int32_t slots[kAhead];  // the first slots of the request's table that this thread looks at
+  const int32_t* sb = nullptr;
   if (APPEND) {
     r = blockIdx.x / R.ctas;
     const int32_t w0 = (blockIdx.x - r * R.ctas) * kWarps, t0 = w0 / R.parts, t = (w0 + warp) / R.parts;
     part = (w0 + warp) % R.parts;
+    sb = R.slot_block + (int64_t)r * A.Hkv * R.kb;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int32_t i = threadIdx.x + u * kThreads;
+      slots[u] = i < A.Hkv * R.kb ? sb[i] : -1;
+    }
     const int32_t cnt = R.counts ? min(max(R.counts[r], 0), R.n_new) : R.n_new, len = R.len[r];
     if (t0 >= cnt || len < 0 || len > INT32_MAX - R.n_new) return;  // positions stay within 31 bits
     mine = t < cnt;
     row = (int64_t)r * R.n_new + t;
     pos = len + t;
     blk0 = (len + t0) / R.bs;
-    const int32_t last = (len + min(cnt - 1, (w0 + kWarps - 1) / R.parts)) / R.bs;
-    for (int32_t i = threadIdx.x; i < A.Hkv * R.span; i += kThreads) slot_of[i] = INT32_MAX;
-    __syncthreads();
-    const int32_t* sb = R.slot_block + (int64_t)r * A.Hkv * R.kb;
-    for (int32_t i = threadIdx.x; i < A.Hkv * R.kb; i += kThreads) {
-      const int32_t b = sb[i];
-      if (b >= blk0 && b <= last) atomicMin(&slot_of[i / R.kb * R.span + (b - blk0)], i % R.kb);
-    }
-    __syncthreads();
+    last = (len + min(cnt - 1, (w0 + kWarps - 1) / R.parts)) / R.bs;
   } else {
     const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
     row = w / R.parts;
     part = (int32_t)(w - row * R.parts);
     mine = row < R.n_rows;
-    pos = mine ? R.positions[row] : -1;
-    mine = mine && pos >= 0;
+    if (mine) pos = R.positions[row];
   }
-  if (!mine) return;
   // The row's head rows in groups of a warp: queries, keys, values. A warp takes every `parts`-th group, a
-  // batch of loads ahead of the work on them; the first ones go out before the angles.
+  // batch of loads ahead of the work on them; the first ones go out before the slots and the angles.
   const int32_t gq = (A.Hq + kSub - 1) / kSub, gk = (A.Hkv + kSub - 1) / kSub;
   const T* from = (const T*)A.qkv + row * A.row_stride + sub * 8;
-  auto load = [&](Eight<T>(&raw)[kInFlight], int32_t g, int32_t first, int32_t heads, const T* in) {
+  auto load = [&](Eight<T>(&raw)[kFly], int32_t g, int32_t first, int32_t heads, const T* in) {
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
+    for (int u = 0; u < kFly; ++u) {
       const int32_t h = (g + u * R.parts - first) * kSub + sg;
       raw[u].zero();
       if (h < heads && on) raw[u].load(in + (int64_t)h * A.d);
     }
   };
   int32_t g = part;
-  Eight<T> raw[kInFlight];
-  bool ahead = g < gq && A.q;
+  Eight<T> raw[kFly];
+  bool ahead = mine && g < gq && A.q;
   if (ahead) load(raw, g, 0, A.Hq, from);
+  if (APPEND) {
+    for (int32_t i = threadIdx.x; i < A.Hkv * R.span; i += kThreads) slot_of[i] = INT32_MAX;
+    __syncthreads();
+    auto match = [&](int32_t i, int32_t b) {
+      if (b >= blk0 && b <= last) atomicMin(&slot_of[i / R.kb * R.span + (b - blk0)], i % R.kb);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) match(threadIdx.x + u * kThreads, slots[u]);
+    for (int32_t i = threadIdx.x + kAhead * kThreads; i < A.Hkv * R.kb; i += kThreads) match(i, sb[i]);
+    __syncthreads();
+  }
+  if (!mine || pos < 0) return;
   for (int32_t f = lane; f < A.half; f += 32) {
     const float inv = A.inv_freq[f];
     angle(turn_per_position(inv), inv, pos, &cs[f], &sn[f]);
@@ -301,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
     }
     Turn t;
     if (kind < 2) t = make_turn<T>(A, (const T*)(kind == 0 ? A.q_weight : A.k_weight), cs, sn, sub);
-    auto work = [&](Eight<T>(&raw)[kInFlight], int32_t g) {
+    auto work = [&](Eight<T>(&raw)[kFly], int32_t g) {
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
+      for (int u = 0; u < kFly; ++u) {
         if (g + u * R.parts >= end) break;
         if (kind < 2) norm_turn<LPG, T>(A, raw[u], t);
         const int32_t h = (g + u * R.parts - first) * kSub + sg;
@@ -317,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
         raw[u].store(out + at);
       }
     };
-    for (; g < end; g += kInFlight * R.parts) {
+    for (; g < end; g += kFly * R.parts) {
       if (!ahead) load(raw, g, first, heads, in);
       ahead = false;
       work(raw, g);

@@ -59,6 +59,13 @@ def test_norm_rope_refuses(lib, bad):
                              a["positions"], r, a["q"], a["k"], a["v"], a["stream"]) == 1
 
 
+def test_packed_rotary_is_the_struct():
+    from sparse_kv_cache_draft_gb300 import binding
+    c = binding._Rotary(1 << 40, 0, 7, 0.25, 64, 1)
+    assert bytes(c) == binding._ROTARY.pack(1 << 40, 0, 7, 0.25, 64, 1)
+    assert binding._ROTARY.size == ctypes.sizeof(binding._Rotary)
+
+
 def test_no_rows_is_no_work(lib):
     r = rotary()
     assert lib.okv_norm_rope(0, 32, 8, 128, 1, None, 6144, None, ctypes.addressof(r), None, None, None, None) == 0
