@@ -115,6 +115,7 @@ struct Turn {
   float2 wc[4], ws[4];
   int other;       // the lane that holds the pairs' other elements
   bool pair, norm; // this lane's dims are rotated; there is a norm
+  float per_d;     // 1 / d
 };
 
 // Every lane calls it; `cs`, `sn`: the token's tables of `half` entries.
@@ -125,6 +126,7 @@ __device__ __forceinline__ Turn make_turn(const RowArgs& A, const T* w, const fl
   const bool low = sub < step;
   t.pair = sub < 2 * step;
   t.norm = w != nullptr;
+  t.per_d = 1.f / (float)A.d;
   t.other = A.interleaved || !t.pair ? lane : low ? lane + step : lane - step;
   float c[8], s[8], a[8], b[8];
 #pragma unroll
@@ -156,35 +158,39 @@ __device__ __forceinline__ Turn make_turn(const RowArgs& A, const T* w, const fl
   return t;
 }
 
-// x' of a lane: from the lane that holds it, or the neighbour within the lane.
-__device__ __forceinline__ void others(Eight<__nv_bfloat16>& x, const Turn& t, int interleaved) {
+// x' of a lane: from the lane that holds it, or the neighbour within the lane. `some`: there are dims that
+// are not rotated, whose x' is zero (it may be infinite, and its factor is zero).
+template <bool INTER>
+__device__ __forceinline__ void others(Eight<__nv_bfloat16>& x, const Turn& t, bool some) {
   uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = interleaved ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(0xffffffffu, w[i], t.other);
-    if (!t.pair) w[i] = 0;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = INTER ? __byte_perm(w[i], 0, 0x1032) : __shfl_sync(0xffffffffu, w[i], t.other);
+  if (some && !t.pair) w[0] = w[1] = w[2] = w[3] = 0;
   x.u = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void others(Eight<float>& x, const Turn& t, int interleaved) {
+template <bool INTER>
+__device__ __forceinline__ void others(Eight<float>& x, const Turn& t, bool some) {
   float v[8];
   x.get(v);
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const float a = v[i], b = v[i + 1];
-    v[i] = interleaved ? b : __shfl_sync(0xffffffffu, a, t.other);
-    v[i + 1] = interleaved ? a : __shfl_sync(0xffffffffu, b, t.other);
-    if (!t.pair) v[i] = v[i + 1] = 0.f;
+    v[i] = INTER ? b : __shfl_sync(0xffffffffu, a, t.other);
+    v[i + 1] = INTER ? a : __shfl_sync(0xffffffffu, b, t.other);
+  }
+  if (some && !t.pair) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
   }
   x.set(v);
 }
 
 // Norm and rotation of a head row held by the LPG lanes of a subgroup (zeros in lanes past d). Every lane of
 // the warp calls it.
-template <int LPG, typename T>
+template <int LPG, bool INTER, typename T>
 __device__ __forceinline__ void norm_turn(const RowArgs& A, Eight<T>& raw, const Turn& t) {
   Eight<T> mate = raw;
-  others(mate, t, A.interleaved);
+  others<INTER>(mate, t, 2 * A.half != A.d);
   float x[8], y[8];
   raw.get(x);
   mate.get(y);
@@ -196,7 +202,7 @@ __device__ __forceinline__ void norm_turn(const RowArgs& A, Eight<T>& raw, const
     float ss = s2.x + s2.y;
 #pragma unroll
     for (int off = LPG / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    r.x = r.y = rsqrtf(fmaf(ss, 1.f / (float)A.d, A.eps));
+    r.x = r.y = rsqrtf(fmaf(ss, t.per_d, A.eps));
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -221,7 +227,7 @@ struct RowsTo {
   void* pool;                  // [R][Hkv][kb][2][bs][d]
 };
 
-template <typename T, int LPG, bool APPEND>
+template <typename T, int LPG, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, const RowsTo R) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32, kSub = 32 / LPG;  // head rows of a warp
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
     for (int u = 0; u < kFly; ++u) {
       const int32_t h = (g + u * R.parts - first) * kSub + sg;
       raw[u].zero();
-      if (h < heads && on) raw[u].load(in + (int64_t)h * A.d);
+      if (h < heads && on) raw[u].load(in + h * A.d);
     }
   };
   int32_t g = part;
@@ -314,18 +320,20 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
     }
     Turn t;
     if (kind < 2) t = make_turn<T>(A, (const T*)(kind == 0 ? A.q_weight : A.k_weight), cs, sn, sub);
+    const int32_t* slot_at = APPEND ? slot_of + (pos / R.bs - blk0) : nullptr;
+    const int32_t slot_size = APPEND ? 2 * R.bs * A.d : 0;  // elements
     auto work = [&](Eight<T>(&raw)[kFly], int32_t g) {
 #pragma unroll
       for (int u = 0; u < kFly; ++u) {
         if (g + u * R.parts >= end) break;
-        if (kind < 2) norm_turn<LPG, T>(A, raw[u], t);
+        if (kind < 2) norm_turn<LPG, INTER, T>(A, raw[u], t);
         const int32_t h = (g + u * R.parts - first) * kSub + sg;
         if (h >= heads || !on) continue;
-        int64_t at = (int64_t)h * A.d;
+        int64_t at = h * A.d;  // elements of a row: at most 4096 * 256
         if (APPEND && kind > 0) {
-          const int32_t slot = slot_of[h * R.span + (pos / R.bs - blk0)];
+          const int32_t slot = slot_at[h * R.span];
           if (slot == INT32_MAX) continue;
-          at = ((int64_t)h * R.kb + slot) * 2 * R.bs * A.d;
+          at = (int64_t)(h * R.kb + slot) * slot_size;
         }
         raw[u].store(out + at);
       }
@@ -368,10 +376,15 @@ cudaError_t run_rows(const RowArgs& A, RowsTo R, cudaStream_t s) {
     kernel<<<(unsigned)ctas, kThreads, smem, s>>>(A, R);
     return cudaGetLastError();
   };
-  return lpg == 4    ? go(rows_kernel<T, 4, APPEND>)
-         : lpg == 8  ? go(rows_kernel<T, 8, APPEND>)
-         : lpg == 16 ? go(rows_kernel<T, 16, APPEND>)
-                     : go(rows_kernel<T, 32, APPEND>);
+  if (A.interleaved)
+    return lpg == 4    ? go(rows_kernel<T, 4, APPEND, true>)
+           : lpg == 8  ? go(rows_kernel<T, 8, APPEND, true>)
+           : lpg == 16 ? go(rows_kernel<T, 16, APPEND, true>)
+                       : go(rows_kernel<T, 32, APPEND, true>);
+  return lpg == 4    ? go(rows_kernel<T, 4, APPEND, false>)
+         : lpg == 8  ? go(rows_kernel<T, 8, APPEND, false>)
+         : lpg == 16 ? go(rows_kernel<T, 16, APPEND, false>)
+                     : go(rows_kernel<T, 32, APPEND, false>);
 }
 
 // ---- a context's append ----------------------------------------------------------------------------
@@ -474,7 +487,12 @@ __global__ void __launch_bounds__(kThreads) append_qkv_kernel(const RowArgs A, c
       Eight<T> raw;
       raw.zero();
       if (h < heads && on) raw.load(in + (int64_t)h * A.d + sub * 8);
-      if (kind < 2) norm_turn<LPG, T>(A, raw, t);
+      if (kind < 2) {
+        if (A.interleaved)
+          norm_turn<LPG, true, T>(A, raw, t);
+        else
+          norm_turn<LPG, false, T>(A, raw, t);
+      }
       if (h >= heads || !on) continue;
       if (kind == 0)
         raw.store((T*)A.q + ((int64_t)r * A.Hq + h) * A.d + sub * 8);

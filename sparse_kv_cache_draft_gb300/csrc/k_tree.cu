@@ -743,7 +743,8 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
     };
     // Two warpgroups take turns at the tensor cores, O of a tile and S of the next at a time: while one has
     // them, the other is at its softmax. Left to themselves they end up side by side, waiting for each other
-    // at both (measured at 64 tokens x 32 requests: 153 us against 1xx).
+    // at both (64 tokens x 32 requests, 64 / 8 heads, d 128, 2048 tokens of context: 153 us
+    // against 144).
     int32_t turns = 0;
     auto my_turn = [&] { return NW == 1 || (w == 0 && turns == 0) || warp_wait(B.turn[w], (turns - (w == 0)) & 1); };
     auto pass_on = [&] {
