@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
     angle(turn_per_position(inv), inv, pos, &cs[f], &sn[f]);
   }
   __syncwarp();
+#pragma unroll
   for (int kind = 0; kind < 3; ++kind) {
     const int32_t heads = kind == 0 ? A.Hq : A.Hkv, first = kind == 0 ? 0 : kind == 1 ? gq : gq + gk, end = kind == 0 ? gq : first + gk;
     if (g >= end) continue;
