@@ -214,6 +214,43 @@ def test_append_takes_the_lowest_of_equal_slots():
     assert torch.equal(pool, want)
 
 
+def test_rows_and_pool_past_31_bits():
+    """The last rows of more than 2^31 elements, and the last request of a pool as large."""
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, append_qkv_static, norm_rope
+    gen = torch.Generator().manual_seed(8)
+    Hq, H, d = 32, 8, 128
+    n = (1 << 31) // (48 * d) + 3
+    rope = make_rotary(d, d, torch.bfloat16, gen, True, False)
+    qkv = torch.zeros(n, 48 * d, dtype=torch.bfloat16, device="cuda")
+    qkv[-5:] = torch.randn(5, 48 * d, generator=gen).to(torch.bfloat16).cuda()
+    pos = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    pos[-5:] = torch.arange(5, dtype=torch.int32, device="cuda")
+    k = torch.empty(n, H, d, dtype=torch.bfloat16, device="cuda")
+    norm_rope(qkv, pos, None, k, None, q_heads=Hq, kv_heads=H, head_dim=d, rotary=Rotary(**rope))
+    _, wk, _, _, bk = tree_ref.rows(qkv[-5:], pos[-5:], Hq, H, d, **rope)
+    near(k[-5:], wk, bk, "k")
+    rows = qkv[-5:].clone()
+    del qkv, k
+    R, bs, kb = 70, 16, 1024
+    pool = torch.zeros(R, H, kb, 2, bs, d, dtype=torch.bfloat16, device="cuda")
+    assert pool.numel() > 1 << 31
+    sb = torch.full((R, H, kb), -1, dtype=torch.int32, device="cuda")
+    sb[-1, :, -1] = 3
+    counts = torch.zeros(R, dtype=torch.int32, device="cuda")
+    counts[-1] = 5
+    lengths = torch.full((R,), 50, dtype=torch.int32, device="cuda")
+    x = torch.zeros(R, 5, 48 * d, dtype=torch.bfloat16, device="cuda")
+    x[-1] = rows
+    append_qkv_static(x, lengths, counts, pool, sb, None, q_heads=Hq, kv_heads=H, head_dim=d, block_size=bs, slots=kb,
+                      rotary=Rotary(**rope))
+    _, wk, wv, _, bk = tree_ref.rows(rows, 50 + torch.arange(5, device="cuda"), Hq, H, d, **rope)
+    near(pool[-1, :, -1, 0, 2:7].transpose(0, 1), wk, bk, "key")
+    assert torch.equal(pool[-1, :, -1, 1, 2:7].transpose(0, 1).double(), wv)
+    pool[-1, :, -1, :, 2:7] = 0
+    assert not bool(pool.any())
+
+
 def test_rows_from_a_graph_and_another_stream():
     import torch
     from sparse_kv_cache_draft_gb300 import Rotary, norm_rope

@@ -90,6 +90,10 @@ SHAPES = [  # R, T, Hq, Hkv, d, bs, kb, dtype, holes
     (1, 2, 1, 1, 160, 7, 30, "bf16", True),
     (60, 3, 8, 8, 128, 16, 9, "bf16", True),       # whole items and split ones
     (90, 33, 32, 4, 64, 16, 6, "bf16", True),
+    (1, 1, 1, 1, 32, 1, 1, "bf16", False),         # the smallest
+    (1, 64, 8, 1, 128, 64, 1024, "bf16", True),    # the longest tables beside the largest tiles
+    (1, 20, 8, 1, 256, 64, 1024, "bf16", True),
+    (1, 9, 8, 1, 64, 1, 1024, "bf16", True),
     (2, 12, 8, 2, 64, 16, 32, "f32", False),
     (3, 1, 2, 1, 128, 16, 21, "f32", True),
     (2, 64, 8, 1, 128, 16, 33, "f32", True),
@@ -99,6 +103,8 @@ SHAPES = [  # R, T, Hq, Hkv, d, bs, kb, dtype, holes
     (2, 2, 8, 1, 64, 16, 40, "f32", True),          # 16 rows
     (2, 5, 8, 2, 192, 33, 9, "f32", True),
     (70, 9, 8, 8, 32, 16, 5, "f32", True),
+    (1, 1, 1, 1, 32, 1, 1, "f32", False),
+    (1, 3, 8, 1, 256, 64, 1024, "f32", True),
 ]
 
 
@@ -198,6 +204,23 @@ def test_same_bits_every_time_and_from_a_graph(R, T, kb):
     g1.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pool_past_31_bits(dtype):
+    """The last request of a pool of more than 2^31 elements."""
+    import torch
+    R, T, Hq, H, d, bs, kb = 70, 3, 8, 8, 128, 16, 1024
+    x = make(1, T, Hq, H, d, bs, kb, dtype, seed=23, lengths=[kb * bs - 5], stale=0.0)
+    assert R * x["pool"].numel() > 2 ** 31
+    y = dict(counts=torch.zeros(R, dtype=torch.int32, device="cuda"))
+    y["counts"][-1] = T
+    for n in ("pool", "slot_block", "lengths", "q", "k", "v", "mask"):
+        y[n] = torch.zeros((R,) + x[n].shape[1:], dtype=x[n].dtype, device="cuda")
+        y[n][-1] = x[n][0]
+    out = call(y)
+    assert bool((out[:-1] == -7.0).all())
+    check(x, out[-1:])
 
 
 def test_calls_from_several_threads():
