@@ -1029,26 +1029,97 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   }
 }
 
-// The shape of least time by a count of tile times: an item takes its tiles and `fixed` more, and `join` more
-// where its CTAs merge; `slots` CTAs run at once, of clusters an eighth fewer (a cluster stays within a GPC,
-// whose SMs it seldom fills). Items that fill the GPU go whole, the last ones split.
-Shape pick_shape(int64_t items, int32_t groups, int64_t slots, int32_t tiles, double fixed, double join) {
-  Shape best{1, (int32_t)items, groups};
-  double least = 1e30;
-  for (int32_t c = 1; c <= kMaxSplit && c <= tiles; ++c) {
-    const int64_t room = c == 1 ? slots : slots * 7 / 8;
-    const int64_t whole = c == 1 ? items : items / slots * slots / c * c, rest = items - whole;
-    const double t = (double)((whole + slots - 1) / slots) * (tiles + fixed) +
-                     (double)((rest * c + room - 1) / room) * ((double)tiles / c + fixed + join);
-    if (t < least) least = t, best = Shape{c, (int32_t)whole, groups};
-  }
-  return best;
-}
-
 int sm_count() {
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return sms;
+}
+
+cudaLaunchConfig_t cluster_config(int64_t ctas, int threads, size_t smem, int32_t split, cudaStream_t s, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = split;
+  at->val.clusterDim.y = 1;
+  at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cfg;
+}
+
+// CTAs of clusters of c that run at once, for c = 2 .. 8: a property of the kernel and the device (a cluster
+// stays within a GPC), asked for once per thread.
+struct ClusterRoom {
+  const void* kernel;
+  size_t smem;
+  int dev;
+  int64_t ctas[kMaxSplit + 1];
+};
+template <typename... P>
+const ClusterRoom& cluster_room(void (*kernel)(P...), int threads, size_t smem) {
+  constexpr int kKept = 32;
+  static thread_local ClusterRoom kept[kKept];
+  static thread_local int used = 0, oldest = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  for (int i = 0; i < used; ++i)
+    if (kept[i].kernel == (const void*)kernel && kept[i].smem == smem && kept[i].dev == dev) return kept[i];
+  ClusterRoom& r = used < kKept ? kept[used++] : kept[oldest++ % kKept];
+  r.kernel = (const void*)kernel;
+  r.smem = smem;
+  r.dev = dev;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  for (int32_t c = 2; c <= kMaxSplit; ++c) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = cluster_config(c, threads, smem, c, nullptr, &at);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    r.ctas[c] = (int64_t)n * c;
+  }
+  return r;
+}
+
+// A kernel that allocates tensor memory counts as one CTA per SM whatever it allocates; this one, which nothing
+// launches, as many as threads and shared memory let in.
+__global__ void room_of_smem_kernel() {}
+
+// What a launch costs, in tile times of a CTA alone on its SM: an item takes its tiles, `fixed` more, and `join`
+// more where its CTAs merge; beyond `dense` CTAs per SM more of them finish no more tiles in a time. From launches of
+// every split: bf16, d 128, 2048 tokens, 16 rows x 4: 0.76 us a tile of 64, and 152 tiles in that time is HBM's rate;
+// 512 rows: 2.1 us a tile of 128; binary32, 64 rows: 5.3 us a tile, two CTAs on an SM hide each other's waits.
+struct Costs {
+  double fixed, join, dense;
+};
+constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1}, kF32Costs{2.3, 0.5, 1.3};
+
+double wave_cost(int64_t ctas, double tiles, const Costs& t, int64_t sms) {
+  const double crowd = (double)ctas / ((double)sms * t.dense);
+  return tiles * (crowd > 1 ? crowd : 1) + t.fixed;
+}
+
+// The shape of least cost, of equal ones the one with more CTAs. Items that fill the GPU go whole and the last ones
+// split, in pairs: a larger cluster waits behind whole items until all of its CTAs find a place (48 requests of 16
+// tokens: 74.4 us in pairs, 79.6 whole or in threes; 12 requests: 22.2 us in threes, 26.6 in pairs, 30.7 whole).
+Shape pick_shape(int64_t items, int32_t groups, int32_t per_sm, int32_t tiles, const Costs& t, const ClusterRoom& room) {
+  const int64_t sms = sm_count(), slots = sms * per_sm;
+  const double full = wave_cost(slots, tiles, t, sms);
+  Shape best{1, (int32_t)items, groups};
+  double least = (double)(items / slots) * full + (items % slots ? wave_cost(items % slots, tiles, t, sms) : 0);
+  for (int32_t c = 2; c <= kMaxSplit && c <= tiles; ++c) {
+    const int64_t whole = items / slots * slots / c * c, n = (items - whole) * c, r = room.ctas[c];
+    if (!r || !n || (whole && c > 2)) continue;
+    const double part = (double)tiles / c;
+    const double cost = (double)(whole / slots) * full + (double)(n / r) * (wave_cost(r, part, t, sms) + t.join) +
+                        (n % r ? wave_cost(n % r, part, t, sms) + t.join : 0);
+    if (cost < least + 1e-6) least = cost, best = Shape{c, (int32_t)whole, groups};
+  }
+  return best;
 }
 
 template <typename... P, typename... Q>
@@ -1056,18 +1127,8 @@ cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& sha
   // the limit is the same for every launch: another thread's may come between this and the launch
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(shape.whole + (items - shape.whole) * shape.split));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = shape.split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = shape.split > 1 ? 1 : 0;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = cluster_config(shape.whole + (items - shape.whole) * shape.split, threads, smem, shape.split, s, &at);
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
@@ -1076,10 +1137,11 @@ cudaError_t run_f32(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t spt = kTile / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
   const int32_t groups = (A.T * A.G.g + 16 * RG - 1) / (16 * RG);
   const size_t smem = f32_smem(DV * 32, RG, A.G.kb, tiles);
-  int64_t per_sm = (int64_t)(228 * 1024) / (int64_t)(smem + 1024);
+  int32_t per_sm = (int32_t)(228 * 1024 / (smem + 1024));
   if (per_sm > f32_ctas(DV)) per_sm = f32_ctas(DV);
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
-  const Shape shape = pick_shape(items, groups, sm_count() * (per_sm < 1 ? 1 : per_sm), tiles, 3, 2);
+  const ClusterRoom& room = cluster_room(tree_f32_kernel<DV, RG>, kF32Threads, smem);
+  const Shape shape = pick_shape(items, groups, per_sm < 1 ? 1 : per_sm, tiles, kF32Costs, room);
   return launch_cluster(tree_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape);
 }
 
@@ -1157,7 +1219,8 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const size_t least = (two ? 233472 / 3 : 233472 / 2);
   if (smem < least) smem = least;
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
-  const Shape shape = pick_shape(items, groups, (int64_t)sm_count() * (two ? 2 : 1), tiles, 3, 2);
+  const ClusterRoom& room = cluster_room(room_of_smem_kernel, NW * 160 + 32, smem);
+  const Shape shape = pick_shape(items, groups, two ? 2 : 1, tiles, NW == 1 ? kMmaCosts : kMmaCostsWide, room);
   MmaMaps maps;
   if (cudaError_t e = make_maps<D, NW>(A, spt, q_tok, &maps)) return e;
   return launch_cluster(tree_mma_kernel<D, NW>, items, shape, NW * 160 + 32, smem, s, A, maps, shape, ring, q_tok, q_rows);

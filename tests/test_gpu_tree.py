@@ -206,6 +206,18 @@ def test_same_bits_every_time_and_from_a_graph(R, T, kb):
     assert torch.equal(out, b)
 
 
+def test_first_call_of_a_shape_in_a_capture():
+    import torch
+    x = make(3, 11, 10, 2, 128, 16, 27, "bf16", seed=19)
+    out = torch.full_like(x["q"], -7.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(x, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    check(x, out)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_pool_past_31_bits(dtype):
     """The last request of a pool of more than 2^31 elements."""
