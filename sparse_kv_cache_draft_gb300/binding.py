@@ -1,4 +1,5 @@
-"""ctypes binding of libokv.so: the C ABI of include/okv.h with the same names.
+"""ctypes binding of libokv.so: the C ABI of include/okv.h with the same names. The calls on rows and drafted
+trees that need no context are a compiled module of their own (csrc/py_calls.cpp), reached through here.
 
 Argument marshalling only: tensors become device pointers, streams become cudaStream_t
 handles, host arrays become numpy views. Every step of the path runs in the library's CUDA
@@ -9,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 from dataclasses import dataclass
 
@@ -51,9 +51,6 @@ class _Timing(ctypes.Structure):
 class _Rotary(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
-
-
-_ROTARY = struct.Struct("@PPPfii0P")  # the same, packed (a bytes object passes as a pointer)
 
 
 def load_library():
@@ -219,6 +216,13 @@ class Context:
             raise ValueError(f"{what}: expected contiguous {want} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
         return ctypes.c_void_p(t.data_ptr())
 
+    @staticmethod
+    def _int_ptr(t, shape, dtypes, like, what: str) -> int:
+        if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != like.device:
+            raise ValueError(f"{what}: expected contiguous {' or '.join(str(d) for d in dtypes)} {shape} on {like.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
     @property
     def _qshape(self):
         c = self.cfg
@@ -290,27 +294,29 @@ class Context:
     def append_qkv(self, layer: int, qkv, q, rotary: "Rotary", stream=None):
         """One token per active request from its projection row: qkv [R][(Hq + 2 Hkv) d] (rows may be
         strided) -> q [R][Hq][d], the key and value appended."""
+        import torch
         c = self.cfg
-        dt, _ = _storage(qkv, "qkv")
-        if dt != c.dtype or qkv.dim() != 2 or qkv.shape[0] != c.max_requests:
-            raise ValueError(f"qkv: expected [{c.max_requests}][{(c.q_heads + 2 * c.kv_heads) * c.head_dim}] of the "
-                             f"context's dtype, got {qkv.dtype} {tuple(qkv.shape)}")
-        stride = _row_stride(qkv, (c.q_heads + 2 * c.kv_heads) * c.head_dim)
-        self._check(self.L.okv_append_qkv(self.h, layer, qkv.data_ptr(), stride, rotary._check(qkv.dtype, qkv.get_device(), c.head_dim),
+        width, want = (c.q_heads + 2 * c.kv_heads) * c.head_dim, torch.float32 if c.dtype == F32 else torch.bfloat16
+        if not qkv.is_cuda:
+            raise TypeError("qkv: expected a CUDA tensor")
+        if qkv.dtype != want or qkv.dim() != 2 or qkv.shape[0] != c.max_requests:
+            raise ValueError(f"qkv: expected {want} [{c.max_requests}][{width}], got {qkv.dtype} {tuple(qkv.shape)}")
+        self._check(self.L.okv_append_qkv(self.h, layer, qkv.data_ptr(), _load_calls()._row_stride(qkv, width),
+                                          rotary._check(qkv, c.head_dim),
                                           self._tensor_ptr(q, self._qshape, "q"), _stream_handle(stream)),
                     "okv_append_qkv")
 
     def attend_tree(self, layer: int, q, k, v, mask, out, counts=None, stream=None):
         """Drafted tokens' attention: q, out [R][T][Hq][d], k, v [R][T][Hkv][d], mask [R][T] int64 or uint64
         (bit j: drafted token j is attended), counts [R] int32 or None."""
+        import torch
         c = self.cfg
         T = q.shape[1] if q.dim() == 4 else 0
-        _, dev = _storage(q, "q")
         qs, ks = (c.max_requests, T, c.q_heads, c.head_dim), (c.max_requests, T, c.kv_heads, c.head_dim)
         self._check(self.L.okv_attend_tree(self.h, layer, T,
-                                           _ptr(counts, "counts", (c.max_requests,), _I32, dev) if counts is not None else None,
-                                           self._tensor_ptr(q, qs, "q"), self._tensor_ptr(k, ks, "k"),
-                                           self._tensor_ptr(v, ks, "v"), _ptr(mask, "mask", (c.max_requests, T), _I64, dev),
+                                           self._int_ptr(counts, (c.max_requests,), (torch.int32,), q, "counts") if counts is not None else None,
+                                           self._tensor_ptr(q, qs, "q"), self._tensor_ptr(k, ks, "k"), self._tensor_ptr(v, ks, "v"),
+                                           self._int_ptr(mask, (c.max_requests, T), (torch.int64, torch.uint64), q, "mask"),
                                            self._tensor_ptr(out, qs, "out"), _stream_handle(stream)),
                     "okv_attend_tree")
 
@@ -443,164 +449,30 @@ def attend_static(pool, slot_block, lengths, q, out, *, q_heads: int, kv_heads: 
         raise OkvError(st, "okv_attend_static failed (shape or size outside its limits, or a CUDA error)")
 
 
-# ---- rows, append and drafted trees without a context ------------------------------------------------
+# ---- rows, append and drafted trees ------------------------------------------------------------------
 #
-# A small call's time is the host's, so the checks here are few and flat: a tensor's shape, type, device
-# and contiguity once each, pointers as plain integers.
+# The calls without a context (csrc/py_calls.cpp) need torch, so their module is loaded when one of them is
+# first asked for.
 
-_torch = None      # the module, _DTYPE_OF and the index types once a call has needed them
-_DTYPE_OF = {}
-_I32 = _I64 = ()
+_CALLS = ("Rotary", "norm_rope", "append_qkv_static", "attend_tree_static", "_row_stride")
 
 
-def _load_torch():
-    global _torch, _I32, _I64
+def _load_calls():
     import torch
-    _DTYPE_OF.update({torch.float32: F32, torch.bfloat16: BF16})
-    _I32, _I64 = (torch.int32,), (torch.int64, torch.uint64)
-    _torch = torch
     load_library()
-    return torch
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise ImportError(f"_calls.so cannot be loaded ({e}): build it with `python -m sparse_kv_cache_draft_gb300.build`") from e
+    if _calls.built_for != torch.__version__.split("+")[0]:
+        raise ImportError(f"_calls.so was built for torch {_calls.built_for}, this is {torch.__version__}: build it again with "
+                          "`python -m sparse_kv_cache_draft_gb300.build`")
+    return _calls
 
 
-def _storage(t, name: str):
-    """(okv dtype, device index) of a CUDA tensor of a storage dtype."""
-    _torch or _load_torch()
-    dev = t.get_device()
-    if dev < 0:
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    dt = _DTYPE_OF.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return dt, dev
-
-
-def _ptr(t, name: str, shape, dtypes, dev: int) -> int:
-    """The address of a contiguous tensor of this shape and one of these types on device `dev`."""
-    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on cuda:{dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _row_stride(t, width: int) -> int:
-    """Elements between the rows of t [...][width], whose leading dims are one run of rows."""
-    shape = t.shape
-    if shape[-1] == width and t.is_contiguous():
-        return width
-    stride = t.stride()
-    if shape[-1] != width or (stride[-1] != 1 and width > 1):
-        raise ValueError(f"qkv: expected rows of {width} adjacent elements, got shape {tuple(shape)} strides {stride}")
-    step = None  # between rows, of the dims seen so far from the last one
-    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
-        if n == 1:
-            continue
-        if step is None:
-            step, run = s, s * n
-        elif s != run:
-            raise ValueError(f"qkv: rows are not at one distance: shape {tuple(shape)} strides {stride}")
-        else:
-            run *= n
-    return width if step is None else step
-
-
-class Rotary:
-    """okv_rotary: inv_freq [rotary_dim / 2] float32 (None: no rotation), q_weight and k_weight [head_dim] of
-    the rows' dtype (None: no norm). Keeps the tensors; read at each call."""
-
-    __slots__ = ("tensors", "_ref")
-
-    def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False):
-        torch = _torch or _load_torch()
-        ptr, rot = [0, 0, 0], 0
-        for i, t in enumerate((inv_freq, q_weight, k_weight)):
-            if t is None:
-                continue
-            if t.get_device() < 0 or (t.stride() != (1,) and (t.dim() != 1 or not t.is_contiguous())):
-                raise ValueError(f"{('inv_freq', 'q_weight', 'k_weight')[i]}: expected a contiguous CUDA vector")
-            ptr[i] = t.data_ptr()
-        if inv_freq is not None:
-            if inv_freq.dtype != torch.float32:
-                raise ValueError(f"inv_freq: expected float32, got {inv_freq.dtype}")
-            rot = 2 * inv_freq.numel()
-        self.tensors = (inv_freq, q_weight, k_weight)
-        self._ref = _ROTARY.pack(ptr[0], ptr[1], ptr[2], eps, rot, 1 if interleaved else 0)
-
-    def _check(self, dtype, dev: int, head_dim: int) -> bytes:
-        """The okv_rotary, once the tensors are seen to fit rows of this type, device and head_dim."""
-        inv_freq, qw, kw = self.tensors
-        if inv_freq is not None and inv_freq.get_device() != dev:
-            raise ValueError(f"inv_freq: on {inv_freq.device}, the rows on cuda:{dev}")
-        for w in (qw, kw):
-            if w is not None and (w.dtype != dtype or w.get_device() != dev or w.numel() != head_dim):
-                raise ValueError(f"weights: expected {dtype} [{head_dim}] on cuda:{dev}, got {w.dtype} {tuple(w.shape)} on {w.device}")
-        return self._ref
-
-
-def _current(dev: int, stream):
-    """The handle of `stream`, or of device `dev`'s current stream."""
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _call(fn, dev: int, stream, *args) -> None:
-    """A context-free call with device `dev` current and its stream as the last argument."""
-    if _torch._C._cuda_getDevice() == dev:
-        st = fn(*args, _current(dev, stream))
-    else:
-        with _torch.cuda.device(dev):
-            st = fn(*args, _current(dev, stream))
-    if st != OK:
-        raise OkvError(st, f"{fn.__name__} failed (shape, alignment or size outside its limits, or a CUDA error)")
-
-
-def norm_rope(qkv, positions, q=None, k=None, v=None, *, q_heads: int, kv_heads: int, head_dim: int, rotary: Rotary,
-              stream=None) -> None:
-    """okv_norm_rope: norms and rotates rows qkv [n][(q_heads + 2 kv_heads) head_dim] (rows may be strided) at
-    positions [n] int32 into q [n][q_heads][head_dim], k and v [n][kv_heads][head_dim] (any may be None).
-    Rows with a negative position are not written."""
-    dt, dev = _storage(qkv, "qkv")
-    if qkv.dim() != 2:
-        raise ValueError(f"qkv: expected rows [n][...], got {tuple(qkv.shape)}")
-    n, dtype = qkv.shape[0], qkv.dtype
-    st, kv = (dtype,), (n, kv_heads, head_dim)
-    _call(_lib.okv_norm_rope, dev, stream, n, q_heads, kv_heads, head_dim, dt, qkv.data_ptr(),
-          _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim), _ptr(positions, "positions", (n,), _I32, dev),
-          rotary._check(dtype, dev, head_dim),
-          _ptr(q, "q", (n, q_heads, head_dim), st, dev) if q is not None else None,
-          _ptr(k, "k", kv, st, dev) if k is not None else None, _ptr(v, "v", kv, st, dev) if v is not None else None)
-
-
-def append_qkv_static(qkv, lengths, counts, pool, slot_block, q=None, *, q_heads: int, kv_heads: int, head_dim: int,
-                      block_size: int, slots: int, rotary: Rotary, stream=None) -> None:
-    """okv_append_qkv_static: rows qkv [R][T][(q_heads + 2 kv_heads) head_dim] at positions lengths[r] + t, normed
-    and rotated; queries into q [R][T][q_heads][head_dim] (or None), keys and values into the resident slots of
-    pool [R][kv_heads][slots][2][block_size][head_dim]; counts [R] int32 or None."""
-    dt, dev = _storage(qkv, "qkv")
-    if qkv.dim() != 3:
-        raise ValueError(f"qkv: expected rows [R][T][...], got {tuple(qkv.shape)}")
-    R, T, dtype = qkv.shape[0], qkv.shape[1], qkv.dtype
-    st = (dtype,)
-    _call(_lib.okv_append_qkv_static, dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt, qkv.data_ptr(),
-          _row_stride(qkv, (q_heads + 2 * kv_heads) * head_dim), _ptr(lengths, "lengths", (R,), _I32, dev),
-          _ptr(counts, "counts", (R,), _I32, dev) if counts is not None else None, rotary._check(dtype, dev, head_dim),
-          _ptr(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev),
-          _ptr(slot_block, "slot_block", (R, kv_heads, slots), _I32, dev),
-          _ptr(q, "q", (R, T, q_heads, head_dim), st, dev) if q is not None else None)
-
-
-def attend_tree_static(pool, slot_block, lengths, counts, q, k, v, mask, out, *, q_heads: int, kv_heads: int,
-                       head_dim: int, block_size: int, slots: int, stream=None) -> None:
-    """okv_attend_tree_static: drafted tokens q, out [R][T][q_heads][head_dim], k, v [R][T][kv_heads][head_dim], mask
-    [R][T] int64 or uint64 (bit j: drafted token j is attended), counts [R] int32 or None, over a pool of
-    attend_static's layout."""
-    dt, dev = _storage(pool, "pool")
-    R, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (0, 0)
-    st, qs, ks = (pool.dtype,), (R, T, q_heads, head_dim), (R, T, kv_heads, head_dim)
-    _call(_lib.okv_attend_tree_static, dev, stream, R, T, q_heads, kv_heads, head_dim, block_size, slots, dt,
-          _ptr(pool, "pool", (R, kv_heads, slots, 2, block_size, head_dim), st, dev),
-          _ptr(slot_block, "slot_block", (R, kv_heads, slots), _I32, dev), _ptr(lengths, "lengths", (R,), _I32, dev),
-          _ptr(counts, "counts", (R,), _I32, dev) if counts is not None else None, _ptr(q, "q", qs, st, dev),
-          _ptr(k, "k", ks, st, dev), _ptr(v, "v", ks, st, dev), _ptr(mask, "mask", (R, T), _I64, dev),
-          _ptr(out, "out", qs, st, dev))
+def __getattr__(name: str):
+    if name not in _CALLS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = getattr(_load_calls(), name)
+    globals()[name] = value
+    return value

@@ -282,6 +282,72 @@ def test_rows_from_a_graph_and_another_stream():
     assert all(torch.equal(p, q) for p, q in zip(b, out))
 
 
+def test_rotary_follows_its_tensors():
+    """A parameter whose memory is replaced after the Rotary was made is read where it is at the call."""
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, norm_rope
+    gen = torch.Generator().manual_seed(8)
+    n, Hq, H, d = 5, 4, 2, 64
+    rope = make_rotary(d, d, torch.bfloat16, gen, True, False)
+    other = make_rotary(d, d, torch.bfloat16, gen, True, False)
+    x = torch.randn(n, (Hq + 2 * H) * d, generator=gen).to(torch.bfloat16).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    out = [[torch.zeros(n, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, H, H)] for _ in range(2)]
+    kw = dict(q_heads=Hq, kv_heads=H, head_dim=d)
+    rot = Rotary(**rope)
+    norm_rope(x, pos, *out[0], rotary=Rotary(**other), **kw)
+    for name in ("inv_freq", "q_weight", "k_weight"):
+        if torch.is_tensor(rope[name]):
+            rope[name].data = other[name].clone()
+    norm_rope(x, pos, *out[1], rotary=rot, **kw)
+    assert all(torch.equal(p, q) for p, q in zip(*out))
+    rope["q_weight"].data = torch.ones(d + 16, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="q_weight"):
+        norm_rope(x, pos, *out[1], rotary=rot, **kw)
+
+
+def test_a_stream_is_an_object_or_its_handle():
+    import threading
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, norm_rope
+    gen = torch.Generator().manual_seed(9)
+    n, Hq, H, d = 9, 4, 2, 64
+    rope = make_rotary(d, d, torch.bfloat16, gen, True, False)
+    x = torch.randn(n, (Hq + 2 * H) * d, generator=gen).to(torch.bfloat16).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    kw = dict(q_heads=Hq, kv_heads=H, head_dim=d, rotary=Rotary(**rope))
+    want = [torch.zeros(n, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, H, H)]
+    norm_rope(x, pos, *want, **kw)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for given in (st, st.cuda_stream, 0, None):
+        out = [torch.zeros_like(w) for w in want]
+        torch.cuda.synchronize()
+        norm_rope(x, pos, *out, stream=given, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, out)), given
+    with torch.cuda.stream(st):
+        out = [torch.zeros_like(w) for w in want]
+        norm_rope(x, pos, *out, **kw)
+    st.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, out))
+    for bad in ("0", 1.5):
+        with pytest.raises(AttributeError):
+            norm_rope(x, pos, *out, stream=bad, **kw)
+    same = []
+
+    def work():
+        mine = [torch.zeros_like(w) for w in want]
+        for _ in range(200):
+            norm_rope(x, pos, *mine, **kw)
+        torch.cuda.synchronize()
+        same.append(all(torch.equal(p, q) for p, q in zip(want, mine)))
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert same == [True] * 4
+
+
 def test_binding_refusals():
     import torch
     from sparse_kv_cache_draft_gb300 import OkvError, Rotary, norm_rope

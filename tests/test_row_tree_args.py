@@ -59,11 +59,56 @@ def test_norm_rope_refuses(lib, bad):
                              a["positions"], r, a["q"], a["k"], a["v"], a["stream"]) == 1
 
 
-def test_packed_rotary_is_the_struct():
-    from sparse_kv_cache_draft_gb300 import binding
-    c = binding._Rotary(1 << 40, 0, 7, 0.25, 64, 1)
-    assert bytes(c) == binding._ROTARY.pack(1 << 40, 0, 7, 0.25, 64, 1)
-    assert binding._ROTARY.size == ctypes.sizeof(binding._Rotary)
+def test_rotary_is_the_struct(lib):
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, binding
+    x = torch.zeros(1, 8)
+    assert Rotary()._check(x, 8) == bytes(binding._Rotary(0, 0, 0, 1e-6, 0, 0))
+    assert Rotary(None, None, None, 0.25, True)._check(x, 8) == bytes(binding._Rotary(0, 0, 0, 0.25, 0, 1))
+    assert Rotary(interleaved=1, eps=2).tensors == (None, None, None)
+
+
+def test_calls_refuse_on_the_host(lib):
+    """What a call's arguments are is seen before anything is launched."""
+    import copy
+    import inspect
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, append_qkv_static, attend_tree_static, norm_rope
+    x, p, kw = torch.zeros(2, 24), torch.zeros(2, dtype=torch.int32), dict(q_heads=1, kv_heads=1, head_dim=8, rotary=Rotary())
+    for bad, why in [(lambda: norm_rope(x, p, **kw), "CUDA tensor"), (lambda: norm_rope([1.0], p, **kw), "CUDA tensor, got list"),
+                     (lambda: norm_rope(x, **kw), "missing required argument: 'positions'"), (lambda: norm_rope(), "missing"),
+                     (lambda: norm_rope(x, p, **dict(kw, heads=3)), "unexpected keyword argument 'heads'"),
+                     (lambda: norm_rope(x, p, qkv=x, **kw), "multiple values for argument 'qkv'"),
+                     (lambda: norm_rope(x, p, None, None, None, 1, **kw), "at most 5 positional"),
+                     (lambda: append_qkv_static(x, p, None, x, p, None, **kw), "missing required argument: 'block_size'"),
+                     (lambda: attend_tree_static(x, p, p, None, x, x, x, p, x, q_heads=1, kv_heads=1, head_dim=8, block_size=16), "'slots'"),
+                     (lambda: Rotary(x[0], x[0], x[0], 1e-6, False, 0), "at most 5"), (lambda: Rotary(freq=x), "unexpected"),
+                     (lambda: Rotary(eps="a"), "real number"), (lambda: Rotary(3), "expected a CUDA tensor"),
+                     (lambda: Rotary.__new__(Rotary), "Rotary"), (lambda: type.__call__(Rotary), "Rotary"), (lambda: copy.copy(Rotary()), "Rotary")]:
+        with pytest.raises(TypeError, match=why):
+            bad()
+    with pytest.raises(ValueError, match="contiguous CUDA vector"):
+        Rotary(x[0])
+    assert list(inspect.signature(norm_rope).parameters) == ["qkv", "positions", "q", "k", "v", "q_heads", "kv_heads", "head_dim",
+                                                              "rotary", "stream"]
+
+
+def test_calls_keep_no_references(lib):
+    import sys
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, norm_rope
+    x, p, rot, key = torch.zeros(2, 24), torch.zeros(2, dtype=torch.int32), Rotary(), "".join(["no", "_such"])
+
+    def counts():
+        return [sys.getrefcount(o) for o in (x, p, rot, key, Rotary, Rotary.tensors, norm_rope, None)][:-1]
+    before = counts()
+    for _ in range(50):
+        for f in (lambda: norm_rope(x, p, q_heads=1, kv_heads=1, head_dim=8, rotary=rot), lambda: norm_rope(x, p, **{key: rot}),
+                  lambda: Rotary(x), lambda: Rotary(p, p, p)):
+            with pytest.raises((TypeError, ValueError)):
+                f()
+        Rotary(None, None, None)._check(x, 8)
+    assert counts() == before
 
 
 def test_no_rows_is_no_work(lib):
