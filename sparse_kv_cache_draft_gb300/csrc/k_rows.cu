@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowArgs A, cons
   float* sn = cs + A.half;
   int32_t* slot_of = reinterpret_cast<int32_t*>(smem) + kWarps * 2 * A.half;  // append: [Hkv][span]
   const bool on = sub * 8 < A.d;
+  grid_wait();
+  grid_go();
 
   int64_t row;
   int32_t pos = 0, part, r = 0, blk0 = 0, last = 0;
@@ -380,8 +382,15 @@ cudaError_t run_rows(const RowArgs& A, RowsTo R, cudaStream_t s) {
     if (smem > 48 * 1024) {
       if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448)) return e;
     }
-    kernel<<<(unsigned)ctas, kThreads, smem, s>>>(A, R);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = overlap_attr(s, &at);
+    return cudaLaunchKernelEx(&cfg, kernel, A, R);
   };
   if (A.interleaved)
     return lpg == 4    ? go(rows_kernel<T, 4, APPEND, true>)

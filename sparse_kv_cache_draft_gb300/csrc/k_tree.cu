@@ -284,6 +284,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
   uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 2);
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
+  grid_wait();
+  grid_go();
   const Site s = make_site(A, shape, kRows);
   if (s.rows <= 0) return;
   const int32_t split = s.parts;
@@ -590,16 +592,17 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4;
   const int32_t gr = q_tok * A.G.g;  // rows of a warpgroup: q_tok drafted tokens, all heads of the group
-  const Site s = make_site(A, shape, NW * gr);
-  Slots first_slots;
-  if (is_copy) {  // what needs no length yet, while that is on its way
+  if (is_copy) {  // what reads no memory of the call
     if (lane < 4) tma_prefetch_map(&M.pool + lane);
-    first_slots = load_slots(A, s, 0);
     // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
     constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
     for (int i = lane; i < (int)(offsetof(MmaBars, bad) / 8); i += 32)
       mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 4 ? 128 : 1);
   }
+  grid_wait();
+  const Site s = make_site(A, shape, NW * gr);
+  Slots first_slots;
+  if (is_copy) first_slots = load_slots(A, s, 0);  // needs no length yet, while that is on its way
   if (s.rows <= 0) return;
   const int32_t split = s.parts;
   const bool draft = s.part == split - 1;  // this CTA's tile 0 is the drafted tokens
@@ -708,6 +711,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_go();  // the TMEM is allocated
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
   n = __shfl_sync(0xffffffffu, B.n_tiles, 0);
   if (tid == 0) {
@@ -1035,16 +1039,16 @@ int sm_count() {
   return sms;
 }
 
-cudaLaunchConfig_t cluster_config(int64_t ctas, int threads, size_t smem, int32_t split, cudaStream_t s, cudaLaunchAttribute* at) {
+cudaLaunchConfig_t cluster_config(int64_t ctas, int threads, size_t smem, int32_t split, cudaStream_t s, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  at->id = cudaLaunchAttributeClusterDimension;
-  at->val.clusterDim.x = split;
-  at->val.clusterDim.y = 1;
-  at->val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 1 : 0;
   return cfg;
@@ -1073,8 +1077,8 @@ const ClusterRoom& cluster_room(void (*kernel)(P...), int threads, size_t smem) 
   r.dev = dev;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   for (int32_t c = 2; c <= kMaxSplit; ++c) {
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = cluster_config(c, threads, smem, c, nullptr, &at);
+    cudaLaunchAttribute at[2];
+    const cudaLaunchConfig_t cfg = cluster_config(c, threads, smem, c, nullptr, at);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
@@ -1127,8 +1131,9 @@ cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& sha
   // the limit is the same for every launch: another thread's may come between this and the launch
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = cluster_config(shape.whole + (items - shape.whole) * shape.split, threads, smem, shape.split, s, &at);
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = cluster_config(shape.whole + (items - shape.whole) * shape.split, threads, smem, shape.split, s, at);
+  cfg.numAttrs += overlap_attr(s, at + cfg.numAttrs);
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 

@@ -108,4 +108,17 @@ inline okv_status check_stream(void* stream) {
   return sdev == dev ? OKV_OK : OKV_EINVAL;
 }
 
+// Lets a launch on s begin while the kernel before it ends (its kernel calls grid_wait): at[0] is filled in and 1
+// returned, 0 while s is being captured, where the launches of a graph are plain.
+inline int overlap_attr(cudaStream_t s, cudaLaunchAttribute* at) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  return cs == cudaStreamCaptureStatusNone ? 1 : 0;
+}
+
 }  // namespace okv

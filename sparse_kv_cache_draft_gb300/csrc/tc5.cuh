@@ -6,6 +6,13 @@
 
 namespace okv {
 
+// ---- launches that overlap ------------------------------------------------------------------------
+// A kernel launched with overlap_attr starts as soon as all CTAs of the one before it have called grid_go
+// or ended. It reads and writes device memory, and allocates TMEM that CTAs of the other may still need, only behind
+// grid_wait: there the kernels before it have ended and their writes are seen. Both do nothing in a plain launch.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- TMEM ---------------------------------------------------------------------------------------
 // Allocation is by columns (a power of two, at least 32) and by a whole warp; the warp that
 // allocated frees. An address is (lane << 16) | column; a warp reaches the 32 lanes of its

@@ -285,3 +285,43 @@ def test_mask_as_uint64_and_refusals():
     with pytest.raises(OkvError) as e:
         call(wide)
     assert e.value.status == binding.EINVAL
+
+
+@pytest.mark.parametrize("R,T,d,bs,kb,dtype", [(2, 8, 128, 16, 40, "bf16"), (150, 16, 64, 16, 24, "bf16"), (40, 64, 128, 16, 16, "bf16"),
+                                               (3, 9, 192, 16, 30, "bf16"), (6, 7, 64, 8, 20, "f32")])
+def test_calls_behind_one_another(R, T, d, bs, kb, dtype):
+    """Launches overlap; each call's results and effects are those of calls that wait for one another."""
+    import torch
+    from sparse_kv_cache_draft_gb300 import Rotary, append_qkv_static, norm_rope
+    x = make(R, T, 8, 2, d, bs, kb, dtype, seed=23, stale=0.0)
+    inv = 10000.0 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float32) / d)
+    rot, kw = Rotary(inv, eps=1e-5), dict(q_heads=4, kv_heads=2, head_dim=d)
+    pos = torch.arange(R * T, dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        pool, (y, z) = x["pool"].clone(), (x["q"].clone(), torch.zeros_like(x["q"]))
+        q, (k, v) = torch.empty(R * T, 4, d, dtype=y.dtype, device="cuda"), (torch.empty_like(x["k"]) for _ in range(2))
+        seen = []
+        for i in range(30):
+            norm_rope(y.view(R * T, 8 * d), pos, q, k.view(R * T, 2, d), v.view(R * T, 2, d), rotary=rot, **kw)
+            wait()
+            call(dict(x, pool=pool, q=y, k=k, v=v), out=z)
+            wait()
+            append_qkv_static(z.view(R, T, 8 * d), x["lengths"], None, pool, x["slot_block"], q.view(R, T, 4, d), block_size=bs,
+                              slots=kb, rotary=rot, **kw)
+            wait()
+            if i % 7 == 3:  # a launch that does not overlap, in between
+                z.add_(q.view(R, T, 4, d).repeat(1, 1, 2, 1))
+                wait()
+            y, z = z, y
+            if i == 14:
+                seen.append(y.clone())
+        torch.cuda.synchronize()
+        return seen + [y, z, pool, q, k, v]
+
+    want = chain(torch.cuda.synchronize)
+    assert all(bool(t.isfinite().all()) for t in want)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, chain(lambda: None)))
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert all(torch.equal(a, b) for a, b in zip(want, chain(lambda: None)))
