@@ -13,14 +13,14 @@
 // p 2^-63 turns at most (2^-32 turns at position 2^31).
 //
 // The rows move once in and once out, so HBM is the limit: 16384 rows of 64 / 8 heads of 128 dims in bf16 take
-// 113 us, 5.9 TB/s (0.87 of a copy's rate), ragged chunks of 1024 tokens of 16 requests are appended at 0.83. A head row is 8 elements on
-// each of d / 8 lanes (a subgroup of the next power of two of lanes). A warp takes a row, or a part of its
+// 111 us, 6.0 TB/s (0.89 of a copy's rate), ragged chunks of 1024 tokens of 16 requests are appended at 0.84. A
+// head row is 8 elements on each of d / 8 lanes (a subgroup of the next power of two of lanes). A warp takes a row, or a part of its
 // heads where rows are few: it computes the row's angles once, folds weights, cosines and sines into two
 // factors per element that stay in registers for all of its query (then key) heads, and keeps 64 bytes a lane
 // in flight. What that took, on those 16384 rows: a CTA to a token with its angles in shared memory and a
 // division per head row 291 us; a warp to a row and the factors in registers 148; 64 registers, so that 32
 // warps share an SM (not 16), and the first loads before the angles 117; loops of their own for queries, keys
-// and values, and for the two orders of pairs, 113. Slower: loading each next head row beside the work on the
+// and values, and for the two orders of pairs, 113; a launch that starts while the last one ends 111. Slower: loading each next head row beside the work on the
 // last (160 us and more: the loads' scoreboards are shared), and batches of 6 or of 2 (130 to 145).
 #include <cuda_bf16.h>
 

@@ -12,9 +12,9 @@
 // row; the cluster merges them through distributed shared memory in rank order, so results do not
 // depend on timing and a launch needs no workspace.
 //
-// Measured (32 / 8 heads of 128 dims, 2048 tokens of context, bf16): 16 tokens x 128 requests 171 us, 6.5
-// TB/s, 0.96 of a copy's rate; one request, 8 tokens 12 us. 64 tokens x 32 requests with 64 / 8 heads (512
-// rows to a key head) 134 us, 1.02 PFLOP/s, 0.54 of the measured bf16 rate.
+// Measured (32 / 8 heads of 128 dims, 2048 tokens of context, bf16): 16 tokens x 128 requests 168 us, 6.6
+// TB/s, 0.98 of a copy's rate; one request, 8 tokens 10 us. 64 tokens x 32 requests with 64 / 8 heads (512
+// rows to a key head) 132 us, 1.04 PFLOP/s, 0.55 of the measured bf16 rate.
 #include <cuda_bf16.h>
 
 #include <stddef.h>
@@ -229,15 +229,18 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
 // 128 threads, 16 RG rows x 64 tokens; a warp takes 16 rows and 64 / TH of the tokens with a maximum, sum and
 // output of its own, merged at the end. m16n8k8: S's accumulators are P's operand as they stand, with the
 // tokens 2t and 2t + 1 of a lane as k = t and t + 4, and V's rows read in that order. Rows of d + 4 floats
-// keep all fragment reads free of bank conflicts. 12 tokens x 16 requests, 8 / 2 heads of 64 dims, 512 tokens of
-// context: 21 us against 36 on the CUDA cores; 30 TFLOP/s at the shape above, bound by the splitting of the
-// operands and the reads of shared memory (about 15 instructions to 3 MMAs), not by the MMAs.
+// keep all fragment reads free of bank conflicts. Tokens are copied whole, by bulk copies that zeros stand in for
+// where a token is not valid (by 16-byte pieces the issue of a tile's copies took as long as its scores).
+// 12 tokens x 16 requests, 8 / 2 heads of 64 dims, 512 tokens of context: 18.5 us against 36 on the CUDA cores;
+// 35 TFLOP/s at the shape above (30 before the bulk copies and before the three products took turns), 105 of the
+// 301 that these MMAs alone reach: bound by the splitting of the operands and the reads of shared memory, about
+// 15 instructions to 3 MMAs, at 8 warps on an SM.
 constexpr int kF32Threads = 128;
 
 __host__ __device__ constexpr int f32_pitch(int d) { return d + 4; }
 __host__ __device__ constexpr size_t f32_smem(int d, int rg, int kb, int tiles) {
   const int th = 4 / rg;
-  return (size_t)(16 * rg + 2 * kTile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 16 + ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
+  return (size_t)(16 * rg + 2 * kTile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 48 + ((size_t)kb + 15) / 16 * 16 + (size_t)tiles * 2;
 }
 __host__ __device__ constexpr int f32_ctas(int dv) { return dv <= 4 ? 3 : 2; }  // CTAs of an SM, by registers
 
@@ -251,23 +254,28 @@ __device__ __forceinline__ Parts parts_of(float x) {
   return {hi, __float_as_uint(x - __uint_as_float(hi))};
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// c += a b. The eight products of a step are summed on the tensor cores, which cut sums off (towards zero);
-// the steps are summed here, rounded to nearest.
-__device__ __forceinline__ void mma_f32(float (&c)[4], const Parts (&a)[4], const Parts& b0, const Parts& b1) {
-  float x[4];
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-      : "r"(a[0].lo), "r"(a[1].lo), "r"(a[2].lo), "r"(a[3].lo), "r"(b0.hi), "r"(b1.hi), "f"(0.f));
-  mma_tf32(x, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
-  mma_tf32(x, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+// c[n] += a b[n]. The eight products of a step are summed on the tensor cores, which cut sums off (towards zero);
+// the steps are summed here, rounded to nearest. The three products of a sum wait for one another, so the sums take turns.
+template <int N>
+__device__ __forceinline__ void mma_f32(float (*c)[4], const Parts (&a)[4], const Parts (&b)[N][2]) {
+  float x[N][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] += x[i];
+  for (int n = 0; n < N; ++n) {
+    x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+    mma_tf32(x[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(x[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(x[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] += x[n][i];
 }
 
 template <int DV, int RG>
@@ -280,10 +288,18 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
   float* ms = vs + kTile * pitch;                  // [rows], then [TH][rows] of the warps
   float* ls = ms + (TH + 1) * kRows;               // the same
   uint64_t* bad = reinterpret_cast<uint64_t*>(ls + (TH + 1) * kRows);
-  int32_t* n_tiles = reinterpret_cast<int32_t*>(bad + 1);
-  uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 2);
+  uint64_t* bars = bad + 1;                        // keys, values, queries there
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(bars + 3);
+  uint8_t* nv = reinterpret_cast<uint8_t*>(n_tiles + 4);
   uint16_t* tiles = reinterpret_cast<uint16_t*>(nv + (A.G.kb + 15) / 16 * 16);
 
+  if (threadIdx.x == 0) {
+    *bad = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(bars + i), i < 2 ? kTile : kRows);
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  __syncthreads();
   grid_wait();
   grid_go();
   const Site s = make_site(A, shape, kRows);
@@ -293,11 +309,17 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
   const int rg = warp % RG, th = warp / RG, tok0 = th * kTok;
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   constexpr int kPieces = d / 4, kEach = kTile * kPieces / kF32Threads;  // 16-byte pieces of a token, of a thread's share of a tile
-  if (tid == 0) *bad = 0;
-#pragma unroll 1
-  for (int u = 0; u < kRows * kPieces / kF32Threads; ++u) {
-    const int i = tid + u * kF32Threads, row = i / kPieces, c = i % kPieces;
-    copy16(smem_u32(qs + row * pitch + c * 4), (const float*)A.q + row_offset(A, s, s.row0 + (row < s.rows ? row : 0)) + c * 4, row < s.rows);
+  // Rows are copied whole, each by a thread that counts it at the barrier of its tile.
+  auto copy_row = [&](uint32_t bar, float* to, const float* from) {
+    mbar_expect_tx(bar, d * 4);
+    bulk_load(smem_u32(to), from, d * 4, bar);
+  };
+  if (tid >= 64 && tid < 64 + kRows) {
+    const int row = tid - 64;  // rows past the group's are never read out
+    if (row < s.rows)
+      copy_row(smem_u32(bars + 2), qs + row * pitch, (const float*)A.q + row_offset(A, s, s.row0 + row));
+    else
+      mbar_arrive(smem_u32(bars + 2));
   }
   if (tid < 32) {
     const int32_t n = list_tiles(A, s, load_slots(A, s, 0), spt, nv, tiles);
@@ -310,32 +332,30 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
   const uint8_t* unit = A.pool + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb * A.G.block_bytes;
   const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
   auto entry = [&](int32_t it) { return tiles[s.part + (it - (draft ? 1 : 0)) * split]; };
-  // Tile it's keys (which = 0) or values into shared memory, zeros for what holds no valid token.
+  // Tile it's keys (which = 0) or values into shared memory, by 64 threads, a token each. A value that is no
+  // valid token's is zero, as its weight of zero needs; a key may be anything.
   auto load = [&](int32_t it, int which) {
-    if (it < mine) {
-      const bool is_draft = draft && it == 0;
-      const int32_t slot0 = is_draft ? 0 : tile_of(entry(it)) * spt;
-      const float* to = which ? vs : ks;
-#pragma unroll 2
-      for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
-        const float* from = (const float*)A.pool;
-        bool real;
-        if (is_draft) {
-          real = j < s.cnt;
-          if (real) from = (const float*)(which ? A.v : A.k) + draft_offset(A, s, j) + c * 4;
-        } else {
-          const int32_t in = j * per_bs >> 16, slot = slot0 + in, off = j - in * bs;
-          real = j < tt && slot < A.G.kb && off < nv[slot];
-          if (real) from = reinterpret_cast<const float*>(unit + slot * A.G.block_bytes) + (int64_t)(which * bs + off) * d + c * 4;
-        }
-        copy16(smem_u32(to + j * pitch + c * 4), from, real);
-      }
+    if (it >= mine) return;
+    const int32_t j = tid & 63;
+    const float* from = nullptr;
+    if (draft && it == 0) {
+      if (j < s.cnt) from = (const float*)(which ? A.v : A.k) + draft_offset(A, s, j);
+    } else {
+      const int32_t in = j * per_bs >> 16, slot = tile_of(entry(it)) * spt + in, off = j - in * bs;
+      if (j < tt && slot < A.G.kb && off < nv[slot])
+        from = reinterpret_cast<const float*>(unit + slot * A.G.block_bytes) + (int64_t)(which * bs + off) * d;
     }
-    copy_group();
+    const uint32_t bar = smem_u32(bars + which);
+    float* to = (which ? vs : ks) + j * pitch;
+    if (from) {
+      copy_row(bar, to, from);
+    } else {
+      if (which)
+        for (int c = 0; c < d; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      mbar_arrive(bar);
+    }
   };
-  load(0, 0);
-  load(0, 1);
+  load(0, tid >> 6);
 
   uint64_t sees[2];  // of rows gi and gi + 8 of the warp's 16
 #pragma unroll
@@ -347,7 +367,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
 #pragma unroll
   for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
-  for (int32_t it = 0; it < mine; ++it) {
+  bool ok = mbar_wait_timed(smem_u32(bars + 2), 0), failed = false;
+  for (int32_t it = 0; it < mine && !failed; ++it) {
     const bool is_draft = draft && it == 0;
     uint64_t vis[2] = {sees[0], sees[1]};
     if (!is_draft) {
@@ -360,8 +381,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
       }
       vis[0] = vis[1] = (uint64_t)half[1] << 32 | half[0];
     }
-    copy_wait<1>();
-    __syncthreads();  // the keys are there, the values may be on their way
+    ok = mbar_wait_timed(smem_u32(bars), (uint32_t)(it & 1)) && ok;
     float sc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
@@ -370,8 +390,10 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
 #pragma unroll 4
     for (int k = 0; k < d; k += 8) {
       const Parts a[4] = {parts_of(qa[k]), parts_of(qa[k + 8 * pitch]), parts_of(qa[k + 4]), parts_of(qa[k + 8 * pitch + 4])};
+      Parts b[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f32(sc[n], a, parts_of(kr[n * 8 * pitch + k]), parts_of(kr[n * 8 * pitch + k + 4]));
+      for (int n = 0; n < NT; ++n) b[n][0] = parts_of(kr[n * 8 * pitch + k]), b[n][1] = parts_of(kr[n * 8 * pitch + k + 4]);
+      mma_f32<NT>(sc, a, b);
     }
     // rows gi: sc[.][0], sc[.][1]; gi + 8: sc[.][2], sc[.][3]; tokens tok0 + 8 n + 2 ti and the next
 #pragma unroll
@@ -402,10 +424,10 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
       }
     }
     __syncthreads();
-    load(it + 1, 0);  // the keys have been read
-    copy_wait<1>();
+    if (tid < 64) load(it + 1, 0);  // the keys have been read
+    ok = mbar_wait_timed(smem_u32(bars + 1), (uint32_t)(it & 1)) && ok;
     if (is_draft) {
-      // values that are not finite are zero in the products (each thread looks at what it copied)
+      // values that are not finite are zero in the products
 #pragma unroll 1
       for (int u = 0; u < kEach; ++u) {
         const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
@@ -419,20 +441,35 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
         if (!is_finite(y.w)) y.w = 0.f;
         *at = y;
       }
+      __syncthreads();
     }
-    __syncthreads();  // the values are there
     const float* vr = vs + (tok0 + 2 * ti) * pitch + gi;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const Parts a[4] = {parts_of(sc[n][0]), parts_of(sc[n][2]), parts_of(sc[n][1]), parts_of(sc[n][3])};
 #pragma unroll
-      for (int c = 0; c < d / 8; ++c)
-        mma_f32(o[c], a, parts_of(vr[n * 8 * pitch + c * 8]), parts_of(vr[n * 8 * pitch + pitch + c * 8]));
+      for (int c = 0; c < d / 8; c += 4) {
+        Parts b[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b[e][0] = parts_of(vr[n * 8 * pitch + (c + e) * 8]), b[e][1] = parts_of(vr[n * 8 * pitch + pitch + (c + e) * 8]);
+        mma_f32<4>(o + c, a, b);
+      }
     }
-    __syncthreads();
-    load(it + 1, 1);  // the values have been read
+    failed = __syncthreads_or(!ok) != 0;
+    if (tid >= 64 && !failed) {  // the values have been read
+      fence_proxy_async();       // zeros were written among them
+      load(it + 1, 1);
+    }
+    if (failed && it + 1 < mine) mbar_wait_timed(smem_u32(bars), (uint32_t)((it + 1) & 1));  // copies in flight land (bounded)
   }
-  copy_wait<0>();
+  if (failed || !ok) {  // a row of a CTA that gave up has seen nothing
+    if (A.err && tid == 0) record_error(A.err, kErrTimeout, -3, s.r, 6);
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  }
   __syncthreads();  // every tile read: keys and values give way to the warps' outputs, [TH][rows][d]
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -498,14 +535,14 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
 // the unrounded weights.
 //
 // What bounds it. Up to 128 rows, HBM, but for the CTAs' starts and ends, which the other CTA of the SM
-// covers: 8 us of the 171 are above the bytes' time. Beyond, the chain of one warpgroup: 128 scores of a row
+// covers: 4 us of the 168 are above the bytes' time. Beyond, the chain of one warpgroup: 128 scores of a row
 // in a thread take about 1500 cycles, O and the next S 1100 more and 400 to pass between them, twice in turn
 // where the tensor cores alone would need 2050. The steps that counted, 16 tokens x 128 requests / 64 tokens x
 // 32 requests: first version 217 / 286 us; MMAs issued by a whole warp, so that descriptors are in uniform
 // registers, 186 / 227; tiles of 128 tokens beyond 128 rows - / 204; queries and drafted tokens by TMA, outputs
 // through shared memory - / 182; the last items split, 180 / 165; the running maximum of a warp's rows moved
 // together 173 / 156; turns at the tensor cores - / 140; barriers and slot table set up before the lengths are
-// there 171 / 134. Slower: weights taken against the old maximum and again where it moved (208), scores in
+// there 171 / 134; launches that overlap 168 / 132. Slower: weights taken against the old maximum and again where it moved (208), scores in
 // sets of 32 (151), S of 64 tokens in two buffers beyond 128 rows (152).
 //
 // Rows past the group's are whatever the shared memory behind Q holds: they reach only outputs that
@@ -1096,11 +1133,11 @@ __global__ void room_of_smem_kernel() {}
 // What a launch costs, in tile times of a CTA alone on its SM: an item takes its tiles, `fixed` more, and `join`
 // more where its CTAs merge; beyond `dense` CTAs per SM more of them finish no more tiles in a time. From launches of
 // every split: bf16, d 128, 2048 tokens, 16 rows x 4: 0.76 us a tile of 64, and 152 tiles in that time is HBM's rate;
-// 512 rows: 2.1 us a tile of 128; binary32, 64 rows: 5.3 us a tile, two CTAs on an SM hide each other's waits.
+// 512 rows: 2.1 us a tile of 128; binary32, 64 rows: 4.4 us a tile, two CTAs on an SM hide each other's waits.
 struct Costs {
   double fixed, join, dense;
 };
-constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1}, kF32Costs{2.3, 0.5, 1.3};
+constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1}, kF32Costs{2.8, 0.5, 1.3};
 
 double wave_cost(int64_t ctas, double tiles, const Costs& t, int64_t sms) {
   const double crowd = (double)ctas / ((double)sms * t.dense);
