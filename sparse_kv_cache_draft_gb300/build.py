@@ -18,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libokv.so")
 CALLS = os.path.join(HERE, "_calls.so")
+CXX = os.environ.get("CXX", "g++")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["okv_api.cu", "k_summary.cu", "k_select.cu", "k_gather.cu", "k_attend.cu", "k_rows.cu", "k_tree.cu"]
@@ -46,24 +47,33 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 
-def _calls_job(nv: str, force: bool):
-    """The command that compiles the calls' module (None where its object stands), the object, and torch's libraries."""
+def _build_calls(nv: str, force: bool) -> str:
+    """Compile py_calls.cpp for the Python and torch there are, where its object is not of these sources and those."""
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     made_for = f"{sysconfig.get_config_var('SOABI')} torch {importlib.metadata.version('torch')}\n"
     src, obj, tag = os.path.join(CSRC, "py_calls.cpp"), os.path.join(BUILD_DIR, "py_calls.o"), os.path.join(BUILD_DIR, "py_calls.for")
-    if not os.path.exists(tag) or open(tag).read() != made_for:
-        force = True
-        if os.path.exists(obj):
-            os.remove(obj)
-        with open(tag, "w") as f:
-            f.write(made_for)
-    okv = os.path.join(HERE, "..", "include")
+    if not force and os.path.exists(tag) and open(tag).read() == made_for and not _stale(obj, src):
+        return obj
     include = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nv))), "include")]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", okv]
-    cmd += [a for d in include for a in ("-isystem", d)] + ["-c", src, "-o", obj]
-    return (cmd if force or _stale(obj, src) else None), obj, os.path.join(torch_dir, "lib")
+    tmp = f"{obj}.tmp{os.getpid()}"
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", os.path.join(HERE, "..", "include")] +
+         [a for d in include for a in ("-isystem", d)] + ["-c", src, "-o", tmp], "the compiler for py_calls.cpp")
+    os.replace(tmp, obj)
+    with open(tag, "w") as f:
+        f.write(made_for)
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(obj):
+        return
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    _run([CXX, "-shared", obj, "-o", tmp, "-L", HERE, "-l:libokv.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch_dir, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "link of _calls.so")
+    os.replace(tmp, CALLS)
 
 
 def _run(cmd, what: str) -> str:
@@ -82,25 +92,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, s.replace(".cu", ".o"))
         if force or verbose or _stale(obj, src):
             jobs.append(([nv] + _flags(verbose) + ["-c", src, "-o", obj], f"nvcc for {src}"))
-    kernels = len(jobs)
-    calls_cmd, calls_obj, torch_lib = _calls_job(nv, force)
-    if calls_cmd:
-        jobs.append((calls_cmd, "the compiler for py_calls.cpp"))
-
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls, nv, force) if importlib.util.find_spec("torch") else None
         for log in ex.map(lambda job: _run(*job), jobs):
             if verbose and log:
                 sys.stderr.write(log)
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
-    if kernels or not os.path.exists(LIB):
+    if jobs or not os.path.exists(LIB):
         tmp = LIB + f".tmp{os.getpid()}"
         _run([nv] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcuda"], "link of libokv.so")
         os.replace(tmp, LIB)
-    if not os.path.exists(CALLS) or os.path.getmtime(CALLS) < os.path.getmtime(calls_obj):
-        tmp = CALLS + f".tmp{os.getpid()}"
-        _run([os.environ.get("CXX", "g++"), "-shared", calls_obj, "-o", tmp, "-L", HERE, "-l:libokv.so", "-Wl,-rpath,$ORIGIN",
-              "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "link of _calls.so")
-        os.replace(tmp, CALLS)
+    if calls is not None:
+        _link_calls(calls.result())
     return LIB
 
 
