@@ -1091,33 +1091,34 @@ cudaLaunchConfig_t cluster_config(int64_t ctas, int threads, size_t smem, int32_
   return cfg;
 }
 
-// CTAs of clusters of c that run at once, for c = 2 .. 8: a property of the kernel and the device (a cluster
-// stays within a GPC), asked for once per thread.
+// Nothing launches it: it stands for kernels of as many threads in the question below (one that allocates tensor
+// memory counts as one CTA per SM whatever it allocates).
+__global__ void room_kernel() {}
+
+// CTAs of clusters of c that run at once, for c = 2 .. 8, where an SM holds per_sm of them: a property of the device
+// (a cluster stays within a GPC), asked for once per thread.
 struct ClusterRoom {
-  const void* kernel;
-  size_t smem;
-  int dev;
+  int threads, per_sm, dev;
   int64_t ctas[kMaxSplit + 1];
 };
-template <typename... P>
-const ClusterRoom& cluster_room(void (*kernel)(P...), int threads, size_t smem) {
+const ClusterRoom& cluster_room(int threads, int32_t per_sm) {
   constexpr int kKept = 32;
   static thread_local ClusterRoom kept[kKept];
   static thread_local int used = 0, oldest = 0;
   int dev = 0;
   cudaGetDevice(&dev);
   for (int i = 0; i < used; ++i)
-    if (kept[i].kernel == (const void*)kernel && kept[i].smem == smem && kept[i].dev == dev) return kept[i];
+    if (kept[i].threads == threads && kept[i].per_sm == per_sm && kept[i].dev == dev) return kept[i];
   ClusterRoom& r = used < kKept ? kept[used++] : kept[oldest++ % kKept];
-  r.kernel = (const void*)kernel;
-  r.smem = smem;
+  r.threads = threads;
+  r.per_sm = per_sm;
   r.dev = dev;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  cudaFuncSetAttribute(room_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   for (int32_t c = 2; c <= kMaxSplit; ++c) {
     cudaLaunchAttribute at[2];
-    const cudaLaunchConfig_t cfg = cluster_config(c, threads, smem, c, nullptr, at);
+    const cudaLaunchConfig_t cfg = cluster_config(c, threads, 233472 / per_sm - 1024, c, nullptr, at);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, room_kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -1125,10 +1126,6 @@ const ClusterRoom& cluster_room(void (*kernel)(P...), int threads, size_t smem) 
   }
   return r;
 }
-
-// A kernel that allocates tensor memory counts as one CTA per SM whatever it allocates; this one, which nothing
-// launches, as many as threads and shared memory let in.
-__global__ void room_of_smem_kernel() {}
 
 // What a launch costs, in tile times of a CTA alone on its SM: an item takes its tiles, `fixed` more, and `join`
 // more where its CTAs merge; beyond `dense` CTAs per SM more of them finish no more tiles in a time. From launches of
@@ -1181,9 +1178,9 @@ cudaError_t run_f32(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const size_t smem = f32_smem(DV * 32, RG, A.G.kb, tiles);
   int32_t per_sm = (int32_t)(228 * 1024 / (smem + 1024));
   if (per_sm > f32_ctas(DV)) per_sm = f32_ctas(DV);
+  if (per_sm < 1) per_sm = 1;
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
-  const ClusterRoom& room = cluster_room(tree_f32_kernel<DV, RG>, kF32Threads, smem);
-  const Shape shape = pick_shape(items, groups, per_sm < 1 ? 1 : per_sm, tiles, kF32Costs, room);
+  const Shape shape = pick_shape(items, groups, per_sm, tiles, kF32Costs, cluster_room(kF32Threads, per_sm));
   return launch_cluster(tree_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape);
 }
 
@@ -1261,8 +1258,8 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const size_t least = (two ? 233472 / 3 : 233472 / 2);
   if (smem < least) smem = least;
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
-  const ClusterRoom& room = cluster_room(room_of_smem_kernel, NW * 160 + 32, smem);
-  const Shape shape = pick_shape(items, groups, two ? 2 : 1, tiles, NW == 1 ? kMmaCosts : kMmaCostsWide, room);
+  const int32_t per_sm = two ? 2 : 1;
+  const Shape shape = pick_shape(items, groups, per_sm, tiles, NW == 1 ? kMmaCosts : kMmaCostsWide, cluster_room(NW * 160 + 32, per_sm));
   MmaMaps maps;
   if (cudaError_t e = make_maps<D, NW>(A, spt, q_tok, &maps)) return e;
   return launch_cluster(tree_mma_kernel<D, NW>, items, shape, NW * 160 + 32, smem, s, A, maps, shape, ring, q_tok, q_rows);
