@@ -13,7 +13,7 @@
 // depend on timing and a launch needs no workspace.
 //
 // Measured (32 / 8 heads of 128 dims, 2048 tokens of context, bf16): 16 tokens x 128 requests 168 us, 6.6
-// TB/s, 0.98 of a copy's rate; one request, 8 tokens 10 us. 64 tokens x 32 requests with 64 / 8 heads (512
+// TB/s, 0.98 of a copy's rate; one request, 8 tokens 9 us. 64 tokens x 32 requests with 64 / 8 heads (512
 // rows to a key head) 132 us, 1.04 PFLOP/s, 0.55 of the measured bf16 rate.
 #include <cuda_bf16.h>
 
@@ -29,7 +29,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 64;         // tokens of a tile, at most
-constexpr int kMaxSplit = 8;      // CTAs of a cluster (the portable limit)
+constexpr int kMaxSplit = 12;     // CTAs of a cluster; above 8 a kernel has to ask for it
 constexpr int kMaxSmem = 232448;  // bytes of shared memory a CTA may have
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -185,30 +185,41 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
   const uint64_t bad = ld_cluster_u64(cluster_map(P.bad, split - 1));
   for (int32_t i = s.part * blockDim.x + threadIdx.x; i < total; i += split * blockDim.x) {
     const int32_t row = i / d4, c = i - row * d4;
-    float m[kMaxSplit], ls[kMaxSplit], M = -INFINITY;
-    float4 x[kMaxSplit];
-#pragma unroll
-    for (int p = 0; p < kMaxSplit; ++p) {  // every load on its way before the first is used
-      m[p] = -INFINITY;
-      if (p < split) {
-        m[p] = ld_cluster(cluster_map(P.m + row * 4, p));
-        ls[p] = ld_cluster(cluster_map(P.l + row * 4, p));
-        x[p] = ld_cluster4(cluster_map(P.o + part_chunk(row, c, A.G.d, xor_mask), p));
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < kMaxSplit; ++p) M = fmaxf(M, m[p]);
-    float l = 0.f;
+    float M = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 8;  // every load of a batch on its way before the first is used
+#pragma unroll 1
+    for (int p0 = 0; p0 < split; p0 += kBatch) {
+      float m[kBatch], ls[kBatch];
+      float4 x[kBatch];
 #pragma unroll
-    for (int p = 0; p < kMaxSplit; ++p) {
-      if (p >= split || m[p] == -INFINITY) continue;  // nothing seen there: its outputs were not written
-      const float f = ex2(m[p] - M);
-      l = fmaf(f, ls[p], l);
-      o.x = fmaf(f, x[p].x, o.x);
-      o.y = fmaf(f, x[p].y, o.y);
-      o.z = fmaf(f, x[p].z, o.z);
-      o.w = fmaf(f, x[p].w, o.w);
+      for (int p = 0; p < kBatch; ++p) {
+        m[p] = -INFINITY;
+        if (p0 + p < split) {
+          m[p] = ld_cluster(cluster_map(P.m + row * 4, p0 + p));
+          ls[p] = ld_cluster(cluster_map(P.l + row * 4, p0 + p));
+          x[p] = ld_cluster4(cluster_map(P.o + part_chunk(row, c, A.G.d, xor_mask), p0 + p));
+        }
+      }
+      float mx = M;
+#pragma unroll
+      for (int p = 0; p < kBatch; ++p) mx = fmaxf(mx, m[p]);
+      if (M != -INFINITY) {
+        const float f = ex2(M - mx);
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      }
+      M = mx;
+#pragma unroll
+      for (int p = 0; p < kBatch; ++p) {
+        if (p0 + p >= split || m[p] == -INFINITY) continue;  // nothing seen there: its outputs were not written
+        const float f = ex2(m[p] - M);
+        l = fmaf(f, ls[p], l);
+        o.x = fmaf(f, x[p].x, o.x);
+        o.y = fmaf(f, x[p].y, o.y);
+        o.z = fmaf(f, x[p].z, o.z);
+        o.w = fmaf(f, x[p].w, o.w);
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -543,7 +554,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
 // through shared memory - / 182; the last items split, 180 / 165; the running maximum of a warp's rows moved
 // together 173 / 156; turns at the tensor cores - / 140; barriers and slot table set up before the lengths are
 // there 171 / 134; launches that overlap 168 / 132. Slower: weights taken against the old maximum and again where it moved (208), scores in
-// sets of 32 (151), S of 64 tokens in two buffers beyond 128 rows (152).
+// sets of 32 (151), S of 64 tokens in two buffers beyond 128 rows (152); no faster: one S for both warpgroups in
+// turn with a P of their own, P in halves (132).
 //
 // Rows past the group's are whatever the shared memory behind Q holds: they reach only outputs that
 // are not stored, and warps of such rows skip the softmax.
@@ -1095,7 +1107,7 @@ cudaLaunchConfig_t cluster_config(int64_t ctas, int threads, size_t smem, int32_
 // memory counts as one CTA per SM whatever it allocates).
 __global__ void room_kernel() {}
 
-// CTAs of clusters of c that run at once, for c = 2 .. 8, where an SM holds per_sm of them: a property of the device
+// CTAs of clusters of c that run at once, for c = 2 .. 12, where an SM holds per_sm of them: a property of the device
 // (a cluster stays within a GPC), asked for once per thread.
 struct ClusterRoom {
   int threads, per_sm, dev;
@@ -1114,6 +1126,7 @@ const ClusterRoom& cluster_room(int threads, int32_t per_sm) {
   r.per_sm = per_sm;
   r.dev = dev;
   cudaFuncSetAttribute(room_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  cudaFuncSetAttribute(room_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int32_t c = 2; c <= kMaxSplit; ++c) {
     cudaLaunchAttribute at[2];
     const cudaLaunchConfig_t cfg = cluster_config(c, threads, 233472 / per_sm - 1024, c, nullptr, at);
@@ -1143,7 +1156,8 @@ double wave_cost(int64_t ctas, double tiles, const Costs& t, int64_t sms) {
 
 // The shape of least cost, of equal ones the one with more CTAs. Items that fill the GPU go whole and the last ones
 // split, in pairs: a larger cluster waits behind whole items until all of its CTAs find a place (48 requests of 16
-// tokens: 74.4 us in pairs, 79.6 whole or in threes; 12 requests: 22.2 us in threes, 26.6 in pairs, 30.7 whole).
+// tokens: 72 us in pairs, 78 whole or in threes; 12 requests: 21 us in threes, 25 in pairs, 29 whole; one of 8 tokens
+// 9.2 in twelves, 9.9 in eights, 10.8 in sixteens, which start late; in binary32, one of 4: 19.8, 28.7 and 20.8).
 Shape pick_shape(int64_t items, int32_t groups, int32_t per_sm, int32_t tiles, const Costs& t, const ClusterRoom& room) {
   const int64_t sms = sm_count(), slots = sms * per_sm;
   const double full = wave_cost(slots, tiles, t, sms);
@@ -1164,6 +1178,7 @@ template <typename... P, typename... Q>
 cudaError_t launch_cluster(void (*kernel)(P...), int64_t items, const Shape& shape, int threads, size_t smem, cudaStream_t s, Q&&... args) {
   // the limit is the same for every launch: another thread's may come between this and the launch
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && shape.split > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = cluster_config(shape.whole + (items - shape.whole) * shape.split, threads, smem, shape.split, s, at);
