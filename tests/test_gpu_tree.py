@@ -325,3 +325,30 @@ def test_calls_behind_one_another(R, T, d, bs, kb, dtype):
         assert all(torch.equal(a, b) for a, b in zip(want, chain(lambda: None)))
     with torch.cuda.stream(torch.cuda.Stream()):
         assert all(torch.equal(a, b) for a, b in zip(want, chain(lambda: None)))
+
+
+def test_a_call_behind_an_event_of_another_stream():
+    """A launch that would overlap the one before it still waits for an event that its stream waits for."""
+    import torch
+    x = make(2, 8, 8, 2, 128, 16, 24, "bf16", seed=29)
+    other = torch.randn_like(x["q"])
+    want = [call(dict(x, q=q)) for q in (x["q"], other)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    q, busy = x["q"].clone(), torch.randn(4096, 4096, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for k, source in enumerate((other, x["q"])):
+            with torch.cuda.stream(a):
+                a.wait_stream(b)
+                y = busy @ busy  # some time before the queries are there
+                q.copy_(source)
+                ready = a.record_event()
+            with torch.cuda.stream(b):
+                if i % 2:
+                    call(dict(x, q=other), out=outs[2])  # a launch of ours that the next one may overlap
+                b.wait_event(ready)
+                call(dict(x, q=q), out=outs[k])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[1]) and torch.equal(outs[1], want[0]), i
+    del y
