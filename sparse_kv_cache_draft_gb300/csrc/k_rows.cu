@@ -529,14 +529,16 @@ __global__ void __launch_bounds__(kThreads) append_qkv_kernel(const RowArgs A, c
   }
 }
 
-// grid (n_active, Hkv), d / 8 lanes at work (the tokens of a block go through its summary in order).
+// grid (n active requests from P.first on, Hkv), d / 8 lanes at work (the tokens of a block go through its summary in order).
 // The last of a request's Hkv CTAs to finish (counted in arrivals[r], zero before and after)
 // advances its length.
 template <typename T>
 __global__ void __launch_bounds__(128) append_tree_kernel(const Geom G, const LayerState S, const ReqTables RT, const int32_t layer, const int32_t n_draft,
-                                                          const T* __restrict__ k, const T* __restrict__ v, const int32_t* __restrict__ counts,
-                                                          const int32_t* __restrict__ index, int32_t* __restrict__ arrivals, int32_t* err) {
-  const int32_t r = RT.active[blockIdx.x], h = blockIdx.y, n = counts[r], tid = threadIdx.x;
+                                                          const T* __restrict__ k, const T* __restrict__ v, const __grid_constant__ Accepted P,
+                                                          int32_t* __restrict__ arrivals, int32_t* err) {
+  const int32_t a = P.first + blockIdx.x, r = RT.active[a], h = blockIdx.y, tid = threadIdx.x;
+  const uint8_t* path = P.path + blockIdx.x * P.stride + 1;
+  const int32_t n = path[-1];
   if (n <= 0) return;
   const int32_t pos0 = S.len[r];
   __shared__ int32_t slot;
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(128) append_tree_kernel(const Geom G, const La
       __syncthreads();
     }
     if (c < G.d) {
-      const int64_t at = (((int64_t)r * n_draft + index[(int64_t)r * n_draft + i]) * G.Hkv + h) * G.d + c;
+      const int64_t at = (((int64_t)r * n_draft + path[i]) * G.Hkv + h) * G.d + c;
       Eight<T> x;
       x.load((which ? v : k) + at);
       put(G, places<T>(G, S, RT, layer, r, h, pos, slot, err), which, c, x);
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(128) append_tree_kernel(const Geom G, const La
     arrivals[r] = 0;
     __threadfence();
     S.len[r] = pos0 + n;
-    S.len_act[blockIdx.x] = pos0 + n;
+    S.len_act[a] = pos0 + n;
   }
 }
 
@@ -618,16 +620,15 @@ cudaError_t launch_append_qkv(const RowArgs& A, const Geom& G, const LayerState&
                             : run_append_qkv<__nv_bfloat16>(A, G, S, T, n_active, layer, err, s);
 }
 
-cudaError_t launch_append_tree(const Geom& G, const LayerState& S, const ReqTables& T, int32_t n_active, int32_t layer, int32_t n_draft,
-                               const void* k, const void* v, const int32_t* counts, const int32_t* index, int32_t* arrivals, int32_t* err,
-                               cudaStream_t s) {
-  if (n_active <= 0) return cudaSuccess;
-  const dim3 grid(n_active, G.Hkv);
+cudaError_t launch_append_tree(const Geom& G, const LayerState& S, const ReqTables& T, int32_t n, int32_t layer, int32_t n_draft,
+                               const void* k, const void* v, const Accepted& P, int32_t* arrivals, int32_t* err, cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  const dim3 grid(n, G.Hkv);
   if (G.dtype == OKV_F32)
-    append_tree_kernel<float><<<grid, 128, 0, s>>>(G, S, T, layer, n_draft, (const float*)k, (const float*)v, counts, index, arrivals, err);
+    append_tree_kernel<float><<<grid, 128, 0, s>>>(G, S, T, layer, n_draft, (const float*)k, (const float*)v, P, arrivals, err);
   else
-    append_tree_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(G, S, T, layer, n_draft, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, counts,
-                                                          index, arrivals, err);
+    append_tree_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(G, S, T, layer, n_draft, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, P,
+                                                          arrivals, err);
   return cudaGetLastError();
 }
 

@@ -18,6 +18,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <chrono>
 #include <thread>
 
@@ -28,7 +29,7 @@ using okv::Geom;
 using okv::LayerState;
 using okv::ReqTables;
 
-constexpr int32_t kMaxDraft = 64;  // drafted tokens of a request: the bits of a mask
+constexpr int32_t kMaxDraft = 64;  // drafted tokens of a request: the bits of a mask (a path's counts and indices are bytes)
 
 struct TimedLaunch {
   int kind;
@@ -73,7 +74,6 @@ struct okv_ctx {
   uint32_t* scores2 = nullptr;
   int32_t* stage_arrivals2 = nullptr;
   int32_t* attend_arrivals = nullptr;  // [R * Hkv]: attention split CTAs finished per unit
-  int32_t* accept_dev = nullptr;       // [layers][R][1 + 64]: okv_append_tree's counts [R], then its indices
   int32_t* append_arrivals = nullptr;  // [layers][R]: append CTAs finished per request (kept at zero)
   int32_t* gather_work = nullptr;      // [layers][2]: gather work and exit counters (kept at zero)
   float* step_coef = nullptr;          // [2][layers][R][Hkv][2d]: okv_step's coefficients of its drafts
@@ -94,7 +94,6 @@ struct okv_ctx {
   std::vector<int32_t> local_cap;      // [R] its entries per unit (-1: full-KV request)
   std::vector<int32_t> len_host;       // [L][R]
   std::vector<int> shared_buf;         // [R] host buffer shared with another active request
-  std::vector<int32_t> accept_host;    // [R][1 + 64]: source of okv_append_tree's copy
 
   // streams and events
   cudaStream_t sel_stream = nullptr, copy_stream = nullptr;
@@ -331,7 +330,7 @@ void okv_destroy(okv_ctx* c) {
                   c->err_dev, c->ctr_dev, c->partials, c->coef_buf, c->pred_coef, c->scores, c->stage_arrivals, c->attend_arrivals,
                   c->scores2, c->stage_arrivals2,
                   c->local_of, c->local_used, c->route, c->local_kv_dev, c->local_cap_dev,
-                  c->append_arrivals, c->step_coef, c->gather_work, c->accept_dev};
+                  c->append_arrivals, c->step_coef, c->gather_work};
   for (void* p : bufs)
     if (p) cudaFree(p);
   delete c;
@@ -425,8 +424,7 @@ okv_status okv_create(const okv_config* cfg, okv_ctx** out) {
             alloc((void**)&c->route, (size_t)L * U * G.kb * 4) && alloc((void**)&c->local_kv_dev, G.R * 8) &&
             alloc((void**)&c->local_cap_dev, G.R * 4) && alloc((void**)&c->append_arrivals, (size_t)L * G.R * 4) &&
             alloc((void**)&c->step_coef, (size_t)2 * L * U * 2 * G.d * sizeof(float)) &&
-            alloc((void**)&c->gather_work, (size_t)L * 2 * 4) &&
-            alloc((void**)&c->accept_dev, (size_t)L * G.R * (1 + kMaxDraft) * 4);
+            alloc((void**)&c->gather_work, (size_t)L * 2 * 4);
   // Staging lanes: odd layers stage on a second stream with a workspace of its own, so one layer's
   // per-unit selection tails overlap the next layer's scoring (measured on GB300: +3% decode
   // tok/s at the 32B-class shapes, the same at Qwen3-8B batch 128). OKV_STAGE_LANES=1 keeps one.
@@ -522,7 +520,6 @@ okv_status okv_create(const okv_config* cfg, okv_ctx** out) {
   c->local_cap.assign(G.R, -1);
   c->len_host.assign((size_t)G.L * G.R, 0);
   c->shared_buf.assign(G.R, 0);
-  c->accept_host.assign((size_t)G.R * (1 + kMaxDraft), 0);
 
   if (st == OKV_OK && okv::attend_uses_tensor_cores(G)) {
     // pool as rows of 256 bytes: dims {64 elements, 2 halves, rows}, box = one slot (32 rows)
@@ -811,11 +808,11 @@ okv_status okv_append_tree(okv_ctx* c, int32_t layer, int32_t n_draft, const voi
   if (n_draft <= 0 || n_draft > kMaxDraft) return fail(c, OKV_EINVAL, "okv_append_tree: n_draft %d not in 1..%d", n_draft, kMaxDraft);
   if (!okv::aligned16(k_draft) || !okv::aligned16(v_draft))
     return fail(c, OKV_EINVAL, "okv_append_tree: k_draft and v_draft must be 16-byte aligned");
-  bool any = false;
+  int32_t most = 0;
   for (int32_t r : c->active_list) {
     if (counts[r] < 0 || counts[r] > n_draft)
       return fail(c, OKV_EINVAL, "okv_append_tree: request %d: count %d not in 0..%d", r, counts[r], n_draft);
-    any = any || counts[r] > 0;
+    most = std::max(most, counts[r]);
     for (int32_t i = 0; i < counts[r]; ++i) {
       const int32_t j = index[(size_t)r * n_draft + i];
       if (j < 0 || j >= n_draft) return fail(c, OKV_EINVAL, "okv_append_tree: request %d: index %d not in 0..%d", r, j, n_draft - 1);
@@ -825,21 +822,31 @@ okv_status okv_append_tree(okv_ctx* c, int32_t layer, int32_t n_draft, const voi
   bool capturing = false;
   if (okv_status st = device_check(c, "okv_append_tree", s, &capturing)) return st;
   if (capturing) return fail(c, OKV_ESTATE, "okv_append_tree: stream is being captured");
-  if (!any) return OKV_OK;
+  if (most == 0) return OKV_OK;
   if (c->staged_once[layer]) OKV_CUDA(c, cudaStreamWaitEvent(s, c->ev_staged[layer], 0));
-  // A layer's counts and indices stay in its own part of accept_dev: the copy follows the work on
-  // `stream`, the layer's last append among it. The copy's source is pageable, so it has been read
-  // when the copy call returns (the caller's arrays may be page-locked).
-  memcpy(c->accept_host.data(), counts, (size_t)G.R * 4);
-  memcpy(c->accept_host.data() + G.R, index, (size_t)G.R * n_draft * 4);
-  int32_t* dcounts = c->accept_dev + (size_t)layer * G.R * (1 + kMaxDraft);
-  int32_t* dindex = dcounts + G.R;
-  OKV_CUDA(c, cudaMemcpyAsync(dcounts, c->accept_host.data(), (size_t)G.R * (1 + n_draft) * 4, cudaMemcpyHostToDevice, s));
+  // The paths go as kernel parameters, which the launch has copied when it returns: the caller may reuse its
+  // arrays, and the next call (of another layer, on another stream) shares no buffer with this one. What does not
+  // fit one launch's parameters (128 requests of up to 27 accepted tokens do) takes further ones.
+  const int32_t n_active = (int32_t)c->active_list.size();
+  okv::Accepted P;
+  P.stride = 1 + most;
+  const int32_t per = (int32_t)sizeof(P.path) / P.stride;
   Timer t(c, OKV_K_APPEND, s);
-  OKV_CUDA(c, okv::launch_append_tree(G, layer_state(c, layer), req_tables(c), (int32_t)c->active_list.size(), layer, n_draft, k_draft,
-                                      v_draft, dcounts, dindex, c->append_arrivals + (size_t)layer * G.R, c->err_dev, s));
-  t.stop(1);
-  for (int32_t r : c->active_list) c->len_host[(size_t)layer * G.R + r] += counts[r];
+  int launches = 0;
+  for (P.first = 0; P.first < n_active; P.first += per) {
+    const int32_t n = std::min(per, n_active - P.first);
+    const int32_t* reqs = c->active_list.data() + P.first;
+    for (int32_t a = 0; a < n; ++a) {
+      uint8_t* to = P.path + a * P.stride;
+      to[0] = (uint8_t)counts[reqs[a]];
+      for (int32_t i = 0; i < counts[reqs[a]]; ++i) to[1 + i] = (uint8_t)index[(size_t)reqs[a] * n_draft + i];
+    }
+    OKV_CUDA(c, okv::launch_append_tree(G, layer_state(c, layer), req_tables(c), n, layer, n_draft, k_draft, v_draft, P,
+                                        c->append_arrivals + (size_t)layer * G.R, c->err_dev, s));
+    ++launches;
+    for (int32_t a = 0; a < n; ++a) c->len_host[(size_t)layer * G.R + reqs[a]] += counts[reqs[a]];
+  }
+  t.stop(launches);
   return OKV_OK;
 }
 

@@ -46,10 +46,15 @@ cudaError_t launch_append_rows(const RowArgs& A, const Geom& G, int32_t n_reques
 // key and the value, and the query into A.q. Advances the lengths.
 cudaError_t launch_append_qkv(const RowArgs& A, const Geom& G, const LayerState& S, const ReqTables& T, int32_t n_active, int32_t layer,
                               int32_t* err, cudaStream_t s);
-// The drafted tokens index[r][0 .. counts[r] - 1] of every active request, in that order.
-cudaError_t launch_append_tree(const Geom& G, const LayerState& S, const ReqTables& T, int32_t n_active, int32_t layer, int32_t n_draft,
-                               const void* k, const void* v, const int32_t* counts, const int32_t* index, int32_t* arrivals, int32_t* err,
-                               cudaStream_t s);
+// The accepted paths of one launch, a kernel parameter: active request first + a appends path[a * stride] drafted
+// tokens, those of the bytes behind it, in that order.
+struct Accepted {
+  int32_t first, stride;
+  uint8_t path[3584];  // with the launch's other parameters less than 4 KB
+};
+// The paths of the n active requests from P.first on.
+cudaError_t launch_append_tree(const Geom& G, const LayerState& S, const ReqTables& T, int32_t n, int32_t layer, int32_t n_draft,
+                               const void* k, const void* v, const Accepted& P, int32_t* arrivals, int32_t* err, cudaStream_t s);
 cudaError_t launch_attend_tree(const TreeArgs& A, int32_t n_active, cudaStream_t s);
 
 // ---- checks of the calls without a context ---------------------------------------------------------
