@@ -235,14 +235,17 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
 // Products of binary32 numbers on the tensor cores, as three products of 11-bit parts: x = hi + lo + less
 // than 2^-21 x, hi the upper 11 bits and lo the next 11, and x y = hi hi + hi lo + lo hi within 2^-20 of
 // |x y|; sums in binary32. (On the CUDA cores the reads of shared memory bound both products: 25 TFLOP/s at
-// 64 tokens x 16 requests, 32 / 8 heads, d 128, 2048 tokens of context.) A product with an infinite factor may give NaN.
+// 64 tokens x 16 requests, 32 / 8 heads, d 128, 2048 tokens of context.) The parts of an operand that is not finite, or
+// within 2^-12 of the largest number, do not add up to it: a score is then NaN (hi and lo are infinities of both signs) and
+// its weight with it, an output NaN or infinite, and neither a row's sum of weights nor an output becomes finite again. So a
+// CTA that ends with one that is not finite takes its tiles again, those scores and all outputs by plain products.
 //
 // 128 threads, 16 RG rows x 64 tokens; a warp takes 16 rows and 64 / TH of the tokens with a maximum, sum and
 // output of its own, merged at the end. m16n8k8: S's accumulators are P's operand as they stand, with the
 // tokens 2t and 2t + 1 of a lane as k = t and t + 4, and V's rows read in that order. Rows of d + 4 floats
 // keep all fragment reads free of bank conflicts. Tokens are copied whole, by bulk copies that zeros stand in for
 // where a token is not valid (by 16-byte pieces the issue of a tile's copies took as long as its scores).
-// 12 tokens x 16 requests, 8 / 2 heads of 64 dims, 512 tokens of context: 18.5 us against 36 on the CUDA cores;
+// 12 tokens x 16 requests, 8 / 2 heads of 64 dims, 512 tokens of context: 18.7 us against 36 on the CUDA cores;
 // 35 TFLOP/s at the shape above (30 before the bulk copies and before the three products took turns), 105 of the
 // 301 that these MMAs alone reach: bound by the splitting of the operands and the reads of shared memory, about
 // 15 instructions to 3 MMAs, at 8 warps on an SM.
@@ -369,110 +372,159 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
   load(0, tid >> 6);
 
   uint64_t sees[2];  // of rows gi and gi + 8 of the warp's 16
+  bool real[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int32_t row = rg * 16 + gi + 8 * i;
-    sees[i] = row < s.rows ? A.mask[(int64_t)s.r * A.T + (s.row0 + row) / A.G.g] & low_bits(s.cnt) : 0;
+    real[i] = row < s.rows;
+    sees[i] = real[i] ? A.mask[(int64_t)s.r * A.T + (s.row0 + row) / A.G.g] & low_bits(s.cnt) : 0;
   }
-  float o[d / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[d / 8][4], m[2], l[2];
+  bool ok = mbar_wait_timed(smem_u32(bars + 2), 0), failed = false, again = false;
+  auto phase = [&](int32_t it) { return (uint32_t)((again ? mine + it : it) & 1); };
+  for (;; again = true) {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-  for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-
-  bool ok = mbar_wait_timed(smem_u32(bars + 2), 0), failed = false;
-  for (int32_t it = 0; it < mine && !failed; ++it) {
-    const bool is_draft = draft && it == 0;
-    uint64_t vis[2] = {sees[0], sees[1]};
-    if (!is_draft) {
-      const uint16_t tile = entry(it);
-      uint32_t half[2];
+    for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int32_t it = 0; it < mine && !failed; ++it) {
+      const bool is_draft = draft && it == 0;
+      uint64_t vis[2] = {sees[0], sees[1]};
+      if (!is_draft) {
+        const uint16_t tile = entry(it);
+        uint32_t half[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int32_t j = lane + 32 * u, in = j * per_bs >> 16, slot = tile_of(tile) * spt + in;
-        half[u] = __ballot_sync(0xffffffffu, j < tt && slot < A.G.kb && j - in * bs < nv[min(slot, A.G.kb - 1)]);
-      }
-      vis[0] = vis[1] = (uint64_t)half[1] << 32 | half[0];
-    }
-    ok = mbar_wait_timed(smem_u32(bars), (uint32_t)(it & 1)) && ok;
-    float sc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-    const float* qa = qs + (rg * 16 + gi) * pitch + ti;
-    const float* kr = ks + (tok0 + gi) * pitch + ti;
-#pragma unroll 4
-    for (int k = 0; k < d; k += 8) {
-      const Parts a[4] = {parts_of(qa[k]), parts_of(qa[k + 8 * pitch]), parts_of(qa[k + 4]), parts_of(qa[k + 8 * pitch + 4])};
-      Parts b[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) b[n][0] = parts_of(kr[n * 8 * pitch + k]), b[n][1] = parts_of(kr[n * 8 * pitch + k + 4]);
-      mma_f32<NT>(sc, a, b);
-    }
-    // rows gi: sc[.][0], sc[.][1]; gi + 8: sc[.][2], sc[.][3]; tokens tok0 + 8 n + 2 ti and the next
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = sc[n][2 * i + e];
-          x = vis[i] >> (tok0 + 8 * n + 2 * ti + e) & 1 ? x * scale : -INFINITY;
-          mx = fmaxf(mx, x);
+        for (int u = 0; u < 2; ++u) {
+          const int32_t j = lane + 32 * u, in = j * per_bs >> 16, slot = tile_of(tile) * spt + in;
+          half[u] = __ballot_sync(0xffffffffu, j < tt && slot < A.G.kb && j - in * bs < nv[min(slot, A.G.kb - 1)]);
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
-      m[i] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) sum += sc[n][2 * i + e] = ex2(sc[n][2 * i + e] - ref);
-      l[i] = l[i] * f + sum;  // of this lane's tokens; summed over the four lanes at the end
-#pragma unroll
-      for (int n = 0; n < d / 8; ++n) {
-        o[n][2 * i] *= f;
-        o[n][2 * i + 1] *= f;
+        vis[0] = real[0] ? (uint64_t)half[1] << 32 | half[0] : 0;
+        vis[1] = real[1] ? (uint64_t)half[1] << 32 | half[0] : 0;
       }
-    }
-    __syncthreads();
-    if (tid < 64) load(it + 1, 0);  // the keys have been read
-    ok = mbar_wait_timed(smem_u32(bars + 1), (uint32_t)(it & 1)) && ok;
-    if (is_draft) {
-      // values that are not finite are zero in the products
+      ok = mbar_wait_timed(smem_u32(bars), phase(it)) && ok;
+      float sc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      const float* qa = qs + (rg * 16 + gi) * pitch + ti;
+      const float* kr = ks + (tok0 + gi) * pitch + ti;
+#pragma unroll 4
+      for (int k = 0; k < d; k += 8) {
+        const Parts a[4] = {parts_of(qa[k]), parts_of(qa[k + 8 * pitch]), parts_of(qa[k + 4]), parts_of(qa[k + 8 * pitch + 4])};
+        Parts b[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n][0] = parts_of(kr[n * 8 * pitch + k]), b[n][1] = parts_of(kr[n * 8 * pitch + k + 4]);
+        mma_f32<NT>(sc, a, b);
+      }
+      // rows gi: sc[.][0], sc[.][1]; gi + 8: sc[.][2], sc[.][3]; tokens tok0 + 8 n + 2 ti and the next
+      if (again) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (is_finite(sc[n][e])) continue;
+            const float *x = qs + (rg * 16 + gi + 8 * (e >> 1)) * pitch, *y = ks + (tok0 + 8 * n + 2 * ti + (e & 1)) * pitch;
+            float sum = 0.f;
 #pragma unroll 1
-      for (int u = 0; u < kEach; ++u) {
-        const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
-        float4* at = reinterpret_cast<float4*>(vs + j * pitch + c * 4);
-        float4 y = *at;
-        if (is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w)) continue;
-        atomicOr(reinterpret_cast<unsigned long long*>(bad), 1ull << j);
-        if (!is_finite(y.x)) y.x = 0.f;
-        if (!is_finite(y.y)) y.y = 0.f;
-        if (!is_finite(y.z)) y.z = 0.f;
-        if (!is_finite(y.w)) y.w = 0.f;
-        *at = y;
+            for (int k = 0; k < d; ++k) sum = fmaf(x[k], y[k], sum);
+            sc[n][e] = sum;
+          }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sc[n][2 * i + e];
+            x = vis[i] >> (tok0 + 8 * n + 2 * ti + e) & 1 ? x * scale : -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum += sc[n][2 * i + e] = ex2(sc[n][2 * i + e] - ref);
+        l[i] = l[i] * f + sum;  // of this lane's tokens; summed over the four lanes at the end
+#pragma unroll
+        for (int n = 0; n < d / 8; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
       }
       __syncthreads();
-    }
-    const float* vr = vs + (tok0 + 2 * ti) * pitch + gi;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const Parts a[4] = {parts_of(sc[n][0]), parts_of(sc[n][2]), parts_of(sc[n][1]), parts_of(sc[n][3])};
-#pragma unroll
-      for (int c = 0; c < d / 8; c += 4) {
-        Parts b[4][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          b[e][0] = parts_of(vr[n * 8 * pitch + (c + e) * 8]), b[e][1] = parts_of(vr[n * 8 * pitch + pitch + (c + e) * 8]);
-        mma_f32<4>(o + c, a, b);
+      if (tid < 64) load(it + 1, 0);  // the keys have been read
+      ok = mbar_wait_timed(smem_u32(bars + 1), phase(it)) && ok;
+      if (is_draft) {
+        // values that are not finite are zero in the products
+#pragma unroll 1
+        for (int u = 0; u < kEach; ++u) {
+          const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
+          float4* at = reinterpret_cast<float4*>(vs + j * pitch + c * 4);
+          float4 y = *at;
+          if (is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w)) continue;
+          atomicOr(reinterpret_cast<unsigned long long*>(bad), 1ull << j);
+          if (!is_finite(y.x)) y.x = 0.f;
+          if (!is_finite(y.y)) y.y = 0.f;
+          if (!is_finite(y.z)) y.z = 0.f;
+          if (!is_finite(y.w)) y.w = 0.f;
+          *at = y;
+        }
+        __syncthreads();
       }
+      if (!again) {
+        const float* vr = vs + (tok0 + 2 * ti) * pitch + gi;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const Parts a[4] = {parts_of(sc[n][0]), parts_of(sc[n][2]), parts_of(sc[n][1]), parts_of(sc[n][3])};
+#pragma unroll
+          for (int c = 0; c < d / 8; c += 4) {
+            Parts b[4][2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e][0] = parts_of(vr[n * 8 * pitch + (c + e) * 8]), b[e][1] = parts_of(vr[n * 8 * pitch + pitch + (c + e) * 8]);
+            mma_f32<4>(o + c, a, b);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {  // token 8 n + 2 u + e, whose weights are with lane u of the row
+              const float p = __shfl_sync(0xffffffffu, sc[n][e], (lane & 28) | u), p8 = __shfl_sync(0xffffffffu, sc[n][2 + e], (lane & 28) | u);
+              const float* v = vs + (tok0 + 8 * n + 2 * u + e) * pitch + 2 * ti;
+#pragma unroll
+              for (int c = 0; c < d / 8; ++c) {
+                const float2 y = *reinterpret_cast<const float2*>(v + c * 8);
+                o[c][0] = fmaf(p, y.x, o[c][0]);
+                o[c][1] = fmaf(p, y.y, o[c][1]);
+                o[c][2] = fmaf(p8, y.x, o[c][2]);
+                o[c][3] = fmaf(p8, y.y, o[c][3]);
+              }
+            }
+      }
+      failed = __syncthreads_or(!ok) != 0;
+      if (tid >= 64 && !failed) {  // the values have been read
+        fence_proxy_async();       // zeros were written among them
+        load(it + 1, 1);
+      }
+      if (failed && it + 1 < mine) mbar_wait_timed(smem_u32(bars), phase(it + 1));  // copies in flight land (bounded)
     }
-    failed = __syncthreads_or(!ok) != 0;
-    if (tid >= 64 && !failed) {  // the values have been read
-      fence_proxy_async();       // zeros were written among them
-      load(it + 1, 1);
-    }
-    if (failed && it + 1 < mine) mbar_wait_timed(smem_u32(bars), (uint32_t)((it + 1) & 1));  // copies in flight land (bounded)
+    bool odd = real[0] && !is_finite(l[0]) || real[1] && !is_finite(l[1]);
+#pragma unroll
+    for (int n = 0; n < d / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd |= real[e >> 1] && !is_finite(o[n][e]);
+    if (again || failed || !__syncthreads_or(odd)) break;
+    fence_proxy_async();
+    load(0, tid >> 6);
   }
   if (failed || !ok) {  // a row of a CTA that gave up has seen nothing
     if (A.err && tid == 0) record_error(A.err, kErrTimeout, -3, s.r, 6);
