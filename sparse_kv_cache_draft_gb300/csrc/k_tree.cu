@@ -3,8 +3,9 @@
 // T <= 64 drafted tokens per request, token i seeing every valid token of the request's occupied
 // slots and the drafted tokens whose bit is set in its 64-bit mask. For query head h of KV head k:
 //   o_ih = sum_j softmax_j(q_ih . k_j / sqrt(d)) v_j
-// over those tokens, zero where there are none. The g T rows of a unit (request, KV head) share its
-// keys and values, so a unit's pool is read once for a group of rows.
+// over those tokens, zero where there are none (or none has a weight: every score is -infinity). The g T
+// rows of a unit (request, KV head) share its keys and values, so a unit's pool is read once for a group of
+// rows.
 //
 // The tokens of a unit are taken in tiles of whole slots (at most 64 tokens); tiles without a valid
 // token are left out, the rest are dealt to the CTAs of a thread-block cluster, with the drafted
@@ -212,7 +213,9 @@ __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, 
       M = mx;
 #pragma unroll
       for (int p = 0; p < kBatch; ++p) {
-        if (p0 + p >= split || m[p] == -INFINITY) continue;  // nothing seen there: its outputs were not written
+        // nothing seen there: its outputs may not have been written. Scores that are all NaN leave no maximum
+        // either, but a sum, and the row is then NaN
+        if (p0 + p >= split || (m[p] == -INFINITY && ls[p] == 0.f)) continue;
         const float f = ex2(m[p] - M);
         l = fmaf(f, ls[p], l);
         o.x = fmaf(f, x[p].x, o.x);
@@ -571,8 +574,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
       }
       continue;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    const float inv = 1.f / sum;
+    x = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     const int32_t mrow = s.row0 + row;
     if (*bad) add_not_finite<float>(A, s, *bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, x);
     store4((float*)A.out + row_offset(A, s, mrow) + c * 4, x);
@@ -1076,6 +1079,10 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
         tmem_ld32(o, my + c);
         tmem_wait_ld(o);
         if (!real) continue;
+        if (l_run == 0.f) {  // no weights (but infinite values, perhaps)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
           float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv, __uint_as_float(o[e + 2]) * inv,

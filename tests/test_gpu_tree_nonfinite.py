@@ -14,6 +14,47 @@ KINDS = [("bf16", 8, 128), ("bf16", 64, 128), ("bf16", 6, 256), ("f32", 8, 64), 
 
 @pytest.mark.parametrize("kb", [SPLIT, WHOLE])
 @pytest.mark.parametrize("dtype,T,d", KINDS)
+def test_nan_query_rows_are_nan(dtype, T, d, kb):
+    """... and no other row is."""
+    x = make(1, T, 8, 2, d, 16, kb, dtype, seed=31, lengths=[kb * 16 - 5])
+    x["q"][0, 1, 2] = float("nan")
+    x["q"][0, T - 1, 7, 3] = float("nan")
+    out = call(x)
+    assert bool(out[0, 1, 2].isnan().all()) and bool(out[0, T - 1, 7].isnan().all())
+    check(x, out)
+
+
+@pytest.mark.parametrize("dtype,T,d", KINDS)
+def test_a_nan_key_alone_in_its_tile(dtype, T, d):
+    """Every row of its KV head is NaN: the CTA that has this tile finds no maximum there, and is still heard."""
+    x = make(1, T, 8, 2, d, 16, SPLIT, dtype, seed=32, lengths=[129])
+    at = int((x["slot_block"][0, 1] == 8).nonzero()[0])  # the last block, of one token, goes to the last slot
+    x["slot_block"][0, 1, at], x["slot_block"][0, 1, -1] = -1, 8
+    x["pool"][0, 1, -1] = x["pool"][0, 1, at]
+    x["pool"][0, 1, -1, 0, 0] = float("nan")
+    out = call(x)
+    assert bool(out[0, :, 4:].isnan().all())
+    check(x, out)
+
+
+@pytest.mark.parametrize("kb", [SPLIT, WHOLE])
+@pytest.mark.parametrize("dtype,T,d", KINDS)
+def test_rows_whose_scores_are_all_minus_infinity_are_zero(dtype, T, d, kb):
+    """No token has a weight, as where a row sees none; infinite values are not reached then."""
+    import torch
+    x = make(1, T, 8, 2, d, 16, kb, dtype, seed=33, lengths=[kb * 16 - 5])
+    x["q"][:] = x["q"].abs()
+    x["pool"][0, 0, :, 0, :, 5] = float("-inf")
+    x["pool"][0, 0, 0, 1, 2, 7] = float("inf")
+    x["k"][0, :, 0, 5] = float("-inf")
+    out = call(x)
+    assert torch.equal(out[0, :, :4], torch.zeros_like(out[0, :, :4]))
+    y = {n: t[:, 1:] if n in ("pool", "slot_block") else t[:, :, 4:] if n == "q" else t[:, :, 1:] if n in "kv" else t for n, t in x.items()}
+    check(y, out[:, :, 4:].contiguous())
+
+
+@pytest.mark.parametrize("kb", [SPLIT, WHOLE])
+@pytest.mark.parametrize("dtype,T,d", KINDS)
 def test_infinite_values_of_resident_tokens(dtype, T, d, kb):
     """Infinite in their own dimension for every row of their KV head, of their sign; NaN where both signs meet."""
     x = make(1, T, 8, 2, d, 16, kb, dtype, seed=34, lengths=[kb * 16 - 5])
