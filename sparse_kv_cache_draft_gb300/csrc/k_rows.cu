@@ -159,7 +159,8 @@ __device__ __forceinline__ Turn make_turn(const RowArgs& A, const T* w, const fl
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     t.wc[e] = make_float2(a[2 * e] * c[2 * e], a[2 * e + 1] * c[2 * e + 1]);
-    t.ws[e] = make_float2(b[2 * e] * s[2 * e], b[2 * e + 1] * s[2 * e + 1]);
+    // dims that are not rotated pass: +0 times -0 adds nothing to them, also not the sign of a zero
+    t.ws[e] = t.pair ? make_float2(b[2 * e] * s[2 * e], b[2 * e + 1] * s[2 * e + 1]) : make_float2(-0.f, -0.f);
   }
   return t;
 }
