@@ -77,7 +77,8 @@ inline bool tree_geom(int32_t n_requests, int32_t q_heads, int32_t kv_heads, int
   G.bs = block_size;
   G.kb = slots;
   G.R = n_requests;
-  G.nb_max = INT32_MAX / block_size;  // block ids are checked against each request's length
+  // the blocks of the longest request, the last one part-filled; ids are also checked against each request's length
+  G.nb_max = (int32_t)(((int64_t)INT32_MAX + block_size - 1) / block_size);
   G.dtype = dtype;
   G.elem = dtype == OKV_F32 ? 4 : 2;
   G.block_bytes = (int64_t)2 * block_size * head_dim * G.elem;
