@@ -185,10 +185,15 @@ struct Timer {
   cudaStream_t s;
   cudaEvent_t a = nullptr, b = nullptr;
   Timer(okv_ctx* c_, int k, cudaStream_t s_) : c(c_), kind(k), s(s_) {
-    if (!c->timing) return;
+    if (!c->timing || capturing()) return;  // events of a graph have no times to read
     a = take();
     b = take();
     if (a && b) cudaEventRecord(a, s);
+  }
+  bool capturing() const {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) cudaGetLastError();
+    return cs != cudaStreamCaptureStatusNone;
   }
   cudaEvent_t take() {
     if (!c->event_pool.empty()) {
