@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV)) tree_f32_kernel(con
 // turn with a P of their own, P in halves (132).
 //
 // Rows past the group's are whatever the shared memory behind Q holds: they reach only outputs that
-// are not stored, and warps of such rows skip the softmax.
+// are not stored, have no vote on the running maxima, and warps of such rows skip the softmax.
 //
 // Operand tiles are lines of 64 (or, for d not a multiple of 64, 32) elements: chunk c of a tile is
 // [rows][line] under the 128-byte (64-byte) swizzle, Q and K K-major, V MN-major. A K or V tile is d / line
@@ -911,6 +911,7 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
     const float scale = kLog2e * rsqrtf((float)D);
     uint64_t sees = 0, bad = 0;
     for (int k = 0; k < NW * 4; ++k) bad |= B.bad_of[k];
+    if (!real) m_run = INFINITY;  // no vote below: what such a row holds moves no other row's maximum
     if (draft && real) sees = A.mask[(int64_t)s.r * A.T + (s.row0 + wrow) / A.G.g] & low_bits(s.cnt);
     for (int32_t i = 0; i < n; ++i) {
       uint32_t vis[kTile / 32] = {(uint32_t)sees, (uint32_t)(sees >> 32)};  // who the row sees of the tile
