@@ -155,3 +155,76 @@ def test_paths_of_more_requests_than_one_launch_takes():
         assert a.ctx.read_timing()["launches"]["append"] == 3
     finally:
         a.close()
+
+
+@pytest.mark.parametrize("dtype,Hq,H,d,bs", [("bf16", 8, 2, 128, 16), ("f32", 4, 2, 64, 16), ("bf16", 3, 1, 96, 5), ("bf16", 8, 1, 256, 64),
+                                             ("f32", 2, 2, 32, 1)])
+def test_paths_across_blocks_and_into_kept_copies(dtype, Hq, H, d, bs):
+    """Paths that end inside a resident (and, for request 1, kept) block, that cross one block boundary and several, and
+    that start a new block; stagings in between bring the new blocks in."""
+    kb = 24 if bs > 5 else 100
+    n = 15 * bs
+    a = Rig(dtype, Hq, H, d, {0: n + bs // 2, 1: n + bs - 1 if bs > 1 else n, 3: 1}, partial=(1,), R=5, bs=bs, kb=kb, cap=kb)
+    try:
+        T = 40
+        for layer in range(a.layers):
+            a.ctx.stage(layer, a.draft[layer], 0)
+            a.check(layer, kept=16 if bs > 1 else 15)
+        plans = [{0: 3, 1: 1, 3: 4}, {0: 0, 1: 37, 3: 20}, {0: 18, 1: 9, 3: 0}] if bs > 1 else [{0: 3, 1: 20, 3: 4}, {0: 0, 1: 9, 3: 20}]
+        for step, plan in enumerate(plans):
+            for layer in range(a.layers):
+                k, v = a.drafted(T)
+                paths = {r: path(m, T, 3 + 4 * layer + 2 * step) for r, m in plan.items() if m}
+                a.ctx.append_tree(layer, k, v, paths)
+                a.expect(layer, k, v, paths)
+                a.check(layer)
+            for layer in range(a.layers):
+                a.ctx.stage(layer, a.draft[layer], step + 1)
+                nb = -(-a.length[layer][1] // bs)
+                a.check(layer, kept=nb)
+                assert all(int((a.ctx.read_slot_table(layer)[0][1, h] >= 0).sum()) == nb for h in range(H))
+    finally:
+        a.close()
+
+
+@pytest.mark.parametrize("dtype,Hq,H,d", [("bf16", 8, 2, 128), ("f32", 4, 2, 64)])
+def test_a_path_is_one_token_after_another(dtype, Hq, H, d):
+    """The same state, bit for bit, as that of okv_append for each token of the paths; staging, attention and the next
+    paths run on from there."""
+    import torch
+    a, b = (Rig(dtype, Hq, H, d, {0: 300, 1: 333, 3: 2}, partial=(1,), R=5, kb=12) for _ in range(2))
+    try:
+        T = 40
+        for x in (a, b):
+            for layer in range(x.layers):
+                x.ctx.stage(layer, x.draft[layer], 0)
+        for step, m in enumerate((37, 1, 16)):
+            for layer in range(a.layers):
+                k, v = a.drafted(T)
+                paths = {r: path(m, T, 3 + 2 * r) for r in a.length[layer]}
+                a.ctx.append_tree(layer, k, v, paths)
+                for i in range(m):
+                    pick = torch.tensor([paths[r][i] if r in paths else 0 for r in range(a.R)], device="cuda")
+                    at = torch.arange(a.R, device="cuda")
+                    b.ctx.append(layer, k[at, pick].contiguous(), v[at, pick].contiguous())
+                for x in (a, b):
+                    x.expect(layer, k, v, paths)
+                    x.check(layer)
+                q = torch.randn(a.R, Hq, d, generator=a.gen).to(a.dt).cuda()
+                out = [torch.zeros_like(q) for _ in range(2)]
+                for x, o in zip((a, b), out):
+                    x.ctx.stage(layer, x.draft[layer], step + 1, 0.25)
+                    x.ctx.attend(layer, q, o)
+                torch.cuda.synchronize()
+                assert torch.equal(*out)
+                for f in ("read_slot_table", "read_local", "read_selection", "read_fetch_list"):
+                    got, want = getattr(a.ctx, f)(layer), getattr(b.ctx, f)(layer)
+                    live = sorted(a.length[layer])
+                    if f == "read_local":
+                        live, got, want = [1], got[:2], want[:2]
+                    if f in ("read_selection", "read_fetch_list"):
+                        got, want = got[:1], want[:1]
+                    assert all(np.array_equal(x[live], y[live]) for x, y in zip(got, want)), f
+    finally:
+        a.close()
+        b.close()
