@@ -1324,13 +1324,14 @@ cudaError_t run_mma(const TreeArgs& A, int32_t n_active, cudaStream_t s) {
   const int32_t q_tok = A.T < 128 / A.G.g ? A.T : 128 / A.G.g, gr = q_tok * A.G.g, q_rows = (gr + 7) / 8 * 8;
   const int32_t groups = (A.T * A.G.g + NW * gr - 1) / (NW * gr);
   // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
-  // that share of the shared memory. It is never so small that a third CTA could come to wait for TMEM.
+  // that share of the shared memory. It is never so small that a third CTA, or one of 256 columns beside one of 512, could
+  // come to wait for TMEM (two clusters that each hold what the other waits for would wait for ever).
   const bool two = D <= 128 && NW == 1;
   const size_t share = two ? 115712 : kMaxSmem, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb, tiles);
   int32_t ring = (int32_t)((share - rest) / L::kBuf);
   if (ring > kMaxRing) ring = kMaxRing;
   size_t smem = rest + (size_t)ring * L::kBuf;
-  const size_t least = (two ? 233472 / 3 : 233472 / 2);
+  const size_t third = 233472 / 3, least = two ? third : 2 * third;
   if (smem < least) smem = least;
   const int64_t items = (int64_t)n_active * A.G.Hkv * groups;
   const int32_t per_sm = two ? 2 : 1;
