@@ -222,9 +222,14 @@ OKV_API okv_status okv_append_qkv(okv_ctx* ctx, int32_t layer, const void* qkv, 
  * For every active request and drafted token: softmax(q.k / sqrt(d)) v over every valid token of
  * every occupied slot of its unit and the drafted tokens of its mask, zeros if there are none. A
  * drafted token that a row does not attend has no part in it, whatever its values (infinite and NaN
- * among them). Rows from a request's count on and rows of inactive requests are not written. Waits on
- * `stream` for the layer's last staging. EINVAL as okv_append_qkv; ESTATE if `stream` is being
- * captured and the layer has been staged (a captured wait on the staging is not possible). */
+ * among them). Scores, maxima, sums and outputs are binary32, the sum of weights times values before it is
+ * divided among them; bf16 queries give weights that are rounded to bf16 for their product with the values,
+ * binary32 operands enter the products with 22 of their 24 bits. NaN and infinities go where the formula
+ * takes them (a weight below 2^-126 counts as zero); a row whose every score is -infinity has no weights and
+ * is zero. The same inputs give the same bits. Rows from a request's count on and rows of inactive requests
+ * are not written; out may not overlap the inputs. Waits on `stream` for the layer's last staging. EINVAL as
+ * okv_append_qkv; ESTATE if `stream` is being captured and the layer has been staged (a captured wait on the
+ * staging is not possible). */
 OKV_API okv_status okv_attend_tree(okv_ctx* ctx, int32_t layer, int32_t n_draft, const int32_t* counts,
                                    const void* q, const void* k_draft, const void* v_draft,
                                    const uint64_t* mask, void* out, void* stream);
@@ -313,7 +318,8 @@ typedef struct {
   int64_t full_reads;             /* read from the full copy (local_fills included) */
 } okv_timing;
 
-/* Enable (1) or disable (0) per-launch CUDA-event timing; resets the totals. */
+/* Enable (1) or disable (0) per-launch CUDA-event timing; resets the totals. Launches into a stream that is
+ * being captured are counted, not timed. */
 OKV_API okv_status okv_set_timing(okv_ctx* ctx, int32_t enable);
 /* Synchronise and return the totals since okv_set_timing. */
 OKV_API okv_status okv_read_timing(okv_ctx* ctx, okv_timing* out);

@@ -7,14 +7,14 @@
 // rows of a unit (request, KV head) share its keys and values, so a unit's pool is read once for a group of
 // rows.
 //
-// The tokens of a unit are taken in tiles of whole slots (at most 64 tokens); tiles without a valid
-// token are left out, the rest are dealt to the CTAs of a thread-block cluster, with the drafted
+// The tokens of a unit are taken in tiles of whole slots (at most 64 tokens, or 128 in bf16 beyond 128 rows);
+// tiles without a valid token are left out, the rest are dealt to the CTAs of a thread-block cluster, with the drafted
 // tokens as one more tile of the last CTA. Each CTA keeps a running maximum, sum and output per
 // row; the cluster merges them through distributed shared memory in rank order, so results do not
 // depend on timing and a launch needs no workspace.
 //
-// Measured (32 / 8 heads of 128 dims, 2048 tokens of context, bf16): 16 tokens x 128 requests 168 us, 6.6
-// TB/s, 0.98 of a copy's rate; one request, 8 tokens 9 us. 64 tokens x 32 requests with 64 / 8 heads (512
+// Measured (32 / 8 heads of 128 dims, 2048 tokens of context, bf16): 16 tokens x 128 requests 169 us, 6.6
+// TB/s, 0.97 of a copy's rate; one request, 8 tokens 9 us. 64 tokens x 32 requests with 64 / 8 heads (512
 // rows to a key head) 132 us, 1.04 PFLOP/s, 0.55 of the measured bf16 rate.
 #include <cuda_bf16.h>
 
@@ -1203,7 +1203,8 @@ const ClusterRoom& cluster_room(int threads, int32_t per_sm) {
 // What a launch costs, in tile times of a CTA alone on its SM: an item takes its tiles, `fixed` more, and `join`
 // more where its CTAs merge; beyond `dense` CTAs per SM more of them finish no more tiles in a time. From launches of
 // every split: bf16, d 128, 2048 tokens, 16 rows x 4: 0.76 us a tile of 64, and 152 tiles in that time is HBM's rate;
-// 512 rows: 2.1 us a tile of 128; binary32, 64 rows: 4.4 us a tile, two CTAs on an SM hide each other's waits.
+// 512 rows: 2.1 us a tile of 128; binary32, 64 rows: 4.4 us a tile, two CTAs on an SM hide each other's waits. Every head
+// size takes these: a shape of the next cost gives the same result, later by what the fixed parts differ.
 struct Costs {
   double fixed, join, dense;
 };

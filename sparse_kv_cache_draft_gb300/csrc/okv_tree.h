@@ -66,7 +66,8 @@ inline bool tree_geom(int32_t n_requests, int32_t q_heads, int32_t kv_heads, int
   if (n_requests <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads || q_heads / kv_heads > 8) return false;
   if (head_dim <= 0 || head_dim % 32 || head_dim > 256 || block_size <= 0 || block_size > 64) return false;
   if (slots <= 0 || slots > 1024 || (dtype != OKV_F32 && dtype != OKV_BF16)) return false;
-  // slots, and CTAs of the attention (a unit has 16 at most), are counted in 32 bits
+  // slots, and CTAs of the attention, are counted in 32 bits: a unit has up to 16 groups of rows, whose items are split
+  // over further CTAs only where they are fewer than fill the GPU
   if ((int64_t)n_requests * kv_heads * (slots > 16 ? slots : 16) >= ((int64_t)1 << 31)) return false;
   Geom G{};
   G.L = 1;
