@@ -409,6 +409,62 @@ OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, i
                                           const void* v_draft, const uint64_t* mask, void* out,
                                           void* stream);
 
+/* ---- a bounded cache without a context ----
+ *
+ * For callers that keep a pool of fewer slots than a request has blocks, in okv_attend_static's layout: which slots
+ * give way to the next tokens' blocks, attention of those tokens once they are in, and what each slot
+ * draws of it. One pass of a layer over the next tokens of every request (a chunk of a prompt, or one token):
+ *   okv_evict_static -> okv_append_qkv_static -> okv_attend_chunk_static -> (the caller advances lengths)
+ * with the same lengths and counts in all three. As for the calls above: nothing is allocated, there is no
+ * workspace, calls on different streams are independent, each can be captured, one launch each (two for
+ * okv_attend_chunk_static with weight_out), EINVAL without a launch on what okv_create refuses, NULL or misaligned
+ * pointers and a stream of another device. A request whose length is negative, or past 2^31 - 1 with n_new more
+ * tokens, counts as one without new tokens. */
+
+/* Attention of new tokens over the resident ones. Token t < counts[r] (device [n_requests] int32, clamped to
+ * 0..n_new; NULL for n_new each) of request r is at position p = lengths[r] + t (lengths: device [n_requests] int32,
+ * the tokens before the new ones, as okv_append_qkv_static took them) and sees the tokens of the occupied slots
+ * of its unit at positions j <= p with
+ *   window == 0 or p - j < window or j < sinks
+ * (a sliding window, beside which the first `sinks` tokens stay visible; window, sinks >= 0). q, out: device
+ * [n_requests][n_new][q_heads][head_dim]. Over those tokens
+ *   out = softmax(q.k / sqrt(d)) v            zeros if there are none
+ *   lse = log sum exp(q.k / sqrt(d))          -infinity if there are none; device [n_requests][n_new][q_heads]
+ *                                             binary32, or NULL to leave it out
+ * A token that a row does not see has no part in it, whatever its place holds (infinite and NaN among it); a slot
+ * whose tokens are all behind the last new token counts as empty. Scores, maxima and sums are binary32; bf16 queries give weights that
+ * are rounded to bf16 for their product with the values, binary32 operands enter the products with 22 of their 24 bits. NaN and
+ * infinities go where the formula takes them (a weight below 2^-126 counts as zero). The same inputs give
+ * the same bits. Rows from a request's count on are not written; out and lse may not overlap the inputs.
+ *
+ * With weight_out (device [n_requests][kv_heads][slots] binary32; lse is then needed) also what each slot draws:
+ *   weight_out[r][h][s] = weight[r][h][s] + sum of exp(q.k / sqrt(d) - lse) over the new tokens of r, the query heads
+ *                         of h and the tokens of slot s that they see
+ * for every slot of every request. weight: the same shape, weight_out itself, or NULL for zeros. q_heads / kv_heads *
+ * n_new and n_requests * kv_heads * n_new must be less than 2^31. */
+OKV_API okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new, int32_t q_heads, int32_t kv_heads,
+                                           int32_t head_dim, int32_t block_size, int32_t slots, int32_t dtype,
+                                           const void* pool, const int32_t* slot_block, const int32_t* lengths,
+                                           const int32_t* counts, int32_t window, int32_t sinks, const void* q,
+                                           void* out, float* lse, const float* weight, float* weight_out,
+                                           void* stream);
+
+/* Room for the blocks that the next counts[r] tokens begin (NULL: n_new each): of the blocks whose first token is
+ * among positions lengths[r] .. lengths[r] + counts[r] - 1, those that no slot of a unit holds get one, the newest if there are not
+ * enough. Slots are taken in this order:
+ *   1. empty ones (-1, or a block that begins at or past lengths[r] and is not one of the new ones), by index;
+ *   2. those of least weight (binary32; NaN above all), of equal ones by index, but not a block with one of the first
+ *      `sinks` tokens, one of the last `recent` tokens, or the part-filled last block.
+ * The taken slots, by index, get the placed blocks, ascending, and a weight of zero; the others stay as they are. A part-filled
+ * last block that no slot holds is not brought back: its first tokens are gone. slot_block: device
+ * [n_requests][kv_heads][slots] int32; weight: the same shape binary32; slot_block_out, weight_out: written whole, either the
+ * input itself or not overlapping the inputs. block_size 1 to 64, slots 1 to 1024, n_requests * kv_heads * slots < 2^31;
+ * sinks, recent >= 0. What the pool holds of an evicted block stays until it is written over. */
+OKV_API okv_status okv_evict_static(int32_t n_requests, int32_t n_new, int32_t kv_heads, int32_t block_size,
+                                    int32_t slots, const int32_t* lengths, const int32_t* counts, int32_t sinks,
+                                    int32_t recent, const int32_t* slot_block, const float* weight,
+                                    int32_t* slot_block_out, float* weight_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,7 +9,7 @@ from .binding import BF16, F32, Config, Context, HostBuffer, OkvError, library_p
 
 
 def __getattr__(name: str):
-    """Rotary, norm_rope, append_qkv_static and attend_tree_static, which load torch."""
+    """Rotary, norm_rope, append_qkv_static, attend_tree_static, attend_chunk_static and evict_static, which load torch."""
     if name.startswith("_") or name not in binding._CALLS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     value = getattr(binding, name)

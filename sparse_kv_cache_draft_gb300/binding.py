@@ -100,6 +100,8 @@ def load_library():
             "okv_norm_rope": ([i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp], st),
             "okv_append_qkv_static": ([i32] * 8 + [vp, i64, vp, vp, vp, vp, vp, vp, vp], st),
             "okv_attend_tree_static": ([i32] * 8 + [vp] * 10, st),
+            "okv_attend_chunk_static": ([i32] * 8 + [vp] * 4 + [i32] * 2 + [vp] * 6, st),
+            "okv_evict_static": ([i32] * 5 + [vp] * 2 + [i32] * 2 + [vp] * 5, st),
             "okv_attend_static": ([i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp], st),
         }
         for name, (args, res) in sig.items():
@@ -454,7 +456,7 @@ def attend_static(pool, slot_block, lengths, q, out, *, q_heads: int, kv_heads: 
 # The calls without a context (csrc/py_calls.cpp) need torch, so their module is loaded when one of them is
 # first asked for.
 
-_CALLS = ("Rotary", "norm_rope", "append_qkv_static", "attend_tree_static", "_row_stride")
+_CALLS = ("Rotary", "norm_rope", "append_qkv_static", "attend_tree_static", "attend_chunk_static", "evict_static", "_row_stride")
 
 
 def _load_calls():

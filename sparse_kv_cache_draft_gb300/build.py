@@ -22,7 +22,8 @@ CALLS = os.path.join(HERE, "_calls.so")
 CXX = os.environ.get("CXX", "g++")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["okv_api.cu", "k_summary.cu", "k_select.cu", "k_gather.cu", "k_attend.cu", "k_rows.cu", "k_tree.cu"]
+SOURCES = ["okv_api.cu", "k_summary.cu", "k_select.cu", "k_gather.cu", "k_attend.cu", "k_rows.cu", "k_tree.cu", "k_chunk.cu",
+           "k_weigh.cu", "k_evict.cu"]
 
 
 def nvcc() -> str:
@@ -109,7 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         except (RuntimeError, OSError, ImportError) as e:  # no compiler, headers or package data of torch
             if os.path.exists(CALLS):
                 os.remove(CALLS)
-            sys.stderr.write(f"libokv.so is built; norm_rope, append_qkv_static, attend_tree_static and Rotary are not:\n{e}\n")
+            sys.stderr.write(f"libokv.so is built; norm_rope, append_qkv_static, attend_tree_static, attend_chunk_static, evict_static and Rotary are not:\n{e}\n")
     return LIB
 
 

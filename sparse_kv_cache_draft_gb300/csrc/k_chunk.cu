@@ -1,0 +1,1067 @@
+// Attention of a chunk of new tokens over a paged pool that holds them already.
+//
+// Token t of a request is at position p = length + t and sees the resident tokens at positions j <= p with
+// p - j < window or j < sinks. For query head h of KV head k, over those tokens:
+//   o_th = sum_j softmax_j(q_th . k_j / sqrt(d)) v_j,   lse_th = log sum_j exp(q_th . k_j / sqrt(d))
+// zero and -infinity where there are none. The g T rows (t, head) of a unit (request, KV head) are taken in groups of up
+// to 128 or 256; the slots that any row of a group sees are listed, those that all of its rows see whole first, so that
+// few tiles of a group need a mask whatever the slots' order, and slots that no row sees are not read. Tiles are dealt
+// to the CTAs of a cluster where there are too few groups to fill the GPU, as for drafted trees.
+#include <stddef.h>
+
+#include "okv_chunk.h"
+#include "tiles.cuh"
+
+namespace okv {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One CTA's share of the work.
+struct Span {
+  int32_t r, h, part, parts, cnt, len;
+  int32_t row0, rows;   // rows [row0, row0 + rows) of the unit's g * cnt
+  int32_t p_lo, p_hi;   // positions of the first and the last of them
+};
+
+// The longest groups of a unit, its last rows, come first.
+__device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, int32_t group_rows) {
+  Span s;
+  const int32_t cluster = blockIdx.x / P.split, rank = blockIdx.x - cluster * P.split, wholes = P.whole / P.split;
+  const bool whole = cluster < wholes;
+  const int32_t item = whole ? (int32_t)blockIdx.x : P.whole + cluster - wholes;
+  const int32_t ua = item / P.groups, group = P.groups - 1 - (item - ua * P.groups);
+  s.part = whole ? 0 : rank;
+  s.parts = whole ? 1 : P.split;
+  s.r = ua / A.G.Hkv;
+  s.h = ua - s.r * A.G.Hkv;
+  s.len = A.len[s.r];
+  s.cnt = new_tokens(A, s.r, s.len);
+  s.row0 = group * group_rows;
+  s.rows = min(group_rows, s.cnt * A.G.g - s.row0);
+  s.p_lo = s.len + s.row0 / A.G.g;
+  s.p_hi = s.len + (s.row0 + s.rows - 1) / A.G.g;
+  return s;
+}
+
+// Element offset of row m's vector in q and out, [R][T][Hq][d], times 1 / d: its place in lse.
+__device__ __forceinline__ int64_t row_place(const ChunkArgs& A, const Span& s, int32_t m) {
+  const int32_t t = m / A.G.g, j = m - t * A.G.g;
+  return ((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+}
+
+// The unit's slots that rows of the span see: `whole` of them, which all rows see whole, from the front of the list, the
+// others from its back. By `warps` warps of which each takes a run of slots: count, then place.
+struct List {
+  uint16_t* at;   // [kb]
+  int32_t kb, whole, n;
+  __device__ __forceinline__ int32_t slot(int32_t e) const { return at[e < whole ? e : kb - 1 - (e - whole)]; }
+};
+constexpr int kListWarps = 8;  // at most
+struct Listed {
+  int32_t whole[kListWarps], some[kListWarps];
+};
+// Each warp's share of at most 1024 slots is eight rounds of 32; bit u of a lane's masks is round u.
+__device__ __forceinline__ void count_slots(const ChunkArgs& A, const Span& s, int warp, int warps, Listed& L, uint32_t (&all)[8], uint32_t (&some)[8]) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  const int32_t per = (A.G.kb + 32 * warps - 1) / (32 * warps), first = warp * per * 32;
+  int32_t b[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int32_t i = first + u * 32 + lane;
+    b[u] = u < per && i < A.G.kb ? sb[i] : -1;
+  }
+  int32_t nw = 0, ns = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int32_t c = sight(b[u], A.G.bs, s.p_lo, s.p_hi, A.window, A.sinks);
+    all[u] = __ballot_sync(0xffffffffu, c == 2);
+    some[u] = __ballot_sync(0xffffffffu, c == 1);
+    nw += __popc(all[u]);
+    ns += __popc(some[u]);
+  }
+  if (lane == 0) L.whole[warp] = nw, L.some[warp] = ns;
+}
+__device__ __forceinline__ void place_slots(const ChunkArgs& A, int warp, int warps, const Listed& L, const uint32_t (&all)[8], const uint32_t (&some)[8],
+                                            uint16_t* at) {
+  const int lane = threadIdx.x & 31;
+  const int32_t per = (A.G.kb + 32 * warps - 1) / (32 * warps), first = warp * per * 32;
+  const uint32_t below = (1u << lane) - 1u;
+  int32_t nw = 0, ns = 0;
+  for (int w = 0; w < warp; ++w) nw += L.whole[w], ns += L.some[w];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint16_t slot = (uint16_t)(first + u * 32 + lane);
+    if (all[u] >> lane & 1) at[nw + __popc(all[u] & below)] = slot;
+    if (some[u] >> lane & 1) at[A.G.kb - 1 - (ns + __popc(some[u] & below))] = slot;
+    nw += __popc(all[u]);
+    ns += __popc(some[u]);
+  }
+}
+__device__ __forceinline__ List make_list(const ChunkArgs& A, int warps, const Listed& L, uint16_t* at) {
+  List l{at, A.G.kb, 0, 0};
+  for (int w = 0; w < warps; ++w) l.whole += L.whole[w], l.n += L.some[w];
+  l.n += l.whole;
+  return l;
+}
+
+// Adds what the values that are not finite, of tokens in tiles that were masked, give to four outputs (dims c .. c + 3) of
+// a row that sees them: they are zero in the products, where a weight of zero times them would reach rows that do not.
+template <typename T>
+__device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, const Span& s, const List& L, int32_t spt, int32_t p, int32_t c) {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  for (int32_t e = L.whole / spt * spt; e < L.n; ++e) {
+    if (e / spt % s.parts != s.part) continue;
+    const int32_t slot = L.slot(e);
+    uint64_t bits = seen_of(A.slot_block[unit + slot] * A.G.bs, p, A.G.bs, A.window, A.sinks);
+    const T* v = reinterpret_cast<const T*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)A.G.bs * A.G.d + c;
+    while (bits) {
+      const int32_t j = __ffsll((long long)bits) - 1;
+      bits &= bits - 1;
+      const float x = to_f(v[j * A.G.d]), y = to_f(v[j * A.G.d + 1]), z = to_f(v[j * A.G.d + 2]), w = to_f(v[j * A.G.d + 3]);
+      if (!is_finite(x)) o.x += x;
+      if (!is_finite(y)) o.y += y;
+      if (!is_finite(z)) o.z += z;
+      if (!is_finite(w)) o.w += w;
+    }
+  }
+  return o;
+}
+
+// Merges the cluster's partials and writes outputs and sums. Every thread of every CTA of the cluster calls it.
+template <typename T>
+__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask) {
+  cluster_sync();
+  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, [&](int32_t row, int32_t c, float4 o, float M, float l) {
+    const int64_t at = row_place(A, s, s.row0 + row);
+    store4((T*)A.out + at * A.G.d + c * 4, o);
+    if (c == 0 && A.lse) A.lse[at] = lse_of(M, l);
+  });
+  cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+// ---- tensor cores: bf16 ------------------------------------------------------------------------------
+//
+// As for drafted trees: a CTA holds NW groups of 128 rows (a softmax warpgroup each) over the same tiles of tokens, one
+// warp copies K and V into a ring of buffers, a warp for each group issues its MMAs,
+//   S = Q K^T   128 x tile, Q and K in shared memory, S in TMEM
+//   O += P V    128 x d,    P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
+// and a thread takes a row's softmax; the running maximum moves when a row of the warp passes it by 2^8. Weights are rounded
+// to bf16 for the second product (half a step each), their sum is of the unrounded ones.
+//
+// Up to 128 rows (NW = 1) tiles are 64 tokens, S has two buffers and two CTAs share an SM: HBM is the limit. Beyond
+// (NW = 2) tiles are 128 tokens with one S for each warpgroup, and the warpgroups take turns at the tensor cores.
+//
+// A tile is spt slots of the list. Slots that follow one another in the pool come in one copy for a line, others slot by
+// slot. A slot's lines begin at a multiple of 128 bytes of shared memory: with lines of 64 bytes and an odd block
+// size a line is left free behind each slot.
+template <int NW>
+struct Tiles {
+  static constexpr int kTile = NW == 2 ? 128 : 64;
+  static constexpr int kS = 128 / kTile;  // S buffers
+};
+
+constexpr int kMaxRing = 12;
+struct MmaBars {
+  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2][2], pv_done[2][2], drain[2], turn[2];
+  Listed listed;
+  uint32_t tmem;
+  int32_t failed, bad;
+};
+
+__host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) + ((size_t)kb * 2 + 15) / 16 * 16; }
+
+struct ChunkMaps {
+  CUtensorMap tile, slot, q;  // the pool by spt slots and by one, the queries
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 160 + 32, D <= 128 && NW == 1 ? 2 : 1)
+chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t ring, const int32_t q_tok, const int32_t q_rows,
+                 const int32_t pitch) {
+  constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
+  using L = Lines<D, kTile>;
+  constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
+  constexpr uint32_t kO = 128;
+  constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem;                                                        // [NW][chunks][q_rows][line]
+  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
+  MmaBars& B = *reinterpret_cast<MmaBars*>(rs + (size_t)ring * L::kBuf);
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4;
+  const int32_t g = A.G.g, gr = q_tok * g;  // rows of a warpgroup: q_tok tokens, all heads of the group
+  const int32_t bs = A.G.bs, spt = kTile / pitch;
+  const bool tails = spt * bs < kTile;      // lines of a tile that no token has
+  const uint32_t ring0 = smem_u32(rs);
+  if (is_copy) {  // what reads no memory of the call
+    if (lane < 3) tma_prefetch_map(&M.tile + lane);
+    // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
+    constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
+    for (int i = lane; i < (int)(offsetof(MmaBars, listed) / 8); i += 32)
+      mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 8 ? 128 : 1);
+    if (lane == 0) B.failed = B.bad = 0;
+    fence_mbar_init();
+  } else if (tails && !is_mma) {
+    // lines that no copy writes meet weights of zero
+    for (int32_t i = tid; i < ring * (L::kBuf / 16); i += NW * 128) reinterpret_cast<uint4*>(rs)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  grid_wait();
+  const Span s = make_span(A, shape, NW * gr);
+  if (s.rows <= 0) return;
+  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+
+  // Setup: the softmax warps list the slots, the copy warp starts the queries' copies.
+  uint32_t all[8], some[8];
+  if (is_copy) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      // rows (t, head of the group) of a box follow one another as the group's rows do; a box past the last
+      // request's tokens is filled up with zeros
+      const uint32_t q_bar = smem_u32(&B.q_full);
+      const int32_t boxes = NW > 1 && s.rows > gr ? 2 : 1, tok0 = s.r * A.T;
+      mbar_expect_tx(q_bar, (uint32_t)(boxes * gr * D * 2));
+      for (int w = 0; w < boxes; ++w)
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          tma_load_5d(smem_u32(qs) + (w * L::kChunks + c) * q_rows * L::kBytes, &M.q, q_bar, 0, c, 0, s.h, tok0 + s.row0 / g + w * q_tok);
+    }
+    __syncwarp();
+  } else if (is_mma) {
+    if (warp == NW * 4 + 1) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+  } else {
+    count_slots(A, s, warp, NW * 4, B.listed, all, some);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (!is_copy && !is_mma) place_slots(A, warp, NW * 4, B.listed, all, some, list_at);
+  __syncthreads();
+  grid_go();  // the TMEM is allocated
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  const List list = make_list(A, NW * 4, B.listed, list_at);
+  const int32_t n = ((list.n + spt - 1) / spt - s.part + s.parts - 1) / s.parts;  // this CTA's tiles
+
+  // The uses of the ring are in the order in which the MMAs take them. With two S buffers, S of tile i + 1
+  // comes before O of tile i: K of tile i is use 2i - 1 (the first: 0), V use 2i + 2. With one, K is 2i, V 2i + 1.
+  auto v_use = [](int32_t i) { return kS == 2 ? 2 * i + 2 : 2 * i + 1; };
+  // ... by all lanes of a warp: what follows is by whole warps
+  auto warp_wait = [&](uint64_t& bar, int32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
+  };
+  auto fail = [&] { *(volatile int32_t*)&B.failed = 1; };
+  float m_run = -INFINITY, l_run = 0.f;
+
+  if (is_copy) {
+    int32_t buf = 0, par = 0, issued = 0;  // the next buffer and the parity of its fill
+    const int32_t uses = kS == 2 ? 2 * n + 1 : 2 * n;
+    bool ok = true;
+    for (int32_t use = 0; use < uses && ok; ++use) {
+      const bool v = kS == 2 ? use > 0 && use % 2 == 0 : use % 2 == 1;
+      const int32_t i = kS == 1 ? use / 2 : v ? use / 2 - 1 : (use + 1) / 2, b = buf;
+      const uint32_t bar = smem_u32(&B.full[b]);
+      const int32_t parity = par;
+      if (++buf == ring) buf = 0, par ^= 1;
+      if (i >= n) continue;  // the use that a further K would have
+      if (use >= ring && !warp_wait(B.empty[b], parity ^ 1)) {
+        ok = false;
+        break;
+      }
+      const int32_t e0 = (s.part + i * s.parts) * spt, ne = min(spt, list.n - e0), first = list.slot(e0);
+      bool run = ne == spt && pitch == bs;
+      for (int32_t e = lane; e < ne; e += 32) run = run && list.slot(e0 + e) == first + e;
+      run = __all_sync(0xffffffffu, run);
+      const uint32_t to = ring0 + b * L::kBuf;
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)(ne * bs * D * 2));
+      __syncwarp();
+      if (run) {
+        if (lane < L::kChunks) tma_load_5d(to + lane * L::kChunk, &M.tile, bar, 0, lane, 0, v ? 1 : 0, (int32_t)unit + first);
+      } else {
+        for (int32_t x = lane; x < ne * L::kChunks; x += 32) {
+          const int32_t e = x / L::kChunks, c = x % L::kChunks;
+          tma_load_5d(to + c * L::kChunk + e * pitch * L::kBytes, &M.slot, bar, 0, c, 0, v ? 1 : 0, (int32_t)unit + list.slot(e0 + e));
+        }
+      }
+      issued = use + 1;
+    }
+    if (!ok) {
+      fail();
+      // the copies still in flight land before the shared memory is given up (bounded)
+      for (int32_t use = issued > ring ? issued - ring : 0; use < issued; ++use) mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1));
+    }
+    if (!ok || n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
+  } else if (is_mma) {
+    const bool one = lane == 0;
+    constexpr int kSteps = L::kElems / 16;
+    constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+    const int w = warp - NW * 4 - 1;  // the warpgroup it works for
+    const uint32_t my = tmem + w * kCols;
+    const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
+    const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16) + w * L::kChunks * q_chunk, k_desc = smem_desc_lo(ring0, 16);
+    const uint32_t v_desc = smem_desc_lo(ring0, L::kChunk);
+    int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
+    auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
+      b += by;
+      if (b >= ring) b -= ring, parity ^= 1;
+    };
+    auto k_ready = [&] {
+      if (!warp_wait(B.full[kb], kp)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto qk = [&](int32_t i) {
+      const uint32_t kd = k_desc + kb * (L::kBuf >> 4);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(my + (kS == 2 ? (i & 1) * kTile : 0), q_desc + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2,
+               kHi, kDescQK, c > 0, one);
+      mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
+      mma_commit(smem_u32(&B.empty[kb]), one);
+      step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
+    };
+    // Two warpgroups take turns at the tensor cores, O of a tile and S of the next at a time: while one has
+    // them, the other is at its softmax.
+    int32_t turns = 0;
+    auto my_turn = [&] { return NW == 1 || (w == 0 && turns == 0) || warp_wait(B.turn[w], (turns - (w == 0)) & 1); };
+    auto pass_on = [&] {
+      ++turns;
+      if (NW == 2 && one) mbar_arrive(smem_u32(&B.turn[w ^ 1]));
+    };
+    bool ok = true;
+    if (n > 0) {
+      ok = warp_wait(B.q_full, 0) && k_ready() && my_turn();
+      if (ok) qk(0);
+      pass_on();
+    }
+    for (int32_t i = 0; i < n && ok; ++i) {
+      if (i + 1 < n) ok = k_ready();
+      if (kS == 2 && ok && i + 1 < n) qk(i + 1);
+      ok = ok && warp_wait(B.full[vb], vp) && my_turn();
+      const uint32_t vd = v_desc + vb * (L::kBuf >> 4), p = my + (kS == 2 ? (i & 1) * kTile : 0);
+#pragma unroll
+      for (int half = 0; half < kTile / 64; ++half) {
+        ok = ok && warp_wait(B.p_full[w][i & 1][half], (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = half * 4; c < half * 4 + 4; ++c)
+          mma_ts(my + kO, p + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV, i > 0 || c > 0, one);
+      }
+      if (!ok) break;
+      mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
+      mma_commit(smem_u32(&B.empty[vb]), one);
+      step(vb, vp, 2);
+      if (kS == 1 && i + 1 < n) qk(i + 1);  // S takes the place of the P just used: the products run in order
+      pass_on();
+    }
+    if (!ok) {
+      fail();
+      mma_commit(smem_u32(&B.drain[w]), one);
+      warp_wait(B.drain[w], 0);
+    }
+  } else {
+    const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
+    const bool real = row < gr && wrow < s.rows, active = (warp & 3) * 32 < min(gr, s.rows - w * gr);
+    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
+    const float scale = kLog2e * rsqrtf((float)D);
+    const int32_t p = s.len + (s.row0 + wrow) / g;
+    if (!real) m_run = INFINITY;  // no vote below: what such a row holds moves no other row's maximum
+    uint32_t ends[kWords];        // the places of a tile that a token has
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int32_t c = 32 * u + lane;
+      ends[u] = tails ? __ballot_sync(0xffffffffu, c / pitch < spt && c % pitch < bs) : ~0u;
+    }
+    for (int32_t i = 0; i < n; ++i) {
+      const int32_t e0 = (s.part + i * s.parts) * spt;
+      const bool part_seen = e0 + spt > list.whole;  // who sees what differs, or the tile is not full
+      uint32_t vis[kWords];
+#pragma unroll
+      for (int u = 0; u < kWords; ++u) vis[u] = ends[u];
+      bool held = true;  // the token of line `row` of the tile (of kTile = 64: row & 63) is one that some row may see
+      if (part_seen) {
+        const int32_t ne = min(spt, list.n - e0), line = row & (kTile - 1);
+        uint64_t lo = 0, hi = 0;
+        held = false;
+#pragma unroll 1
+        for (int32_t k0 = 0; k0 < ne; k0 += 32) {
+          const int32_t base = k0 + lane < ne ? A.slot_block[unit + list.slot(e0 + k0 + lane)] * bs : 0;
+#pragma unroll 1
+          for (int32_t k = k0; k < min(ne, k0 + 32); ++k) {
+            const int32_t first = __shfl_sync(0xffffffffu, base, k - k0), at = k * pitch;
+            const uint64_t bits = seen_of(first, p, bs, A.window, A.sinks);
+            if (at < 64) {
+              lo |= bits << at;
+              if (at) hi |= bits >> (64 - at);
+            } else {
+              hi |= bits << (at - 64);
+            }
+            if (line >= at && line < at + bs) held = first <= s.p_hi - (line - at);
+          }
+        }
+        const uint64_t both[2] = {lo, hi};
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) vis[u] = (uint32_t)(both[u / 2] >> 32 * (u & 1));
+      }
+      if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
+        fail();
+        break;
+      }
+      // With two S buffers, S of tile i follows O of tile i - 2, so this passes at once; it keeps each barrier's
+      // waits in step with its phases, where tile i - 1's below is waited for only now and then
+      if (kS == 2 && i > 1 && !warp_wait(B.pv_done[w][i & 1], ((i - 2) >> 1) & 1)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      if (part_seen) {
+        // Values that are not finite meet weights of zero: they are zero in the product. Each warpgroup sees to it,
+        // whichever product comes first; a line is one thread's.
+        if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
+          fail();
+          break;
+        }
+        constexpr int kPieces = D / 8;
+        uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
+        if (row < kTile) {
+          bool any = false;
+#pragma unroll 4
+          for (int c = 0; c < kPieces; ++c) {
+            uint4* x = reinterpret_cast<uint4*>(v + L::piece(row, c));
+            uint4 y = *x;
+            if (clean(y)) *x = y, any = true;
+          }
+          if (any && held) *(volatile int32_t*)&B.bad = 1;
+        }
+        __syncwarp();
+        fence_proxy_async();
+      }
+      bool lost = false;
+      const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
+      uint32_t a[kWords][32];
+      float neg = 0.f;
+      if (active) {
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) tmem_ld32(a[u], st + 32 * u);
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) tmem_wait_ld(a[u]);
+        if (part_seen || tails) {
+#pragma unroll
+          for (int u = 0; u < kWords; ++u)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(vis[u] >> e & 1)) a[u][e] = 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < kWords; ++u)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        if (__any_sync(0xffffffffu, top > m_run + 8.f)) {
+          const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
+          const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
+          m_run = mn;
+          l_run *= f;
+          if (i > 0) {
+            // O has the products of tile i - 1; with one S buffer those came before S of this tile
+            if (kS == 2) lost = !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < D; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(o, my + kO + k);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(my + kO + k, o);
+            }
+          }
+        }
+        neg = m_run == -INFINITY ? 0.f : -m_run;
+      }
+      if (lost) {
+        fail();
+        break;
+      }
+      const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int half = 0; half < kWords / 2; ++half) {
+        if (active) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t* x0 = &a[2 * half][2 * e];
+            const uint32_t* y0 = &a[2 * half + 1][2 * e];
+            float2 x = fma2(make_float2(__uint_as_float(x0[0]), __uint_as_float(x0[1])), scale2, neg2);
+            float2 y = fma2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])), scale2, neg2);
+            x = make_float2(ex2(x.x), ex2(x.y));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum0 = add2(sum0, x);
+            sum1 = add2(sum1, y);
+            pk[e] = pack2(x.x, x.y);
+            pk[16 + e] = pack2(y.x, y.y);
+          }
+          tmem_st32(st + 32 * half, pk);  // over scores that have been read
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&B.p_full[w][i & 1][half]));
+      }
+      sum0 = add2(sum0, sum1);
+      l_run += sum0.x + sum0.y;
+    }
+    if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail();
+    tc_fence_after();
+  }
+  __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
+  const bool failed = *(volatile int32_t*)&B.failed != 0;
+  if (warp < NW * 4) {
+    const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
+    const bool real = row < gr && wrow < s.rows, bad = B.bad && real && l_run != 0.f;
+    const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32, p = s.len + (s.row0 + wrow) / g;  // rows of this warp
+    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + kO;
+    auto extra = [&](uint32_t (&o)[32], int c) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 x = not_finite_of<__nv_bfloat16>(A, s, list, spt, p, c + e);
+        o[e] = __float_as_uint(__uint_as_float(o[e]) + x.x);
+        o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + x.y);
+        o[e + 2] = __float_as_uint(__uint_as_float(o[e + 2]) + x.z);
+        o[e + 3] = __float_as_uint(__uint_as_float(o[e + 3]) + x.w);
+      }
+    };
+    if (rows > 0 && s.parts == 1 && !failed) {
+      // through shared memory (this warp's rows in the place of its queries), to write whole lines
+      constexpr int kPieces = D / 8, kXor = kPieces % 8 ? 3 : 7;  // pieces of eight rows on different banks
+      uint8_t* mine = qs + ((size_t)w * q_rows + (warp & 3) * 32) * D * 2;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      if (real && A.lse) A.lse[row_place(A, s, s.row0 + wrow)] = lse_of(m_run, l_run);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (n > 0) {
+          tmem_ld32(o, my + c);
+          tmem_wait_ld(o);
+        }
+        if (!real) continue;
+        if (l_run == 0.f) {  // no weights (but infinite values, perhaps)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (bad) extra(o, c);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[e + k]) * inv;
+          *reinterpret_cast<uint4*>(mine + ((size_t)lane * kPieces + (((c + e) / 8) ^ (lane & kXor))) * 16) =
+              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+        }
+      }
+      __syncwarp();
+      const uint32_t per_g = (65536 + g - 1) / g;  // m * per_g >> 16 is m / g for the rows of a group
+      const int32_t m0 = w * gr + (warp & 3) * 32;
+      __nv_bfloat16* base = (__nv_bfloat16*)A.out + row_place(A, s, s.row0) * D;  // row0 is the first head of a token
+#pragma unroll 4
+      for (int e = lane; e < min(rows, 32) * kPieces; e += 32) {
+        const int r = e / kPieces, c = e - r * kPieces;
+        const uint32_t m = m0 + r, t = m * per_g >> 16;
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + ((size_t)r * kPieces + (c ^ (r & kXor))) * 16);
+        *reinterpret_cast<uint4*>(base + ((int64_t)t * A.G.Hq + (m - t * g)) * D + c * 8) = x;
+      }
+    } else if (rows > 0 && s.parts > 1) {
+      float* ml = reinterpret_cast<float*>(qs);
+      if (real) {
+        ml[wrow] = failed ? -INFINITY : m_run;
+        ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
+      }
+      if (n > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(o, my + c);
+          tmem_wait_ld(o);
+          if (!real) continue;
+          if (bad) extra(o, c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(rs + part_chunk(wrow, (c + e) / 4, D, 7)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+    }
+  }
+  if (s.parts > 1) merge_chunk<__nv_bfloat16>(A, s, Partial{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4)}, 7);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == NW * 4 + 1) {
+    tc_fence_after();
+    tmem_free(tmem, kCols * NW);
+  }
+}
+
+// ---- binary32 ------------------------------------------------------------------------------------------
+//
+// Products of three parts on the tensor cores (mma_f32), as for drafted trees: 128 threads, 16 RG rows x 64 tokens; a warp
+// takes 16 rows and 64 / TH of the tokens with a maximum, sum and output of its own, merged at the end. The parts of an operand
+// that is not finite, or next to the largest number, do not add up to it: a score is then NaN and an output NaN or
+// infinite, so a CTA that ends with a sum or an output that is not finite takes its tiles again by plain products.
+constexpr int kF32Tile = 64, kF32Threads = 128;
+
+__host__ __device__ constexpr int f32_pitch(int d) { return d + 4; }  // fragment reads free of bank conflicts
+__host__ __device__ constexpr size_t f32_smem(int d, int rg, int kb) {
+  const int th = 4 / rg;
+  return (size_t)(16 * rg + 2 * kF32Tile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 32 + sizeof(Listed) + ((size_t)kb * 2 + 15) / 16 * 16;
+}
+__host__ __device__ constexpr int f32_ctas(int dv, int rg) { return dv <= 4 && rg < 4 ? 3 : dv <= 4 ? 2 : 1; }  // CTAs of an SM, by registers
+
+template <int DV, int RG>
+__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kernel(const ChunkArgs A, const Shape shape, const int32_t q_tok) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int d = DV * 32, pitch = f32_pitch(d), kRows = 16 * RG, TH = 4 / RG, kTok = kF32Tile / TH, NT = kTok / 8;
+  float* qs = reinterpret_cast<float*>(smem);      // [rows][pitch]
+  float* ks = qs + kRows * pitch;                  // [64][pitch]
+  float* vs = ks + kF32Tile * pitch;               // [64][pitch]
+  float* ms = vs + kF32Tile * pitch;               // [rows], then [TH][rows] of the warps
+  float* ls = ms + (TH + 1) * kRows;               // the same
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ls + (TH + 1) * kRows);  // keys, values, queries there
+  int32_t* bad = reinterpret_cast<int32_t*>(bars + 3);
+  Listed& listed = *reinterpret_cast<Listed*>(bars + 4);
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(&listed + 1);
+
+  if (threadIdx.x == 0) {
+    *bad = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(bars + i), i < 2 ? kF32Tile : kRows);
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  __syncthreads();
+  grid_wait();
+  grid_go();
+  const int32_t g = A.G.g;
+  const Span s = make_span(A, shape, q_tok * g);
+  if (s.rows <= 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
+  const int rg = warp % RG, th = warp / RG, tok0 = th * kTok;
+  const int32_t bs = A.G.bs, spt = kF32Tile / bs, tt = spt * bs;
+  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  constexpr int kPieces = d / 4, kEach = kF32Tile * kPieces / kF32Threads;  // 16-byte pieces of a token, of a thread's share of a tile
+  // Rows are copied whole, each by a thread that counts it at the barrier of its tile.
+  auto copy_row = [&](uint32_t bar, float* to, const float* from) {
+    mbar_expect_tx(bar, d * 4);
+    bulk_load(smem_u32(to), from, d * 4, bar);
+  };
+  if (tid < kRows) {  // rows past the group's are never read out
+    if (tid < s.rows)
+      copy_row(smem_u32(bars + 2), qs + tid * pitch, (const float*)A.q + row_place(A, s, s.row0 + tid) * d);
+    else
+      mbar_arrive(smem_u32(bars + 2));
+  }
+  uint32_t whole_of[8], some_of[8];
+  count_slots(A, s, warp, 4, listed, whole_of, some_of);
+  __syncthreads();
+  place_slots(A, warp, 4, listed, whole_of, some_of, list_at);
+  __syncthreads();
+  const List list = make_list(A, 4, listed, list_at);
+  const int32_t mine = ((list.n + spt - 1) / spt - s.part + s.parts - 1) / s.parts;  // this CTA's tiles
+  const float scale = kLog2e / sqrtf((float)d);
+  const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
+  auto first_of = [&](int32_t it) { return (s.part + it * s.parts) * spt; };
+  // Tile it's keys (which = 0) or values into shared memory, by 64 threads, a token each. A value that no row may see
+  // is zero, as its weight of zero needs; a key may be anything.
+  auto load = [&](int32_t it, int which) {
+    if (it >= mine) return;
+    const int32_t j = tid & 63, in = j * per_bs >> 16, off = j - in * bs, e = first_of(it) + in;
+    const float* from = nullptr;
+    if (j < tt && e < list.n) {
+      const int32_t slot = list.slot(e);
+      if (e < list.whole || A.slot_block[unit + slot] * bs <= s.p_hi - off)
+        from = reinterpret_cast<const float*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)(which * bs + off) * d;
+    }
+    const uint32_t bar = smem_u32(bars + which);
+    float* to = (which ? vs : ks) + j * pitch;
+    if (from) {
+      copy_row(bar, to, from);
+    } else {
+      if (which)
+        for (int c = 0; c < d; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      mbar_arrive(bar);
+    }
+  };
+  load(0, tid >> 6);
+
+  bool real[2];
+  int32_t pos[2];  // of rows gi and gi + 8 of the warp's 16
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int32_t row = rg * 16 + gi + 8 * i;
+    real[i] = row < s.rows;
+    pos[i] = s.len + (s.row0 + row) / g;
+  }
+  float o[d / 8][4], m[2], l[2];
+  bool ok = mbar_wait_timed(smem_u32(bars + 2), 0), failed = false, again = false;
+  auto phase = [&](int32_t it) { return (uint32_t)((again ? mine + it : it) & 1); };
+  for (;; again = true) {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int32_t it = 0; it < mine && !failed; ++it) {
+      const int32_t e0 = first_of(it);
+      const bool part_seen = e0 + spt > list.whole;
+      uint64_t vis[2] = {first_bits(real[0] ? tt : 0), first_bits(real[1] ? tt : 0)};
+      if (part_seen) {
+        vis[0] = vis[1] = 0;
+        const int32_t ne = min(spt, list.n - e0);
+#pragma unroll 1
+        for (int32_t k = 0; k < ne; ++k) {
+          const int32_t base = A.slot_block[unit + list.slot(e0 + k)] * bs;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (real[i]) vis[i] |= seen_of(base, pos[i], bs, A.window, A.sinks) << k * bs;
+        }
+      }
+      ok = mbar_wait_timed(smem_u32(bars), phase(it)) && ok;
+      float sc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      const float* qa = qs + (rg * 16 + gi) * pitch + ti;
+      const float* kr = ks + (tok0 + gi) * pitch + ti;
+#pragma unroll(NT > 4 ? 2 : 4)
+      for (int k = 0; k < d; k += 8) {
+        const Parts a[4] = {parts_of(qa[k]), parts_of(qa[k + 8 * pitch]), parts_of(qa[k + 4]), parts_of(qa[k + 8 * pitch + 4])};
+        Parts b[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n][0] = parts_of(kr[n * 8 * pitch + k]), b[n][1] = parts_of(kr[n * 8 * pitch + k + 4]);
+        mma_f32<NT>(sc, a, b);
+      }
+      // rows gi: sc[.][0], sc[.][1]; gi + 8: sc[.][2], sc[.][3]; tokens tok0 + 8 n + 2 ti and the next
+      if (again) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (is_finite(sc[n][e])) continue;
+            const float *x = qs + (rg * 16 + gi + 8 * (e >> 1)) * pitch, *y = ks + (tok0 + 8 * n + 2 * ti + (e & 1)) * pitch;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < d; ++k) sum = fmaf(x[k], y[k], sum);
+            sc[n][e] = sum;
+          }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sc[n][2 * i + e];
+            x = vis[i] >> (tok0 + 8 * n + 2 * ti + e) & 1 ? x * scale : -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum += sc[n][2 * i + e] = ex2(sc[n][2 * i + e] - ref);
+        l[i] = l[i] * f + sum;  // of this lane's tokens; summed over the four lanes at the end
+#pragma unroll
+        for (int n = 0; n < d / 8; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
+      }
+      __syncthreads();
+      if (tid < 64) load(it + 1, 0);  // the keys have been read
+      ok = mbar_wait_timed(smem_u32(bars + 1), phase(it)) && ok;
+      if (part_seen) {
+        // values that are not finite are zero in the products
+#pragma unroll 1
+        for (int u = 0; u < kEach; ++u) {
+          const int i = tid + u * kF32Threads, j = i / kPieces, c = i % kPieces;
+          float4* at = reinterpret_cast<float4*>(vs + j * pitch + c * 4);
+          float4 y = *at;
+          if (is_finite(y.x) && is_finite(y.y) && is_finite(y.z) && is_finite(y.w)) continue;
+          *(volatile int32_t*)bad = 1;
+          if (!is_finite(y.x)) y.x = 0.f;
+          if (!is_finite(y.y)) y.y = 0.f;
+          if (!is_finite(y.z)) y.z = 0.f;
+          if (!is_finite(y.w)) y.w = 0.f;
+          *at = y;
+        }
+        __syncthreads();
+      }
+      if (!again) {
+        const float* vr = vs + (tok0 + 2 * ti) * pitch + gi;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const Parts a[4] = {parts_of(sc[n][0]), parts_of(sc[n][2]), parts_of(sc[n][1]), parts_of(sc[n][3])};
+#pragma unroll
+          for (int c = 0; c < d / 8; c += 4) {
+            Parts b[4][2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e][0] = parts_of(vr[n * 8 * pitch + (c + e) * 8]), b[e][1] = parts_of(vr[n * 8 * pitch + pitch + (c + e) * 8]);
+            mma_f32<4>(o + c, a, b);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {  // token 8 n + 2 u + e, whose weights are with lane u of the row
+              const float p = __shfl_sync(0xffffffffu, sc[n][e], (lane & 28) | u), p8 = __shfl_sync(0xffffffffu, sc[n][2 + e], (lane & 28) | u);
+              const float* v = vs + (tok0 + 8 * n + 2 * u + e) * pitch + 2 * ti;
+#pragma unroll
+              for (int c = 0; c < d / 8; ++c) {
+                const float2 y = *reinterpret_cast<const float2*>(v + c * 8);
+                o[c][0] = fmaf(p, y.x, o[c][0]);
+                o[c][1] = fmaf(p, y.y, o[c][1]);
+                o[c][2] = fmaf(p8, y.x, o[c][2]);
+                o[c][3] = fmaf(p8, y.y, o[c][3]);
+              }
+            }
+      }
+      failed = __syncthreads_or(!ok) != 0;
+      if (tid >= 64 && !failed) {  // the values have been read
+        fence_proxy_async();       // zeros were written among them
+        load(it + 1, 1);
+      }
+      if (failed && it + 1 < mine) mbar_wait_timed(smem_u32(bars), phase(it + 1));  // copies in flight land (bounded)
+    }
+    bool odd = real[0] && !is_finite(l[0]) || real[1] && !is_finite(l[1]);
+#pragma unroll
+    for (int n = 0; n < d / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd |= real[e >> 1] && !is_finite(o[n][e]);
+    if (again || failed || !__syncthreads_or(odd)) break;
+    fence_proxy_async();
+    load(0, tid >> 6);
+  }
+  if (failed || !ok) {  // a row of a CTA that gave up has seen nothing
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  }
+  __syncthreads();  // every tile read: keys and values give way to the warps' outputs, [TH][rows][d]
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    const int row = rg * 16 + gi + 8 * i;
+    float* to = ks + (th * kRows + row) * d + 2 * ti;
+#pragma unroll
+    for (int c = 0; c < d / 8; ++c) *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+    if (ti == 0) {
+      ms[(1 + th) * kRows + row] = m[i];
+      ls[(1 + th) * kRows + row] = l[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < s.rows * kPieces; i += kF32Threads) {
+    const int row = i / kPieces, c = i % kPieces;
+    float M = -INFINITY, sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 1; k <= TH; ++k) M = fmaxf(M, ms[k * kRows + row]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < TH; ++k) {
+      const float f = ex2(ms[(1 + k) * kRows + row] - ref);
+      const float4 y = *reinterpret_cast<const float4*>(ks + (k * kRows + row) * d + c * 4);
+      sum = fmaf(f, ls[(1 + k) * kRows + row], sum);
+      x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+    }
+    if (*bad && sum != 0.f) {
+      const float4 y = not_finite_of<float>(A, s, list, spt, s.len + (s.row0 + row) / g, c * 4);
+      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    if (s.parts > 1) {
+      *reinterpret_cast<float4*>(ks + row * d + c * 4) = x;  // read above by this thread alone
+      if (c == 0) {
+        ms[row] = M;
+        ls[row] = sum;
+      }
+      continue;
+    }
+    const float inv = 1.f / sum;
+    x = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    const int64_t at = row_place(A, s, s.row0 + row);
+    store4((float*)A.out + at * d + c * 4, x);
+    if (c == 0 && A.lse) A.lse[at] = lse_of(M, sum);
+  }
+  if (s.parts > 1) merge_chunk<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls)}, 0);
+}
+
+// ---- launches ----------------------------------------------------------------------------------------------
+
+// Tiles of `tile` tokens that a group of rows may have: of the slots there are, and of those that a window leaves it.
+int32_t most_tiles(const ChunkArgs& A, int32_t spt, int32_t group_tok) {
+  const int64_t bs = A.G.bs, seen = ((int64_t)A.window + group_tok + bs - 1) / bs + 1 + ((int64_t)A.sinks + bs - 1) / bs;
+  const int64_t slots = seen < A.G.kb ? seen : A.G.kb;
+  return (int32_t)((slots + spt - 1) / spt);
+}
+
+constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1}, kF32Costs{2.8, 0.5, 1.3};  // as for drafted trees
+
+template <int DV, int RG>
+cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {
+  const int32_t q_tok = 16 * RG / A.G.g, groups = (A.T + q_tok - 1) / q_tok;
+  const size_t smem = f32_smem(DV * 32, RG, A.G.kb);
+  int32_t per_sm = (int32_t)(228 * 1024 / (smem + 1024));
+  if (per_sm > f32_ctas(DV, RG)) per_sm = f32_ctas(DV, RG);
+  if (per_sm < 1) per_sm = 1;
+  const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
+  const Shape shape = pick_shape(items, groups, per_sm, most_tiles(A, kF32Tile / A.G.bs, q_tok), kF32Costs, cluster_room(kF32Threads, per_sm));
+  return launch_cluster(chunk_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape, q_tok);
+}
+
+template <int DV>
+cudaError_t run_f32_rows(const ChunkArgs& A, cudaStream_t s) {
+  const int32_t rows = A.T * A.G.g;
+  return rows <= 16 ? run_f32<DV, 1>(A, s) : rows <= 32 ? run_f32<DV, 2>(A, s) : run_f32<DV, 4>(A, s);
+}
+
+cudaError_t run_f32_d(const ChunkArgs& A, cudaStream_t s) {
+  switch (A.G.d / 32) {
+    case 1: return run_f32_rows<1>(A, s);
+    case 2: return run_f32_rows<2>(A, s);
+    case 3: return run_f32_rows<3>(A, s);
+    case 4: return run_f32_rows<4>(A, s);
+    case 5: return run_f32_rows<5>(A, s);
+    case 6: return run_f32_rows<6>(A, s);
+    case 7: return run_f32_rows<7>(A, s);
+    default: return run_f32_rows<8>(A, s);
+  }
+}
+
+// Maps of 5 dims over lines and chunks: the pool as [slots][K, V][tokens], a box of one chunk of the tokens of spt slots
+// or of one; the queries as [tokens][KV heads][group], a box of q_tok tokens of a KV head.
+template <int D, int Tile>
+cudaError_t make_maps(const ChunkArgs& A, int32_t spt, int32_t q_tok, ChunkMaps* m) {
+  using L = Lines<D, Tile>;
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  auto encode = [&](CUtensorMap* map, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[3], const cuuint32_t (&box)[3]) {
+    const cuuint64_t d[5] = {(cuuint64_t)L::kElems, (cuuint64_t)L::kChunks, dims[0], dims[1], dims[2]};
+    const cuuint64_t st[4] = {(cuuint64_t)L::kBytes, strides[0], strides[1], strides[2]};
+    const cuuint32_t b[5] = {(cuuint32_t)L::kElems, 1, box[0], box[1], box[2]}, step[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), d, st, b, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              L::kElems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t token = (cuuint64_t)D * 2, half = token * A.G.bs, all = (cuuint64_t)A.G.R * A.T;
+  const cuuint64_t g = A.G.g, hkv = A.G.Hkv, bs = A.G.bs, slots = (cuuint64_t)A.pool_rows;
+  const bool ok = encode(&m->tile, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, (cuuint32_t)spt}) &&
+                  encode(&m->slot, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, 1}) &&
+                  encode(&m->q, A.q, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok});
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int NW>
+cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
+  constexpr int kTile = Tiles<NW>::kTile;
+  using L = Lines<D, kTile>;
+  const int32_t pitch = A.G.bs * L::kBytes % 128 ? A.G.bs + 1 : A.G.bs, spt = kTile / pitch;
+  // a warpgroup's rows: all heads of as many tokens as fit 128
+  const int32_t q_tok = A.T < 128 / A.G.g ? A.T : 128 / A.G.g, gr = q_tok * A.G.g, q_rows = (gr + 7) / 8 * 8;
+  const int32_t groups = (A.T + NW * q_tok - 1) / (NW * q_tok);
+  // Two CTAs on an SM where TMEM allows (2 x 256 columns), else one: the ring takes what is left of
+  // that share of the shared memory. It is never so small that a third CTA, or one of 256 columns beside one of 512, could
+  // come to wait for TMEM (two clusters that each hold what the other waits for would wait for ever).
+  const bool two = D <= 128 && NW == 1;
+  const size_t share = two ? 115712 : kMaxSmem, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb);
+  int32_t ring = (int32_t)((share - rest) / L::kBuf);
+  if (ring > kMaxRing) ring = kMaxRing;
+  size_t smem = rest + (size_t)ring * L::kBuf;
+  const size_t third = 233472 / 3, least = two ? third : 2 * third;
+  if (smem < least) smem = least;
+  const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
+  const int32_t per_sm = two ? 2 : 1;
+  const Shape shape = pick_shape(items, groups, per_sm, most_tiles(A, spt, NW * q_tok), NW == 1 ? kMmaCosts : kMmaCostsWide,
+                                 cluster_room(NW * 160 + 32, per_sm));
+  ChunkMaps maps;
+  if (cudaError_t e = make_maps<D, kTile>(A, spt, q_tok, &maps)) return e;
+  return launch_cluster(chunk_mma_kernel<D, NW>, items, shape, NW * 160 + 32, smem, s, A, maps, shape, ring, q_tok, q_rows, pitch);
+}
+
+cudaError_t run_mma_d(const ChunkArgs& A, cudaStream_t s) {
+  const bool wide = (int64_t)A.T * A.G.g > 128;
+  switch (A.G.d) {
+    case 32: return wide ? run_mma<32, 2>(A, s) : run_mma<32, 1>(A, s);
+    case 64: return wide ? run_mma<64, 2>(A, s) : run_mma<64, 1>(A, s);
+    case 96: return wide ? run_mma<96, 2>(A, s) : run_mma<96, 1>(A, s);
+    case 128: return wide ? run_mma<128, 2>(A, s) : run_mma<128, 1>(A, s);
+    case 160: return run_mma<160, 1>(A, s);
+    case 192: return run_mma<192, 1>(A, s);
+    case 224: return run_mma<224, 1>(A, s);
+    default: return run_mma<256, 1>(A, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_chunk(const ChunkArgs& A, cudaStream_t s) { return A.G.dtype == OKV_F32 ? run_f32_d(A, s) : run_mma_d(A, s); }
+
+}  // namespace okv
+
+extern "C" okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                              int32_t block_size, int32_t slots, int32_t dtype, const void* pool, const int32_t* slot_block,
+                                              const int32_t* lengths, const int32_t* counts, int32_t window, int32_t sinks, const void* q,
+                                              void* out, float* lse, const float* weight, float* weight_out, void* stream) {
+  using namespace okv;
+  Geom G{};
+  if (!tree_geom(n_requests, q_heads, kv_heads, head_dim, block_size, slots, dtype, &G)) return OKV_EINVAL;
+  if (n_new <= 0 || (int64_t)n_requests * kv_heads * n_new > INT32_MAX || (int64_t)n_new * G.g > INT32_MAX) return OKV_EINVAL;
+  if (window < 0 || sinks < 0) return OKV_EINVAL;
+  if (!pool || !slot_block || !lengths || !q || !out || (weight_out && !lse) || (weight && !weight_out)) return OKV_EINVAL;
+  if (!aligned16(pool) || !aligned16(q) || !aligned16(out)) return OKV_EINVAL;
+  if (okv_status st = check_stream(stream)) return st;
+  ChunkArgs A{};
+  A.G = G;
+  A.T = n_new;
+  A.pool = (const uint8_t*)pool;
+  A.slot_block = slot_block;
+  A.len = lengths;
+  A.counts = counts;
+  A.q = q;
+  A.out = out;
+  A.lse = lse;
+  A.window = window ? window : INT32_MAX;
+  A.sinks = sinks;
+  A.weight = weight;
+  A.weight_out = weight_out;
+  A.pool_rows = (int64_t)n_requests * kv_heads * slots;
+  if (launch_attend_chunk(A, (cudaStream_t)stream) != cudaSuccess) return OKV_ECUDA;
+  if (weight_out && launch_weigh_chunk(A, (cudaStream_t)stream) != cudaSuccess) return OKV_ECUDA;
+  return OKV_OK;
+}

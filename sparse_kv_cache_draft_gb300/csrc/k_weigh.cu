@@ -1,0 +1,451 @@
+// The attention weight that each slot of a paged pool draws from a chunk of new tokens.
+//
+//   weight_out[s] = weight[s] + sum over the rows (t, head) of the unit and the tokens j of slot s that the row sees of
+//                   exp(q . k_j / sqrt(d) - lse)
+// with the sums lse that the attention of the chunk (k_chunk.cu) left. A CTA takes a tile of the unit's slots and every row
+// that sees any of them, so that a slot's sum is one CTA's, in one order, and nothing is added by atomics. The product is
+// taken as K Q^T: a thread then has one token and sums over the rows in registers, without an exchange.
+#include <stddef.h>
+
+#include "okv_chunk.h"
+#include "tiles.cuh"
+
+namespace okv {
+namespace {
+
+// One CTA's share: a tile of slots of a unit.
+struct Site {
+  int32_t r, h, cnt, len;
+  int32_t slot0, slots;  // of the unit
+};
+__device__ __forceinline__ Site make_site(const ChunkArgs& A, int32_t spt, int32_t tiles) {
+  Site s;
+  const int32_t ua = blockIdx.x / tiles;
+  s.slot0 = (blockIdx.x - ua * tiles) * spt;
+  s.slots = min(spt, A.G.kb - s.slot0);
+  s.r = ua / A.G.Hkv;
+  s.h = ua - s.r * A.G.Hkv;
+  s.len = A.len[s.r];
+  s.cnt = new_tokens(A, s.r, s.len);
+  return s;
+}
+
+// Rows [lo, hi) of the unit's g cnt that see token `off` of block b.
+struct Rows {
+  int32_t lo, hi;
+};
+__device__ __forceinline__ Rows rows_of(const ChunkArgs& A, const Site& s, int32_t b, int32_t off) {
+  const int64_t t0 = (int64_t)b * A.G.bs + off - s.len;  // the first token that is not before it
+  if (b < 0 || t0 >= s.cnt) return {0, 0};
+  int64_t t1 = t0 + s.len < A.sinks ? s.cnt : t0 + A.window;
+  if (t1 > s.cnt) t1 = s.cnt;
+  const int64_t from = t0 > 0 ? t0 : 0;
+  if (t1 <= from) return {0, 0};
+  return {(int32_t)from * A.G.g, (int32_t)t1 * A.G.g};
+}
+
+// The exponent's part of a row: p = 2^(score * scale + shift). Rows that see nothing have no weights.
+__device__ __forceinline__ float shift_of(const ChunkArgs& A, const Site& s, int32_t m) {
+  if (m >= s.cnt * A.G.g) return -INFINITY;
+  const int32_t t = m / A.G.g, j = m - t * A.G.g;
+  const float x = A.lse[((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j];
+  return x == -INFINITY ? x : -x * kLog2e;
+}
+
+// Slots that nothing is added to.
+__device__ __forceinline__ void copy_weights(const ChunkArgs& A, const Site& s) {
+  const int64_t first = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb + s.slot0;
+  for (int32_t k = threadIdx.x; k < s.slots; k += blockDim.x) A.weight_out[first + k] = A.weight ? A.weight[first + k] : 0.f;
+}
+
+// ---- tensor cores: bf16 ------------------------------------------------------------------------------
+//
+// K of the tile (128 tokens) stays in shared memory, the rows' queries come in tiles of up to 128 through a ring, and
+//   S^T = K Q^T   128 tokens x 128 rows, in two TMEM buffers, each a warpgroup's in turn
+// so that one warpgroup sums while the other's product runs. Two CTAs share an SM up to d 128. As many exponentials as
+// the tensor cores have multiply-adds / d: both are near their rates at once.
+constexpr int kTok = 128, kThreads = 320;  // two warpgroups, a warp that copies, one that multiplies
+
+struct Bars {
+  uint64_t k_full, full[4], empty[4], s_full[2], s_empty[2], drain;
+  int32_t lo, hi, failed;
+  uint32_t tmem;
+  float shift[2][2][128];
+  float part[2][128];
+};
+
+__device__ __forceinline__ void wg_sync(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
+
+struct WeighMaps {
+  CUtensorMap tile, slot, q;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
+weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const int32_t tiles, const int32_t ring, const int32_t q_tok, const int32_t pitch) {
+  using L = Lines<D, kTok>;
+  constexpr uint32_t kDesc = mma_desc_bf16(128, 128, false);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ks = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* rs = ks + L::kBuf;  // [ring][chunks][128][line]
+  Bars& B = *reinterpret_cast<Bars*>(rs + (size_t)ring * L::kBuf);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const bool is_copy = warp == 8, is_mma = warp == 9;
+  const int32_t g = A.G.g, gr = q_tok * g, bs = A.G.bs, spt = kTok / pitch;
+  if (is_copy) {
+    if (lane < 3) tma_prefetch_map(&M.tile + lane);
+    for (int i = lane; i < (int)(offsetof(Bars, lo) / 8); i += 32) {
+      constexpr int kSE = offsetof(Bars, s_empty) / 8;
+      mbar_init(smem_u32(&B.k_full + i), i >= kSE && i < kSE + 2 ? 128 : 1);
+    }
+    if (lane == 0) B.lo = INT32_MAX, B.hi = 0, B.failed = 0;
+    fence_mbar_init();
+  } else if (!is_mma) {
+    // rows of a tile that no copy fills: their scores are zero, their weights with them
+    if (gr < 128)
+      for (int32_t i = tid; i < ring * (L::kBuf / 16); i += 256) reinterpret_cast<uint4*>(rs)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  grid_wait();
+  const Site s = make_site(A, spt, tiles);
+  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  const int j = tid & 127, k = j / pitch, off = j - k * pitch;
+  Rows mine{0, 0};
+  if (!is_copy && !is_mma && k < s.slots && off < bs) mine = rows_of(A, s, A.slot_block[unit + s.slot0 + k], off);
+  __syncthreads();
+  if (tid < 128) {
+    const int32_t lo = __reduce_min_sync(0xffffffffu, mine.lo < mine.hi ? mine.lo : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, mine.hi);
+    if (lane == 0 && hi) atomicMin(&B.lo, lo), atomicMax(&B.hi, hi);
+  }
+  __syncthreads();
+  if (B.hi == 0) {  // no row sees any of them
+    grid_go();
+    copy_weights(A, s);
+    return;
+  }
+  const int32_t first = B.lo / gr, n = (B.hi + gr - 1) / gr - first;  // tiles of rows
+  if (is_mma) tmem_alloc(smem_u32(&B.tmem), 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_go();  // the TMEM is allocated
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  auto warp_wait = [&](uint64_t& bar, int32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
+  };
+  auto fail = [&] { *(volatile int32_t*)&B.failed = 1; };
+
+  if (is_copy) {
+    fence_proxy_async();
+    __syncwarp();
+    const uint32_t k_bar = smem_u32(&B.k_full);
+    if (lane == 0) mbar_expect_tx(k_bar, (uint32_t)(s.slots * bs * D * 2));
+    __syncwarp();
+    if (pitch == bs && s.slots == spt) {
+      if (lane < L::kChunks) tma_load_5d(smem_u32(ks) + lane * L::kChunk, &M.tile, k_bar, 0, lane, 0, 0, (int32_t)unit + s.slot0);
+    } else {
+      for (int32_t x = lane; x < s.slots * L::kChunks; x += 32) {
+        const int32_t e = x / L::kChunks, c = x % L::kChunks;
+        tma_load_5d(smem_u32(ks) + c * L::kChunk + e * pitch * L::kBytes, &M.slot, k_bar, 0, c, 0, 0, (int32_t)unit + s.slot0 + e);
+      }
+    }
+    int32_t issued = 0;
+    for (; issued < n; ++issued) {
+      const int32_t b = issued % ring;
+      if (issued >= ring && !warp_wait(B.empty[b], (issued / ring - 1) & 1)) {
+        fail();
+        break;
+      }
+      const uint32_t bar = smem_u32(&B.full[b]);
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)(gr * D * 2));
+      __syncwarp();
+      if (lane < L::kChunks)
+        tma_load_5d(smem_u32(rs) + b * L::kBuf + lane * L::kChunk, &M.q, bar, 0, lane, 0, s.h, s.r * A.T + (first + issued) * q_tok);
+    }
+    // what is in flight lands before the shared memory is given up, whatever the others did (bounded)
+    for (int32_t i = issued > ring ? issued - ring : 0; i < issued; ++i) mbar_wait_timed(smem_u32(&B.full[i % ring]), (i / ring) & 1);
+    mbar_wait_timed(k_bar, 0);
+  } else if (is_mma) {
+    const bool one = lane == 0;
+    constexpr int kSteps = L::kElems / 16;
+    constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+    const uint32_t kd = smem_desc_lo(smem_u32(ks), 16), qd = smem_desc_lo(smem_u32(rs), 16);
+    bool ok = warp_wait(B.k_full, 0);
+    for (int32_t i = 0; i < n && ok; ++i) {
+      const int w = i & 1, b = i % ring;
+      ok = warp_wait(B.full[b], (i / ring) & 1) && (i < 2 || warp_wait(B.s_empty[w], (i / 2 - 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(tmem + w * 128, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, qd + b * (L::kBuf >> 4) + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi,
+               kDesc, c > 0, one);
+      mma_commit(smem_u32(&B.s_full[w]), one);
+      mma_commit(smem_u32(&B.empty[b]), one);
+    }
+    if (!ok) fail();
+    mma_commit(smem_u32(&B.drain), one);
+    warp_wait(B.drain, 0);
+  } else {
+    const int w = warp >> 2;
+    const uint32_t my = tmem + w * 128 + ((uint32_t)(warp & 3) << 21);
+    const float scale = kLog2e * rsqrtf((float)D);
+    const float2 scale2 = make_float2(scale, scale);
+    float total = 0.f;
+    if (w < n) B.shift[w][0][j] = j < gr ? shift_of(A, s, (first + w) * gr + j) : -INFINITY;
+    wg_sync(w);
+    for (int32_t i = w; i < n; i += 2) {
+      const float* shift = B.shift[w][i / 2 & 1];
+      const float next = i + 2 < n && j < gr ? shift_of(A, s, (first + i + 2) * gr + j) : -INFINITY;
+      const int32_t m0 = (first + i) * gr, lo = mine.lo - m0, span = mine.hi - mine.lo;
+      const bool full = lo <= 0 && mine.hi >= m0 + gr, some = mine.lo < m0 + gr && mine.hi > m0;
+      if (!warp_wait(B.s_full[w], (i / 2) & 1)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+      if (__any_sync(0xffffffffu, some)) {
+        const bool masked = __any_sync(0xffffffffu, !full) != 0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(x, my + c);
+          tmem_wait_ld(x);
+          if (c == 96) {  // all of it read
+            tc_fence_before();
+            mbar_arrive(smem_u32(&B.s_empty[w]));
+          }
+          float4 sh[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sh[e] = *reinterpret_cast<const float4*>(shift + c + 4 * e);
+          float2 p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2,
+                                  e & 1 ? make_float2(sh[e / 2].z, sh[e / 2].w) : make_float2(sh[e / 2].x, sh[e / 2].y));
+            p[e] = make_float2(ex2(y.x), ex2(y.y));
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if ((uint32_t)(c + 2 * e - lo) >= (uint32_t)span) p[e].x = 0.f;
+              if ((uint32_t)(c + 2 * e + 1 - lo) >= (uint32_t)span) p[e].y = 0.f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            sum0 = add2(sum0, p[e]);
+            sum1 = add2(sum1, p[e + 1]);
+          }
+        }
+      } else {
+        tc_fence_before();
+        mbar_arrive(smem_u32(&B.s_empty[w]));
+      }
+      sum0 = add2(sum0, sum1);
+      total += sum0.x + sum0.y;
+      B.shift[w][(i / 2 & 1) ^ 1][j] = next;
+      wg_sync(w);
+    }
+    B.part[w][j] = total;
+  }
+  __syncthreads();
+  const bool failed = *(volatile int32_t*)&B.failed != 0;
+  for (int32_t e = tid; e < s.slots; e += kThreads) {
+    const int64_t at = unit + s.slot0 + e;
+    float sum = 0.f;
+    for (int32_t i = e * pitch; i < e * pitch + bs && !failed; ++i) sum += B.part[0][i] + B.part[1][i];
+    A.weight_out[at] = (A.weight ? A.weight[at] : 0.f) + sum;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (is_mma) {
+    tc_fence_after();
+    tmem_free(tmem, 256);
+  }
+}
+
+// ---- binary32 ------------------------------------------------------------------------------------------
+//
+// Products of three parts (mma_f32), K of 64 tokens as the rows, queries in tiles of 32 as the columns; a score that is not
+// finite (an operand's parts may not add up to it) is taken again by plain products. A warp has 16 tokens.
+constexpr int kF32Tok = 64, kF32Rows = 32, kF32Threads = 128;
+__host__ __device__ constexpr int f32_pitch(int d) { return d + 4; }
+__host__ __device__ constexpr size_t f32_smem(int d) { return (size_t)(kF32Tok + kF32Rows) * f32_pitch(d) * 4 + (kF32Rows + kF32Tok) * 4 + 16; }
+
+template <int DV>
+__global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs A, const int32_t tiles, const int32_t q_tok) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int d = DV * 32, pitch = f32_pitch(d), kPieces = d / 4, NT = kF32Rows / 8;
+  float* ks = reinterpret_cast<float*>(smem);  // [64][pitch]
+  float* qs = ks + kF32Tok * pitch;            // [32][pitch]
+  float* shift = qs + kF32Rows * pitch;        // [32]
+  float* part = shift + kF32Rows;              // [64]
+  int32_t* range = reinterpret_cast<int32_t*>(part + kF32Tok);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
+  const int32_t g = A.G.g, gr = q_tok * g, bs = A.G.bs, spt = kF32Tok / bs;
+  if (tid == 0) range[0] = INT32_MAX, range[1] = 0;
+  grid_wait();
+  grid_go();
+  const Site s = make_site(A, spt, tiles);
+  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
+  auto rows_at = [&](int32_t j) {
+    const int32_t k = j / bs;
+    return k < s.slots ? rows_of(A, s, A.slot_block[unit + s.slot0 + k], j - k * bs) : Rows{0, 0};
+  };
+  const Rows mine[2] = {rows_at(warp * 16 + gi), rows_at(warp * 16 + gi + 8)};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int32_t lo = __reduce_min_sync(0xffffffffu, mine[i].lo < mine[i].hi ? mine[i].lo : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, mine[i].hi);
+    if (lane == 0 && hi) atomicMin(&range[0], lo), atomicMax(&range[1], hi);
+  }
+  __syncthreads();
+  if (range[1] == 0) {
+    copy_weights(A, s);
+    return;
+  }
+  const int32_t first = range[0] / gr, end = (range[1] + gr - 1) / gr;
+  for (int32_t i = tid; i < kF32Tok * kPieces; i += kF32Threads) {
+    const int32_t j = i / kPieces, c = i % kPieces, k = j / bs;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < s.slots) x = *reinterpret_cast<const float4*>(A.pool + (unit + s.slot0 + k) * A.G.block_bytes + ((int64_t)(j - k * bs) * d + c * 4) * 4);
+    *reinterpret_cast<float4*>(ks + j * pitch + c * 4) = x;
+  }
+  const float scale = kLog2e / sqrtf((float)d);
+  float total[2] = {0.f, 0.f};
+  for (int32_t i = first; i < end; ++i) {
+    __syncthreads();  // the tile before has been read
+    const int32_t m0 = i * gr;
+    for (int32_t x = tid; x < kF32Rows * kPieces; x += kF32Threads) {
+      const int32_t row = x / kPieces, c = x % kPieces, m = m0 + row, t = m / g;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < gr && t < s.cnt)
+        y = *reinterpret_cast<const float4*>((const float*)A.q + ((((int64_t)s.r * A.T + t) * A.G.Hq + s.h * g + m - t * g) * d + c * 4));
+      *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = y;
+    }
+    if (tid < kF32Rows) shift[tid] = tid < gr ? shift_of(A, s, m0 + tid) : -INFINITY;
+    __syncthreads();
+    float sc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    const float* ka = ks + (warp * 16 + gi) * pitch + ti;
+    const float* qr = qs + gi * pitch + ti;
+#pragma unroll 4
+    for (int k = 0; k < d; k += 8) {
+      const Parts a[4] = {parts_of(ka[k]), parts_of(ka[k + 8 * pitch]), parts_of(ka[k + 4]), parts_of(ka[k + 8 * pitch + 4])};
+      Parts b[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) b[n][0] = parts_of(qr[n * 8 * pitch + k]), b[n][1] = parts_of(qr[n * 8 * pitch + k + 4]);
+      mma_f32<NT>(sc, a, b);
+    }
+    // tokens gi (sc[.][0], sc[.][1]) and gi + 8; rows 8 n + 2 ti and the next
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 8 * n + 2 * ti + (e & 1);
+        const Rows& v = mine[e >> 1];
+        if (m0 + row < v.lo || m0 + row >= v.hi || row >= gr) continue;
+        float x = sc[n][e];
+        if (!is_finite(x)) {
+          const float *y = ks + (warp * 16 + gi + 8 * (e >> 1)) * pitch, *z = qs + row * pitch;
+          x = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < d; ++k) x = fmaf(y[k], z[k], x);
+        }
+        sum[e >> 1] += ex2(fmaf(x, scale, shift[row]));
+      }
+    total[0] += sum[0];
+    total[1] += sum[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    total[i] += __shfl_xor_sync(0xffffffffu, total[i], 1);
+    total[i] += __shfl_xor_sync(0xffffffffu, total[i], 2);
+    if (ti == 0) part[warp * 16 + gi + 8 * i] = total[i];
+  }
+  __syncthreads();
+  for (int32_t e = tid; e < s.slots; e += kF32Threads) {
+    const int64_t at = unit + s.slot0 + e;
+    float sum = 0.f;
+    for (int32_t i = e * bs; i < e * bs + bs; ++i) sum += part[i];
+    A.weight_out[at] = (A.weight ? A.weight[at] : 0.f) + sum;
+  }
+}
+
+// ---- launches ----------------------------------------------------------------------------------------------
+
+template <typename... P, typename... Q>
+cudaError_t launch_plain(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t s, Q&&... args) {
+  return launch_cluster(kernel, ctas, Shape{1, (int32_t)ctas, 1}, threads, smem, s, std::forward<Q>(args)...);
+}
+
+template <int DV>
+cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {
+  const int32_t spt = kF32Tok / A.G.bs, tiles = (A.G.kb + spt - 1) / spt;
+  return launch_plain(weigh_f32_kernel<DV>, (int64_t)A.G.R * A.G.Hkv * tiles, kF32Threads, f32_smem(DV * 32), s, A, tiles, kF32Rows / A.G.g);
+}
+
+template <int D>
+cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
+  using L = Lines<D, kTok>;
+  const int32_t pitch = A.G.bs * L::kBytes % 128 ? A.G.bs + 1 : A.G.bs, spt = kTok / pitch, tiles = (A.G.kb + spt - 1) / spt;
+  const int32_t q_tok = A.T < 128 / A.G.g ? A.T : 128 / A.G.g;
+  const size_t third = 233472 / 3;  // no third CTA comes to wait for TMEM
+  const size_t rest = 1024 + sizeof(Bars), share = D <= 128 ? 115712 : kMaxSmem;
+  int32_t ring = (int32_t)((share - rest) / L::kBuf) - 1;
+  if (ring > 4) ring = 4;
+  size_t smem = rest + (size_t)(ring + 1) * L::kBuf;
+  if (smem < third) smem = third;
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  WeighMaps m;
+  auto encode = [&](CUtensorMap* map, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[3], const cuuint32_t (&box)[3]) {
+    const cuuint64_t d[5] = {(cuuint64_t)L::kElems, (cuuint64_t)L::kChunks, dims[0], dims[1], dims[2]};
+    const cuuint64_t st[4] = {(cuuint64_t)L::kBytes, strides[0], strides[1], strides[2]};
+    const cuuint32_t b[5] = {(cuuint32_t)L::kElems, 1, box[0], box[1], box[2]}, step[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), d, st, b, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              L::kElems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t token = (cuuint64_t)D * 2, half = token * A.G.bs, all = (cuuint64_t)A.G.R * A.T;
+  const cuuint64_t g = A.G.g, hkv = A.G.Hkv, bs = A.G.bs, slots = (cuuint64_t)A.pool_rows;
+  if (!encode(&m.tile, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, (cuuint32_t)spt}) ||
+      !encode(&m.slot, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, 1}) ||
+      !encode(&m.q, A.q, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok}))
+    return cudaErrorInvalidValue;
+  return launch_plain(weigh_mma_kernel<D>, (int64_t)A.G.R * A.G.Hkv * tiles, kThreads, smem, s, A, m, tiles, ring, q_tok, pitch);
+}
+
+}  // namespace
+
+cudaError_t launch_weigh_chunk(const ChunkArgs& A, cudaStream_t s) {
+  const int32_t v = A.G.d / 32;
+  if (A.G.dtype == OKV_F32) {
+    switch (v) {
+      case 1: return run_f32<1>(A, s);
+      case 2: return run_f32<2>(A, s);
+      case 3: return run_f32<3>(A, s);
+      case 4: return run_f32<4>(A, s);
+      case 5: return run_f32<5>(A, s);
+      case 6: return run_f32<6>(A, s);
+      case 7: return run_f32<7>(A, s);
+      default: return run_f32<8>(A, s);
+    }
+  }
+  switch (v) {
+    case 1: return run_mma<32>(A, s);
+    case 2: return run_mma<64>(A, s);
+    case 3: return run_mma<96>(A, s);
+    case 4: return run_mma<128>(A, s);
+    case 5: return run_mma<160>(A, s);
+    case 6: return run_mma<192>(A, s);
+    case 7: return run_mma<224>(A, s);
+    default: return run_mma<256>(A, s);
+  }
+}
+
+}  // namespace okv

@@ -446,6 +446,72 @@ PyObject* attend_tree_static(PyObject*, PyObject* const* args, Py_ssize_t nargs,
   });
 }
 
+Signature<17> chunk_sig{"attend_chunk_static", 9, 0b00011111000111111,
+                        {"pool", "slot_block", "lengths", "counts", "q", "out", "lse", "weight", "weight_out", "q_heads", "kv_heads", "head_dim", "block_size",
+                         "slots", "window", "sinks", "stream"}, {}};
+
+PyObject* attend_chunk_static(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  return guarded([&]() -> PyObject* {
+    PyObject* a[17];
+    chunk_sig.bind(args, nargs, kwnames, a);
+    int dev;
+    const int32_t dt = storage(a[0], "pool", &dev);
+    const at::Tensor& qt = tensor(a[4], "q");
+    if (qt.dim() != 4) refuse(a[4], "q", PyUnicode_FromString("new tokens [R][T][q_heads][head_dim]"));
+    const Types& st = dt == OKV_F32 ? kF32 : kBf16;
+    const int64_t R = qt.size(0), T = qt.size(1), hq = as_i32(a[9], "q_heads"), hkv = as_i32(a[10], "kv_heads"),
+                  d = as_i32(a[11], "head_dim"), bs = as_i32(a[12], "block_size"), kb = as_i32(a[13], "slots");
+    const int32_t window = given(a[14]) ? as_i32(a[14], "window") : 0, sinks = given(a[15]) ? as_i32(a[15], "sinks") : 0;
+    const int32_t r = count(R, "q"), t = count(T, "q");
+    void* pool = address(a[0], "pool", {R, hkv, kb, 2, bs, d}, st, dev);
+    void* slot_block = address(a[1], "slot_block", {R, hkv, kb}, kInt, dev);
+    void* lengths = address(a[2], "lengths", {R}, kInt, dev);
+    void* counts = optional(a[3], "counts", {R}, kInt, dev);
+    void* q = address(a[4], "q", {R, T, hq, d}, st, dev);
+    void* out = address(a[5], "out", {R, T, hq, d}, st, dev);
+    void* lse = optional(a[6], "lse", {R, T, hq}, kF32, dev);
+    void* weight = optional(a[7], "weight", {R, hkv, kb}, kF32, dev);
+    void* weight_out = given(a[8]) ? address(a[8], "weight_out", {R, hkv, kb}, kF32, dev) : weight;
+    if (weight_out && !lse) raise(PyExc_ValueError, "lse: the weights need it");
+    Launch at(dev, a[16]);
+    return launch("okv_attend_chunk_static", [&] {
+      return okv_attend_chunk_static(r, t, (int32_t)hq, (int32_t)hkv, (int32_t)d, (int32_t)bs, (int32_t)kb, dt, pool, (const int32_t*)slot_block,
+                                     (const int32_t*)lengths, (const int32_t*)counts, window, sinks, q, out, (float*)lse, (const float*)weight,
+                                     (float*)weight_out, at.stream);
+    });
+  });
+}
+
+Signature<13> evict_sig{"evict_static", 6, 0b0001111001111,
+                        {"slot_block", "weight", "lengths", "counts", "slot_block_out", "weight_out", "n_new", "kv_heads", "block_size", "slots", "sinks",
+                         "recent", "stream"}, {}};
+
+PyObject* evict_static(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  return guarded([&]() -> PyObject* {
+    PyObject* a[13];
+    evict_sig.bind(args, nargs, kwnames, a);
+    const at::Tensor& sb = tensor(a[0], "slot_block");
+    if (!sb.is_cuda()) raise(PyExc_TypeError, "slot_block: expected a CUDA tensor");
+    if (sb.dim() != 3) refuse(a[0], "slot_block", PyUnicode_FromString("slot tables [R][kv_heads][slots]"));
+    const int dev = (int)sb.get_device();
+    const int32_t n_new = as_i32(a[6], "n_new"), hkv = as_i32(a[7], "kv_heads"), bs = as_i32(a[8], "block_size"), kb = as_i32(a[9], "slots");
+    const int32_t sinks = given(a[10]) ? as_i32(a[10], "sinks") : 0, recent = given(a[11]) ? as_i32(a[11], "recent") : 0;
+    const int64_t R = sb.size(0);
+    const int32_t r = count(R, "slot_block");
+    void* slot_block = address(a[0], "slot_block", {R, hkv, kb}, kInt, dev);
+    void* weight = address(a[1], "weight", {R, hkv, kb}, kF32, dev);
+    void* lengths = address(a[2], "lengths", {R}, kInt, dev);
+    void* counts = optional(a[3], "counts", {R}, kInt, dev);
+    void* slot_block_out = given(a[4]) ? address(a[4], "slot_block_out", {R, hkv, kb}, kInt, dev) : slot_block;
+    void* weight_out = given(a[5]) ? address(a[5], "weight_out", {R, hkv, kb}, kF32, dev) : weight;
+    Launch at(dev, a[12]);
+    return launch("okv_evict_static", [&] {
+      return okv_evict_static(r, n_new, hkv, bs, kb, (const int32_t*)lengths, (const int32_t*)counts, sinks, recent, (const int32_t*)slot_block,
+                              (const float*)weight, (int32_t*)slot_block_out, (float*)weight_out, at.stream);
+    });
+  });
+}
+
 PyObject* py_row_stride(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 2) raise(PyExc_TypeError, "_row_stride() takes 2 arguments (%zd given)", n);
@@ -469,6 +535,17 @@ PyMethodDef methods[] = {
      "okv_attend_tree_static: drafted tokens q, out [R][T][q_heads][head_dim], k, v [R][T][kv_heads][head_dim], mask\n"
      "[R][T] int64 or uint64 (bit j: drafted token j is attended), counts [R] int32 or None, over a pool of\n"
      "attend_static's layout."},
+    {"attend_chunk_static", (PyCFunction)(void*)attend_chunk_static, METH_FASTCALL | METH_KEYWORDS,
+     "attend_chunk_static($module, pool, slot_block, lengths, counts, q, out, lse=None, weight=None, weight_out=None, *, q_heads, kv_heads, head_dim, block_size, slots, window=0, sinks=0, stream=None)\n--\n\n"
+     "okv_attend_chunk_static: new tokens q, out [R][T][q_heads][head_dim] at positions lengths[r] + t, over the resident\n"
+     "tokens at their positions and before (and less than window before, or among the first sinks); lse [R][T][q_heads]\n"
+     "float32; weight [R][kv_heads][slots] float32 has what each slot draws added to it, in place or into weight_out\n"
+     "(which alone starts from zero); counts [R] int32 or None; over a pool of attend_static's layout."},
+    {"evict_static", (PyCFunction)(void*)evict_static, METH_FASTCALL | METH_KEYWORDS,
+     "evict_static($module, slot_block, weight, lengths, counts, slot_block_out=None, weight_out=None, *, n_new, kv_heads, block_size, slots, sinks=0, recent=0, stream=None)\n--\n\n"
+     "okv_evict_static: slots of slot_block [R][kv_heads][slots] int32 for the blocks that the next counts[r] tokens begin (None:\n"
+     "n_new each), empty ones, then those of least weight [R][kv_heads][slots] float32, but not of the first sinks or the last\n"
+     "recent tokens; in place, or into slot_block_out and weight_out."},
     {"_row_stride", (PyCFunction)(void*)py_row_stride, METH_FASTCALL,
      "_row_stride($module, t, width, /)\n--\n\nElements between the rows of t [...][width], whose leading dims are one run of rows."},
     {}};
@@ -478,7 +555,7 @@ PyModuleDef module_def{PyModuleDef_HEAD_INIT, "_calls", "Calls on rows and draft
 }  // namespace
 
 PyMODINIT_FUNC PyInit__calls() {
-  if (!rotary_sig.intern() || !rows_sig.intern() || !append_sig.intern() || !tree_sig.intern()) return nullptr;
+  if (!rotary_sig.intern() || !rows_sig.intern() || !append_sig.intern() || !tree_sig.intern() || !chunk_sig.intern() || !evict_sig.intern()) return nullptr;
   PyObject* binding = PyImport_ImportModule("sparse_kv_cache_draft_gb300.binding");
   if (!binding) return nullptr;
   g_error = PyObject_GetAttrString(binding, "OkvError");
