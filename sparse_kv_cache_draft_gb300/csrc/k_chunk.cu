@@ -133,11 +133,12 @@ __device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, const Span& s, 
   return o;
 }
 
-// Merges the cluster's partials and writes outputs and sums. Every thread of every CTA of the cluster calls it.
+// Merges the cluster's partials and writes outputs and sums. The first `threads` threads of every CTA of the cluster call it,
+// the others cluster_sync twice.
 template <typename T>
-__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask) {
+__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask, int32_t threads) {
   cluster_sync();
-  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, [&](int32_t row, int32_t c, float4 o, float M, float l) {
+  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, threads, [&](int32_t row, int32_t c, float4 o, float M, float l) {
     const int64_t at = row_place(A, s, s.row0 + row);
     store4((T*)A.out + at * A.G.d + c * 4, o);
     if (c == 0 && A.lse) A.lse[at] = lse_of(M, l);
@@ -186,8 +187,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Two warpgroups hold 128 scores to a thread, more registers than each thread of the block can have: the others, a whole
+// warpgroup (one warp idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
+template <int NW>
+constexpr int mma_threads() { return NW == 2 ? 384 : 192; }
+constexpr int kUpRegs = 224, kDownRegs = 56;
+
 template <int D, int NW>
-__global__ void __launch_bounds__(NW * 160 + 32, D <= 128 && NW == 1 ? 2 : 1)
+__global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
 chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t ring, const int32_t q_tok, const int32_t q_rows,
                  const int32_t pitch) {
   constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
@@ -203,7 +210,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4;
+  const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4 && warp <= NW * 5, is_soft = warp < NW * 4;
   const int32_t g = A.G.g, gr = q_tok * g;  // rows of a warpgroup: q_tok tokens, all heads of the group
   const int32_t bs = A.G.bs, spt = kTile / pitch;
   const bool tails = spt * bs < kTile;      // lines of a tile that no token has
@@ -216,7 +223,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 8 ? 128 : 1);
     if (lane == 0) B.failed = B.bad = 0;
     fence_mbar_init();
-  } else if (tails && !is_mma) {
+  } else if (tails && is_soft) {
     // lines that no copy writes meet weights of zero
     for (int32_t i = tid; i < ring * (L::kBuf / 16); i += NW * 128) reinterpret_cast<uint4*>(rs)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
@@ -243,7 +250,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
           tma_load_5d(smem_u32(qs) + (w * L::kChunks + c) * q_rows * L::kBytes, &M.q, q_bar, 0, c, 0, s.h, tok0 + s.row0 / g + w * q_tok);
     }
     __syncwarp();
-  } else if (is_mma) {
+  } else if (!is_soft) {
     if (warp == NW * 4 + 1) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
   } else {
     count_slots(A, s, warp, NW * 4, B.listed, all, some);
@@ -251,7 +258,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (!is_copy && !is_mma) place_slots(A, warp, NW * 4, B.listed, all, some, list_at);
+  if (is_soft) place_slots(A, warp, NW * 4, B.listed, all, some, list_at);
   __syncthreads();
   grid_go();  // the TMEM is allocated
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
@@ -266,8 +273,10 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
   };
   auto fail = [&] { *(volatile int32_t*)&B.failed = 1; };
-  float m_run = -INFINITY, l_run = 0.f;
 
+  if (!is_soft) {
+    if (NW == 2) registers_down<kDownRegs>();
+  }
   if (is_copy) {
     int32_t buf = 0, par = 0, issued = 0;  // the next buffer and the parity of its fill
     const int32_t uses = kS == 2 ? 2 * n + 1 : 2 * n;
@@ -375,7 +384,18 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       mma_commit(smem_u32(&B.drain[w]), one);
       warp_wait(B.drain[w], 0);
     }
+  }
+  if (!is_soft) {  // the others' ends: see below
+    __syncthreads();
+    if (s.parts > 1) cluster_sync(), cluster_sync();
+    __syncthreads();
+    if (warp == NW * 4 + 1) {
+      tc_fence_after();
+      tmem_free(tmem, kCols * NW);
+    }
   } else {
+    if (NW == 2) registers_up<kUpRegs>();
+    float m_run = -INFINITY, l_run = 0.f;
     const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
     const bool real = row < gr && wrow < s.rows, active = (warp & 3) * 32 < min(gr, s.rows - w * gr);
     const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
@@ -530,14 +550,10 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     }
     if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail();
     tc_fence_after();
-  }
-  __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
-  const bool failed = *(volatile int32_t*)&B.failed != 0;
-  if (warp < NW * 4) {
-    const int w = warp >> 2, row = tid & 127, wrow = w * gr + row;
-    const bool real = row < gr && wrow < s.rows, bad = B.bad && real && l_run != 0.f;
-    const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32, p = s.len + (s.row0 + wrow) / g;  // rows of this warp
-    const uint32_t my = tmem + w * kCols + ((uint32_t)(warp & 3) << 21) + kO;
+    __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
+    const bool failed = *(volatile int32_t*)&B.failed != 0;
+    const bool bad = B.bad && real && l_run != 0.f;
+    const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32;  // of this warp
     auto extra = [&](uint32_t (&o)[32], int c) {
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
@@ -559,7 +575,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         uint32_t o[32];
         __syncwarp();
         if (n > 0) {
-          tmem_ld32(o, my + c);
+          tmem_ld32(o, my + kO + c);
           tmem_wait_ld(o);
         }
         if (!real) continue;
@@ -599,7 +615,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           __syncwarp();
-          tmem_ld32(o, my + c);
+          tmem_ld32(o, my + kO + c);
           tmem_wait_ld(o);
           if (!real) continue;
           if (bad) extra(o, c);
@@ -609,13 +625,9 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         }
       }
     }
-  }
-  if (s.parts > 1) merge_chunk<__nv_bfloat16>(A, s, Partial{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4)}, 7);
-  tc_fence_before();
-  __syncthreads();
-  if (warp == NW * 4 + 1) {
-    tc_fence_after();
-    tmem_free(tmem, kCols * NW);
+    if (s.parts > 1) merge_chunk<__nv_bfloat16>(A, s, Partial{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4)}, 7, NW * 128);
+    tc_fence_before();
+    __syncthreads();
   }
 }
 
@@ -919,7 +931,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
     store4((float*)A.out + at * d + c * 4, x);
     if (c == 0 && A.lse) A.lse[at] = lse_of(M, sum);
   }
-  if (s.parts > 1) merge_chunk<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls)}, 0);
+  if (s.parts > 1) merge_chunk<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls)}, 0, kF32Threads);
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------
@@ -1008,10 +1020,10 @@ cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
   const int32_t per_sm = two ? 2 : 1;
   const Shape shape = pick_shape(items, groups, per_sm, most_tiles(A, spt, NW * q_tok), NW == 1 ? kMmaCosts : kMmaCostsWide,
-                                 cluster_room(NW * 160 + 32, per_sm));
+                                 cluster_room(mma_threads<NW>(), per_sm));
   ChunkMaps maps;
   if (cudaError_t e = make_maps<D, kTile>(A, spt, q_tok, &maps)) return e;
-  return launch_cluster(chunk_mma_kernel<D, NW>, items, shape, NW * 160 + 32, smem, s, A, maps, shape, ring, q_tok, q_rows, pitch);
+  return launch_cluster(chunk_mma_kernel<D, NW>, items, shape, mma_threads<NW>(), smem, s, A, maps, shape, ring, q_tok, q_rows, pitch);
 }
 
 cudaError_t run_mma_d(const ChunkArgs& A, cudaStream_t s) {

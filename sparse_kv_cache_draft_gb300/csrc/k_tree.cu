@@ -147,7 +147,7 @@ template <typename T>
 __device__ __forceinline__ void merge_cluster(const TreeArgs& A, const Site& s, const Partial& P, uint32_t bad_at, int32_t xor_mask) {
   cluster_sync();
   const uint64_t bad = ld_cluster_u64(cluster_map(bad_at, s.parts - 1));
-  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, [&](int32_t row, int32_t c, float4 o, float, float) {
+  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, blockDim.x, [&](int32_t row, int32_t c, float4 o, float, float) {
     const int32_t mrow = s.row0 + row;
     if (bad) add_not_finite<T>(A, s, bad & A.mask[(int64_t)s.r * A.T + mrow / A.G.g], c * 4, o);
     store4((T*)A.out + row_offset(A, s, mrow) + c * 4, o);

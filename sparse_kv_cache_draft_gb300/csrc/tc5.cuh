@@ -13,6 +13,12 @@ namespace okv {
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Registers of a thread from here on, by whole warpgroups: what some give up others may take.
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---- TMEM ---------------------------------------------------------------------------------------
 // Allocation is by columns (a power of two, at least 32) and by a whole warp; the warp that
 // allocated frees. An address is (lane << 16) | column; a warp reaches the 32 lanes of its

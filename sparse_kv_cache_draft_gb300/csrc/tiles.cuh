@@ -46,11 +46,13 @@ __device__ __forceinline__ uint32_t part_chunk(int32_t row, int32_t chunk, int32
 }
 
 // Merges the partials of a cluster's `split` CTAs, this one (`part`) a share of the outputs: finish(row, c, o, M, l) takes
-// dims 4 c .. 4 c + 3 of a row, its maximum and its sum. Between two cluster_sync that every thread of the cluster takes part in.
+// dims 4 c .. 4 c + 3 of a row, its maximum and its sum. By the first `threads` threads of each CTA, between two cluster_sync that
+// every thread of the cluster takes part in.
 template <typename F>
-__device__ __forceinline__ void merge_rows(int32_t part, int32_t split, int32_t rows, int32_t d, const Partial& P, int32_t xor_mask, F finish) {
+__device__ __forceinline__ void merge_rows(int32_t part, int32_t split, int32_t rows, int32_t d, const Partial& P, int32_t xor_mask, int32_t threads,
+                                           F finish) {
   const int32_t d4 = d / 4, total = rows * d4;
-  for (int32_t i = part * blockDim.x + threadIdx.x; i < total; i += split * blockDim.x) {
+  for (int32_t i = part * threads + threadIdx.x; i < total; i += split * threads) {
     const int32_t row = i / d4, c = i - row * d4;
     float M = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
