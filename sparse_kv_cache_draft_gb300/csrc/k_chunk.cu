@@ -169,7 +169,7 @@ struct Tiles {
 
 constexpr int kMaxRing = 12;
 struct MmaBars {
-  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2][2], pv_done[2][2], drain[2], turn[2];
+  uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2][2], pv_done[2][2], drain;
   Listed listed;
   uint32_t tmem;
   int32_t failed, bad;
@@ -188,7 +188,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two warpgroups hold 128 scores to a thread, more registers than each thread of the block can have: the others, a whole
-// warpgroup (one warp idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
+// warpgroup (two warps idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
 template <int NW>
 constexpr int mma_threads() { return NW == 2 ? 384 : 192; }
 constexpr int kUpRegs = 224, kDownRegs = 56;
@@ -210,17 +210,16 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool is_copy = warp == NW * 4, is_mma = warp > NW * 4 && warp <= NW * 5, is_soft = warp < NW * 4;
+  const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_soft = warp < NW * 4;
   const int32_t g = A.G.g, gr = q_tok * g;  // rows of a warpgroup: q_tok tokens, all heads of the group
   const int32_t bs = A.G.bs, spt = kTile / pitch;
   const bool tails = spt * bs < kTile;      // lines of a tile that no token has
   const uint32_t ring0 = smem_u32(rs);
   if (is_copy) {  // what reads no memory of the call
     if (lane < 3) tma_prefetch_map(&M.tile + lane);
-    // the barriers, one to a lane: a buffer is free when every warpgroup's product has read it
-    constexpr int kEmpty = offsetof(MmaBars, empty) / 8, kP = offsetof(MmaBars, p_full) / 8;
+    constexpr int kP = offsetof(MmaBars, p_full) / 8;
     for (int i = lane; i < (int)(offsetof(MmaBars, listed) / 8); i += 32)
-      mbar_init(smem_u32(B.full + i), i >= kEmpty && i < kEmpty + kMaxRing ? NW : i >= kP && i < kP + 8 ? 128 : 1);
+      mbar_init(smem_u32(B.full + i), i >= kP && i < kP + 8 ? 128 : 1);
     if (lane == 0) B.failed = B.bad = 0;
     fence_mbar_init();
   } else if (tails && is_soft) {
@@ -251,7 +250,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     }
     __syncwarp();
   } else if (!is_soft) {
-    if (warp == NW * 4 + 1) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
+    if (is_mma) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
   } else {
     count_slots(A, s, warp, NW * 4, B.listed, all, some);
   }
@@ -288,9 +287,13 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       const int32_t parity = par;
       if (++buf == ring) buf = 0, par ^= 1;
       if (i >= n) continue;  // the use that a further K would have
-      if (use >= ring && !warp_wait(B.empty[b], parity ^ 1)) {
-        ok = false;
-        break;
+      if (use >= ring) {
+        // with one S buffer K of tile j is free once S of tile j is there, V of tile j - 1 as well
+        const int32_t j = (use - ring + 1) / 2;
+        if (!(kS == 1 ? warp_wait(B.empty[j % kMaxRing], j / kMaxRing & 1) : warp_wait(B.empty[b], parity ^ 1))) {
+          ok = false;
+          break;
+        }
       }
       const int32_t e0 = (s.part + i * s.parts) * spt, ne = min(spt, list.n - e0), first = list.slot(e0);
       bool run = ne == spt && pitch == bs;
@@ -316,80 +319,124 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     }
     if (!ok || n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
   } else if (is_mma) {
-    const bool one = lane == 0;
+    // One warp for both warpgroups, in a fixed order: O of a tile and S of the next for one, then for the other. An answer from a
+    // barrier takes 150 to 350 cycles while the tensor cores read shared memory, so each barrier is asked ahead, behind
+    // MMAs that keep them busy meanwhile, and waited for only where it had not been passed by then. (A warp for
+    // each warpgroup, in turns, left the tensor cores idle for 400 of 1980 cycles a turn.)
+    if (elect_one()) {
     constexpr int kSteps = L::kElems / 16;
     constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
-    const int w = warp - NW * 4 - 1;  // the warpgroup it works for
-    const uint32_t my = tmem + w * kCols;
     const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
-    const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16) + w * L::kChunks * q_chunk, k_desc = smem_desc_lo(ring0, 16);
-    const uint32_t v_desc = smem_desc_lo(ring0, L::kChunk);
+    const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16), k_desc = smem_desc_lo(ring0, 16), v_desc = smem_desc_lo(ring0, L::kChunk);
     int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
+    bool ok = true;
     auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
       b += by;
       if (b >= ring) b -= ring, parity ^= 1;
     };
-    auto k_ready = [&] {
-      if (!warp_wait(B.full[kb], kp)) return false;
+    auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
+    auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
+      if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
       tc_fence_after();
-      return true;
     };
-    auto qk = [&](int32_t i) {
-      const uint32_t kd = k_desc + kb * (L::kBuf >> 4);
+    auto s_at = [&](int32_t i, int w) { return tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0); };
+    auto qk = [&](int32_t i, int w, int c0, int c1) {  // steps c0 .. c1 - 1 of S
+      const uint32_t kd = k_desc + kb * (L::kBuf >> 4), qd = q_desc + w * L::kChunks * q_chunk;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        mma_ss(my + (kS == 2 ? (i & 1) * kTile : 0), q_desc + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2,
-               kHi, kDescQK, c > 0, one);
-      mma_commit(smem_u32(&B.s_full[w][i & 1]), one);
-      mma_commit(smem_u32(&B.empty[kb]), one);
-      step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
+      for (int c = c0; c < c1; ++c)
+        mma_ss1(s_at(i, w), qd + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDescQK, c > 0);
+      if (c1 < D / 16) return;
+      mma_commit1(smem_u32(&B.s_full[w][i & 1]));
+      if (kS == 2) mma_commit1(smem_u32(&B.empty[kb]));
+      if (w == NW - 1) step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
     };
-    // Two warpgroups take turns at the tensor cores, O of a tile and S of the next at a time: while one has
-    // them, the other is at its softmax.
-    int32_t turns = 0;
-    auto my_turn = [&] { return NW == 1 || (w == 0 && turns == 0) || warp_wait(B.turn[w], (turns - (w == 0)) & 1); };
-    auto pass_on = [&] {
-      ++turns;
-      if (NW == 2 && one) mbar_arrive(smem_u32(&B.turn[w ^ 1]));
+    auto pv = [&](int32_t i, int w, int half) {
+      const uint32_t vd = v_desc + vb * (L::kBuf >> 4);
+#pragma unroll
+      for (int c = half * 4; c < half * 4 + 4; ++c)
+        mma_ts1(tmem + w * kCols + kO, s_at(i, w) + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV, i > 0 || c > 0);
+      if (half + 1 < kTile / 64) return;
+      if (kS == 2 || i + 1 == n) mma_commit1(smem_u32(&B.pv_done[w][i & 1]));
+      if (kS == 2) mma_commit1(smem_u32(&B.empty[vb]));
+      if (w == NW - 1) step(vb, vp, 2);
     };
-    bool ok = true;
+    constexpr int kHalf = D / 32;  // steps of half an S
     if (n > 0) {
-      ok = warp_wait(B.q_full, 0) && k_ready() && my_turn();
-      if (ok) qk(0);
-      pass_on();
+      passed(false, B.q_full, 0);
+      passed(false, B.full[kb], kp);
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        if (ok) qk(0, w, 0, D / 16);
+      if (ok) passed(false, B.full[vb], vp);
     }
-    for (int32_t i = 0; i < n && ok; ++i) {
-      if (i + 1 < n) ok = k_ready();
-      if (kS == 2 && ok && i + 1 < n) qk(i + 1);
-      ok = ok && warp_wait(B.full[vb], vp) && my_turn();
-      const uint32_t vd = v_desc + vb * (L::kBuf >> 4), p = my + (kS == 2 ? (i & 1) * kTile : 0);
-#pragma unroll
-      for (int half = 0; half < kTile / 64; ++half) {
-        ok = ok && warp_wait(B.p_full[w][i & 1][half], (i >> 1) & 1);
+    if (kS == 2) {
+      bool k_there = false;
+      for (int32_t i = 0; i < n && ok; ++i) {
+        if (i + 1 < n) {
+          passed(k_there, B.full[kb], kp);
+          if (ok) qk(i + 1, 0, 0, D / 16);
+        }
+        passed(ask(B.p_full[0][i & 1][0], (i >> 1) & 1), B.p_full[0][i & 1][0], (i >> 1) & 1);
         if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = half * 4; c < half * 4 + 4; ++c)
-          mma_ts(my + kO, p + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV, i > 0 || c > 0, one);
+        pv(i, 0, 0);
+        if (i + 1 < n) {
+          passed(ask(B.full[vb], vp), B.full[vb], vp);
+          k_there = i + 2 < n && ask(B.full[kb], kp);
+        }
       }
-      if (!ok) break;
-      mma_commit(smem_u32(&B.pv_done[w][i & 1]), one);
-      mma_commit(smem_u32(&B.empty[vb]), one);
-      step(vb, vp, 2);
-      if (kS == 1 && i + 1 < n) qk(i + 1);  // S takes the place of the P just used: the products run in order
-      pass_on();
+    } else {
+      bool next = false;  // what was asked last
+      if (n > 1 && ok) passed(false, B.full[kb], kp);
+      for (int32_t i = 0; i < n && ok; ++i) {
+        const int32_t parity = (i >> 1) & 1;
+        const bool more = i + 1 < n;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          uint64_t(&p)[2] = B.p_full[w][i & 1];
+          passed(next, p[0], parity);
+          if (!ok) break;
+          bool there = ask(p[1], parity);
+          pv(i, w, 0);
+          passed(there, p[1], parity);
+          if (!ok) break;
+          pv(i, w, 1);
+          if (!more) {
+            next = false;
+            continue;
+          }
+          // S takes the place of the P just used: the products run in order
+          if (w == 0) {
+            qk(i + 1, 0, 0, kHalf);
+            next = ask(B.p_full[NW - 1][i & 1][0], parity);
+            qk(i + 1, 0, kHalf, D / 16);
+          } else {
+            const bool v_there = ask(B.full[vb], vp);
+            qk(i + 1, 1, 0, kHalf);
+            passed(v_there, B.full[vb], vp);
+            int32_t b = kb, bp = kp;
+            step(b, bp, 2);
+            const bool k_there = i + 2 < n && ask(B.full[b], bp);
+            next = ask(B.p_full[0][(i + 1) & 1][0], ((i + 1) >> 1) & 1);
+            if (!ok) break;
+            qk(i + 1, 1, kHalf, D / 16);
+            if (i + 2 < n) passed(k_there, B.full[kb], kp);
+          }
+        }
+      }
     }
     if (!ok) {
       fail();
-      mma_commit(smem_u32(&B.drain[w]), one);
-      warp_wait(B.drain[w], 0);
+      mma_commit1(smem_u32(&B.drain));
+      mbar_wait_timed(smem_u32(&B.drain), 0);
     }
+    }
+    __syncwarp();
   }
   if (!is_soft) {  // the others' ends: see below
     __syncthreads();
     if (s.parts > 1) cluster_sync(), cluster_sync();
     __syncthreads();
-    if (warp == NW * 4 + 1) {
+    if (is_mma) {
       tc_fence_after();
       tmem_free(tmem, kCols * NW);
     }
@@ -402,6 +449,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     const float scale = kLog2e * rsqrtf((float)D);
     const int32_t p = s.len + (s.row0 + wrow) / g;
     if (!real) m_run = INFINITY;  // no vote below: what such a row holds moves no other row's maximum
+    float neg = real ? 0.f : -INFINITY;  // -m_run, 0 where there is none yet
     uint32_t ends[kWords];        // the places of a tile that a token has
 #pragma unroll
     for (int u = 0; u < kWords; ++u) {
@@ -443,6 +491,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         fail();
         break;
       }
+      if (kS == 1 && w == NW - 1 && row == 0) mbar_arrive(smem_u32(&B.empty[i % kMaxRing]));
       // With two S buffers, S of tile i follows O of tile i - 2, so this passes at once; it keeps each barrier's
       // waits in step with its phases, where tile i - 1's below is waited for only now and then
       if (kS == 2 && i > 1 && !warp_wait(B.pv_done[w][i & 1], ((i - 2) >> 1) & 1)) {
@@ -474,31 +523,55 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       }
       bool lost = false;
       const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
-      uint32_t a[kWords][32];
-      float neg = 0.f;
+      uint32_t a[kWords][32], pk[32];
+      float2 sum0, sum1;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      // scores of 64 columns as they count
+      auto mask = [&](int u0, int u1) {
+        if (!part_seen && !tails) return;
+#pragma unroll
+        for (int u = u0; u < u1; ++u)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(vis[u] >> e & 1)) a[u][e] = 0xFF800000u;
+      };
+      // the weights of 64 columns against m_run, and, where asked for, the maximum of as many
+      auto weights = [&](int half, int with_max) {
+        const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t *x0 = &a[2 * half][2 * e], *y0 = &a[2 * half + 1][2 * e];
+          float2 x = fma2(make_float2(__uint_as_float(x0[0]), __uint_as_float(x0[1])), scale2, neg2);
+          float2 y = fma2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])), scale2, neg2);
+          x = make_float2(ex2(x.x), ex2(x.y));
+          y = make_float2(ex2(y.x), ex2(y.y));
+          sum0 = add2(sum0, x);
+          sum1 = add2(sum1, y);
+          pk[e] = pack2(x.x, x.y);
+          pk[16 + e] = pack2(y.x, y.y);
+          if (with_max) {
+#pragma unroll
+            for (int u = 0; u < kWords; ++u) mx[u] = max3(mx[u], __uint_as_float(a[u][2 * e]), __uint_as_float(a[u][2 * e + 1]));
+          }
+        }
+      };
+      sum0 = sum1 = make_float2(0.f, 0.f);
       if (active) {
 #pragma unroll
         for (int u = 0; u < kWords; ++u) tmem_ld32(a[u], st + 32 * u);
 #pragma unroll
         for (int u = 0; u < kWords; ++u) tmem_wait_ld(a[u]);
-        if (part_seen || tails) {
-#pragma unroll
-          for (int u = 0; u < kWords; ++u)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(vis[u] >> e & 1)) a[u][e] = 0xFF800000u;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int u = 0; u < kWords; ++u)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]));
+        mask(0, kWords);
+        // The maximum moves in few tiles: the first weights are taken against the old one beside the search for the
+        // new one, and again where it moves (S is still there).
+        weights(0, 1);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         if (__any_sync(0xffffffffu, top > m_run + 8.f)) {
           const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
           const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
           m_run = mn;
           l_run *= f;
+          neg = m_run == -INFINITY ? 0.f : -m_run;
           if (i > 0) {
             // O has the products of tile i - 1; with one S buffer those came before S of this tile
             if (kS == 2) lost = !warp_wait(B.pv_done[w][(i - 1) & 1], ((i - 1) >> 1) & 1);
@@ -513,32 +586,23 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
               tmem_st16(my + kO + k, o);
             }
           }
+          tmem_ld32(a[0], st);
+          tmem_ld32(a[1], st + 32);
+          tmem_wait_ld(a[0]);
+          tmem_wait_ld(a[1]);
+          mask(0, 2);
+          sum0 = sum1 = make_float2(0.f, 0.f);
+          weights(0, 0);
         }
-        neg = m_run == -INFINITY ? 0.f : -m_run;
       }
       if (lost) {
         fail();
         break;
       }
-      const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
       for (int half = 0; half < kWords / 2; ++half) {
         if (active) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t* x0 = &a[2 * half][2 * e];
-            const uint32_t* y0 = &a[2 * half + 1][2 * e];
-            float2 x = fma2(make_float2(__uint_as_float(x0[0]), __uint_as_float(x0[1])), scale2, neg2);
-            float2 y = fma2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])), scale2, neg2);
-            x = make_float2(ex2(x.x), ex2(x.y));
-            y = make_float2(ex2(y.x), ex2(y.y));
-            sum0 = add2(sum0, x);
-            sum1 = add2(sum1, y);
-            pk[e] = pack2(x.x, x.y);
-            pk[16 + e] = pack2(y.x, y.y);
-          }
+          if (half) weights(half, 0);
           tmem_st32(st + 32 * half, pk);  // over scores that have been read
           tmem_wait_st();
         }
@@ -548,7 +612,8 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       sum0 = add2(sum0, sum1);
       l_run += sum0.x + sum0.y;
     }
-    if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], ((n - 1) >> 1) & 1)) fail();
+    // with one S buffer the last tile's alone is counted there
+    if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], kS == 2 ? ((n - 1) >> 1) & 1 : 0)) fail();
     tc_fence_after();
     __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
     const bool failed = *(volatile int32_t*)&B.failed != 0;
