@@ -195,19 +195,21 @@ constexpr int kUpRegs = 224, kDownRegs = 56;
 
 template <int D, int NW>
 __global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
-chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t ring, const int32_t q_tok, const int32_t q_rows,
+chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok, const int32_t q_rows,
                  const int32_t pitch) {
   constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
   using L = Lines<D, kTile>;
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
   constexpr uint32_t kO = 128;
   constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qs = smem;                                                        // [NW][chunks][q_rows][line]
-  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
-  MmaBars& B = *reinterpret_cast<MmaBars*>(rs + (size_t)ring * L::kBuf);
+  // barriers and list, then the tiles at a multiple of 1024: where the block's shared memory begins at one, nothing is lost
+  extern __shared__ __align__(1024) uint8_t smem[];
+  MmaBars& B = *reinterpret_cast<MmaBars*>(smem);
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
+  const uint32_t begin = smem_u32(smem), behind = begin + (uint32_t)mma_misc(A.G.kb);
+  uint8_t* qs = smem + ((behind + 1023) / 1024 * 1024 - begin);              // [NW][chunks][q_rows][line]
+  uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
+  const int32_t ring = begin % 1024 ? rings - 1 : rings;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_soft = warp < NW * 4;
@@ -385,42 +387,37 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         }
       }
     } else {
-      bool next = false;  // what was asked last
-      if (n > 1 && ok) passed(false, B.full[kb], kp);
+      bool next = false, v_there = true, k_there = false;  // what was asked last
       for (int32_t i = 0; i < n && ok; ++i) {
         const int32_t parity = (i >> 1) & 1;
         const bool more = i + 1 < n;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           uint64_t(&p)[2] = B.p_full[w][i & 1];
+          if (w == 0 && i > 0) passed(v_there, B.full[vb], vp);
           passed(next, p[0], parity);
           if (!ok) break;
-          bool there = ask(p[1], parity);
+          const bool there = ask(p[1], parity);
           pv(i, w, 0);
           passed(there, p[1], parity);
           if (!ok) break;
           pv(i, w, 1);
-          if (!more) {
-            next = false;
-            continue;
-          }
+          next = false;
+          if (!more) continue;
           // S takes the place of the P just used: the products run in order
-          if (w == 0) {
-            qk(i + 1, 0, 0, kHalf);
-            next = ask(B.p_full[NW - 1][i & 1][0], parity);
-            qk(i + 1, 0, kHalf, D / 16);
+          if (w == 0) passed(k_there, B.full[kb], kp);
+          if (!ok) break;
+          qk(i + 1, w, 0, kHalf);
+          if (w + 1 < NW) {
+            next = ask(B.p_full[w + 1][i & 1][0], parity);
           } else {
-            const bool v_there = ask(B.full[vb], vp);
-            qk(i + 1, 1, 0, kHalf);
-            passed(v_there, B.full[vb], vp);
-            int32_t b = kb, bp = kp;
-            step(b, bp, 2);
-            const bool k_there = i + 2 < n && ask(B.full[b], bp);
+            int32_t k2 = kb, kp2 = kp;
+            step(k2, kp2, 2);
+            v_there = ask(B.full[vb], vp);
+            k_there = i + 2 < n && ask(B.full[k2], kp2);
             next = ask(B.p_full[0][(i + 1) & 1][0], ((i + 1) >> 1) & 1);
-            if (!ok) break;
-            qk(i + 1, 1, kHalf, D / 16);
-            if (i + 2 < n) passed(k_there, B.full[kb], kp);
           }
+          qk(i + 1, w, kHalf, D / 16);
         }
       }
     }
@@ -1076,7 +1073,7 @@ cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
   // that share of the shared memory. It is never so small that a third CTA, or one of 256 columns beside one of 512, could
   // come to wait for TMEM (two clusters that each hold what the other waits for would wait for ever).
   const bool two = D <= 128 && NW == 1;
-  const size_t share = two ? 115712 : kMaxSmem, rest = 1024 + (size_t)NW * q_rows * D * 2 + mma_misc(A.G.kb);
+  const size_t share = two ? 115712 : kMaxSmem, rest = (mma_misc(A.G.kb) + 1023) / 1024 * 1024 + (size_t)NW * q_rows * D * 2;
   int32_t ring = (int32_t)((share - rest) / L::kBuf);
   if (ring > kMaxRing) ring = kMaxRing;
   size_t smem = rest + (size_t)ring * L::kBuf;
