@@ -24,7 +24,8 @@ struct Span {
   int32_t p_lo, p_hi;   // positions of the first and the last of them
 };
 
-// The longest groups of a unit, its last rows, come first.
+// Where a CTA's share is; the longest groups of a unit, its last rows, come first. What needs the lengths is filled in below, so
+// that they are on their way beside the slot table.
 __device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, int32_t group_rows) {
   Span s;
   const int32_t cluster = blockIdx.x / P.split, rank = blockIdx.x - cluster * P.split, wholes = P.whole / P.split;
@@ -35,13 +36,15 @@ __device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, in
   s.parts = whole ? 1 : P.split;
   s.r = ua / A.G.Hkv;
   s.h = ua - s.r * A.G.Hkv;
+  s.row0 = group * group_rows;
+  return s;
+}
+__device__ __forceinline__ void fill_span(const ChunkArgs& A, int32_t group_rows, Span& s) {
   s.len = A.len[s.r];
   s.cnt = new_tokens(A, s.r, s.len);
-  s.row0 = group * group_rows;
   s.rows = min(group_rows, s.cnt * A.G.g - s.row0);
   s.p_lo = s.len + s.row0 / A.G.g;
   s.p_hi = s.len + (s.row0 + s.rows - 1) / A.G.g;
-  return s;
 }
 
 // Element offset of row m's vector in q and out, [R][T][Hq][d], times 1 / d: its place in lse.
@@ -54,56 +57,74 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // The unit's slots that rows of the span see: `whole` of them, which all rows see whole, from the front of the list, the
-// others from its back. By `warps` warps of which each takes a run of slots: count, then place.
-struct List {
-  uint16_t* at;   // [kb]
-  int32_t kb, whole, n;
-  __device__ __forceinline__ int32_t slot(int32_t e) const { return at[e < whole ? e : kb - 1 - (e - whole)]; }
-};
-constexpr int kListWarps = 8;  // at most
+// others from its back, the first positions of the first kBases of those beside it. By `warps` warps of which each takes
+// a run of at most 256 slots: load, count, then place.
+constexpr int kListWarps = 8, kBases = 128;
 struct Listed {
-  int32_t whole[kListWarps], some[kListWarps];
+  int32_t whole[kListWarps], some[kListWarps], base[kBases];
 };
-// Each warp's share of at most 1024 slots is eight rounds of 32; bit u of a lane's masks is round u.
-__device__ __forceinline__ void count_slots(const ChunkArgs& A, const Span& s, int warp, int warps, Listed& L, uint32_t (&all)[8], uint32_t (&some)[8]) {
-  const int lane = threadIdx.x & 31;
+struct List {
+  const uint16_t* at;  // [kb]
+  const int32_t *base, *ids;
+  int32_t kb, bs, whole, n;
+  __device__ __forceinline__ int32_t slot(int32_t e) const { return at[e < whole ? e : kb - 1 - (e - whole)]; }
+  // What position p sees of entry e, as bits of its tokens.
+  __device__ __forceinline__ uint64_t seen(int32_t e, int32_t p, int32_t window, int32_t sinks) const {
+    return e < whole ? first_bits(bs) : seen_of(first(e), p, bs, window, sinks);
+  }
+  __device__ __forceinline__ int32_t first(int32_t e) const { return e - whole < kBases ? base[e - whole] : ids[slot(e)] * bs; }  // e >= whole
+};
+struct Ids {
+  int32_t b[8];  // of slots first + 32 u + lane
+  int32_t per, first;
+};
+__device__ __forceinline__ Ids load_ids(const ChunkArgs& A, const Span& s, int warp, int warps) {
   const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-  const int32_t per = (A.G.kb + 32 * warps - 1) / (32 * warps), first = warp * per * 32;
-  int32_t b[8];
+  Ids x;
+  x.per = (A.G.kb + 32 * warps - 1) / (32 * warps);
+  x.first = warp * x.per * 32;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const int32_t i = first + u * 32 + lane;
-    b[u] = u < per && i < A.G.kb ? sb[i] : -1;
+    const int32_t i = x.first + u * 32 + (threadIdx.x & 31);
+    x.b[u] = u < x.per && i < A.G.kb ? sb[i] : -1;
   }
+  return x;
+}
+__device__ __forceinline__ void count_slots(const ChunkArgs& A, const Span& s, const Ids& x, int warp, Listed& L, uint32_t (&all)[8], uint32_t (&some)[8]) {
   int32_t nw = 0, ns = 0;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const int32_t c = sight(b[u], A.G.bs, s.p_lo, s.p_hi, A.window, A.sinks);
+    if (u >= x.per) break;
+    const int32_t c = sight(x.b[u], A.G.bs, s.p_lo, s.p_hi, A.window, A.sinks);
     all[u] = __ballot_sync(0xffffffffu, c == 2);
     some[u] = __ballot_sync(0xffffffffu, c == 1);
     nw += __popc(all[u]);
     ns += __popc(some[u]);
   }
-  if (lane == 0) L.whole[warp] = nw, L.some[warp] = ns;
+  if ((threadIdx.x & 31) == 0) L.whole[warp] = nw, L.some[warp] = ns;
 }
-__device__ __forceinline__ void place_slots(const ChunkArgs& A, int warp, int warps, const Listed& L, const uint32_t (&all)[8], const uint32_t (&some)[8],
+__device__ __forceinline__ void place_slots(const ChunkArgs& A, const Ids& x, int warp, Listed& L, const uint32_t (&all)[8], const uint32_t (&some)[8],
                                             uint16_t* at) {
   const int lane = threadIdx.x & 31;
-  const int32_t per = (A.G.kb + 32 * warps - 1) / (32 * warps), first = warp * per * 32;
   const uint32_t below = (1u << lane) - 1u;
   int32_t nw = 0, ns = 0;
   for (int w = 0; w < warp; ++w) nw += L.whole[w], ns += L.some[w];
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const uint16_t slot = (uint16_t)(first + u * 32 + lane);
+    if (u >= x.per) break;
+    const uint16_t slot = (uint16_t)(x.first + u * 32 + lane);
     if (all[u] >> lane & 1) at[nw + __popc(all[u] & below)] = slot;
-    if (some[u] >> lane & 1) at[A.G.kb - 1 - (ns + __popc(some[u] & below))] = slot;
+    if (some[u] >> lane & 1) {
+      const int32_t e = ns + __popc(some[u] & below);
+      at[A.G.kb - 1 - e] = slot;
+      if (e < kBases) L.base[e] = x.b[u] * A.G.bs;
+    }
     nw += __popc(all[u]);
     ns += __popc(some[u]);
   }
 }
-__device__ __forceinline__ List make_list(const ChunkArgs& A, int warps, const Listed& L, uint16_t* at) {
-  List l{at, A.G.kb, 0, 0};
+__device__ __forceinline__ List make_list(const ChunkArgs& A, const Span& s, int warps, const Listed& L, const uint16_t* at) {
+  List l{at, L.base, A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb, A.G.kb, A.G.bs, 0, 0};
   for (int w = 0; w < warps; ++w) l.whole += L.whole[w], l.n += L.some[w];
   l.n += l.whole;
   return l;
@@ -118,7 +139,7 @@ __device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, const Span& s, 
   for (int32_t e = L.whole / spt * spt; e < L.n; ++e) {
     if (e / spt % s.parts != s.part) continue;
     const int32_t slot = L.slot(e);
-    uint64_t bits = seen_of(A.slot_block[unit + slot] * A.G.bs, p, A.G.bs, A.window, A.sinks);
+    uint64_t bits = L.seen(e, p, A.window, A.sinks);
     const T* v = reinterpret_cast<const T*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)A.G.bs * A.G.d + c;
     while (bits) {
       const int32_t j = __ffsll((long long)bits) - 1;
@@ -178,8 +199,22 @@ struct MmaBars {
 __host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) + ((size_t)kb * 2 + 15) / 16 * 16; }
 
 struct ChunkMaps {
-  CUtensorMap tile, slot, q;  // the pool by spt slots and by one, the queries
+  CUtensorMap tile, slot, q, out;  // the pool by spt slots and by one, the queries, the outputs
 };
+
+// Whether line `row` of a tile holds a value that is not finite.
+template <int D, int Tile>
+__device__ __forceinline__ bool any_not_finite(const uint8_t* tile, int row) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(tile + Lines<D, Tile>::piece(row, c));
+    // an exponent of ones carries into the sign's place
+    any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) | ((x.z & 0x7F807F80u) + 0x00800080u) |
+           ((x.w & 0x7F807F80u) + 0x00800080u);
+  }
+  return (any & 0x80008000u) != 0;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -188,9 +223,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two warpgroups hold 128 scores to a thread, more registers than each thread of the block can have: the others, a whole
-// warpgroup (two warps idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
+// warpgroup (one warp idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
 template <int NW>
-constexpr int mma_threads() { return NW == 2 ? 384 : 192; }
+constexpr int mma_threads() { return NW == 2 ? 384 : 224; }
 constexpr int kUpRegs = 224, kDownRegs = 56;
 
 template <int D, int NW>
@@ -203,7 +238,8 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   constexpr uint32_t kO = 128;
   constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
   // barriers and list, then the tiles at a multiple of 1024: where the block's shared memory begins at one, nothing is lost
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  uint8_t* smem = smem_1024;
   MmaBars& B = *reinterpret_cast<MmaBars*>(smem);
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
   const uint32_t begin = smem_u32(smem), behind = begin + (uint32_t)mma_misc(A.G.kb);
@@ -212,13 +248,13 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   const int32_t ring = begin % 1024 ? rings - 1 : rings;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_soft = warp < NW * 4;
+  const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_copy_v = warp == NW * 4 + 2, is_soft = warp < NW * 4;
   const int32_t g = A.G.g, gr = q_tok * g;  // rows of a warpgroup: q_tok tokens, all heads of the group
   const int32_t bs = A.G.bs, spt = kTile / pitch;
   const bool tails = spt * bs < kTile;      // lines of a tile that no token has
   const uint32_t ring0 = smem_u32(rs);
   if (is_copy) {  // what reads no memory of the call
-    if (lane < 3) tma_prefetch_map(&M.tile + lane);
+    if (lane < 4) tma_prefetch_map(&M.tile + lane);
     constexpr int kP = offsetof(MmaBars, p_full) / 8;
     for (int i = lane; i < (int)(offsetof(MmaBars, listed) / 8); i += 32)
       mbar_init(smem_u32(B.full + i), i >= kP && i < kP + 8 ? 128 : 1);
@@ -230,7 +266,10 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     fence_proxy_async();
   }
   grid_wait();
-  const Span s = make_span(A, shape, NW * gr);
+  Span s = make_span(A, shape, NW * gr);
+  Ids ids;
+  if (is_soft) ids = load_ids(A, s, warp, NW * 4);
+  fill_span(A, NW * gr, s);
   if (s.rows <= 0) return;
   const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
 
@@ -254,16 +293,16 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   } else if (!is_soft) {
     if (is_mma) tmem_alloc(smem_u32(&B.tmem), kCols * NW);
   } else {
-    count_slots(A, s, warp, NW * 4, B.listed, all, some);
+    count_slots(A, s, ids, warp, B.listed, all, some);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (is_soft) place_slots(A, warp, NW * 4, B.listed, all, some, list_at);
+  if (is_soft) place_slots(A, ids, warp, B.listed, all, some, list_at);
   __syncthreads();
   grid_go();  // the TMEM is allocated
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
-  const List list = make_list(A, NW * 4, B.listed, list_at);
+  const List list = make_list(A, s, NW * 4, B.listed, list_at);
   const int32_t n = ((list.n + spt - 1) / spt - s.part + s.parts - 1) / s.parts;  // this CTA's tiles
 
   // The uses of the ring are in the order in which the MMAs take them. With two S buffers, S of tile i + 1
@@ -278,48 +317,47 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   if (!is_soft) {
     if (NW == 2) registers_down<kDownRegs>();
   }
-  if (is_copy) {
-    int32_t buf = 0, par = 0, issued = 0;  // the next buffer and the parity of its fill
-    const int32_t uses = kS == 2 ? 2 * n + 1 : 2 * n;
-    bool ok = true;
-    for (int32_t use = 0; use < uses && ok; ++use) {
-      const bool v = kS == 2 ? use > 0 && use % 2 == 0 : use % 2 == 1;
-      const int32_t i = kS == 1 ? use / 2 : v ? use / 2 - 1 : (use + 1) / 2, b = buf;
-      const uint32_t bar = smem_u32(&B.full[b]);
-      const int32_t parity = par;
-      if (++buf == ring) buf = 0, par ^= 1;
-      if (i >= n) continue;  // the use that a further K would have
-      if (use >= ring) {
-        // with one S buffer K of tile j is free once S of tile j is there, V of tile j - 1 as well
-        const int32_t j = (use - ring + 1) / 2;
-        if (!(kS == 1 ? warp_wait(B.empty[j % kMaxRing], j / kMaxRing & 1) : warp_wait(B.empty[b], parity ^ 1))) {
-          ok = false;
-          break;
-        }
-      }
+  if (is_copy || is_copy_v) {
+    // A warp for K and one for V. What they ask shared memory for, between MMAs that read it, takes them as long as a tile's
+    // products: with one warp for both and slots in any order, it and not the copies set the pace.
+    const bool v = is_copy_v;
+    int32_t use = v ? v_use(0) : 0, issued = 0;
+    for (; issued < n; ++issued) {
+      const int32_t i = issued, b = use % ring;
       const int32_t e0 = (s.part + i * s.parts) * spt, ne = min(spt, list.n - e0), first = list.slot(e0);
+      const int32_t my_slot = lane < ne * L::kChunks ? list.slot(e0 + lane / L::kChunks) : 0;
       bool run = ne == spt && pitch == bs;
       for (int32_t e = lane; e < ne; e += 32) run = run && list.slot(e0 + e) == first + e;
       run = __all_sync(0xffffffffu, run);
-      const uint32_t to = ring0 + b * L::kBuf;
+      if (use >= ring) {
+        // with one S buffer K of tile j is free once S of tile j is there, V of tile j - 1 as well
+        const int32_t j = (use - ring + 1) / 2;
+        if (!(kS == 1 ? warp_wait(B.empty[j % kMaxRing], j / kMaxRing & 1) : warp_wait(B.empty[b], use / ring - 1 & 1))) {
+          fail();
+          break;
+        }
+      }
+      const uint32_t to = ring0 + b * L::kBuf, bar = smem_u32(&B.full[b]);
       if (lane == 0) mbar_expect_tx(bar, (uint32_t)(ne * bs * D * 2));
       __syncwarp();
       if (run) {
         if (lane < L::kChunks) tma_load_5d(to + lane * L::kChunk, &M.tile, bar, 0, lane, 0, v ? 1 : 0, (int32_t)unit + first);
       } else {
         for (int32_t x = lane; x < ne * L::kChunks; x += 32) {
-          const int32_t e = x / L::kChunks, c = x % L::kChunks;
-          tma_load_5d(to + c * L::kChunk + e * pitch * L::kBytes, &M.slot, bar, 0, c, 0, v ? 1 : 0, (int32_t)unit + list.slot(e0 + e));
+          const int32_t e = x / L::kChunks, c = x % L::kChunks, slot = x == lane ? my_slot : list.slot(e0 + e);
+          tma_load_5d(to + c * L::kChunk + e * pitch * L::kBytes, &M.slot, bar, 0, c, 0, v ? 1 : 0, (int32_t)unit + slot);
         }
       }
-      issued = use + 1;
+      use += kS == 2 && use == 0 ? 1 : 2;
     }
-    if (!ok) {
-      fail();
+    if (issued < n) {
       // the copies still in flight land before the shared memory is given up (bounded)
-      for (int32_t use = issued > ring ? issued - ring : 0; use < issued; ++use) mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1));
+      for (int32_t i = max(0, issued - ring); i < issued; ++i) {
+        const int32_t u = v ? v_use(i) : kS == 1 ? 2 * i : max(0, 2 * i - 1);
+        mbar_wait_timed(smem_u32(&B.full[u % ring]), (uint32_t)(u / ring & 1));
+      }
     }
-    if (!ok || n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
+    if (!v && (issued < n || n == 0)) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
   } else if (is_mma) {
     // One warp for both warpgroups, in a fixed order: O of a tile and S of the next for one, then for the other. An answer from a
     // barrier takes 150 to 350 cycles while the tensor cores read shared memory, so each barrier is asked ahead, behind
@@ -459,30 +497,43 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       uint32_t vis[kWords];
 #pragma unroll
       for (int u = 0; u < kWords; ++u) vis[u] = ends[u];
-      bool held = true;  // the token of line `row` of the tile (of kTile = 64: row & 63) is one that some row may see
       if (part_seen) {
-        const int32_t ne = min(spt, list.n - e0), line = row & (kTile - 1);
+        const int32_t ne = min(spt, list.n - e0);
         uint64_t lo = 0, hi = 0;
-        held = false;
-#pragma unroll 1
-        for (int32_t k0 = 0; k0 < ne; k0 += 32) {
-          const int32_t base = k0 + lane < ne ? A.slot_block[unit + list.slot(e0 + k0 + lane)] * bs : 0;
-#pragma unroll 1
-          for (int32_t k = k0; k < min(ne, k0 + 32); ++k) {
-            const int32_t first = __shfl_sync(0xffffffffu, base, k - k0), at = k * pitch;
-            const uint64_t bits = seen_of(first, p, bs, A.window, A.sinks);
-            if (at < 64) {
-              lo |= bits << at;
-              if (at) hi |= bits >> (64 - at);
-            } else {
-              hi |= bits << (at - 64);
-            }
-            if (line >= at && line < at + bs) held = first <= s.p_hi - (line - at);
+#pragma unroll 2
+        for (int32_t k = 0; k < ne; ++k) {
+          const uint64_t bits = list.seen(e0 + k, p, A.window, A.sinks);
+          const int32_t at = k * pitch;
+          if (at < 64) {
+            lo |= bits << at;
+            if (at) hi |= bits >> (64 - at);
+          } else {
+            hi |= bits << (at - 64);
           }
         }
         const uint64_t both[2] = {lo, hi};
 #pragma unroll
         for (int u = 0; u < kWords; ++u) vis[u] = (uint32_t)(both[u / 2] >> 32 * (u & 1));
+        // Values that are not finite meet weights of zero: they are zero in the product. Each warpgroup sees to it,
+        // whichever product comes first; a line is one thread's.
+        if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
+          fail();
+          break;
+        }
+        uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
+        if (row < kTile && any_not_finite<D, kTile>(v, row)) {
+          const int32_t k = row / pitch, e = e0 + k;
+#pragma unroll 1
+          for (int c = 0; c < D / 8; ++c) {
+            uint4* x = reinterpret_cast<uint4*>(v + L::piece(row, c));
+            uint4 y = *x;
+            if (clean(y)) *x = y;
+          }
+          // a token that some row may see?
+          if (k < ne && (e < list.whole || list.first(e) <= s.p_hi - (row - k * pitch))) *(volatile int32_t*)&B.bad = 1;
+        }
+        __syncwarp();
+        fence_proxy_async();
       }
       if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
         fail();
@@ -496,28 +547,6 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         break;
       }
       tc_fence_after();
-      if (part_seen) {
-        // Values that are not finite meet weights of zero: they are zero in the product. Each warpgroup sees to it,
-        // whichever product comes first; a line is one thread's.
-        if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
-          fail();
-          break;
-        }
-        constexpr int kPieces = D / 8;
-        uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
-        if (row < kTile) {
-          bool any = false;
-#pragma unroll 4
-          for (int c = 0; c < kPieces; ++c) {
-            uint4* x = reinterpret_cast<uint4*>(v + L::piece(row, c));
-            uint4 y = *x;
-            if (clean(y)) *x = y, any = true;
-          }
-          if (any && held) *(volatile int32_t*)&B.bad = 1;
-        }
-        __syncwarp();
-        fence_proxy_async();
-      }
       bool lost = false;
       const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
       uint32_t a[kWords][32], pk[32];
@@ -561,9 +590,16 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         mask(0, kWords);
         // The maximum moves in few tiles: the first weights are taken against the old one beside the search for the
         // new one, and again where it moves (S is still there).
-        weights(0, 1);
+        if (i > 0) {
+          weights(0, 1);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kWords; ++u)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx[u] = max3(mx[u], __uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        if (__any_sync(0xffffffffu, top > m_run + 8.f)) {
+        if (__any_sync(0xffffffffu, top > m_run + 8.f) || i == 0) {
           const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
           const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
           m_run = mn;
@@ -627,32 +663,54 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       }
     };
     if (rows > 0 && s.parts == 1 && !failed) {
-      // through shared memory (this warp's rows in the place of its queries), to write whole lines
+      // through shared memory (in the place of the queries), to write whole lines: a warpgroup's by TMA as the queries came, or,
+      // where some of its rows are not the request's, a warp's row by row
       constexpr int kPieces = D / 8, kXor = kPieces % 8 ? 3 : 7;  // pieces of eight rows on different banks
-      uint8_t* mine = qs + ((size_t)w * q_rows + (warp & 3) * 32) * D * 2;
+      constexpr int kAtOnce = NW == 2 && D % 64 == 0 ? 64 : 32;
+      const bool full = (w + 1) * gr <= s.rows;
+      uint8_t* own = qs + (size_t)w * q_rows * D * 2;
+      uint8_t* mine = own + (size_t)(warp & 3) * 32 * D * 2;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if (real && A.lse) A.lse[row_place(A, s, s.row0 + wrow)] = lse_of(m_run, l_run);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
+      for (int c0 = 0; c0 < D; c0 += kAtOnce) {
+        uint32_t o[kAtOnce / 32][32];
         __syncwarp();
         if (n > 0) {
-          tmem_ld32(o, my + kO + c);
-          tmem_wait_ld(o);
+#pragma unroll
+          for (int u = 0; u < kAtOnce / 32; ++u) tmem_ld32(o[u], my + kO + c0 + 32 * u);
+#pragma unroll
+          for (int u = 0; u < kAtOnce / 32; ++u) tmem_wait_ld(o[u]);
         }
         if (!real) continue;
-        if (l_run == 0.f) {  // no weights (but infinite values, perhaps)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
+        for (int u = 0; u < kAtOnce / 32; ++u) {
+          const int c = c0 + 32 * u;
+          if (l_run == 0.f) {  // no weights (but infinite values, perhaps)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[u][e] = 0;
+          }
+          if (bad) extra(o[u], c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[u][e + k]) * inv;
+            const int piece = (c + e) / 8;
+            uint8_t* to = full ? own + (piece / (L::kBytes / 16)) * (q_rows * L::kBytes) + L::at(row, piece % (L::kBytes / 16))
+                               : mine + ((size_t)lane * kPieces + (piece ^ (lane & kXor))) * 16;
+            *reinterpret_cast<uint4*>(to) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+          }
         }
-        if (bad) extra(o, c);
+      }
+      if (full) {
+        fence_proxy_async();
+        asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "r"((gr + 31) / 32 * 32) : "memory");  // the warps that have rows
+        if (row == 0) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[e + k]) * inv;
-          *reinterpret_cast<uint4*>(mine + ((size_t)lane * kPieces + (((c + e) / 8) ^ (lane & kXor))) * 16) =
-              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_store_5d(&M.out, smem_u32(own) + c * q_rows * L::kBytes, 0, c, 0, s.h, s.r * A.T + s.row0 / g + w * q_tok);
+          bulk_stores_read();
         }
       }
       __syncwarp();
@@ -660,7 +718,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       const int32_t m0 = w * gr + (warp & 3) * 32;
       __nv_bfloat16* base = (__nv_bfloat16*)A.out + row_place(A, s, s.row0) * D;  // row0 is the first head of a token
 #pragma unroll 4
-      for (int e = lane; e < min(rows, 32) * kPieces; e += 32) {
+      for (int e = full ? 32 * kPieces : lane; e < min(rows, 32) * kPieces; e += 32) {
         const int r = e / kPieces, c = e - r * kPieces;
         const uint32_t m = m0 + r, t = m * per_g >> 16;
         const uint4 x = *reinterpret_cast<const uint4*>(mine + ((size_t)r * kPieces + (c ^ (r & kXor))) * 16);
@@ -732,7 +790,9 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
   grid_wait();
   grid_go();
   const int32_t g = A.G.g;
-  const Span s = make_span(A, shape, q_tok * g);
+  Span s = make_span(A, shape, q_tok * g);
+  const Ids ids = load_ids(A, s, threadIdx.x >> 5, 4);
+  fill_span(A, q_tok * g, s);
   if (s.rows <= 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
   const int rg = warp % RG, th = warp / RG, tok0 = th * kTok;
@@ -751,11 +811,11 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
       mbar_arrive(smem_u32(bars + 2));
   }
   uint32_t whole_of[8], some_of[8];
-  count_slots(A, s, warp, 4, listed, whole_of, some_of);
+  count_slots(A, s, ids, warp, listed, whole_of, some_of);
   __syncthreads();
-  place_slots(A, warp, 4, listed, whole_of, some_of, list_at);
+  place_slots(A, ids, warp, listed, whole_of, some_of, list_at);
   __syncthreads();
-  const List list = make_list(A, 4, listed, list_at);
+  const List list = make_list(A, s, 4, listed, list_at);
   const int32_t mine = ((list.n + spt - 1) / spt - s.part + s.parts - 1) / s.parts;  // this CTA's tiles
   const float scale = kLog2e / sqrtf((float)d);
   const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
@@ -768,7 +828,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
     const float* from = nullptr;
     if (j < tt && e < list.n) {
       const int32_t slot = list.slot(e);
-      if (e < list.whole || A.slot_block[unit + slot] * bs <= s.p_hi - off)
+      if (e < list.whole || list.first(e) <= s.p_hi - off)
         from = reinterpret_cast<const float*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)(which * bs + off) * d;
     }
     const uint32_t bar = smem_u32(bars + which);
@@ -808,10 +868,9 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
         const int32_t ne = min(spt, list.n - e0);
 #pragma unroll 1
         for (int32_t k = 0; k < ne; ++k) {
-          const int32_t base = A.slot_block[unit + list.slot(e0 + k)] * bs;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (real[i]) vis[i] |= seen_of(base, pos[i], bs, A.window, A.sinks) << k * bs;
+            if (real[i]) vis[i] |= list.seen(e0 + k, pos[i], A.window, A.sinks) << k * bs;
         }
       }
       ok = mbar_wait_timed(smem_u32(bars), phase(it)) && ok;
@@ -1039,7 +1098,7 @@ cudaError_t run_f32_d(const ChunkArgs& A, cudaStream_t s) {
 }
 
 // Maps of 5 dims over lines and chunks: the pool as [slots][K, V][tokens], a box of one chunk of the tokens of spt slots
-// or of one; the queries as [tokens][KV heads][group], a box of q_tok tokens of a KV head.
+// or of one; the queries and outputs as [tokens][KV heads][group], a box of q_tok tokens of a KV head.
 template <int D, int Tile>
 cudaError_t make_maps(const ChunkArgs& A, int32_t spt, int32_t q_tok, ChunkMaps* m) {
   using L = Lines<D, Tile>;
@@ -1057,7 +1116,8 @@ cudaError_t make_maps(const ChunkArgs& A, int32_t spt, int32_t q_tok, ChunkMaps*
   const cuuint64_t g = A.G.g, hkv = A.G.Hkv, bs = A.G.bs, slots = (cuuint64_t)A.pool_rows;
   const bool ok = encode(&m->tile, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, (cuuint32_t)spt}) &&
                   encode(&m->slot, A.pool, {bs, 2, slots}, {token, half, 2 * half}, {(cuuint32_t)bs, 1, 1}) &&
-                  encode(&m->q, A.q, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok});
+                  encode(&m->q, A.q, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok}) &&
+                  encode(&m->out, A.out, {g, hkv, all}, {token, token * g, token * g * hkv}, {(cuuint32_t)g, 1, (cuuint32_t)q_tok});
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
