@@ -156,9 +156,10 @@ __device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, const Span& s, 
 
 // Merges the cluster's partials and writes outputs and sums. The first `threads` threads of every CTA of the cluster call it,
 // the others cluster_sync twice.
-template <typename T>
-__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask, int32_t threads) {
+template <typename T, typename F>
+__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask, int32_t threads, F more) {
   cluster_sync();
+  more();
   merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, threads, [&](int32_t row, int32_t c, float4 o, float M, float l) {
     const int64_t at = row_place(A, s, s.row0 + row);
     store4((T*)A.out + at * A.G.d + c * 4, o);
@@ -198,6 +199,12 @@ struct MmaBars {
 
 __host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) + ((size_t)kb * 2 + 15) / 16 * 16; }
 
+// Up to 128 rows the weights that slots draw are summed on the way: [entries][q_rows] sums of a row's weights over a slot's
+// tokens, against the maximum of then, [tiles][q_rows], both of this CTA's tiles; with the final maxima and sums they are
+// joined at the end. (Taken afterwards, from the log sums, they cost a second pass over K: 128 requests x 1 token
+// 479 us against NNN.)
+__host__ __device__ constexpr size_t drawn_bytes(int tiles, int spt, int q_rows) { return (size_t)tiles * (spt + 1) * q_rows * 4; }
+
 struct ChunkMaps {
   CUtensorMap tile, slot, q, out;  // the pool by spt slots and by one, the queries, the outputs
 };
@@ -228,10 +235,10 @@ template <int NW>
 constexpr int mma_threads() { return NW == 2 ? 384 : 224; }
 constexpr int kUpRegs = 224, kDownRegs = 56;
 
-template <int D, int NW>
+template <int D, int NW, bool kDraw>
 __global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
 chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok, const int32_t q_rows,
-                 const int32_t pitch) {
+                 const int32_t pitch, const int32_t most) {
   constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
   using L = Lines<D, kTile>;
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
@@ -242,7 +249,11 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   uint8_t* smem = smem_1024;
   MmaBars& B = *reinterpret_cast<MmaBars*>(smem);
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);                   // [kb]
-  const uint32_t begin = smem_u32(smem), behind = begin + (uint32_t)mma_misc(A.G.kb);
+  const int32_t spt = kTile / pitch;
+  // kDraw: [most tiles][spt][q_rows] sums, [most tiles][q_rows] maxima
+  float* drawn = reinterpret_cast<float*>(smem + mma_misc(A.G.kb));
+  float* drawn_m = drawn + (size_t)most * spt * q_rows;
+  const uint32_t begin = smem_u32(smem), behind = begin + (uint32_t)(mma_misc(A.G.kb) + (kDraw ? drawn_bytes(most, spt, q_rows) : 0));
   uint8_t* qs = smem + ((behind + 1023) / 1024 * 1024 - begin);              // [NW][chunks][q_rows][line]
   uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
   const int32_t ring = begin % 1024 ? rings - 1 : rings;
@@ -250,7 +261,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_copy_v = warp == NW * 4 + 2, is_soft = warp < NW * 4;
   const int32_t g = A.G.g, gr = q_tok * g;  // rows of a warpgroup: q_tok tokens, all heads of the group
-  const int32_t bs = A.G.bs, spt = kTile / pitch;
+  const int32_t bs = A.G.bs;
   const bool tails = spt * bs < kTile;      // lines of a tile that no token has
   const uint32_t ring0 = smem_u32(rs);
   if (is_copy) {  // what reads no memory of the call
@@ -270,7 +281,14 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   Ids ids;
   if (is_soft) ids = load_ids(A, s, warp, NW * 4);
   fill_span(A, NW * gr, s);
-  if (s.rows <= 0) return;
+  if (s.rows <= 0) {
+    if (kDraw && s.part == 0)
+      for (int32_t i = tid; i < A.G.kb; i += mma_threads<NW>()) {
+        const int64_t at = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb + i;
+        A.weight_out[at] = A.weight ? A.weight[at] : 0.f;
+      }
+    return;
+  }
   const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
 
   // Setup: the softmax warps list the slots, the copy warp starts the queries' copies.
@@ -299,6 +317,14 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   __syncthreads();
   tc_fence_after();
   if (is_soft) place_slots(A, ids, warp, B.listed, all, some, list_at);
+  if (kDraw && is_soft && s.part == 0) {  // slots that no row sees draw nothing
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (u >= ids.per) break;
+      const int32_t i = ids.first + u * 32 + lane;
+      if (i < A.G.kb && !((all[u] | some[u]) >> lane & 1)) A.weight_out[unit + i] = A.weight ? A.weight[unit + i] : 0.f;
+    }
+  }
   __syncthreads();
   grid_go();  // the TMEM is allocated
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
@@ -561,12 +587,17 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
           for (int e = 0; e < 32; ++e)
             if (!(vis[u] >> e & 1)) a[u][e] = 0xFF800000u;
       };
+      auto maxima = [&](int e) {
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) mx[u] = max3(mx[u], __uint_as_float(a[u][2 * e]), __uint_as_float(a[u][2 * e + 1]));
+      };
       // the weights of 64 columns against m_run, and, where asked for, the maximum of as many
       auto weights = [&](int half, int with_max) {
         const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t *x0 = &a[2 * half][2 * e], *y0 = &a[2 * half + 1][2 * e];
+          if (kDraw && with_max) maxima(e);
           float2 x = fma2(make_float2(__uint_as_float(x0[0]), __uint_as_float(x0[1])), scale2, neg2);
           float2 y = fma2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])), scale2, neg2);
           x = make_float2(ex2(x.x), ex2(x.y));
@@ -575,9 +606,10 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
           sum1 = add2(sum1, y);
           pk[e] = pack2(x.x, x.y);
           pk[16 + e] = pack2(y.x, y.y);
-          if (with_max) {
-#pragma unroll
-            for (int u = 0; u < kWords; ++u) mx[u] = max3(mx[u], __uint_as_float(a[u][2 * e]), __uint_as_float(a[u][2 * e + 1]));
+          if (!kDraw && with_max) maxima(e);  // here: before the weights it costs registers
+          if (kDraw) {
+            a[2 * half][2 * e] = __float_as_uint(x.x), a[2 * half][2 * e + 1] = __float_as_uint(x.y);
+            a[2 * half + 1][2 * e] = __float_as_uint(y.x), a[2 * half + 1][2 * e + 1] = __float_as_uint(y.y);
           }
         }
       };
@@ -594,9 +626,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
           weights(0, 1);
         } else {
 #pragma unroll
-          for (int u = 0; u < kWords; ++u)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx[u] = max3(mx[u], __uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]));
+          for (int e = 0; e < 16; ++e) maxima(e);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         if (__any_sync(0xffffffffu, top > m_run + 8.f) || i == 0) {
@@ -644,6 +674,36 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       }
       sum0 = add2(sum0, sum1);
       l_run += sum0.x + sum0.y;
+      if (kDraw && active) {
+        // sums of slots, behind the product's start
+        float* to = drawn + (size_t)i * spt * q_rows + row;
+        float sum = 0.f;
+        if (pitch % 16 == 0) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e & 3] += __uint_as_float(a[k / 2][k % 2 * 16 + e]);
+            sum += (x[0] + x[1]) + (x[2] + x[3]);
+            if ((k + 1) * 16 % pitch) continue;
+            if (real) *to = sum;
+            to += q_rows;
+            sum = 0.f;
+          }
+        } else {
+          int32_t left = pitch;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) {
+            sum += __uint_as_float(a[c / 32][c % 32]);
+            if (--left) continue;
+            if (real && c < spt * pitch) *to = sum;
+            to += q_rows;
+            sum = 0.f;
+            left = pitch;
+          }
+        }
+        if (real) drawn_m[i * q_rows + row] = m_run;
+      }
     }
     // with one S buffer the last tile's alone is counted there
     if (n > 0 && !warp_wait(B.pv_done[w][(n - 1) & 1], kS == 2 ? ((n - 1) >> 1) & 1 : 0)) fail();
@@ -745,7 +805,41 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         }
       }
     }
-    if (s.parts > 1) merge_chunk<__nv_bfloat16>(A, s, Partial{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4)}, 7, NW * 128);
+    const Partial mine_of{smem_u32(rs), smem_u32(qs), smem_u32(qs) + (uint32_t)(NW * q_rows * 4)};
+    auto join = [&] {
+      // what a row's weights of a tile are worth by now, then the slots' sums over the rows
+      if (real) {
+        float m = m_run, l = l_run;
+        if (s.parts > 1) {
+          m = -INFINITY, l = 0.f;
+          for (int32_t k = 0; k < s.parts; ++k) m = fmaxf(m, ld_cluster(cluster_map(mine_of.m + row * 4, k)));
+          for (int32_t k = 0; k < s.parts; ++k) {
+            const float mk = ld_cluster(cluster_map(mine_of.m + row * 4, k)), lk = ld_cluster(cluster_map(mine_of.l + row * 4, k));
+            if (lk != 0.f) l += (mk == -INFINITY ? 1.f : ex2(mk - m)) * lk;  // scores that are all NaN have a sum, but no maximum
+          }
+        }
+        for (int32_t i = 0; i < n; ++i) {
+          float& at = drawn_m[i * q_rows + row];
+          // without a maximum the weights are zeros, or not numbers, as their sum then
+          at = l == 0.f ? 0.f : at == -INFINITY ? l * 0.f : ex2(at - m) / l;
+        }
+      }
+      asm volatile("bar.sync 9, 128;" ::: "memory");
+      for (int32_t x = row; x < n * spt; x += 128) {
+        const int32_t i = x / spt, e = (s.part + i * s.parts) * spt + x - i * spt;
+        if (e >= list.n) break;
+        float sum = 0.f;
+        for (int32_t k = 0; k < s.rows; ++k) {
+          const float f = drawn_m[i * q_rows + k];
+          // a row whose sum is not a number makes all that it sees so, and nothing else
+          if (f == f || list.seen(e, s.len + k / g, A.window, A.sinks)) sum = fmaf(drawn[(size_t)x * q_rows + k], f, sum);
+        }
+        const int64_t at = unit + list.slot(e);
+        A.weight_out[at] = (A.weight ? A.weight[at] : 0.f) + (failed ? 0.f : sum);
+      }
+    };
+    if (kDraw && s.parts == 1) join();
+    if (s.parts > 1) merge_chunk<__nv_bfloat16>(A, s, mine_of, 7, NW * 128, [&] { if (kDraw) join(); });
     tc_fence_before();
     __syncthreads();
   }
@@ -1052,7 +1146,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
     store4((float*)A.out + at * d + c * 4, x);
     if (c == 0 && A.lse) A.lse[at] = lse_of(M, sum);
   }
-  if (s.parts > 1) merge_chunk<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls)}, 0, kF32Threads);
+  if (s.parts > 1) merge_chunk<float>(A, s, Partial{smem_u32(ks), smem_u32(ms), smem_u32(ls)}, 0, kF32Threads, [] {});
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------
@@ -1121,8 +1215,8 @@ cudaError_t make_maps(const ChunkArgs& A, int32_t spt, int32_t q_tok, ChunkMaps*
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int NW>
-cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
+template <int D, int NW, bool kDraw = false>
+cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   constexpr int kTile = Tiles<NW>::kTile;
   using L = Lines<D, kTile>;
   const int32_t pitch = A.G.bs * L::kBytes % 128 ? A.G.bs + 1 : A.G.bs, spt = kTile / pitch;
@@ -1133,7 +1227,14 @@ cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
   // that share of the shared memory. It is never so small that a third CTA, or one of 256 columns beside one of 512, could
   // come to wait for TMEM (two clusters that each hold what the other waits for would wait for ever).
   const bool two = D <= 128 && NW == 1;
-  const size_t share = two ? 115712 : kMaxSmem, rest = (mma_misc(A.G.kb) + 1023) / 1024 * 1024 + (size_t)NW * q_rows * D * 2;
+  // the slots' sums, where the ring keeps the four buffers that it needs
+  const int32_t most = most_tiles(A, spt, NW * q_tok);
+  const size_t share = two ? 115712 : kMaxSmem, tiles0 = (size_t)NW * q_rows * D * 2, sums = kDraw ? drawn_bytes(most, spt, q_rows) : 0;
+  if constexpr (NW == 1 && !kDraw) {
+    if (A.weight_out && groups == 1 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 1024 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
+  }
+  *drawn = kDraw;
+  const size_t rest = (mma_misc(A.G.kb) + sums + 1023) / 1024 * 1024 + tiles0;
   int32_t ring = (int32_t)((share - rest) / L::kBuf);
   if (ring > kMaxRing) ring = kMaxRing;
   size_t smem = rest + (size_t)ring * L::kBuf;
@@ -1141,30 +1242,35 @@ cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
   if (smem < least) smem = least;
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
   const int32_t per_sm = two ? 2 : 1;
-  const Shape shape = pick_shape(items, groups, per_sm, most_tiles(A, spt, NW * q_tok), NW == 1 ? kMmaCosts : kMmaCostsWide,
+  const Shape shape = pick_shape(items, groups, per_sm, most, NW == 1 ? kMmaCosts : kMmaCostsWide,
                                  cluster_room(mma_threads<NW>(), per_sm));
   ChunkMaps maps;
   if (cudaError_t e = make_maps<D, kTile>(A, spt, q_tok, &maps)) return e;
-  return launch_cluster(chunk_mma_kernel<D, NW>, items, shape, mma_threads<NW>(), smem, s, A, maps, shape, ring, q_tok, q_rows, pitch);
+  return launch_cluster(chunk_mma_kernel<D, NW, kDraw>, items, shape, mma_threads<NW>(), smem, s, A, maps, shape, ring, q_tok, q_rows, pitch, most);
 }
 
-cudaError_t run_mma_d(const ChunkArgs& A, cudaStream_t s) {
+// *drawn: whether the slots' weights are summed on the way.
+cudaError_t run_mma_d(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   const bool wide = (int64_t)A.T * A.G.g > 128;
   switch (A.G.d) {
-    case 32: return wide ? run_mma<32, 2>(A, s) : run_mma<32, 1>(A, s);
-    case 64: return wide ? run_mma<64, 2>(A, s) : run_mma<64, 1>(A, s);
-    case 96: return wide ? run_mma<96, 2>(A, s) : run_mma<96, 1>(A, s);
-    case 128: return wide ? run_mma<128, 2>(A, s) : run_mma<128, 1>(A, s);
-    case 160: return run_mma<160, 1>(A, s);
-    case 192: return run_mma<192, 1>(A, s);
-    case 224: return run_mma<224, 1>(A, s);
-    default: return run_mma<256, 1>(A, s);
+    case 32: return wide ? run_mma<32, 2>(A, drawn, s) : run_mma<32, 1>(A, drawn, s);
+    case 64: return wide ? run_mma<64, 2>(A, drawn, s) : run_mma<64, 1>(A, drawn, s);
+    case 96: return wide ? run_mma<96, 2>(A, drawn, s) : run_mma<96, 1>(A, drawn, s);
+    case 128: return wide ? run_mma<128, 2>(A, drawn, s) : run_mma<128, 1>(A, drawn, s);
+    case 160: return run_mma<160, 1>(A, drawn, s);
+    case 192: return run_mma<192, 1>(A, drawn, s);
+    case 224: return run_mma<224, 1>(A, drawn, s);
+    default: return run_mma<256, 1>(A, drawn, s);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attend_chunk(const ChunkArgs& A, cudaStream_t s) { return A.G.dtype == OKV_F32 ? run_f32_d(A, s) : run_mma_d(A, s); }
+cudaError_t launch_attend_chunk(const ChunkArgs& A, cudaStream_t s) {
+  bool drawn = false;
+  const cudaError_t e = A.G.dtype == OKV_F32 ? run_f32_d(A, s) : run_mma_d(A, &drawn, s);
+  return e != cudaSuccess || drawn || !A.weight_out ? e : launch_weigh_chunk(A, s);
+}
 
 }  // namespace okv
 
@@ -1195,7 +1301,5 @@ extern "C" okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new,
   A.weight = weight;
   A.weight_out = weight_out;
   A.pool_rows = (int64_t)n_requests * kv_heads * slots;
-  if (launch_attend_chunk(A, (cudaStream_t)stream) != cudaSuccess) return OKV_ECUDA;
-  if (weight_out && launch_weigh_chunk(A, (cudaStream_t)stream) != cudaSuccess) return OKV_ECUDA;
-  return OKV_OK;
+  return launch_attend_chunk(A, (cudaStream_t)stream) == cudaSuccess ? OKV_OK : OKV_ECUDA;
 }

@@ -166,26 +166,44 @@ weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const i
     for (int32_t i = issued > ring ? issued - ring : 0; i < issued; ++i) mbar_wait_timed(smem_u32(&B.full[i % ring]), (i / ring) & 1);
     mbar_wait_timed(k_bar, 0);
   } else if (is_mma) {
-    const bool one = lane == 0;
-    constexpr int kSteps = L::kElems / 16;
-    constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
-    const uint32_t kd = smem_desc_lo(smem_u32(ks), 16), qd = smem_desc_lo(smem_u32(rs), 16);
-    bool ok = warp_wait(B.k_full, 0);
-    for (int32_t i = 0; i < n && ok; ++i) {
-      const int w = i & 1, b = i % ring;
-      ok = warp_wait(B.full[b], (i / ring) & 1) && (i < 2 || warp_wait(B.s_empty[w], (i / 2 - 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
+    if (elect_one()) {
+      constexpr int kSteps = L::kElems / 16;
+      constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+      const uint32_t kd = smem_desc_lo(smem_u32(ks), 16), qd = smem_desc_lo(smem_u32(rs), 16);
+      bool ok = true;
+      // barriers are asked ahead, behind MMAs that keep the tensor cores busy meanwhile
+      auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
+      auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
+        if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
+        tc_fence_after();
+      };
+      passed(false, B.k_full, 0);
+      bool q_there = false, s_there = false;
+      int32_t b = 0, parity = 0;
+      for (int32_t i = 0; i < n && ok; ++i) {
+        const int w = i & 1;
+        passed(q_there, B.full[b], parity);
+        if (i > 1) passed(s_there, B.s_empty[w], (i / 2 - 1) & 1);
+        if (!ok) break;
+        const uint32_t q = qd + b * (L::kBuf >> 4);
+        uint64_t& done = B.empty[b];
+        if (++b == ring) b = 0, parity ^= 1;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        mma_ss(tmem + w * 128, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, qd + b * (L::kBuf >> 4) + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi,
-               kDesc, c > 0, one);
-      mma_commit(smem_u32(&B.s_full[w]), one);
-      mma_commit(smem_u32(&B.empty[b]), one);
+        for (int c = 0; c < D / 16; ++c) {
+          if (c == D / 32) {
+            q_there = i + 1 < n && ask(B.full[b], parity);
+            s_there = i > 0 && ask(B.s_empty[w ^ 1], ((i + 1) / 2 - 1) & 1);
+          }
+          mma_ss1(tmem + w * 128, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, q + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDesc, c > 0);
+        }
+        mma_commit1(smem_u32(&B.s_full[w]));
+        mma_commit1(smem_u32(&done));
+      }
+      if (!ok) fail();
+      mma_commit1(smem_u32(&B.drain));
+      mbar_wait_timed(smem_u32(&B.drain), 0);
     }
-    if (!ok) fail();
-    mma_commit(smem_u32(&B.drain), one);
-    warp_wait(B.drain, 0);
+    __syncwarp();
   } else {
     const int w = warp >> 2;
     const uint32_t my = tmem + w * 128 + ((uint32_t)(warp & 3) << 21);

@@ -22,6 +22,7 @@ struct ChunkArgs {
   int64_t pool_rows;          // slots in `pool`: R * Hkv * kb
 };
 
+// Outputs, log sums and, with A.weight_out, what the slots draw.
 cudaError_t launch_attend_chunk(const ChunkArgs& A, cudaStream_t s);
 // weight_out = weight + what each slot draws of the rows whose sums are in A.lse.
 cudaError_t launch_weigh_chunk(const ChunkArgs& A, cudaStream_t s);
