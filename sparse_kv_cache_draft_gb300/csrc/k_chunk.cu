@@ -230,10 +230,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two warpgroups hold 128 scores to a thread, more registers than each thread of the block can have: the others, a whole
-// warpgroup (one warp idle), give up what they do not need. 2 x 224 + 56 is what 3 x 168 were at the launch.
+// warpgroup (one warp idle), give up what they do not need. 2 x 216 + 72 is what 3 x 168 were at the launch.
 template <int NW>
 constexpr int mma_threads() { return NW == 2 ? 384 : 224; }
-constexpr int kUpRegs = 224, kDownRegs = 56;
+constexpr int kUpRegs = 216, kDownRegs = 72;
 
 template <int D, int NW, bool kDraw>
 __global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
