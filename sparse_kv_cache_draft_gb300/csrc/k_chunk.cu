@@ -9,20 +9,12 @@
 // to the CTAs of a cluster where there are too few groups to fill the GPU, as for drafted trees.
 #include <stddef.h>
 
-#include "okv_chunk.h"
-#include "tiles.cuh"
+#include "chunk.cuh"
 
 namespace okv {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-
-// One CTA's share of the work.
-struct Span {
-  int32_t r, h, part, parts, cnt, len;
-  int32_t row0, rows;   // rows [row0, row0 + rows) of the unit's g * cnt
-  int32_t p_lo, p_hi;   // positions of the first and the last of them
-};
 
 // Where a CTA's share is; the longest groups of a unit, its last rows, come first. What needs the lengths is filled in below, so
 // that they are on their way beside the slot table.
@@ -39,95 +31,8 @@ __device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, in
   s.row0 = group * group_rows;
   return s;
 }
-__device__ __forceinline__ void fill_span(const ChunkArgs& A, int32_t group_rows, Span& s) {
-  s.len = A.len[s.r];
-  s.cnt = new_tokens(A, s.r, s.len);
-  s.rows = min(group_rows, s.cnt * A.G.g - s.row0);
-  s.p_lo = s.len + s.row0 / A.G.g;
-  s.p_hi = s.len + (s.row0 + s.rows - 1) / A.G.g;
-}
-
-// Element offset of row m's vector in q and out, [R][T][Hq][d], times 1 / d: its place in lse.
-__device__ __forceinline__ int64_t row_place(const ChunkArgs& A, const Span& s, int32_t m) {
-  const int32_t t = m / A.G.g, j = m - t * A.G.g;
-  return ((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j;
-}
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-}
-
-// The unit's slots that rows of the span see: `whole` of them, which all rows see whole, from the front of the list, the
-// others from its back, the first positions of the first kBases of those beside it. By `warps` warps of which each takes
-// a run of at most 256 slots: load, count, then place.
-constexpr int kListWarps = 8, kBases = 128;
-struct Listed {
-  int32_t whole[kListWarps], some[kListWarps], base[kBases];
-};
-struct List {
-  const uint16_t* at;  // [kb]
-  const int32_t *base, *ids;
-  int32_t kb, bs, whole, n;
-  __device__ __forceinline__ int32_t slot(int32_t e) const { return at[e < whole ? e : kb - 1 - (e - whole)]; }
-  // What position p sees of entry e, as bits of its tokens.
-  __device__ __forceinline__ uint64_t seen(int32_t e, int32_t p, int32_t window, int32_t sinks) const {
-    return e < whole ? first_bits(bs) : seen_of(first(e), p, bs, window, sinks);
-  }
-  __device__ __forceinline__ int32_t first(int32_t e) const { return e - whole < kBases ? base[e - whole] : ids[slot(e)] * bs; }  // e >= whole
-};
-struct Ids {
-  int32_t b[8];  // of slots first + 32 u + lane
-  int32_t per, first;
-};
-__device__ __forceinline__ Ids load_ids(const ChunkArgs& A, const Span& s, int warp, int warps) {
-  const int32_t* sb = A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-  Ids x;
-  x.per = (A.G.kb + 32 * warps - 1) / (32 * warps);
-  x.first = warp * x.per * 32;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int32_t i = x.first + u * 32 + (threadIdx.x & 31);
-    x.b[u] = u < x.per && i < A.G.kb ? sb[i] : -1;
-  }
-  return x;
-}
-__device__ __forceinline__ void count_slots(const ChunkArgs& A, const Span& s, const Ids& x, int warp, Listed& L, uint32_t (&all)[8], uint32_t (&some)[8]) {
-  int32_t nw = 0, ns = 0;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    if (u >= x.per) break;
-    const int32_t c = sight(x.b[u], A.G.bs, s.p_lo, s.p_hi, A.window, A.sinks);
-    all[u] = __ballot_sync(0xffffffffu, c == 2);
-    some[u] = __ballot_sync(0xffffffffu, c == 1);
-    nw += __popc(all[u]);
-    ns += __popc(some[u]);
-  }
-  if ((threadIdx.x & 31) == 0) L.whole[warp] = nw, L.some[warp] = ns;
-}
-__device__ __forceinline__ void place_slots(const ChunkArgs& A, const Ids& x, int warp, Listed& L, const uint32_t (&all)[8], const uint32_t (&some)[8],
-                                            uint16_t* at) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t below = (1u << lane) - 1u;
-  int32_t nw = 0, ns = 0;
-  for (int w = 0; w < warp; ++w) nw += L.whole[w], ns += L.some[w];
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    if (u >= x.per) break;
-    const uint16_t slot = (uint16_t)(x.first + u * 32 + lane);
-    if (all[u] >> lane & 1) at[nw + __popc(all[u] & below)] = slot;
-    if (some[u] >> lane & 1) {
-      const int32_t e = ns + __popc(some[u] & below);
-      at[A.G.kb - 1 - e] = slot;
-      if (e < kBases) L.base[e] = x.b[u] * A.G.bs;
-    }
-    nw += __popc(all[u]);
-    ns += __popc(some[u]);
-  }
-}
-__device__ __forceinline__ List make_list(const ChunkArgs& A, const Span& s, int warps, const Listed& L, const uint16_t* at) {
-  List l{at, L.base, A.slot_block + ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb, A.G.kb, A.G.bs, 0, 0};
-  for (int w = 0; w < warps; ++w) l.whole += L.whole[w], l.n += L.some[w];
-  l.n += l.whole;
-  return l;
 }
 
 // Adds what the values that are not finite, of tokens in tiles that were masked, give to four outputs (dims c .. c + 3) of
@@ -244,7 +149,8 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
   constexpr uint32_t kO = 128;
   constexpr uint32_t kDescQK = mma_desc_bf16(128, kTile, false), kDescPV = mma_desc_bf16(128, D, true);
-  // barriers and list, then the tiles at a multiple of 1024: where the block's shared memory begins at one, nothing is lost
+  // barriers and list, then the tiles at a multiple of 1024: where the block's shared memory begins at one, nothing is lost (the
+  // ring is at least four buffers either way, which a cluster's partials need)
   extern __shared__ __align__(1024) uint8_t smem_1024[];
   uint8_t* smem = smem_1024;
   MmaBars& B = *reinterpret_cast<MmaBars*>(smem);
@@ -256,7 +162,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
   const uint32_t begin = smem_u32(smem), behind = begin + (uint32_t)(mma_misc(A.G.kb) + (kDraw ? drawn_bytes(most, spt, q_rows) : 0));
   uint8_t* qs = smem + ((behind + 1023) / 1024 * 1024 - begin);              // [NW][chunks][q_rows][line]
   uint8_t* rs = qs + (size_t)NW * q_rows * D * 2;                            // [ring][chunks][tile][line]
-  const int32_t ring = begin % 1024 ? rings - 1 : rings;
+  const int32_t ring = min(rings, (int32_t)((begin + dynamic_smem() - smem_u32(rs)) / L::kBuf));
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_copy = warp == NW * 4, is_mma = warp == NW * 4 + 1, is_copy_v = warp == NW * 4 + 2, is_soft = warp < NW * 4;
@@ -1231,13 +1137,14 @@ cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   const int32_t most = most_tiles(A, spt, NW * q_tok);
   const size_t share = two ? 115712 : kMaxSmem, tiles0 = (size_t)NW * q_rows * D * 2, sums = kDraw ? drawn_bytes(most, spt, q_rows) : 0;
   if constexpr (NW == 1 && !kDraw) {
-    if (A.weight_out && groups == 1 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 1024 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
+    if (A.weight_out && groups == 1 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
   }
   *drawn = kDraw;
   const size_t rest = (mma_misc(A.G.kb) + sums + 1023) / 1024 * 1024 + tiles0;
   int32_t ring = (int32_t)((share - rest) / L::kBuf);
   if (ring > kMaxRing) ring = kMaxRing;
-  size_t smem = rest + (size_t)ring * L::kBuf;
+  size_t smem = rest + (size_t)ring * L::kBuf + 1024;
+  if (smem > share) smem = share;
   const size_t third = 233472 / 3, least = two ? third : 2 * third;
   if (smem < least) smem = least;
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;

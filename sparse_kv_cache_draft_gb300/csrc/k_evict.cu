@@ -1,17 +1,18 @@
 // Slots of a paged pool for the blocks of new tokens: empty ones first, then those whose tokens have drawn the least
 // attention weight.
 //
-// A warp takes a unit (request, KV head), its slots' ids and weights in registers, slot 32 u + lane in round u. The m-th smallest
-// weight is found bit by bit over the weights' ordered images, from the highest bit in which any two differ (sorting
-// them would move every slot), and slots of that weight go by their index. Everything is integer work on a few
-// kilobytes: a call is a launch and two rounds of memory.
+// A unit (request, KV head) is a warp's up to 128 slots, the CTA's eight warps' beyond, four slots to a thread at most, ids and
+// weights in registers. The m-th smallest weight is found bit by bit over the weights' ordered images, from the highest bit in
+// which any two differ (sorting them would move every slot), and slots of that weight go by their index. Everything is
+// integer work on a few kilobytes: a call is a launch, two rounds of memory and the sums over the unit.
 #include "okv_tree.h"
 #include "tc5.cuh"
 
 namespace okv {
 namespace {
 
-constexpr int kWarps = 4;      // units of a CTA
+constexpr int kUnits = 4;      // of a CTA, of a warp each
+constexpr int kWide = 8;       // warps of a unit
 constexpr int kRange = 2048;   // new blocks looked at: the last kb that no slot holds are among the last 2 kb
 constexpr int kMaxSlots = 1024;
 
@@ -31,25 +32,63 @@ __device__ __forceinline__ uint32_t image_of(float w) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-template <int N>  // rounds: slots up to 32 N
-__global__ void __launch_bounds__(kWarps * 32) evict_kernel(const EvictArgs A) {
-  __shared__ uint32_t held_of[kWarps][kRange / 32];
-  __shared__ uint16_t new_of[kWarps][32 * N];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* held = held_of[warp];
-  uint16_t* fresh = new_of[warp];
-  for (int i = lane; i < kRange / 32; i += 32) held[i] = 0;
+// Sums, least and most over a unit's W warps, in `x` by turns: the values before are read behind one barrier, and the ones before
+// those behind two.
+template <int W>
+struct Unit {
+  int32_t (*x)[kWide];  // [2][warps]
+  int warp, turn;
+  template <typename F>
+  __device__ __forceinline__ int32_t over(int32_t mine, F join) {
+    if (W == 1) return mine;
+    int32_t* at = x[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) at[warp] = mine;
+    __syncthreads();
+    int32_t v = at[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = join(v, at[i]);
+    return v;
+  }
+  __device__ __forceinline__ int32_t sum(int32_t v) {
+    return over(__reduce_add_sync(0xffffffffu, v), [](int32_t a, int32_t b) { return a + b; });
+  }
+  // ... of the warps before this one; `all` is a warp's
+  __device__ __forceinline__ int32_t before(int32_t all) {
+    if (W == 1) return 0;
+    int32_t* at = x[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) at[warp] = all;
+    __syncthreads();
+    int32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += i < warp ? at[i] : 0;
+    return v;
+  }
+};
+
+template <int N, int W>  // slots up to 32 N W
+__global__ void __launch_bounds__((W == 1 ? kUnits : W) * 32) evict_kernel(const EvictArgs A) {
+  constexpr int kHere = W == 1 ? kUnits : 1;
+  __shared__ uint32_t held_of[kHere][kRange / 32];
+  __shared__ uint16_t new_of[kHere][32 * N * W];
+  __shared__ int32_t sums[2][kWide];
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, here = W == 1 ? threadIdx.x >> 5 : 0;
+  const int first_slot = warp * N * 32 + lane;
+  uint32_t* held = held_of[here];
+  uint16_t* fresh = new_of[here];
+  for (int i = threadIdx.x % (W * 32); i < kRange / 32; i += W * 32) held[i] = 0;
   grid_wait();
   grid_go();
-  const int64_t ua = (int64_t)blockIdx.x * kWarps + warp;
-  if (ua >= (int64_t)A.R * A.Hkv) return;
+  const int64_t ua = (int64_t)blockIdx.x * kHere + here;
+  if (ua >= (int64_t)A.R * A.Hkv) return;  // a warp that has its unit to itself
   const int32_t r = (int32_t)(ua / A.Hkv), kb = A.kb, bs = A.bs;
   const int64_t at = ua * kb;
   int32_t id[N];
   float w[N];
 #pragma unroll
   for (int u = 0; u < N; ++u) {
-    const int32_t i = 32 * u + lane;
+    const int32_t i = 32 * u + first_slot;
     id[u] = i < kb ? A.slot_block[at + i] : -1;
     w[u] = i < kb ? A.weight[at + i] : 0.f;
   }
@@ -58,16 +97,23 @@ __global__ void __launch_bounds__(kWarps * 32) evict_kernel(const EvictArgs A) {
   const int32_t n = left_out ? 0 : A.counts ? min(max(A.counts[r], 0), A.T) : A.T;
   const int32_t begin = (int32_t)(((int64_t)max(len, 0) + bs - 1) / bs), stop = (int32_t)(((int64_t)max(len, 0) + n + bs - 1) / bs);
   const int32_t base = max(begin, stop - kRange), span = stop - base;
+  auto sync = [] {
+    if (W == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  Unit<W> unit{sums, warp, 0};
 
   // which slots may be taken, and which new blocks there are already
   uint32_t empty = 0, old = 0, key[N];  // bit u: the slot of round u
-  __syncwarp();
+  sync();
 #pragma unroll
   for (int u = 0; u < N; ++u) {
     const int32_t b = id[u];
     const int64_t first = (int64_t)b * bs;
     key[u] = image_of(w[u]);
-    if (32 * u + lane >= kb) continue;
+    if (32 * u + first_slot >= kb) continue;
     if (b < 0 || (first >= len && b >= stop)) {
       empty |= 1u << u;
     } else if (first >= len) {
@@ -76,50 +122,52 @@ __global__ void __launch_bounds__(kWarps * 32) evict_kernel(const EvictArgs A) {
       old |= 1u << u;
     }
   }
-  __syncwarp();
-  uint32_t want[2];  // of new blocks base + 64 lane ..
+  sync();
+  uint32_t want[2];  // of new blocks base + 64 lane .., by every warp
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int32_t left = span - (2 * lane + k) * 32;
     want[k] = ~held[2 * lane + k] & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u);
   }
   const int32_t mine = __popc(want[0]) + __popc(want[1]);
-  int32_t before = mine;
-#pragma unroll
-  for (int k = 1; k < 32; k *= 2) {
-    const int32_t x = __shfl_up_sync(0xffffffffu, before, k);
-    if (lane >= k) before += x;
-  }
-  const int32_t wanted = __shfl_sync(0xffffffffu, before, 31);
-  const int32_t n_empty = __reduce_add_sync(0xffffffffu, __popc(empty)), n_old = __reduce_add_sync(0xffffffffu, __popc(old));
-  const int32_t m = min(wanted, n_empty + n_old);
+  const int32_t wanted = __reduce_add_sync(0xffffffffu, mine);
   uint32_t taken = 0;
-  if (m > 0) {
-    // the m newest of them, in order
-    int32_t nth = before - mine - (wanted - m);
+  if (wanted > 0) {  // the unit's as a whole
+    const int32_t n_empty = unit.sum(__popc(empty)), n_old = unit.sum(__popc(old)), m = min(wanted, n_empty + n_old);
+    if (warp == 0) {
+      // the m newest of them, in order
+      int32_t up = mine;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (uint32_t x = want[k]; x; x &= x - 1, ++nth)
-        if (nth >= 0) fresh[nth] = (uint16_t)((2 * lane + k) * 32 + __ffs(x) - 1);
+      for (int k = 1; k < 32; k *= 2) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, up, k);
+        if (lane >= k) up += x;
+      }
+      int32_t nth = up - mine - (wanted - m);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        for (uint32_t x = want[k]; x; x &= x - 1, ++nth)
+          if (nth >= 0) fresh[nth] = (uint16_t)((2 * lane + k) * 32 + __ffs(x) - 1);
+    }
     const uint32_t below = (1u << lane) - 1u;
-    // `from` of the slots with their bit in `of`, by index
-    auto take = [&](uint32_t of, int32_t from) {
+    // each slot with its bit in `of`, by index: use(u, how many there are before it)
+    auto each = [&](uint32_t of, auto use) {
+      int32_t rank = unit.before(__reduce_add_sync(0xffffffffu, __popc(of)));
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         const uint32_t all = __ballot_sync(0xffffffffu, of >> u & 1);
-        if ((of >> u & 1) && __popc(all & below) < from) taken |= 1u << u;
-        from -= __popc(all);
+        if (of >> u & 1) use(u, rank + __popc(all & below));
+        rank += __popc(all);
       }
     };
-    take(empty, m);
+    each(empty, [&](int u, int32_t rank) { taken |= (uint32_t)(rank < m) << u; });
     const int32_t need = m - n_empty;
     if (need > 0) {
       uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
       for (int u = 0; u < N; ++u)
         if (old >> u & 1) lo = min(lo, key[u]), hi = max(hi, key[u]);
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
+      lo = (uint32_t)unit.over((int32_t)__reduce_min_sync(0xffffffffu, lo), [](int32_t a, int32_t b) { return (int32_t)min((uint32_t)a, (uint32_t)b); });
+      hi = (uint32_t)unit.over((int32_t)__reduce_max_sync(0xffffffffu, hi), [](int32_t a, int32_t b) { return (int32_t)max((uint32_t)a, (uint32_t)b); });
       // the need-th smallest image: the bits that all share, then bit by bit
       const int bits = 32 - __clz(lo ^ hi);
       uint32_t kth = bits == 32 ? 0u : lo >> bits << bits;
@@ -129,8 +177,13 @@ __global__ void __launch_bounds__(kWarps * 32) evict_kernel(const EvictArgs A) {
         int32_t c = 0;
 #pragma unroll
         for (int u = 0; u < N; ++u) c += (old >> u & 1) && key[u] < up;
-        c = __reduce_add_sync(0xffffffffu, c);
+        c = unit.sum(c);
         if (c < need) kth = up, less = c;
+        if (c == need) {  // the need smallest are those below `up`
+          kth = up;
+          less = need;
+          break;
+        }
       }
       uint32_t same = 0;
 #pragma unroll
@@ -139,39 +192,34 @@ __global__ void __launch_bounds__(kWarps * 32) evict_kernel(const EvictArgs A) {
         if (key[u] < kth) taken |= 1u << u;
         if (key[u] == kth) same |= 1u << u;
       }
-      take(same, need - less);
+      each(same, [&](int u, int32_t rank) { taken |= (uint32_t)(rank < need - less) << u; });
     }
-    __syncwarp();
-    int32_t rank = 0;
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const uint32_t all = __ballot_sync(0xffffffffu, taken >> u & 1);
-      if (taken >> u & 1) {
-        id[u] = base + fresh[rank + __popc(all & below)];
-        w[u] = 0.f;
-      }
-      rank += __popc(all);
-    }
+    sync();
+    each(taken, [&](int u, int32_t rank) {
+      id[u] = base + fresh[rank];
+      w[u] = 0.f;
+    });
   }
 #pragma unroll
   for (int u = 0; u < N; ++u) {
-    const int32_t i = 32 * u + lane;
+    const int32_t i = 32 * u + first_slot;
     if (i >= kb) continue;
     A.slot_block_out[at + i] = id[u];
     A.weight_out[at + i] = w[u];
   }
 }
 
-template <int N>
+template <int N, int W>
 cudaError_t run(const EvictArgs& A, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(((int64_t)A.R * A.Hkv + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
+  const int64_t units = (int64_t)A.R * A.Hkv;
+  cfg.gridDim = dim3((unsigned)(W == 1 ? (units + kUnits - 1) / kUnits : units));
+  cfg.blockDim = dim3((W == 1 ? kUnits : W) * 32);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_attr(s, attr);
-  return cudaLaunchKernelEx(&cfg, evict_kernel<N>, A);
+  return cudaLaunchKernelEx(&cfg, evict_kernel<N, W>, A);
 }
 
 }  // namespace
@@ -188,6 +236,6 @@ extern "C" okv_status okv_evict_static(int32_t n_requests, int32_t n_new, int32_
   if (okv_status st = check_stream(stream)) return st;
   const EvictArgs A{n_requests, kv_heads, block_size, slots, n_new, sinks, recent, lengths, counts, slot_block, weight, slot_block_out, weight_out};
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = slots <= 32 ? run<1>(A, s) : slots <= 128 ? run<4>(A, s) : slots <= 256 ? run<8>(A, s) : slots <= 512 ? run<16>(A, s) : run<32>(A, s);
+  const cudaError_t e = slots <= 32 ? run<1, 1>(A, s) : slots <= 128 ? run<4, 1>(A, s) : slots <= 256 ? run<1, kWide>(A, s) : slots <= 512 ? run<2, kWide>(A, s) : run<4, kWide>(A, s);
   return e == cudaSuccess ? OKV_OK : OKV_ECUDA;
 }

@@ -2,13 +2,11 @@
 //
 //   weight_out[s] = weight[s] + sum over the rows (t, head) of the unit and the tokens j of slot s that the row sees of
 //                   exp(q . k_j / sqrt(d) - lse)
-// with the sums lse that the attention of the chunk (k_chunk.cu) left. A CTA takes a tile of the unit's slots and every row
-// that sees any of them, so that a slot's sum is one CTA's, in one order, and nothing is added by atomics. The product is
-// taken as K Q^T: a thread then has one token and sums over the rows in registers, without an exchange.
+// with the sums lse that the attention of the chunk (k_chunk.cu) left. A CTA takes some of the unit's slots and every row
+// that sees any of them, so that a slot's sum is one CTA's, in one order, and nothing is added by atomics.
 #include <stddef.h>
 
-#include "okv_chunk.h"
-#include "tiles.cuh"
+#include "chunk.cuh"
 
 namespace okv {
 namespace {
@@ -60,227 +58,309 @@ __device__ __forceinline__ void copy_weights(const ChunkArgs& A, const Site& s) 
 
 // ---- tensor cores: bf16 ------------------------------------------------------------------------------
 //
-// K of the tile (128 tokens) stays in shared memory, the rows' queries come in tiles of up to 128 through a ring, and
-//   S^T = K Q^T   128 tokens x 128 rows, in two TMEM buffers, each a warpgroup's in turn
-// so that one warpgroup sums while the other's product runs. Two CTAs share an SM up to d 128. As many exponentials as
-// the tensor cores have multiply-adds / d: both are near their rates at once.
-constexpr int kTok = 128, kThreads = 320;  // two warpgroups, a warp that copies, one that multiplies
+// K of two tiles of up to 128 tokens stays in shared memory, the rows' queries come in tiles of up to 128 through a ring,
+// each for both:
+//   S = Q K^T   128 rows x 128 tokens, in two TMEM buffers of each tile
+// Four warpgroups take half the tokens of a tile each. A thread has a row of S, whose log sum is a number of its own, and keeps a
+// sum for each of its 64 tokens over all its rows; the sums of the warps' lanes are joined once, at the end. Per score that is
+// an exponential, half a fused multiply-add and half an addition: exponentials and products both take 1024 cycles of
+// two tiles. Four warps on a scheduler hide one another's waits. Slower: K Q^T, a token to a thread and its log sums from
+// shared memory, 300 cycles and more a load beside the MMAs that read it; two warpgroups of 128 sums to a thread.
+// Slots are listed as for the attention, so that few tiles need a mask.
+constexpr int kTok = 128, kRing = 4, kWgs = 4, kThreads = kWgs * 128 + 128, kUpRegs = 104, kDownRegs = 64;  // 4 x 104 + 64 = 5 x 96
 
 struct Bars {
-  uint64_t k_full, full[4], empty[4], s_full[2], s_empty[2], drain;
+  uint64_t k_full, full[kRing], empty[kRing], s_full[2][2], s_empty[2][2], drain;
+  Listed listed;
   int32_t lo, hi, failed;
   uint32_t tmem;
-  float shift[2][2][128];
-  float part[2][128];
 };
-
-__device__ __forceinline__ void wg_sync(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
+__host__ __device__ constexpr size_t weigh_misc(int kb) { return sizeof(Bars) + ((size_t)kb * 2 + 15) / 16 * 16; }
 
 struct WeighMaps {
   CUtensorMap tile, slot, q;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
-weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const int32_t tiles, const int32_t ring, const int32_t q_tok, const int32_t pitch) {
+__global__ void __launch_bounds__(kThreads, 1)
+weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const int32_t tiles, const int32_t rings, const int32_t q_tok, const int32_t pitch) {
   using L = Lines<D, kTok>;
-  constexpr uint32_t kDesc = mma_desc_bf16(128, 128, false);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* ks = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* rs = ks + L::kBuf;  // [ring][chunks][128][line]
-  Bars& B = *reinterpret_cast<Bars*>(rs + (size_t)ring * L::kBuf);
+  constexpr uint32_t kDesc = mma_desc_bf16(128, kTok, false);
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  Bars& B = *reinterpret_cast<Bars*>(smem_1024);
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(&B + 1);
+  const uint32_t begin = smem_u32(smem_1024), behind = begin + (uint32_t)weigh_misc(A.G.kb);
+  uint8_t* ks = smem_1024 + ((behind + 1023) / 1024 * 1024 - begin);  // two tiles
+  uint8_t* rs = ks + 2 * L::kBuf;                                      // [ring][chunks][128][line]
+  // a kilobyte may be lost to where the block's memory begins
+  const int32_t ring = min(rings, (int32_t)((begin + dynamic_smem() - smem_u32(rs)) / L::kBuf));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool is_copy = warp == 8, is_mma = warp == 9;
+  const bool is_copy = warp == 16, is_mma = warp == 17, is_soft = warp < 16, lists = warp < 8;
   const int32_t g = A.G.g, gr = q_tok * g, bs = A.G.bs, spt = kTok / pitch;
   if (is_copy) {
     if (lane < 3) tma_prefetch_map(&M.tile + lane);
-    for (int i = lane; i < (int)(offsetof(Bars, lo) / 8); i += 32) {
-      constexpr int kSE = offsetof(Bars, s_empty) / 8;
-      mbar_init(smem_u32(&B.k_full + i), i >= kSE && i < kSE + 2 ? 128 : 1);
-    }
+    constexpr int kSE = offsetof(Bars, s_empty) / 8;
+    for (int i = lane; i < (int)(offsetof(Bars, listed) / 8); i += 32) mbar_init(smem_u32(&B.k_full + i), i >= kSE && i < kSE + 4 ? 256 : 1);
     if (lane == 0) B.lo = INT32_MAX, B.hi = 0, B.failed = 0;
     fence_mbar_init();
-  } else if (!is_mma) {
-    // rows of a tile that no copy fills: their scores are zero, their weights with them
-    if (gr < 128)
-      for (int32_t i = tid; i < ring * (L::kBuf / 16); i += 256) reinterpret_cast<uint4*>(rs)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
   }
   grid_wait();
-  const Site s = make_site(A, spt, tiles);
-  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-  const int j = tid & 127, k = j / pitch, off = j - k * pitch;
-  Rows mine{0, 0};
-  if (!is_copy && !is_mma && k < s.slots && off < bs) mine = rows_of(A, s, A.slot_block[unit + s.slot0 + k], off);
-  __syncthreads();
-  if (tid < 128) {
-    const int32_t lo = __reduce_min_sync(0xffffffffu, mine.lo < mine.hi ? mine.lo : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, mine.hi);
-    if (lane == 0 && hi) atomicMin(&B.lo, lo), atomicMax(&B.hi, hi);
-  }
-  __syncthreads();
-  if (B.hi == 0) {  // no row sees any of them
+  Span s;
+  const int32_t ua = blockIdx.x / tiles, e0 = (blockIdx.x - ua * tiles) * 2 * spt;  // the CTA's entries begin at e0
+  s.r = ua / A.G.Hkv;
+  s.h = ua - s.r * A.G.Hkv;
+  s.row0 = s.part = 0;
+  s.parts = 1;
+  const int64_t unit = (int64_t)ua * A.G.kb;
+  Ids ids;
+  if (lists) ids = load_ids(A, s, warp, 8);
+  fill_span(A, INT32_MAX, s);
+  uint32_t all[8] = {}, some[8] = {};
+  auto copy_weights = [&] {  // of slots that no row sees
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (u >= ids.per) break;
+      const int32_t i = ids.first + u * 32 + lane;
+      if (i < A.G.kb && !((all[u] | some[u]) >> lane & 1)) A.weight_out[unit + i] = A.weight ? A.weight[unit + i] : 0.f;
+    }
+  };
+  if (s.rows <= 0) {
     grid_go();
-    copy_weights(A, s);
+    if (lists && e0 == 0) copy_weights();
     return;
   }
-  const int32_t first = B.lo / gr, n = (B.hi + gr - 1) / gr - first;  // tiles of rows
-  if (is_mma) tmem_alloc(smem_u32(&B.tmem), 256);
+  if (lists) count_slots(A, s, ids, warp, B.listed, all, some);
+  __syncthreads();
+  if (lists) {
+    place_slots(A, ids, warp, B.listed, all, some, list_at);
+    if (e0 == 0) copy_weights();
+  }
+  __syncthreads();
+  const List list = make_list(A, s, 8, B.listed, list_at);
+  if (e0 >= list.n) {
+    grid_go();
+    return;
+  }
+  const int32_t ne = min(2 * spt, list.n - e0);
+  // the rows that see any of them
+  if (lists) {  // 256 threads: an entry each
+    int32_t lo = INT32_MAX, hi = 0;
+    if (tid < ne) {
+      const int32_t e = e0 + tid;
+      lo = 0, hi = s.rows;
+      if (e >= list.whole) {
+        const int32_t base = list.first(e);
+        lo = max(0, base - s.len) * g;
+        if (base >= A.sinks) {
+          const int64_t last = (int64_t)base - s.len + bs - 1 + A.window;
+          if (last < s.cnt) hi = max((int32_t)last, 0) * g;
+        }
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0 && hi) atomicMin(&B.lo, lo), atomicMax(&B.hi, hi);
+  } else if (is_mma) {
+    tmem_alloc(smem_u32(&B.tmem), 512);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_go();  // the TMEM is allocated
   const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  const int32_t first = B.lo / gr, n = max(0, (B.hi + gr - 1) / gr - first);  // tiles of rows
+  const int used = ne > spt ? 2 : 1;                                          // tiles
   auto warp_wait = [&](uint64_t& bar, int32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
   };
   auto fail = [&] { *(volatile int32_t*)&B.failed = 1; };
 
-  if (is_copy) {
-    fence_proxy_async();
-    __syncwarp();
-    const uint32_t k_bar = smem_u32(&B.k_full);
-    if (lane == 0) mbar_expect_tx(k_bar, (uint32_t)(s.slots * bs * D * 2));
-    __syncwarp();
-    if (pitch == bs && s.slots == spt) {
-      if (lane < L::kChunks) tma_load_5d(smem_u32(ks) + lane * L::kChunk, &M.tile, k_bar, 0, lane, 0, 0, (int32_t)unit + s.slot0);
-    } else {
-      for (int32_t x = lane; x < s.slots * L::kChunks; x += 32) {
-        const int32_t e = x / L::kChunks, c = x % L::kChunks;
-        tma_load_5d(smem_u32(ks) + c * L::kChunk + e * pitch * L::kBytes, &M.slot, k_bar, 0, c, 0, 0, (int32_t)unit + s.slot0 + e);
-      }
-    }
-    int32_t issued = 0;
-    for (; issued < n; ++issued) {
-      const int32_t b = issued % ring;
-      if (issued >= ring && !warp_wait(B.empty[b], (issued / ring - 1) & 1)) {
-        fail();
-        break;
-      }
-      const uint32_t bar = smem_u32(&B.full[b]);
-      if (lane == 0) mbar_expect_tx(bar, (uint32_t)(gr * D * 2));
+  if (!is_soft) {
+    registers_down<kDownRegs>();
+    if (is_copy && n > 0) {
+      const uint32_t k_bar = smem_u32(&B.k_full);
+      if (lane == 0) mbar_expect_tx(k_bar, (uint32_t)(ne * bs * D * 2));
       __syncwarp();
-      if (lane < L::kChunks)
-        tma_load_5d(smem_u32(rs) + b * L::kBuf + lane * L::kChunk, &M.q, bar, 0, lane, 0, s.h, s.r * A.T + (first + issued) * q_tok);
-    }
-    // what is in flight lands before the shared memory is given up, whatever the others did (bounded)
-    for (int32_t i = issued > ring ? issued - ring : 0; i < issued; ++i) mbar_wait_timed(smem_u32(&B.full[i % ring]), (i / ring) & 1);
-    mbar_wait_timed(k_bar, 0);
-  } else if (is_mma) {
-    if (elect_one()) {
-      constexpr int kSteps = L::kElems / 16;
-      constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
-      const uint32_t kd = smem_desc_lo(smem_u32(ks), 16), qd = smem_desc_lo(smem_u32(rs), 16);
-      bool ok = true;
-      // barriers are asked ahead, behind MMAs that keep the tensor cores busy meanwhile
-      auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
-      auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
-        if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
-        tc_fence_after();
-      };
-      passed(false, B.k_full, 0);
-      bool q_there = false, s_there = false;
-      int32_t b = 0, parity = 0;
-      for (int32_t i = 0; i < n && ok; ++i) {
-        const int w = i & 1;
-        passed(q_there, B.full[b], parity);
-        if (i > 1) passed(s_there, B.s_empty[w], (i / 2 - 1) & 1);
-        if (!ok) break;
-        const uint32_t q = qd + b * (L::kBuf >> 4);
-        uint64_t& done = B.empty[b];
-        if (++b == ring) b = 0, parity ^= 1;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          if (c == D / 32) {
-            q_there = i + 1 < n && ask(B.full[b], parity);
-            s_there = i > 0 && ask(B.s_empty[w ^ 1], ((i + 1) / 2 - 1) & 1);
+      for (int t = 0; t < used; ++t) {
+        const int32_t f0 = e0 + t * spt, nf = min(spt, list.n - f0), slot0 = list.slot(f0);
+        const uint32_t to = smem_u32(ks) + t * L::kBuf;
+        bool run = nf == spt && pitch == bs;
+        for (int32_t e = lane; e < nf; e += 32) run = run && list.slot(f0 + e) == slot0 + e;
+        if (__all_sync(0xffffffffu, run)) {
+          if (lane < L::kChunks) tma_load_5d(to + lane * L::kChunk, &M.tile, k_bar, 0, lane, 0, 0, (int32_t)unit + slot0);
+        } else {
+          for (int32_t x = lane; x < nf * L::kChunks; x += 32) {
+            const int32_t e = x / L::kChunks, c = x % L::kChunks;
+            tma_load_5d(to + c * L::kChunk + e * pitch * L::kBytes, &M.slot, k_bar, 0, c, 0, 0, (int32_t)unit + list.slot(f0 + e));
           }
-          mma_ss1(tmem + w * 128, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, q + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDesc, c > 0);
         }
-        mma_commit1(smem_u32(&B.s_full[w]));
-        mma_commit1(smem_u32(&done));
       }
-      if (!ok) fail();
-      mma_commit1(smem_u32(&B.drain));
-      mbar_wait_timed(smem_u32(&B.drain), 0);
+      int32_t issued = 0, b = 0, parity = 1;
+      for (; issued < n; ++issued) {
+        if (issued >= ring && !warp_wait(B.empty[b], parity)) {
+          fail();
+          break;
+        }
+        const uint32_t bar = smem_u32(&B.full[b]);
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(gr * D * 2));
+        __syncwarp();
+        if (lane < L::kChunks)
+          tma_load_5d(smem_u32(rs) + b * L::kBuf + lane * L::kChunk, &M.q, bar, 0, lane, 0, s.h, s.r * A.T + (first + issued) * q_tok);
+        if (++b == ring) b = 0, parity ^= 1;
+      }
+      // what is in flight lands before the shared memory is given up, whatever the others did (bounded)
+      for (int32_t i = max(0, issued - ring); i < issued; ++i) mbar_wait_timed(smem_u32(&B.full[i % ring]), (i / ring) & 1);
+      mbar_wait_timed(k_bar, 0);
+    } else if (is_mma && n > 0) {
+      if (elect_one()) {
+        constexpr int kSteps = L::kElems / 16;
+        constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+        const uint32_t kd = smem_desc_lo(smem_u32(ks), 16), qd = smem_desc_lo(smem_u32(rs), 16);
+        bool ok = true;
+        // barriers are asked ahead, behind MMAs that keep the tensor cores busy meanwhile
+        auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
+        auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
+          if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
+          tc_fence_after();
+        };
+        passed(false, B.k_full, 0);
+        bool q_there = false, s_there = false;
+        int32_t b = 0, parity = 0;
+        for (int32_t i = 0; i < n && ok; ++i) {
+          const uint32_t q = qd + b * (L::kBuf >> 4);
+          uint64_t& done = B.empty[b];
+          passed(q_there, B.full[b], parity);
+          if (++b == ring) b = 0, parity ^= 1;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if (v == used) break;
+            if (i > 1) passed(s_there, B.s_empty[v][i & 1], (i / 2 - 1) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              if (c == D / 32) {
+                if (v + 1 < used) {
+                  s_there = i > 1 && ask(B.s_empty[v + 1][i & 1], (i / 2 - 1) & 1);
+                } else {
+                  q_there = i + 1 < n && ask(B.full[b], parity);
+                  s_there = i > 0 && ask(B.s_empty[0][(i + 1) & 1], ((i + 1) / 2 - 1) & 1);
+                }
+              }
+              mma_ss1(tmem + v * 256 + (i & 1) * kTok, q + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2,
+                      kd + v * (L::kBuf >> 4) + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDesc, c > 0);
+            }
+            mma_commit1(smem_u32(&B.s_full[v][i & 1]));
+          }
+          if (ok) mma_commit1(smem_u32(&done));
+        }
+        if (!ok) fail();
+        mma_commit1(smem_u32(&B.drain));
+        mbar_wait_timed(smem_u32(&B.drain), 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    __syncthreads();  // as the sums' warps below
+    __syncthreads();
+    if (is_mma) {
+      tc_fence_after();
+      tmem_free(tmem, 512);
+    }
   } else {
-    const int w = warp >> 2;
-    const uint32_t my = tmem + w * 128 + ((uint32_t)(warp & 3) << 21);
+    registers_up<kUpRegs>();
+    const int w = warp >> 2, t = w >> 1, half = w & 1, row = tid & 127;
+    const int32_t f0 = e0 + t * spt, nf = min(spt, list.n - f0);
+    const bool masked = f0 + nf > list.whole;
     const float scale = kLog2e * rsqrtf((float)D);
-    const float2 scale2 = make_float2(scale, scale);
-    float total = 0.f;
-    if (w < n) B.shift[w][0][j] = j < gr ? shift_of(A, s, (first + w) * gr + j) : -INFINITY;
-    wg_sync(w);
-    for (int32_t i = w; i < n; i += 2) {
-      const float* shift = B.shift[w][i / 2 & 1];
-      const float next = i + 2 < n && j < gr ? shift_of(A, s, (first + i + 2) * gr + j) : -INFINITY;
-      const int32_t m0 = (first + i) * gr, lo = mine.lo - m0, span = mine.hi - mine.lo;
-      const bool full = lo <= 0 && mine.hi >= m0 + gr, some = mine.lo < m0 + gr && mine.hi > m0;
-      if (!warp_wait(B.s_full[w], (i / 2) & 1)) {
+    float2 acc[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) acc[c] = make_float2(0.f, 0.f);
+    // the log sum of this thread's row of a tile, whose rows are q_tok tokens behind the last one's; of one that does not
+    // count, as of one that sees nothing
+    int32_t m = first * gr + row, p = s.len + m / g;  // of the row
+    const float* lse_at = A.lse + row_place(A, s, m);
+    const int32_t m_end = row < gr ? s.rows : 0;
+    float lse = t < used && m < m_end ? *lse_at : -INFINITY;
+    bool there = false;  // the next scores, asked for ahead
+    for (int32_t i = 0; i < n && t < used; ++i, p += q_tok) {
+      m += gr;
+      lse_at += q_tok * A.G.Hq;
+      const float next = i + 1 < n && m < m_end ? *lse_at : -INFINITY;  // on its way for a tile's time
+      uint64_t vis = ~0ull;
+      if (masked) {
+        vis = 0;
+#pragma unroll 1
+        for (int32_t k = 0; k < nf; ++k) {
+          const int32_t at = k * pitch - half * 64;
+          if (at >= 64 || at + bs <= 0) continue;
+          const uint64_t bits = list.seen(f0 + k, p, A.window, A.sinks);
+          vis |= at >= 0 ? bits << at : bits >> -at;
+        }
+      }
+      if (!__all_sync(0xffffffffu, there) && !warp_wait(B.s_full[t][i & 1], (i >> 1) & 1)) {
         fail();
         break;
       }
       tc_fence_after();
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-      if (__any_sync(0xffffffffu, some)) {
-        const bool masked = __any_sync(0xffffffffu, !full) != 0;
+      const uint32_t at = tmem + t * 256 + ((uint32_t)(warp & 3) << 21) + (i & 1) * kTok + half * 64;
+      const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(-lse * kLog2e, -lse * kLog2e);
+      const bool counts = lse != -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(x, my + c);
-          tmem_wait_ld(x);
-          if (c == 96) {  // all of it read
-            tc_fence_before();
-            mbar_arrive(smem_u32(&B.s_empty[w]));
+      for (int q = 0; q < 4; ++q) {
+        uint32_t x[16];
+        tmem_ld16(x, at + q * 16);
+        tmem_wait_ld(x);
+        if (q == 3) {
+          tc_fence_before();
+          mbar_arrive(smem_u32(&B.s_empty[t][i & 1]));
+          there = i + 1 < n && mbar_test(smem_u32(&B.s_full[t][(i + 1) & 1]), ((i + 1) >> 1) & 1);
+        }
+        // two loops: with the mask's tests in it the one that needs none takes twice its instructions
+        if (counts && !masked) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 p = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2);
+            acc[q * 8 + c] = add2(acc[q * 8 + c], make_float2(ex2(p.x), ex2(p.y)));
           }
-          float4 sh[8];
+        } else if (counts) {
+          const uint32_t bits = (uint32_t)(vis >> 16 * q);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sh[e] = *reinterpret_cast<const float4*>(shift + c + 4 * e);
-          float2 p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2,
-                                  e & 1 ? make_float2(sh[e / 2].z, sh[e / 2].w) : make_float2(sh[e / 2].x, sh[e / 2].y));
-            p[e] = make_float2(ex2(y.x), ex2(y.y));
-          }
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if ((uint32_t)(c + 2 * e - lo) >= (uint32_t)span) p[e].x = 0.f;
-              if ((uint32_t)(c + 2 * e + 1 - lo) >= (uint32_t)span) p[e].y = 0.f;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            sum0 = add2(sum0, p[e]);
-            sum1 = add2(sum1, p[e + 1]);
+          for (int c = 0; c < 8; ++c) {
+            const float2 p = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2);
+            acc[q * 8 + c] = add2(acc[q * 8 + c], make_float2(bits >> (2 * c) & 1 ? ex2(p.x) : 0.f, bits >> (2 * c + 1) & 1 ? ex2(p.y) : 0.f));
           }
         }
-      } else {
-        tc_fence_before();
-        mbar_arrive(smem_u32(&B.s_empty[w]));
+        __syncwarp();
       }
-      sum0 = add2(sum0, sum1);
-      total += sum0.x + sum0.y;
-      B.shift[w][(i / 2 & 1) ^ 1][j] = next;
-      wg_sync(w);
+      lse = next;
     }
-    B.part[w][j] = total;
-  }
-  __syncthreads();
-  const bool failed = *(volatile int32_t*)&B.failed != 0;
-  for (int32_t e = tid; e < s.slots; e += kThreads) {
-    const int64_t at = unit + s.slot0 + e;
-    float sum = 0.f;
-    for (int32_t i = e * pitch; i < e * pitch + bs && !failed; ++i) sum += B.part[0][i] + B.part[1][i];
-    A.weight_out[at] = (A.weight ? A.weight[at] : 0.f) + sum;
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (is_mma) {
-    tc_fence_after();
-    tmem_free(tmem, 256);
+    // over the lanes: each step hands half of a lane's tokens to its partner; tokens 2 lane and 2 lane + 1 are left
+    float v[64];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[2 * c] = acc[c].x, v[2 * c + 1] = acc[c].y;
+#pragma unroll
+    for (int step = 32; step >= 2; step /= 2) {
+      const bool up = lane & (step / 2);
+#pragma unroll
+      for (int c = 0; c < step; ++c) {
+        const float keep = up ? v[c + step] : v[c], give = up ? v[c] : v[c + step];
+        v[c] = keep + __shfl_xor_sync(0xffffffffu, give, step / 2);
+      }
+    }
+    __syncthreads();  // nothing reads or fills the ring any more
+    float* part = reinterpret_cast<float*>(rs);  // [tiles][warps of a quarter][128]
+    *reinterpret_cast<float2*>(part + (t * 4 + (warp & 3)) * 128 + half * 64 + lane * 2) = make_float2(v[0], v[1]);
+    asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
+    const bool failed = *(volatile int32_t*)&B.failed != 0;
+    for (int32_t k = tid & 255; k < nf; k += 256) {
+      const int64_t at = unit + list.slot(f0 + k);
+      const float* x = part + t * 512 + k * pitch;
+      float sum = 0.f;
+      for (int32_t j = 0; j < bs && !failed; ++j) sum += (x[j] + x[j + 128]) + (x[j + 256] + x[j + 384]);
+      A.weight_out[at] = (A.weight ? A.weight[at] : 0.f) + sum;
+    }
+    tc_fence_before();
+    __syncthreads();
   }
 }
 
@@ -410,14 +490,15 @@ cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {
 template <int D>
 cudaError_t run_mma(const ChunkArgs& A, cudaStream_t s) {
   using L = Lines<D, kTok>;
-  const int32_t pitch = A.G.bs * L::kBytes % 128 ? A.G.bs + 1 : A.G.bs, spt = kTok / pitch, tiles = (A.G.kb + spt - 1) / spt;
+  const int32_t pitch = A.G.bs * L::kBytes % 128 ? A.G.bs + 1 : A.G.bs, spt = kTok / pitch, tiles = (A.G.kb + 2 * spt - 1) / (2 * spt);
   const int32_t q_tok = A.T < 128 / A.G.g ? A.T : 128 / A.G.g;
-  const size_t third = 233472 / 3;  // no third CTA comes to wait for TMEM
-  const size_t rest = 1024 + sizeof(Bars), share = D <= 128 ? 115712 : kMaxSmem;
-  int32_t ring = (int32_t)((share - rest) / L::kBuf) - 1;
-  if (ring > 4) ring = 4;
-  size_t smem = rest + (size_t)(ring + 1) * L::kBuf;
-  if (smem < third) smem = third;
+  // one CTA to an SM, by its TMEM: never so small that another kernel's that takes TMEM finds a place beside it
+  const size_t rest = (weigh_misc(A.G.kb) + 1023) / 1024 * 1024 + 2 * L::kBuf, least = 2 * (233472 / 3);
+  int32_t ring = (int32_t)((kMaxSmem - rest) / L::kBuf);
+  if (ring > kRing) ring = kRing;
+  size_t smem = rest + (size_t)ring * L::kBuf + 1024;
+  if (smem > kMaxSmem) smem = kMaxSmem;
+  if (smem < least) smem = least;
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   WeighMaps m;

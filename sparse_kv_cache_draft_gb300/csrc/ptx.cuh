@@ -12,6 +12,12 @@ constexpr uint32_t kWaitLimit = 1u << 24;  // mbarrier polls before a wait gives
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
+// Bytes of dynamic shared memory the block was launched with.
+__device__ __forceinline__ uint32_t dynamic_smem() {
+  uint32_t n;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+  return n;
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
