@@ -36,13 +36,15 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // Adds what the values that are not finite, of tokens in tiles that were masked, give to four outputs (dims c .. c + 3) of
-// a row that sees them: they are zero in the products, where a weight of zero times them would reach rows that do not.
+// a row that sees them: they are zero in the products, where a weight of zero times them would reach rows that do not. (Arguments one by
+// one: a struct whose address is taken is written to local memory by every thread, whether it comes here or not.)
 template <typename T>
-__device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, const Span& s, const List& L, int32_t spt, int32_t p, int32_t c) {
+__device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, int64_t unit, const uint16_t* at, const int32_t* base, int32_t whole, int32_t n, int32_t part,
+                                              int32_t parts, int32_t spt, int32_t p, int32_t c) {
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int64_t unit = ((int64_t)s.r * A.G.Hkv + s.h) * A.G.kb;
-  for (int32_t e = L.whole / spt * spt; e < L.n; ++e) {
-    if (e / spt % s.parts != s.part) continue;
+  const List L{at, base, A.slot_block + unit, A.G.kb, A.G.bs, whole, n};
+  for (int32_t e = whole / spt * spt; e < n; ++e) {
+    if (e / spt % parts != part) continue;
     const int32_t slot = L.slot(e);
     uint64_t bits = L.seen(e, p, A.window, A.sinks);
     const T* v = reinterpret_cast<const T*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)A.G.bs * A.G.d + c;
@@ -106,8 +108,7 @@ __host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) +
 
 // Up to 128 rows the weights that slots draw are summed on the way: [entries][q_rows] sums of a row's weights over a slot's
 // tokens, against the maximum of then, [tiles][q_rows], both of this CTA's tiles; with the final maxima and sums they are
-// joined at the end. (Taken afterwards, from the log sums, they cost a second pass over K: 128 requests x 1 token
-// 479 us against NNN.)
+// joined at the end. Where a slot is a multiple of eight columns of a tile, as the sums come by eight.
 __host__ __device__ constexpr size_t drawn_bytes(int tiles, int spt, int q_rows) { return (size_t)tiles * (spt + 1) * q_rows * 4; }
 
 struct ChunkMaps {
@@ -142,7 +143,7 @@ constexpr int kUpRegs = 216, kDownRegs = 72;
 
 template <int D, int NW, bool kDraw>
 __global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
-chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok, const int32_t q_rows,
+chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok, const int32_t q_rows,
                  const int32_t pitch, const int32_t most) {
   constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
   using L = Lines<D, kTile>;
@@ -423,6 +424,9 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       const int32_t c = 32 * u + lane;
       ends[u] = tails ? __ballot_sync(0xffffffffu, c / pitch < spt && c % pitch < bs) : ~0u;
     }
+    uint32_t closes = 0;          // bit k: columns 8 k .. 8 k + 7 of a tile are the last of a slot
+    if (kDraw)
+      for (int k = 0; k < 8; ++k) closes |= (uint32_t)((k + 1) * 8 % pitch == 0) << k;
     for (int32_t i = 0; i < n; ++i) {
       const int32_t e0 = (s.part + i * s.parts) * spt;
       const bool part_seen = e0 + spt > list.whole;  // who sees what differs, or the tile is not full
@@ -432,40 +436,51 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       if (part_seen) {
         const int32_t ne = min(spt, list.n - e0);
         uint64_t lo = 0, hi = 0;
-#pragma unroll 2
-        for (int32_t k = 0; k < ne; ++k) {
-          const uint64_t bits = list.seen(e0 + k, p, A.window, A.sinks);
-          const int32_t at = k * pitch;
-          if (at < 64) {
-            lo |= bits << at;
-            if (at) hi |= bits >> (64 - at);
-          } else {
-            hi |= bits << (at - 64);
+#pragma unroll 1
+        for (int32_t k0 = 0; k0 < ne; k0 += 32) {
+          // the entries' first positions, one to a lane: shared memory answers late beside the MMAs. Of an entry that all see
+          // whole, one that all do.
+          const int32_t mine = k0 + lane < ne && e0 + k0 + lane >= list.whole ? list.first(e0 + k0 + lane) : INT32_MIN;
+#pragma unroll 4
+          for (int32_t k = k0; k < min(ne, k0 + 32); ++k) {
+            const int32_t base = __shfl_sync(0xffffffffu, mine, k - k0), at = k * pitch;
+            const uint64_t bits = base == INT32_MIN ? first_bits(bs) : seen_of(base, p, bs, A.window, A.sinks);
+            if (at < 64) {
+              lo |= bits << at;
+              if (at) hi |= bits >> (64 - at);
+            } else {
+              hi |= bits << (at - 64);
+            }
           }
         }
         const uint64_t both[2] = {lo, hi};
 #pragma unroll
         for (int u = 0; u < kWords; ++u) vis[u] = (uint32_t)(both[u / 2] >> 32 * (u & 1));
-        // Values that are not finite meet weights of zero: they are zero in the product. Each warpgroup sees to it,
-        // whichever product comes first; a line is one thread's.
-        if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
-          fail();
-          break;
-        }
-        uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
-        if (row < kTile && any_not_finite<D, kTile>(v, row)) {
-          const int32_t k = row / pitch, e = e0 + k;
-#pragma unroll 1
-          for (int c = 0; c < D / 8; ++c) {
-            uint4* x = reinterpret_cast<uint4*>(v + L::piece(row, c));
-            uint4 y = *x;
-            if (clean(y)) *x = y;
+        // Values that are not finite meet weights of zero: they are zero in the products. The first warpgroup sees to it, whose
+        // product is the first of both; a line is one thread's.
+        if (w == 0) {
+          if (!warp_wait(B.full[v_use(i) % ring], (v_use(i) / ring) & 1)) {
+            fail();
+            break;
           }
-          // a token that some row may see?
-          if (k < ne && (e < list.whole || list.first(e) <= s.p_hi - (row - k * pitch))) *(volatile int32_t*)&B.bad = 1;
+          uint8_t* v = rs + (size_t)(v_use(i) % ring) * L::kBuf;
+          const bool any = row < kTile && any_not_finite<D, kTile>(v, row);
+          if (__any_sync(0xffffffffu, any)) {
+            if (any) {
+              const int32_t k = row / pitch, e = e0 + k;
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* x = reinterpret_cast<uint4*>(v + L::piece(row, c));
+                uint4 y = *x;
+                if (clean(y)) *x = y;
+              }
+              // a token that some row may see?
+              if (k < ne && (e < list.whole || list.first(e) <= s.p_hi - (row - k * pitch))) *(volatile int32_t*)&B.bad = 1;
+            }
+            __syncwarp();
+            fence_proxy_async();
+          }
         }
-        __syncwarp();
-        fence_proxy_async();
       }
       if (!warp_wait(B.s_full[w][i & 1], (i >> 1) & 1)) {
         fail();
@@ -482,7 +497,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
       bool lost = false;
       const uint32_t st = my + (kS == 2 ? (i & 1) * kTile : 0);
       uint32_t a[kWords][32], pk[32];
-      float2 sum0, sum1;
+      float2 sums[kDraw ? 8 : 2];  // of the weights; with kDraw of eight columns each
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       // scores of 64 columns as they count
       auto mask = [&](int u0, int u1) {
@@ -503,23 +518,23 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t *x0 = &a[2 * half][2 * e], *y0 = &a[2 * half + 1][2 * e];
-          if (kDraw && with_max) maxima(e);
           float2 x = fma2(make_float2(__uint_as_float(x0[0]), __uint_as_float(x0[1])), scale2, neg2);
           float2 y = fma2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])), scale2, neg2);
           x = make_float2(ex2(x.x), ex2(x.y));
           y = make_float2(ex2(y.x), ex2(y.y));
-          sum0 = add2(sum0, x);
-          sum1 = add2(sum1, y);
+          float2 &sx = sums[kDraw ? e / 4 : 0], &sy = sums[kDraw ? 4 + e / 4 : 1];
+          sx = add2(sx, x);
+          sy = add2(sy, y);
           pk[e] = pack2(x.x, x.y);
           pk[16 + e] = pack2(y.x, y.y);
-          if (!kDraw && with_max) maxima(e);  // here: before the weights it costs registers
-          if (kDraw) {
-            a[2 * half][2 * e] = __float_as_uint(x.x), a[2 * half][2 * e + 1] = __float_as_uint(x.y);
-            a[2 * half + 1][2 * e] = __float_as_uint(y.x), a[2 * half + 1][2 * e + 1] = __float_as_uint(y.y);
-          }
+          if (with_max) maxima(e);
         }
       };
-      sum0 = sum1 = make_float2(0.f, 0.f);
+      auto no_sums = [&] {
+#pragma unroll
+        for (float2& x : sums) x = make_float2(0.f, 0.f);
+      };
+      no_sums();
       if (active) {
 #pragma unroll
         for (int u = 0; u < kWords; ++u) tmem_ld32(a[u], st + 32 * u);
@@ -560,7 +575,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
           tmem_wait_ld(a[0]);
           tmem_wait_ld(a[1]);
           mask(0, 2);
-          sum0 = sum1 = make_float2(0.f, 0.f);
+          no_sums();
           weights(0, 0);
         }
       }
@@ -578,37 +593,26 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
         tc_fence_before();
         mbar_arrive(smem_u32(&B.p_full[w][i & 1][half]));
       }
-      sum0 = add2(sum0, sum1);
-      l_run += sum0.x + sum0.y;
-      if (kDraw && active) {
-        // sums of slots, behind the product's start
+      if constexpr (kDraw) {
+        // sums of slots, behind the product's start; a slot is eight columns or a multiple of them
+        float all = 0.f, sum = 0.f;
         float* to = drawn + (size_t)i * spt * q_rows + row;
-        float sum = 0.f;
-        if (pitch % 16 == 0) {
+        const bool keep = active && real;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e & 3] += __uint_as_float(a[k / 2][k % 2 * 16 + e]);
-            sum += (x[0] + x[1]) + (x[2] + x[3]);
-            if ((k + 1) * 16 % pitch) continue;
-            if (real) *to = sum;
-            to += q_rows;
-            sum = 0.f;
-          }
-        } else {
-          int32_t left = pitch;
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) {
-            sum += __uint_as_float(a[c / 32][c % 32]);
-            if (--left) continue;
-            if (real && c < spt * pitch) *to = sum;
-            to += q_rows;
-            sum = 0.f;
-            left = pitch;
-          }
+        for (int k = 0; k < 8; ++k) {
+          const float x = sums[k].x + sums[k].y;
+          all += x;
+          sum += x;
+          if (!(closes >> k & 1)) continue;
+          if (keep) *to = sum;
+          to += q_rows;
+          sum = 0.f;
         }
-        if (real) drawn_m[i * q_rows + row] = m_run;
+        l_run += all;
+        if (keep) drawn_m[i * q_rows + row] = m_run;
+      } else {
+        sums[0] = add2(sums[0], sums[1]);
+        l_run += sums[0].x + sums[0].y;
       }
     }
     // with one S buffer the last tile's alone is counted there
@@ -621,7 +625,7 @@ chunk_mma_kernel(const ChunkArgs A, const __grid_constant__ ChunkMaps M, const S
     auto extra = [&](uint32_t (&o)[32], int c) {
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
-        const float4 x = not_finite_of<__nv_bfloat16>(A, s, list, spt, p, c + e);
+        const float4 x = not_finite_of<__nv_bfloat16>(A, unit, list.at, list.base, list.whole, list.n, s.part, s.parts, spt, p, c + e);
         o[e] = __float_as_uint(__uint_as_float(o[e]) + x.x);
         o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + x.y);
         o[e + 2] = __float_as_uint(__uint_as_float(o[e + 2]) + x.z);
@@ -767,7 +771,7 @@ __host__ __device__ constexpr size_t f32_smem(int d, int rg, int kb) {
 __host__ __device__ constexpr int f32_ctas(int dv, int rg) { return dv <= 4 && rg < 4 ? 3 : dv <= 4 ? 2 : 1; }  // CTAs of an SM, by registers
 
 template <int DV, int RG>
-__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kernel(const ChunkArgs A, const Shape shape, const int32_t q_tok) {
+__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kernel(const __grid_constant__ ChunkArgs A, const Shape shape, const int32_t q_tok) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int d = DV * 32, pitch = f32_pitch(d), kRows = 16 * RG, TH = 4 / RG, kTok = kF32Tile / TH, NT = kTok / 8;
   float* qs = reinterpret_cast<float*>(smem);      // [rows][pitch]
@@ -1035,7 +1039,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
       x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
     }
     if (*bad && sum != 0.f) {
-      const float4 y = not_finite_of<float>(A, s, list, spt, s.len + (s.row0 + row) / g, c * 4);
+      const float4 y = not_finite_of<float>(A, unit, list.at, list.base, list.whole, list.n, s.part, s.parts, spt, s.len + (s.row0 + row) / g, c * 4);
       x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
     }
     if (s.parts > 1) {
@@ -1137,7 +1141,7 @@ cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   const int32_t most = most_tiles(A, spt, NW * q_tok);
   const size_t share = two ? 115712 : kMaxSmem, tiles0 = (size_t)NW * q_rows * D * 2, sums = kDraw ? drawn_bytes(most, spt, q_rows) : 0;
   if constexpr (NW == 1 && !kDraw) {
-    if (A.weight_out && groups == 1 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
+    if (A.weight_out && groups == 1 && pitch % 8 == 0 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
   }
   *drawn = kDraw;
   const size_t rest = (mma_misc(A.G.kb) + sums + 1023) / 1024 * 1024 + tiles0;
