@@ -1,7 +1,7 @@
 // Slots of a paged pool for the blocks of new tokens: empty ones first, then those whose tokens have drawn the least
 // attention weight.
 //
-// A unit (request, KV head) is a warp's up to 128 slots, the CTA's eight warps' beyond, four slots to a thread at most, ids and
+// A unit (request, KV head) is a warp's up to 128 slots, four to a thread, and a CTA's beyond, one to a thread, ids and
 // weights in registers. The m-th smallest weight is found bit by bit over the weights' ordered images, from the highest bit in
 // which any two differ (sorting them would move every slot), and slots of that weight go by their index. Everything is
 // integer work on a few kilobytes: a call is a launch, two rounds of memory and the sums over the unit.
@@ -12,7 +12,6 @@ namespace okv {
 namespace {
 
 constexpr int kUnits = 4;      // of a CTA, of a warp each
-constexpr int kWide = 8;       // warps of a unit
 constexpr int kRange = 2048;   // new blocks looked at: the last kb that no slot holds are among the last 2 kb
 constexpr int kMaxSlots = 1024;
 
@@ -32,49 +31,61 @@ __device__ __forceinline__ uint32_t image_of(float w) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-// Sums, least and most over a unit's W warps, in `x` by turns: the values before are read behind one barrier, and the ones before
-// those behind two.
-template <int W>
+// What a unit's W warps know together.
+template <int N, int W>
 struct Unit {
-  int32_t (*x)[kWide];  // [2][warps]
-  int warp, turn;
-  template <typename F>
-  __device__ __forceinline__ int32_t over(int32_t mine, F join) {
-    if (W == 1) return mine;
-    int32_t* at = x[turn];
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) at[warp] = mine;
-    __syncthreads();
-    int32_t v = at[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) v = join(v, at[i]);
-    return v;
-  }
-  __device__ __forceinline__ int32_t sum(int32_t v) {
-    return over(__reduce_add_sync(0xffffffffu, v), [](int32_t a, int32_t b) { return a + b; });
-  }
-  // ... of the warps before this one; `all` is a warp's
+  static_assert(W == 1 || N == 1, "a slot to a thread");
+  int32_t* x;  // [W]
+  int warp;
+  __device__ __forceinline__ int32_t count(int32_t mine) { return W == 1 ? __reduce_add_sync(0xffffffffu, mine) : __syncthreads_count(mine); }
+  // what the warps before this one have; `all` is a warp's
   __device__ __forceinline__ int32_t before(int32_t all) {
     if (W == 1) return 0;
-    int32_t* at = x[turn];
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) at[warp] = all;
+    const int lane = threadIdx.x & 31;
     __syncthreads();
-    int32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) v += i < warp ? at[i] : 0;
-    return v;
+    if (lane == 0) x[warp] = all;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < warp ? x[lane] : 0);
   }
 };
+
+// The need-th smallest of the images of a warp's slots, K to a lane (0xFFFFFFFF: none), and how many are below it: the bits that
+// all share, then bit by bit.
+struct Kth {
+  uint32_t image;
+  int32_t less;
+};
+template <int K>
+__device__ __forceinline__ Kth kth_of(const uint32_t (&key)[K], int32_t need) {
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (int u = 0; u < K; ++u) lo = min(lo, key[u]), hi = max(hi, key[u]);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  const int bits = 32 - __clz(lo ^ hi);
+  Kth k{bits == 32 ? 0u : lo >> bits << bits, 0};
+  for (int bit = bits - 1; bit >= 0; --bit) {
+    const uint32_t up = k.image | 1u << bit;
+    int32_t c = 0;
+#pragma unroll
+    for (int u = 0; u < K; ++u) c += key[u] < up;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c <= need) k.image = up, k.less = c;
+    if (c == need) break;  // the need smallest are those below `up`
+  }
+  return k;
+}
 
 template <int N, int W>  // slots up to 32 N W
 __global__ void __launch_bounds__((W == 1 ? kUnits : W) * 32) evict_kernel(const EvictArgs A) {
   constexpr int kHere = W == 1 ? kUnits : 1;
   __shared__ uint32_t held_of[kHere][kRange / 32];
   __shared__ uint16_t new_of[kHere][32 * N * W];
-  __shared__ int32_t sums[2][kWide];
+  __shared__ int16_t rank_of[kHere][kRange / 32];
+  __shared__ int32_t sums[W], kept_less;
+  __shared__ uint32_t keys[W == 1 ? 1 : 32 * W];
   const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, here = W == 1 ? threadIdx.x >> 5 : 0;
-  const int first_slot = warp * N * 32 + lane;
+  const int first_slot = warp * N * 32 + lane;  // and of the new blocks, of which W == 1 takes 32 at a time
   uint32_t* held = held_of[here];
   uint16_t* fresh = new_of[here];
   for (int i = threadIdx.x % (W * 32); i < kRange / 32; i += W * 32) held[i] = 0;
@@ -103,7 +114,7 @@ __global__ void __launch_bounds__((W == 1 ? kUnits : W) * 32) evict_kernel(const
     else
       __syncthreads();
   };
-  Unit<W> unit{sums, warp, 0};
+  Unit<N, W> unit{sums, warp};
 
   // which slots may be taken, and which new blocks there are already
   uint32_t empty = 0, old = 0, key[N];  // bit u: the slot of round u
@@ -133,20 +144,24 @@ __global__ void __launch_bounds__((W == 1 ? kUnits : W) * 32) evict_kernel(const
   const int32_t wanted = __reduce_add_sync(0xffffffffu, mine);
   uint32_t taken = 0;
   if (wanted > 0) {  // the unit's as a whole
-    const int32_t n_empty = unit.sum(__popc(empty)), n_old = unit.sum(__popc(old)), m = min(wanted, n_empty + n_old);
+    const int32_t n_empty = unit.count(__popc(empty)), n_old = unit.count(__popc(old)), m = min(wanted, n_empty + n_old);
+    // the m newest of them, in order: each bit's rank from those of the words before it
+    int32_t up = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, up, k);
+      if (lane >= k) up += x;
+    }
+    sync();  // `held` has been read
     if (warp == 0) {
-      // the m newest of them, in order
-      int32_t up = mine;
-#pragma unroll
-      for (int k = 1; k < 32; k *= 2) {
-        const int32_t x = __shfl_up_sync(0xffffffffu, up, k);
-        if (lane >= k) up += x;
-      }
-      int32_t nth = up - mine - (wanted - m);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        for (uint32_t x = want[k]; x; x &= x - 1, ++nth)
-          if (nth >= 0) fresh[nth] = (uint16_t)((2 * lane + k) * 32 + __ffs(x) - 1);
+      held[2 * lane] = want[0], held[2 * lane + 1] = want[1];
+      rank_of[here][2 * lane] = (int16_t)(up - mine), rank_of[here][2 * lane + 1] = (int16_t)(up - __popc(want[1]));
+    }
+    sync();
+    for (int32_t i = first_slot; i < span; i += 32 * W) {
+      const uint32_t word = held[i >> 5];
+      const int32_t nth = rank_of[here][i >> 5] + __popc(word & ((1u << (i & 31)) - 1u)) - (wanted - m);
+      if ((word >> (i & 31) & 1) && nth >= 0) fresh[nth] = (uint16_t)i;
     }
     const uint32_t below = (1u << lane) - 1u;
     // each slot with its bit in `of`, by index: use(u, how many there are before it)
@@ -162,37 +177,34 @@ __global__ void __launch_bounds__((W == 1 ? kUnits : W) * 32) evict_kernel(const
     each(empty, [&](int u, int32_t rank) { taken |= (uint32_t)(rank < m) << u; });
     const int32_t need = m - n_empty;
     if (need > 0) {
-      uint32_t lo = 0xFFFFFFFFu, hi = 0;
+      Kth k;
+      if constexpr (W == 1) {
 #pragma unroll
-      for (int u = 0; u < N; ++u)
-        if (old >> u & 1) lo = min(lo, key[u]), hi = max(hi, key[u]);
-      lo = (uint32_t)unit.over((int32_t)__reduce_min_sync(0xffffffffu, lo), [](int32_t a, int32_t b) { return (int32_t)min((uint32_t)a, (uint32_t)b); });
-      hi = (uint32_t)unit.over((int32_t)__reduce_max_sync(0xffffffffu, hi), [](int32_t a, int32_t b) { return (int32_t)max((uint32_t)a, (uint32_t)b); });
-      // the need-th smallest image: the bits that all share, then bit by bit
-      const int bits = 32 - __clz(lo ^ hi);
-      uint32_t kth = bits == 32 ? 0u : lo >> bits << bits;
-      int32_t less = 0;  // slots below kth
-      for (int bit = bits - 1; bit >= 0; --bit) {
-        const uint32_t up = kth | 1u << bit;
-        int32_t c = 0;
+        for (int u = 0; u < N; ++u)
+          if (!(old >> u & 1)) key[u] = 0xFFFFFFFFu;
+        k = kth_of(key, need);
+      } else {
+        // by one warp: an exchange of all for each bit takes longer than a warp's look at all slots (1024 of them 10 us)
+        keys[threadIdx.x] = old ? key[0] : 0xFFFFFFFFu;
+        __syncthreads();
+        if (warp == 0) {
+          uint32_t all[W];
 #pragma unroll
-        for (int u = 0; u < N; ++u) c += (old >> u & 1) && key[u] < up;
-        c = unit.sum(c);
-        if (c < need) kth = up, less = c;
-        if (c == need) {  // the need smallest are those below `up`
-          kth = up;
-          less = need;
-          break;
+          for (int u = 0; u < W; ++u) all[u] = keys[32 * u + lane];
+          k = kth_of(all, need);
+          if (lane == 0) sums[0] = (int32_t)k.image, kept_less = k.less;
         }
+        __syncthreads();
+        k = Kth{(uint32_t)sums[0], kept_less};
       }
       uint32_t same = 0;
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         if (!(old >> u & 1)) continue;
-        if (key[u] < kth) taken |= 1u << u;
-        if (key[u] == kth) same |= 1u << u;
+        if (key[u] < k.image) taken |= 1u << u;
+        if (key[u] == k.image) same |= 1u << u;
       }
-      each(same, [&](int u, int32_t rank) { taken |= (uint32_t)(rank < need - less) << u; });
+      each(same, [&](int u, int32_t rank) { taken |= (uint32_t)(rank < need - k.less) << u; });
     }
     sync();
     each(taken, [&](int u, int32_t rank) {
@@ -236,6 +248,6 @@ extern "C" okv_status okv_evict_static(int32_t n_requests, int32_t n_new, int32_
   if (okv_status st = check_stream(stream)) return st;
   const EvictArgs A{n_requests, kv_heads, block_size, slots, n_new, sinks, recent, lengths, counts, slot_block, weight, slot_block_out, weight_out};
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = slots <= 32 ? run<1, 1>(A, s) : slots <= 128 ? run<4, 1>(A, s) : slots <= 256 ? run<1, kWide>(A, s) : slots <= 512 ? run<2, kWide>(A, s) : run<4, kWide>(A, s);
+  const cudaError_t e = slots <= 32 ? run<1, 1>(A, s) : slots <= 128 ? run<4, 1>(A, s) : slots <= 256 ? run<1, 8>(A, s) : slots <= 512 ? run<1, 16>(A, s) : run<1, 32>(A, s);
   return e == cudaSuccess ? OKV_OK : OKV_ECUDA;
 }
