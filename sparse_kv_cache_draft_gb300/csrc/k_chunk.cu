@@ -1061,8 +1061,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
 
 // ---- launches ----------------------------------------------------------------------------------------------
 
-// Tiles of `tile` tokens that a group of rows may have: of the slots there are, and of those that a window leaves it.
-int32_t most_tiles(const ChunkArgs& A, int32_t spt, int32_t group_tok) {
+// Tiles that a group of rows has if no block is in two slots: of the slots there are, and of those that a window leaves it.
+int32_t likely_tiles(const ChunkArgs& A, int32_t spt, int32_t group_tok) {
   const int64_t bs = A.G.bs, seen = ((int64_t)A.window + group_tok + bs - 1) / bs + 1 + ((int64_t)A.sinks + bs - 1) / bs;
   const int64_t slots = seen < A.G.kb ? seen : A.G.kb;
   return (int32_t)((slots + spt - 1) / spt);
@@ -1078,7 +1078,7 @@ cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {
   if (per_sm > f32_ctas(DV, RG)) per_sm = f32_ctas(DV, RG);
   if (per_sm < 1) per_sm = 1;
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
-  const Shape shape = pick_shape(items, groups, per_sm, most_tiles(A, kF32Tile / A.G.bs, q_tok), kF32Costs, cluster_room(kF32Threads, per_sm));
+  const Shape shape = pick_shape(items, groups, per_sm, likely_tiles(A, kF32Tile / A.G.bs, q_tok), kF32Costs, cluster_room(kF32Threads, per_sm));
   return launch_cluster(chunk_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape, q_tok);
 }
 
@@ -1137,8 +1137,8 @@ cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   // that share of the shared memory. It is never so small that a third CTA, or one of 256 columns beside one of 512, could
   // come to wait for TMEM (two clusters that each hold what the other waits for would wait for ever).
   const bool two = D <= 128 && NW == 1;
-  // the slots' sums, where the ring keeps the four buffers that it needs
-  const int32_t most = most_tiles(A, spt, NW * q_tok);
+  // the slots' sums, where the ring keeps the four buffers that it needs: of all slots, which may all hold the same block
+  const int32_t most = (A.G.kb + spt - 1) / spt;
   const size_t share = two ? 115712 : kMaxSmem, tiles0 = (size_t)NW * q_rows * D * 2, sums = kDraw ? drawn_bytes(most, spt, q_rows) : 0;
   if constexpr (NW == 1 && !kDraw) {
     if (A.weight_out && groups == 1 && pitch % 8 == 0 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
@@ -1153,7 +1153,7 @@ cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   if (smem < least) smem = least;
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
   const int32_t per_sm = two ? 2 : 1;
-  const Shape shape = pick_shape(items, groups, per_sm, most, NW == 1 ? kMmaCosts : kMmaCostsWide,
+  const Shape shape = pick_shape(items, groups, per_sm, likely_tiles(A, spt, NW * q_tok), NW == 1 ? kMmaCosts : kMmaCostsWide,
                                  cluster_room(mma_threads<NW>(), per_sm));
   ChunkMaps maps;
   if (cudaError_t e = make_maps<D, kTile>(A, spt, q_tok, &maps)) return e;

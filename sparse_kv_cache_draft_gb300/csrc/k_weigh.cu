@@ -413,18 +413,33 @@ __global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs 
   }
   const float scale = kLog2e / sqrtf((float)d);
   float total[2] = {0.f, 0.f};
-  for (int32_t i = first; i < end; ++i) {
-    __syncthreads();  // the tile before has been read
+  // a tile of queries comes into registers while the one before is at its products
+  constexpr int kEach = kF32Rows * kPieces / kF32Threads;
+  float4 rows[kEach];
+  float row_shift = 0.f;
+  auto fetch = [&](int32_t i) {
     const int32_t m0 = i * gr;
-    for (int32_t x = tid; x < kF32Rows * kPieces; x += kF32Threads) {
-      const int32_t row = x / kPieces, c = x % kPieces, m = m0 + row, t = m / g;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < gr && t < s.cnt)
-        y = *reinterpret_cast<const float4*>((const float*)A.q + ((((int64_t)s.r * A.T + t) * A.G.Hq + s.h * g + m - t * g) * d + c * 4));
-      *reinterpret_cast<float4*>(qs + row * pitch + c * 4) = y;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int32_t x = tid + u * kF32Threads, row = x / kPieces, c = x % kPieces, m = m0 + row, t = m / g;
+      rows[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < end && row < gr && t < s.cnt)
+        rows[u] = *reinterpret_cast<const float4*>((const float*)A.q + ((((int64_t)s.r * A.T + t) * A.G.Hq + s.h * g + m - t * g) * d + c * 4));
     }
-    if (tid < kF32Rows) shift[tid] = tid < gr ? shift_of(A, s, m0 + tid) : -INFINITY;
+    if (tid < kF32Rows) row_shift = i < end && tid < gr ? shift_of(A, s, m0 + tid) : -INFINITY;
+  };
+  fetch(first);
+  for (int32_t i = first; i < end; ++i) {
+    const int32_t m0 = i * gr;
+    __syncthreads();  // the tile before has been read
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int32_t x = tid + u * kF32Threads;
+      *reinterpret_cast<float4*>(qs + x / kPieces * pitch + x % kPieces * 4) = rows[u];
+    }
+    if (tid < kF32Rows) shift[tid] = row_shift;
     __syncthreads();
+    fetch(i + 1);
     float sc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
