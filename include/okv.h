@@ -416,9 +416,10 @@ OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, i
  * draws of it. One pass of a layer over the next tokens of every request (a chunk of a prompt, or one token):
  *   okv_evict_static -> okv_append_qkv_static -> okv_attend_chunk_static -> (the caller advances lengths)
  * with the same lengths and counts in all three. As for the calls above: nothing is allocated, there is no
- * workspace, calls on different streams are independent, each can be captured, one launch each (two for
- * okv_attend_chunk_static with weight_out), EINVAL without a launch on what okv_create refuses, NULL or misaligned
- * pointers and a stream of another device. A request whose length is negative, or past 2^31 - 1 with n_new more
+ * workspace, calls on different streams are independent, each can be captured, one launch each (up to two
+ * for okv_attend_chunk_static with weight_out), EINVAL without a launch on what okv_create refuses, NULL or misaligned
+ * pointers and a stream of another device. A copy or product that never completes is given up after about two seconds: the rows
+ * of its group are then not written, or incomplete. A request whose length is negative, or past 2^31 - 1 with n_new more
  * tokens, counts as one without new tokens. */
 
 /* Attention of new tokens over the resident ones. Token t < counts[r] (device [n_requests] int32, clamped to

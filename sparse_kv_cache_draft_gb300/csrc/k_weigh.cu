@@ -6,6 +6,8 @@
 // that sees any of them, so that a slot's sum is one CTA's, in one order, and nothing is added by atomics.
 #include <stddef.h>
 
+#include <type_traits>
+
 #include "chunk.cuh"
 
 namespace okv {
@@ -286,8 +288,8 @@ weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const i
       m += gr;
       lse_at += q_tok * A.G.Hq;
       const float next = i + 1 < n && m < m_end ? *lse_at : -INFINITY;  // on its way for a tile's time
-      uint64_t vis = ~0ull;
-      if (masked) {
+      uint64_t vis = lse != -INFINITY ? ~0ull : 0;
+      if (masked && vis) {
         vis = 0;
 #pragma unroll 1
         for (int32_t k = 0; k < nf; ++k) {
@@ -304,34 +306,32 @@ weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const i
       tc_fence_after();
       const uint32_t at = tmem + t * 256 + ((uint32_t)(warp & 3) << 21) + (i & 1) * kTok + half * 64;
       const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(-lse * kLog2e, -lse * kLog2e);
-      const bool counts = lse != -INFINITY;
+      // twice, with the loads: one loop for both takes the mask's tests for every score, three instructions to two of the sums
+      auto add = [&](auto with_mask) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t x[16];
-        tmem_ld16(x, at + q * 16);
-        tmem_wait_ld(x);
-        if (q == 3) {
-          tc_fence_before();
-          mbar_arrive(smem_u32(&B.s_empty[t][i & 1]));
-          there = i + 1 < n && mbar_test(smem_u32(&B.s_full[t][(i + 1) & 1]), ((i + 1) >> 1) & 1);
-        }
-        // two loops: with the mask's tests in it the one that needs none takes twice its instructions
-        if (counts && !masked) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float2 p = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2);
-            acc[q * 8 + c] = add2(acc[q * 8 + c], make_float2(ex2(p.x), ex2(p.y)));
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[16];
+          tmem_ld16(x, at + q * 16);
+          tmem_wait_ld(x);
+          if (q == 3) {
+            tc_fence_before();
+            mbar_arrive(smem_u32(&B.s_empty[t][i & 1]));
+            there = i + 1 < n && mbar_test(smem_u32(&B.s_full[t][(i + 1) & 1]), ((i + 1) >> 1) & 1);
           }
-        } else if (counts) {
           const uint32_t bits = (uint32_t)(vis >> 16 * q);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float2 p = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2);
-            acc[q * 8 + c] = add2(acc[q * 8 + c], make_float2(bits >> (2 * c) & 1 ? ex2(p.x) : 0.f, bits >> (2 * c + 1) & 1 ? ex2(p.y) : 0.f));
+            float2 e = make_float2(ex2(p.x), ex2(p.y));
+            if (with_mask) e = make_float2(bits >> (2 * c) & 1 ? e.x : 0.f, bits >> (2 * c + 1) & 1 ? e.y : 0.f);
+            acc[q * 8 + c] = add2(acc[q * 8 + c], e);
           }
         }
-        __syncwarp();
-      }
+      };
+      if (__any_sync(0xffffffffu, masked || !vis))
+        add(std::true_type());
+      else
+        add(std::false_type());
       lse = next;
     }
     // over the lanes: each step hands half of a lane's tokens to its partner; tokens 2 lane and 2 lane + 1 are left
