@@ -8,8 +8,8 @@ namespace okv {
 
 // New tokens of request r: 0 where its length leaves no room for n_new more positions.
 __device__ __forceinline__ int32_t new_tokens(const ChunkArgs& A, int32_t r, int32_t len) {
-  if (len < 0 || (int64_t)len + A.T > INT32_MAX) return 0;
-  return A.counts ? min(max(A.counts[r], 0), A.T) : A.T;
+  const int32_t n = A.counts ? A.counts[r] : A.T;  // on its way beside the length
+  return len < 0 || (int64_t)len + A.T > INT32_MAX ? 0 : min(max(n, 0), A.T);
 }
 
 __device__ __forceinline__ uint64_t first_bits(int32_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }

@@ -642,6 +642,12 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
       uint8_t* mine = own + (size_t)(warp & 3) * 32 * D * 2;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if (real && A.lse) A.lse[row_place(A, s, s.row0 + wrow)] = lse_of(m_run, l_run);
+      auto store = [&](int chunk) {  // a line of the rows, on its way while the next one is made
+        fence_proxy_async();
+        asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "r"((gr + 31) / 32 * 32) : "memory");  // the warps that have rows
+        if (row == 0)
+          tma_store_5d(&M.out, smem_u32(own) + chunk * q_rows * L::kBytes, 0, chunk, 0, s.h, s.r * A.T + s.row0 / g + w * q_tok);
+      };
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += kAtOnce) {
         uint32_t o[kAtOnce / 32][32];
@@ -652,9 +658,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
 #pragma unroll
           for (int u = 0; u < kAtOnce / 32; ++u) tmem_wait_ld(o[u]);
         }
-        if (!real) continue;
 #pragma unroll
         for (int u = 0; u < kAtOnce / 32; ++u) {
+          if (!real) break;
           const int c = c0 + 32 * u;
           if (l_run == 0.f) {  // no weights (but infinite values, perhaps)
 #pragma unroll
@@ -672,17 +678,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
             *reinterpret_cast<uint4*>(to) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
           }
         }
+        if (full && (c0 + kAtOnce) % L::kElems == 0) store(c0 / L::kElems);
       }
-      if (full) {
-        fence_proxy_async();
-        asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "r"((gr + 31) / 32 * 32) : "memory");  // the warps that have rows
-        if (row == 0) {
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_store_5d(&M.out, smem_u32(own) + c * q_rows * L::kBytes, 0, c, 0, s.h, s.r * A.T + s.row0 / g + w * q_tok);
-          bulk_stores_read();
-        }
-      }
+      if (full && row == 0) bulk_stores_read();
       __syncwarp();
       const uint32_t per_g = (65536 + g - 1) / g;  // m * per_g >> 16 is m / g for the rows of a group
       const int32_t m0 = w * gr + (warp & 3) * 32;
