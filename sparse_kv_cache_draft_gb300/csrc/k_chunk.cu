@@ -7,6 +7,11 @@
 // to 128 or 256; the slots that any row of a group sees are listed, those that all of its rows see whole first, so that
 // few tiles of a group need a mask whatever the slots' order, and slots that no row sees are not read. Tiles are dealt
 // to the CTAs of a cluster where there are too few groups to fill the GPU, as for drafted trees.
+//
+// Measured (32 / 8 heads of 128 dims, bf16): 4 requests x 1024 tokens with 64 / 8 heads behind 31K 2.53 to 2.66 ms, 1.63 to 1.71
+// PFLOP/s, 0.84 to 0.88 of the measured rate; 2048 tokens behind 14K 350 us, 1.46 PFLOP/s (two rounds of 256 groups on 152 SMs);
+// one token for 128 requests over 2048 resident ones 162 us, 0.97 of a copy's rate, 186 with the slots' weights; one token of one
+// request 9.3 us.
 #include <stddef.h>
 
 #include "chunk.cuh"
@@ -77,15 +82,23 @@ __device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, c
 
 // ---- tensor cores: bf16 ------------------------------------------------------------------------------
 //
-// As for drafted trees: a CTA holds NW groups of 128 rows (a softmax warpgroup each) over the same tiles of tokens, one
-// warp copies K and V into a ring of buffers, a warp for each group issues its MMAs,
+// A CTA holds NW groups of 128 rows (a softmax warpgroup each) over the same tiles of tokens; a warp copies K and one V into a
+// ring of buffers, and one thread issues the MMAs of all groups:
 //   S = Q K^T   128 x tile, Q and K in shared memory, S in TMEM
 //   O += P V    128 x d,    P in TMEM in the place of its S (bf16), V in shared memory, O in TMEM
-// and a thread takes a row's softmax; the running maximum moves when a row of the warp passes it by 2^8. Weights are rounded
-// to bf16 for the second product (half a step each), their sum is of the unrounded ones.
+// A thread takes a row's softmax; the running maximum moves when a row of the warp passes it by 2^8. Weights are rounded to bf16
+// for the second product (half a step each), their sum is of the unrounded ones.
 //
 // Up to 128 rows (NW = 1) tiles are 64 tokens, S has two buffers and two CTAs share an SM: HBM is the limit. Beyond
-// (NW = 2) tiles are 128 tokens with one S for each warpgroup, and the warpgroups take turns at the tensor cores.
+// (NW = 2) tiles are 128 tokens with one S for each warpgroup, and while one has its products the other is at its softmax.
+// What bounds it then: 32 MMAs of 64 cycles to a tile of both, and about 2600 cycles for it; the exponentials of 256 rows take
+// 1024. A CTA's start and end are about 12 thousand cycles beside that.
+//
+// The steps that counted, 1024 tokens x 4 requests behind 31K, 64 / 8 heads: first version, with MMAs issued by a whole warp for
+// each warpgroup in turns, 3657 us; registers of the other warps to the softmax's 3425; one elected thread, in whose branch the
+// operands are known to be uniform, and the first weights beside the search for the maximum 2786; K and V waited for where
+// they are used 2609; no spills 2532. 256 tokens x 16 requests over 2048 resident ones: 168 us, 148 by then, 122 with a warp for K and
+// one for V, shorter lists and outputs by TMA.
 //
 // A tile is spt slots of the list. Slots that follow one another in the pool come in one copy for a line, others slot by
 // slot. A slot's lines begin at a multiple of 128 bytes of shared memory: with lines of 64 bytes and an odd block
@@ -143,8 +156,8 @@ constexpr int kUpRegs = 216, kDownRegs = 72;
 
 template <int D, int NW, bool kDraw>
 __global__ void __launch_bounds__(mma_threads<NW>(), D <= 128 && NW == 1 ? 2 : 1)
-chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok, const int32_t q_rows,
-                 const int32_t pitch, const int32_t most) {
+chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkMaps M, const Shape shape, const int32_t rings, const int32_t q_tok,
+                 const int32_t q_rows, const int32_t pitch, const int32_t most) {
   constexpr int kTile = Tiles<NW>::kTile, kS = Tiles<NW>::kS, kWords = kTile / 32;
   using L = Lines<D, kTile>;
   constexpr uint32_t kCols = D <= 128 ? 256 : 512;  // TMEM columns of a warpgroup: S in the first 128, O behind
@@ -297,106 +310,106 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     // MMAs that keep them busy meanwhile, and waited for only where it had not been passed by then. (A warp for
     // each warpgroup, in turns, left the tensor cores idle for 400 of 1980 cycles a turn.)
     if (elect_one()) {
-    constexpr int kSteps = L::kElems / 16;
-    constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
-    const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
-    const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16), k_desc = smem_desc_lo(ring0, 16), v_desc = smem_desc_lo(ring0, L::kChunk);
-    int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
-    bool ok = true;
-    auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
-      b += by;
-      if (b >= ring) b -= ring, parity ^= 1;
-    };
-    auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
-    auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
-      if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
-      tc_fence_after();
-    };
-    auto s_at = [&](int32_t i, int w) { return tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0); };
-    auto qk = [&](int32_t i, int w, int c0, int c1) {  // steps c0 .. c1 - 1 of S
-      const uint32_t kd = k_desc + kb * (L::kBuf >> 4), qd = q_desc + w * L::kChunks * q_chunk;
+      constexpr int kSteps = L::kElems / 16;
+      constexpr uint32_t kHi = smem_desc_hi(L::kGroup, L::kSwizzle);
+      const uint32_t q_chunk = (uint32_t)(q_rows * L::kBytes) >> 4;
+      const uint32_t q_desc = smem_desc_lo(smem_u32(qs), 16), k_desc = smem_desc_lo(ring0, 16), v_desc = smem_desc_lo(ring0, L::kChunk);
+      int32_t kb = 0, kp = 0, vb = v_use(0), vp = 0;  // buffers and parities of the next K and V
+      bool ok = true;
+      auto step = [&](int32_t& b, int32_t& parity, int32_t by) {
+        b += by;
+        if (b >= ring) b -= ring, parity ^= 1;
+      };
+      auto ask = [&](uint64_t& bar, int32_t parity) { return mbar_test(smem_u32(&bar), (uint32_t)parity); };
+      auto passed = [&](bool asked, uint64_t& bar, int32_t parity) {
+        if (!asked) ok = ok && mbar_wait_timed(smem_u32(&bar), (uint32_t)parity);
+        tc_fence_after();
+      };
+      auto s_at = [&](int32_t i, int w) { return tmem + w * kCols + (kS == 2 ? (i & 1) * kTile : 0); };
+      auto qk = [&](int32_t i, int w, int c0, int c1) {  // steps c0 .. c1 - 1 of S
+        const uint32_t kd = k_desc + kb * (L::kBuf >> 4), qd = q_desc + w * L::kChunks * q_chunk;
 #pragma unroll
-      for (int c = c0; c < c1; ++c)
-        mma_ss1(s_at(i, w), qd + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDescQK, c > 0);
-      if (c1 < D / 16) return;
-      mma_commit1(smem_u32(&B.s_full[w][i & 1]));
-      if (kS == 2) mma_commit1(smem_u32(&B.empty[kb]));
-      if (w == NW - 1) step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
-    };
-    auto pv = [&](int32_t i, int w, int half) {
-      const uint32_t vd = v_desc + vb * (L::kBuf >> 4);
+        for (int c = c0; c < c1; ++c)
+          mma_ss1(s_at(i, w), qd + c / kSteps * q_chunk + c % kSteps * 2, kd + c / kSteps * (L::kChunk >> 4) + c % kSteps * 2, kHi, kDescQK, c > 0);
+        if (c1 < D / 16) return;
+        mma_commit1(smem_u32(&B.s_full[w][i & 1]));
+        if (kS == 2) mma_commit1(smem_u32(&B.empty[kb]));
+        if (w == NW - 1) step(kb, kp, kS == 2 && i == 0 ? 1 : 2);
+      };
+      auto pv = [&](int32_t i, int w, int half) {
+        const uint32_t vd = v_desc + vb * (L::kBuf >> 4);
 #pragma unroll
-      for (int c = half * 4; c < half * 4 + 4; ++c)
-        mma_ts1(tmem + w * kCols + kO, s_at(i, w) + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV, i > 0 || c > 0);
-      if (half + 1 < kTile / 64) return;
-      if (kS == 2 || i + 1 == n) mma_commit1(smem_u32(&B.pv_done[w][i & 1]));
-      if (kS == 2) mma_commit1(smem_u32(&B.empty[vb]));
-      if (w == NW - 1) step(vb, vp, 2);
-    };
-    constexpr int kHalf = D / 32;  // steps of half an S
-    if (n > 0) {
-      passed(false, B.q_full, 0);
-      passed(false, B.full[kb], kp);
+        for (int c = half * 4; c < half * 4 + 4; ++c)
+          mma_ts1(tmem + w * kCols + kO, s_at(i, w) + c * 8, vd + c * 2 * (L::kGroup >> 4), kHi, kDescPV, i > 0 || c > 0);
+        if (half + 1 < kTile / 64) return;
+        if (kS == 2 || i + 1 == n) mma_commit1(smem_u32(&B.pv_done[w][i & 1]));
+        if (kS == 2) mma_commit1(smem_u32(&B.empty[vb]));
+        if (w == NW - 1) step(vb, vp, 2);
+      };
+      constexpr int kHalf = D / 32;  // steps of half an S
+      if (n > 0) {
+        passed(false, B.q_full, 0);
+        passed(false, B.full[kb], kp);
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
-        if (ok) qk(0, w, 0, D / 16);
-      if (ok) passed(false, B.full[vb], vp);
-    }
-    if (kS == 2) {
-      bool k_there = false;
-      for (int32_t i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) {
-          passed(k_there, B.full[kb], kp);
-          if (ok) qk(i + 1, 0, 0, D / 16);
-        }
-        passed(ask(B.p_full[0][i & 1][0], (i >> 1) & 1), B.p_full[0][i & 1][0], (i >> 1) & 1);
-        if (!ok) break;
-        pv(i, 0, 0);
-        if (i + 1 < n) {
-          passed(ask(B.full[vb], vp), B.full[vb], vp);
-          k_there = i + 2 < n && ask(B.full[kb], kp);
-        }
+        for (int w = 0; w < NW; ++w)
+          if (ok) qk(0, w, 0, D / 16);
+        if (ok) passed(false, B.full[vb], vp);
       }
-    } else {
-      bool next = false, v_there = true, k_there = false;  // what was asked last
-      for (int32_t i = 0; i < n && ok; ++i) {
-        const int32_t parity = (i >> 1) & 1;
-        const bool more = i + 1 < n;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          uint64_t(&p)[2] = B.p_full[w][i & 1];
-          if (w == 0 && i > 0) passed(v_there, B.full[vb], vp);
-          passed(next, p[0], parity);
-          if (!ok) break;
-          const bool there = ask(p[1], parity);
-          pv(i, w, 0);
-          passed(there, p[1], parity);
-          if (!ok) break;
-          pv(i, w, 1);
-          next = false;
-          if (!more) continue;
-          // S takes the place of the P just used: the products run in order
-          if (w == 0) passed(k_there, B.full[kb], kp);
-          if (!ok) break;
-          qk(i + 1, w, 0, kHalf);
-          if (w + 1 < NW) {
-            next = ask(B.p_full[w + 1][i & 1][0], parity);
-          } else {
-            int32_t k2 = kb, kp2 = kp;
-            step(k2, kp2, 2);
-            v_there = ask(B.full[vb], vp);
-            k_there = i + 2 < n && ask(B.full[k2], kp2);
-            next = ask(B.p_full[0][(i + 1) & 1][0], ((i + 1) >> 1) & 1);
+      if (kS == 2) {
+        bool k_there = false;
+        for (int32_t i = 0; i < n && ok; ++i) {
+          if (i + 1 < n) {
+            passed(k_there, B.full[kb], kp);
+            if (ok) qk(i + 1, 0, 0, D / 16);
           }
-          qk(i + 1, w, kHalf, D / 16);
+          passed(ask(B.p_full[0][i & 1][0], (i >> 1) & 1), B.p_full[0][i & 1][0], (i >> 1) & 1);
+          if (!ok) break;
+          pv(i, 0, 0);
+          if (i + 1 < n) {
+            passed(ask(B.full[vb], vp), B.full[vb], vp);
+            k_there = i + 2 < n && ask(B.full[kb], kp);
+          }
+        }
+      } else {
+        bool next = false, v_there = true, k_there = false;  // what was asked last
+        for (int32_t i = 0; i < n && ok; ++i) {
+          const int32_t parity = (i >> 1) & 1;
+          const bool more = i + 1 < n;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            uint64_t(&p)[2] = B.p_full[w][i & 1];
+            if (w == 0 && i > 0) passed(v_there, B.full[vb], vp);
+            passed(next, p[0], parity);
+            if (!ok) break;
+            const bool there = ask(p[1], parity);
+            pv(i, w, 0);
+            passed(there, p[1], parity);
+            if (!ok) break;
+            pv(i, w, 1);
+            next = false;
+            if (!more) continue;
+            // S takes the place of the P just used: the products run in order
+            if (w == 0) passed(k_there, B.full[kb], kp);
+            if (!ok) break;
+            qk(i + 1, w, 0, kHalf);
+            if (w + 1 < NW) {
+              next = ask(B.p_full[w + 1][i & 1][0], parity);
+            } else {
+              int32_t k2 = kb, kp2 = kp;
+              step(k2, kp2, 2);
+              v_there = ask(B.full[vb], vp);
+              k_there = i + 2 < n && ask(B.full[k2], kp2);
+              next = ask(B.p_full[0][(i + 1) & 1][0], ((i + 1) >> 1) & 1);
+            }
+            qk(i + 1, w, kHalf, D / 16);
+          }
         }
       }
-    }
-    if (!ok) {
-      fail();
-      mma_commit1(smem_u32(&B.drain));
-      mbar_wait_timed(smem_u32(&B.drain), 0);
-    }
+      if (!ok) {
+        fail();
+        mma_commit1(smem_u32(&B.drain));
+        mbar_wait_timed(smem_u32(&B.drain), 0);
+      }
     }
     __syncwarp();
   }
@@ -1139,7 +1152,8 @@ cudaError_t run_mma(const ChunkArgs& A, bool* drawn, cudaStream_t s) {
   const int32_t most = (A.G.kb + spt - 1) / spt;
   const size_t share = two ? 115712 : kMaxSmem, tiles0 = (size_t)NW * q_rows * D * 2, sums = kDraw ? drawn_bytes(most, spt, q_rows) : 0;
   if constexpr (NW == 1 && !kDraw) {
-    if (A.weight_out && groups == 1 && pitch % 8 == 0 && drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf <= share) return run_mma<D, NW, true>(A, drawn, s);
+    const size_t all = drawn_bytes(most, spt, q_rows) + mma_misc(A.G.kb) + 2048 + tiles0 + 4 * L::kBuf;
+    if (A.weight_out && groups == 1 && pitch % 8 == 0 && all <= share) return run_mma<D, NW, true>(A, drawn, s);
   }
   *drawn = kDraw;
   const size_t rest = (mma_misc(A.G.kb) + sums + 1023) / 1024 * 1024 + tiles0;
