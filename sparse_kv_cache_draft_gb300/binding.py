@@ -1,5 +1,5 @@
-"""ctypes binding of libokv.so: the C ABI of include/okv.h with the same names. The calls on rows and drafted
-trees that need no context are a compiled module of their own (csrc/py_calls.cpp), reached through here.
+"""ctypes binding of libokv.so: the C ABI of include/okv.h with the same names. The calls on rows, drafted
+trees and bounded caches that need no context are a compiled module of their own (csrc/py_calls.cpp), reached through here.
 
 Argument marshalling only: tensors become device pointers, streams become cudaStream_t
 handles, host arrays become numpy views. Every step of the path runs in the library's CUDA

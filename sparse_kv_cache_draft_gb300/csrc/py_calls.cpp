@@ -1,4 +1,4 @@
-// Python calls on rows and drafted trees that need no context: arguments are checked and passed to the C ABI.
+// Python calls on rows, drafted trees and bounded caches that need no context: arguments are checked and passed to the C ABI.
 //
 // A small call's time is the host's. With the checks in Python and the arguments through ctypes, a call on one row
 // took 10.2 us on a Grace core (5.2 of checks, 1.8 for its Rotary, 1.1 of ctypes, 2.1 in the launch) where its
@@ -550,7 +550,7 @@ PyMethodDef methods[] = {
      "_row_stride($module, t, width, /)\n--\n\nElements between the rows of t [...][width], whose leading dims are one run of rows."},
     {}};
 
-PyModuleDef module_def{PyModuleDef_HEAD_INIT, "_calls", "Calls on rows and drafted trees that need no context.", -1, methods};
+PyModuleDef module_def{PyModuleDef_HEAD_INIT, "_calls", "Calls on rows, drafted trees and bounded caches that need no context.", -1, methods};
 
 }  // namespace
 
