@@ -775,29 +775,34 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
 constexpr int kF32Tile = 64, kF32Threads = 128;
 
 __host__ __device__ constexpr int f32_pitch(int d) { return d + 4; }  // fragment reads free of bank conflicts
-__host__ __device__ constexpr size_t f32_smem(int d, int rg, int kb) {
+__host__ __device__ constexpr size_t f32_smem(int d, int rg, int stages, int kb) {
   const int th = 4 / rg;
-  return (size_t)(16 * rg + 2 * kF32Tile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 32 + sizeof(Listed) + ((size_t)kb * 2 + 15) / 16 * 16;
+  return (size_t)(16 * rg + 2 * stages * kF32Tile) * f32_pitch(d) * 4 + (size_t)(th + 1) * 16 * rg * 8 + 48 + sizeof(Listed) + ((size_t)kb * 2 + 15) / 16 * 16;
 }
-__host__ __device__ constexpr int f32_ctas(int dv, int rg) { return dv <= 4 && rg < 4 ? 3 : dv <= 4 ? 2 : 1; }  // CTAs of an SM, by registers
+// CTAs of an SM, by registers, or one with two stages of tiles
+__host__ __device__ constexpr int f32_ctas(int dv, int rg, int stages) { return stages == 2 ? 1 : dv <= 4 && rg < 4 ? 3 : dv <= 4 ? 2 : 1; }
 
-template <int DV, int RG>
-__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kernel(const __grid_constant__ ChunkArgs A, const Shape shape, const int32_t q_tok) {
+// Where CTAs are few a tile's keys and values come while the one before it is at work (ST = 2); otherwise the CTAs of an SM hide
+// one another's waits, with room for more of them.
+template <int DV, int RG, int ST>
+__global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG, ST)) chunk_f32_kernel(const __grid_constant__ ChunkArgs A, const Shape shape, const int32_t q_tok) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int d = DV * 32, pitch = f32_pitch(d), kRows = 16 * RG, TH = 4 / RG, kTok = kF32Tile / TH, NT = kTok / 8;
   float* qs = reinterpret_cast<float*>(smem);      // [rows][pitch]
-  float* ks = qs + kRows * pitch;                  // [64][pitch]
-  float* vs = ks + kF32Tile * pitch;               // [64][pitch]
-  float* ms = vs + kF32Tile * pitch;               // [rows], then [TH][rows] of the warps
+  float* ks0 = qs + kRows * pitch;                 // [ST][64][pitch]
+  float* vs0 = ks0 + ST * kF32Tile * pitch;        // [ST][64][pitch]
+  float* ms = vs0 + ST * kF32Tile * pitch;         // [rows], then [TH][rows] of the warps
   float* ls = ms + (TH + 1) * kRows;               // the same
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ls + (TH + 1) * kRows);  // keys, values, queries there
-  int32_t* bad = reinterpret_cast<int32_t*>(bars + 3);
-  Listed& listed = *reinterpret_cast<Listed*>(bars + 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ls + (TH + 1) * kRows);  // keys, values (of a stage), queries there
+  uint64_t* q_bar = bars + 2 * ST;
+  int32_t* bad = reinterpret_cast<int32_t*>(q_bar + 1);
+  Listed& listed = *reinterpret_cast<Listed*>(bars + 6);
   uint16_t* list_at = reinterpret_cast<uint16_t*>(&listed + 1);
 
   if (threadIdx.x == 0) {
     *bad = 0;
-    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(bars + i), i < 2 ? kF32Tile : kRows);
+    for (int i = 0; i < 2 * ST; ++i) mbar_init(smem_u32(bars + i), kF32Tile);
+    mbar_init(smem_u32(q_bar), kRows);
     fence_mbar_init();
     fence_proxy_async();
   }
@@ -821,9 +826,9 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
   };
   if (tid < kRows) {  // rows past the group's are never read out
     if (tid < s.rows)
-      copy_row(smem_u32(bars + 2), qs + tid * pitch, (const float*)A.q + row_place(A, s, s.row0 + tid) * d);
+      copy_row(smem_u32(q_bar), qs + tid * pitch, (const float*)A.q + row_place(A, s, s.row0 + tid) * d);
     else
-      mbar_arrive(smem_u32(bars + 2));
+      mbar_arrive(smem_u32(q_bar));
   }
   uint32_t whole_of[8], some_of[8];
   count_slots(A, s, ids, warp, listed, whole_of, some_of);
@@ -835,6 +840,12 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
   const float scale = kLog2e / sqrtf((float)d);
   const uint32_t per_bs = (65536 + bs - 1) / bs;  // j * per_bs >> 16 is j / bs for j < 64
   auto first_of = [&](int32_t it) { return (s.part + it * s.parts) * spt; };
+  bool failed = false, again = false;
+  auto use = [&](int32_t it) { return again ? mine + it : it; };
+  auto stage = [&](int32_t it) { return ST == 2 ? use(it) & 1 : 0; };
+  auto there = [&](int32_t it, int which) {
+    return mbar_wait_timed(smem_u32(bars + 2 * stage(it) + which), (uint32_t)(ST == 2 ? use(it) >> 1 : use(it)) & 1);
+  };
   // Tile it's keys (which = 0) or values into shared memory, by 64 threads, a token each. A value that no row may see
   // is zero, as its weight of zero needs; a key may be anything.
   auto load = [&](int32_t it, int which) {
@@ -846,8 +857,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
       if (e < list.whole || list.first(e) <= s.p_hi - off)
         from = reinterpret_cast<const float*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)(which * bs + off) * d;
     }
-    const uint32_t bar = smem_u32(bars + which);
-    float* to = (which ? vs : ks) + j * pitch;
+    const uint32_t bar = smem_u32(bars + 2 * stage(it) + which);
+    float* to = (which ? vs0 : ks0) + (stage(it) * kF32Tile + j) * pitch;
     if (from) {
       copy_row(bar, to, from);
     } else {
@@ -867,9 +878,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
     pos[i] = s.len + (s.row0 + row) / g;
   }
   float o[d / 8][4], m[2], l[2];
-  bool ok = mbar_wait_timed(smem_u32(bars + 2), 0), failed = false, again = false;
-  auto phase = [&](int32_t it) { return (uint32_t)((again ? mine + it : it) & 1); };
-  for (;; again = true) {
+  bool ok = mbar_wait_timed(smem_u32(q_bar), 0);
+  for (;;) {
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
 #pragma unroll
@@ -877,6 +887,12 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
     for (int32_t it = 0; it < mine && !failed; ++it) {
       const int32_t e0 = first_of(it);
       const bool part_seen = e0 + spt > list.whole;
+      const float* ks = ks0 + stage(it) * kF32Tile * pitch;
+      float* vs = vs0 + stage(it) * kF32Tile * pitch;
+      if (ST == 2) {
+        fence_proxy_async();  // zeros were written among the values of the tile before the last
+        load(it + 1, tid >> 6);
+      }
       uint64_t vis[2] = {first_bits(real[0] ? tt : 0), first_bits(real[1] ? tt : 0)};
       if (part_seen) {
         vis[0] = vis[1] = 0;
@@ -888,7 +904,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
             if (real[i]) vis[i] |= list.seen(e0 + k, pos[i], A.window, A.sinks) << k * bs;
         }
       }
-      ok = mbar_wait_timed(smem_u32(bars), phase(it)) && ok;
+      ok = there(it, 0) && ok;
       float sc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
@@ -944,9 +960,11 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
           o[n][2 * i + 1] *= f;
         }
       }
-      __syncthreads();
-      if (tid < 64) load(it + 1, 0);  // the keys have been read
-      ok = mbar_wait_timed(smem_u32(bars + 1), phase(it)) && ok;
+      if (ST == 1) {
+        __syncthreads();
+        if (tid < 64) load(it + 1, 0);  // the keys have been read
+      }
+      ok = there(it, 1) && ok;
       if (part_seen) {
         // values that are not finite are zero in the products
 #pragma unroll 1
@@ -998,11 +1016,14 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
             }
       }
       failed = __syncthreads_or(!ok) != 0;
-      if (tid >= 64 && !failed) {  // the values have been read
-        fence_proxy_async();       // zeros were written among them
+      if (ST == 1 && tid >= 64 && !failed) {  // the values have been read
+        fence_proxy_async();                  // zeros were written among them
         load(it + 1, 1);
       }
-      if (failed && it + 1 < mine) mbar_wait_timed(smem_u32(bars), phase(it + 1));  // copies in flight land (bounded)
+      if (failed && it + 1 < mine) {  // copies in flight land (bounded)
+        there(it + 1, 0);
+        if (ST == 2) there(it + 1, 1);
+      }
     }
     bool odd = real[0] && !is_finite(l[0]) || real[1] && !is_finite(l[1]);
 #pragma unroll
@@ -1011,8 +1032,10 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG)) chunk_f32_kerne
       for (int e = 0; e < 4; ++e) odd |= real[e >> 1] && !is_finite(o[n][e]);
     if (again || failed || !__syncthreads_or(odd)) break;
     fence_proxy_async();
+    again = true;
     load(0, tid >> 6);
   }
+  float* ks = ks0;
   if (failed || !ok) {  // a row of a CTA that gave up has seen nothing
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
@@ -1081,30 +1104,37 @@ int32_t likely_tiles(const ChunkArgs& A, int32_t spt, int32_t group_tok) {
 
 constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1}, kF32Costs{2.8, 0.5, 1.3};  // as for drafted trees
 
-template <int DV, int RG>
+template <int DV, int RG, int ST>
 cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {
   const int32_t q_tok = 16 * RG / A.G.g, groups = (A.T + q_tok - 1) / q_tok;
-  const size_t smem = f32_smem(DV * 32, RG, A.G.kb);
+  const size_t smem = f32_smem(DV * 32, RG, ST, A.G.kb);
   int32_t per_sm = (int32_t)(228 * 1024 / (smem + 1024));
-  if (per_sm > f32_ctas(DV, RG)) per_sm = f32_ctas(DV, RG);
+  if (per_sm > f32_ctas(DV, RG, ST)) per_sm = f32_ctas(DV, RG, ST);
   if (per_sm < 1) per_sm = 1;
   const int64_t items = (int64_t)A.G.R * A.G.Hkv * groups;
   const Shape shape = pick_shape(items, groups, per_sm, likely_tiles(A, kF32Tile / A.G.bs, q_tok), kF32Costs, cluster_room(kF32Threads, per_sm));
-  return launch_cluster(chunk_f32_kernel<DV, RG>, items, shape, kF32Threads, smem, s, A, shape, q_tok);
+  return launch_cluster(chunk_f32_kernel<DV, RG, ST>, items, shape, kF32Threads, smem, s, A, shape, q_tok);
 }
 
 // Rows of a CTA: 64 share a tile's keys and values four ways, but where even the largest clusters would leave SMs empty fewer
 // rows end sooner (1 request x 40 tokens, 8 / 2 heads of 128 dims, 3000 tokens of context: 50 us by 64, 42 by 32, 30 by 16; 4 x 512
-// tokens: 509, 632, 703).
+// tokens: 509, 632, 703). Two stages of tiles where an SM has one CTA anyway (1 token, 16 / 8 heads, 12K of context: 53 us against 81;
+// 40 tokens as above, with more CTAs than SMs, 30.6 against 29.7).
 template <int DV>
 cudaError_t run_f32_rows(const ChunkArgs& A, cudaStream_t s) {
   const int32_t rows = A.T * A.G.g, sms = sm_count();
-  auto fills = [&](int32_t of) {
+  auto ctas = [&](int32_t of) {  // at most
     const int32_t q_tok = of / A.G.g;
-    return (int64_t)A.G.R * A.G.Hkv * ((A.T + q_tok - 1) / q_tok) * kMaxSplit >= sms;
+    return (int64_t)A.G.R * A.G.Hkv * ((A.T + q_tok - 1) / q_tok) * kMaxSplit;
   };
-  if (rows <= 16 || !fills(32)) return run_f32<DV, 1>(A, s);
-  return rows <= 32 || !fills(64) ? run_f32<DV, 2>(A, s) : run_f32<DV, 4>(A, s);
+  if (rows <= 16 || ctas(32) < sms) {
+    if constexpr (DV <= 6) {  // by shared memory
+      if (ctas(16) <= sms) return run_f32<DV, 1, 2>(A, s);
+    }
+    return run_f32<DV, 1, 1>(A, s);
+  }
+  if (rows <= 32 || ctas(64) < sms) return run_f32<DV, 2, 1>(A, s);
+  return run_f32<DV, 4, 1>(A, s);
 }
 
 cudaError_t run_f32_d(const ChunkArgs& A, cudaStream_t s) {
