@@ -23,7 +23,7 @@ CXX = os.environ.get("CXX", "g++")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["okv_api.cu", "k_summary.cu", "k_select.cu", "k_gather.cu", "k_attend.cu", "k_rows.cu", "k_tree.cu", "k_chunk.cu",
-           "k_weigh.cu", "k_evict.cu"]
+           "k_chunk_f32.cu", "k_weigh.cu", "k_evict.cu"]
 
 
 def nvcc() -> str:

@@ -124,4 +124,74 @@ __device__ __forceinline__ List make_list(const ChunkArgs& A, const Span& s, int
   return l;
 }
 
+// ---- a CTA's rows of the attention --------------------------------------------------------------------
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Where a CTA's share is; the longest groups of a unit, its last rows, come first. What needs the lengths is filled in below, so
+// that they are on their way beside the slot table.
+__device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, int32_t group_rows) {
+  Span s;
+  const int32_t cluster = blockIdx.x / P.split, rank = blockIdx.x - cluster * P.split, wholes = P.whole / P.split;
+  const bool whole = cluster < wholes;
+  const int32_t item = whole ? (int32_t)blockIdx.x : P.whole + cluster - wholes;
+  const int32_t ua = item / P.groups, group = P.groups - 1 - (item - ua * P.groups);
+  s.part = whole ? 0 : rank;
+  s.parts = whole ? 1 : P.split;
+  s.r = ua / A.G.Hkv;
+  s.h = ua - s.r * A.G.Hkv;
+  s.row0 = group * group_rows;
+  return s;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+}
+
+// Adds what the values that are not finite, of tokens in tiles that were masked, give to four outputs (dims c .. c + 3) of
+// a row that sees them: they are zero in the products, where a weight of zero times them would reach rows that do not. (Arguments one by
+// one: a struct whose address is taken is written to local memory by every thread, whether it comes here or not.)
+template <typename T>
+__device__ __noinline__ float4 not_finite_of(const ChunkArgs& A, int64_t unit, const uint16_t* at, const int32_t* base, int32_t whole, int32_t n, int32_t part,
+                                              int32_t parts, int32_t spt, int32_t p, int32_t c) {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const List L{at, base, A.slot_block + unit, A.G.kb, A.G.bs, whole, n};
+  for (int32_t e = whole / spt * spt; e < n; ++e) {
+    if (e / spt % parts != part) continue;
+    const int32_t slot = L.slot(e);
+    uint64_t bits = L.seen(e, p, A.window, A.sinks);
+    const T* v = reinterpret_cast<const T*>(A.pool + (unit + slot) * A.G.block_bytes) + (int64_t)A.G.bs * A.G.d + c;
+    while (bits) {
+      const int32_t j = __ffsll((long long)bits) - 1;
+      bits &= bits - 1;
+      const float x = to_f(v[j * A.G.d]), y = to_f(v[j * A.G.d + 1]), z = to_f(v[j * A.G.d + 2]), w = to_f(v[j * A.G.d + 3]);
+      if (!is_finite(x)) o.x += x;
+      if (!is_finite(y)) o.y += y;
+      if (!is_finite(z)) o.z += z;
+      if (!is_finite(w)) o.w += w;
+    }
+  }
+  return o;
+}
+
+// Merges the cluster's partials and writes outputs and sums. The first `threads` threads of every CTA of the cluster call it,
+// the others cluster_sync twice.
+template <typename T, typename F>
+__device__ __forceinline__ void merge_chunk(const ChunkArgs& A, const Span& s, const Partial& P, int32_t xor_mask, int32_t threads, F more) {
+  cluster_sync();
+  more();
+  merge_rows(s.part, s.parts, s.rows, A.G.d, P, xor_mask, threads, [&](int32_t row, int32_t c, float4 o, float M, float l) {
+    const int64_t at = row_place(A, s, s.row0 + row);
+    store4((T*)A.out + at * A.G.d + c * 4, o);
+    if (c == 0 && A.lse) A.lse[at] = lse_of(M, l);
+  });
+  cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+// ---- launches ------------------------------------------------------------------------------------------
+// Tiles that a group of rows has if no block is in two slots: of the slots there are, and of those that a window leaves it.
+inline int32_t likely_tiles(const ChunkArgs& A, int32_t spt, int32_t group_tok) {
+  const int64_t bs = A.G.bs, seen = ((int64_t)A.window + group_tok + bs - 1) / bs + 1 + ((int64_t)A.sinks + bs - 1) / bs;
+  const int64_t slots = seen < A.G.kb ? seen : A.G.kb;
+  return (int32_t)((slots + spt - 1) / spt);
+}
+
 }  // namespace okv

@@ -24,6 +24,8 @@ struct ChunkArgs {
 
 // Outputs, log sums and, with A.weight_out, what the slots draw.
 cudaError_t launch_attend_chunk(const ChunkArgs& A, cudaStream_t s);
+// Outputs and log sums of binary32 operands (k_chunk_f32.cu).
+cudaError_t launch_chunk_f32(const ChunkArgs& A, cudaStream_t s);
 // weight_out = weight + what each slot draws of the rows whose sums are in A.lse.
 cudaError_t launch_weigh_chunk(const ChunkArgs& A, cudaStream_t s);
 

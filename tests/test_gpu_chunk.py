@@ -161,7 +161,8 @@ def test_rows_that_see_nothing(dtype, d, kb, T):
     assert not got[0][:2].any() and torch.isinf(got[1][:2]).all() and torch.equal(got[2][:2], x["weight"][:2])
 
 
-@pytest.mark.parametrize("dtype,d,kb,T", [("bf16", 128, 12, 40), ("bf16", 128, 120, 9), ("bf16", 64, 12, 70), ("bf16", 96, 30, 50), ("f32", 64, 12, 30)])
+@pytest.mark.parametrize("dtype,d,kb,T", [("bf16", 128, 12, 40), ("bf16", 128, 120, 9), ("bf16", 64, 12, 70), ("bf16", 96, 30, 50), ("f32", 64, 12, 30),
+                                             ("f32", 64, 12, 9), ("f32", 128, 40, 9)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (9, 4)])
 def test_values_that_are_not_finite(dtype, d, kb, T, window, sinks):
     """Infinite and NaN keys and values of new tokens reach exactly the rows that see them."""
