@@ -24,6 +24,18 @@ def test_the_same_block_in_many_slots(T, dtype, d, bs, window, sinks):
     check(x, call(x))
 
 
+@pytest.mark.parametrize("T,dtype,d", [(3, "bf16", 128), (30, "bf16", 64), (90, "bf16", 128), (70, "bf16", 256), (90, "bf16", 96), (3, "f32", 64), (60, "f32", 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 6)])
+def test_rows_past_a_count_may_hold_anything(T, dtype, d, window, sinks):
+    """Queries of rows from a request's count on are no part of any other row, nor of what slots draw."""
+    x = make(4, T, 6, 2, d, 16, 30, dtype, seed=51, lengths=[300, 17, 400, 0], counts=[T - 2, 1, 0, T - 1])
+    x.update(window=window, sinks=sinks)
+    for r, c in enumerate((T - 2, 1, 0, T - 1)):
+        x["q"][r, c:, 0::2] = float("nan")
+        x["q"][r, c:, 1::2] = float("inf")
+    check(x, call(x))
+
+
 def test_calls_behind_one_another():
     """Steps that feed one another without a wait between them give what the same steps give one at a time: room, rows,
     attention with weights in place, of every kind of kernel."""
