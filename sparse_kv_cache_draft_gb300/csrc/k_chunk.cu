@@ -15,6 +15,7 @@
 #include <stddef.h>
 
 #include "chunk.cuh"
+#include "ring.h"
 
 namespace okv {
 namespace {
@@ -53,7 +54,7 @@ struct MmaBars {
   uint64_t full[kMaxRing], empty[kMaxRing], q_full, s_full[2][2], p_full[2][2][2], pv_done[2][2], drain;
   Listed listed;
   uint32_t tmem;
-  int32_t failed, bad;
+  int32_t failed, bad, issued[2];  // issued: tiles whose keys, and whose values, were asked for
 };
 
 __host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) + ((size_t)kb * 2 + 15) / 16 * 16; }
@@ -190,9 +191,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
   const List list = make_list(A, s, NW * 4, B.listed, list_at);
   const int32_t n = ((list.n + spt - 1) / spt - s.part + s.parts - 1) / s.parts;  // this CTA's tiles
 
-  // The uses of the ring are in the order in which the MMAs take them. With two S buffers, S of tile i + 1
-  // comes before O of tile i: K of tile i is use 2i - 1 (the first: 0), V use 2i + 2. With one, K is 2i, V 2i + 1.
-  auto v_use = [](int32_t i) { return kS == 2 ? 2 * i + 2 : 2 * i + 1; };
+  using Order = RingOrder<kS>;
+  auto v_use = [](int32_t i) { return Order::value(i); };
   // ... by all lanes of a warp: what follows is by whole warps
   auto warp_wait = [&](uint64_t& bar, int32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_timed(smem_u32(&bar), (uint32_t)parity)) != 0;
@@ -206,9 +206,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     // A warp for K and one for V. What they ask shared memory for, between MMAs that read it, takes them as long as a tile's
     // products: with one warp for both and slots in any order, it and not the copies set the pace.
     const bool v = is_copy_v;
-    int32_t use = v ? v_use(0) : 0, issued = 0;
+    int32_t issued = 0;
     for (; issued < n; ++issued) {
-      const int32_t i = issued, b = use % ring;
+      const int32_t i = issued, use = v ? v_use(i) : Order::key(i), b = use % ring;
       const int32_t e0 = (s.part + i * s.parts) * spt, ne = min(spt, list.n - e0), first = list.slot(e0);
       const int32_t my_slot = lane < ne * L::kChunks ? list.slot(e0 + lane / L::kChunks) : 0;
       bool run = ne == spt && pitch == bs;
@@ -233,16 +233,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
           tma_load_5d(to + c * L::kChunk + e * pitch * L::kBytes, &M.slot, bar, 0, c, 0, v ? 1 : 0, (int32_t)unit + slot);
         }
       }
-      use += kS == 2 && use == 0 ? 1 : 2;
     }
-    if (issued < n) {
-      // the copies still in flight land before the shared memory is given up (bounded)
-      for (int32_t i = max(0, issued - ring); i < issued; ++i) {
-        const int32_t u = v ? v_use(i) : kS == 1 ? 2 * i : max(0, 2 * i - 1);
-        mbar_wait_timed(smem_u32(&B.full[u % ring]), (uint32_t)(u / ring & 1));
-      }
-    }
-    if (!v && (issued < n || n == 0)) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
+    if (lane == 0) B.issued[v] = issued;
+    if (!v && n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp waits for it
   } else if (is_mma) {
     // One warp for both warpgroups, in a fixed order: O of a tile and S of the next for one, then for the other. An answer from a
     // barrier takes 150 to 350 cycles while the tensor cores read shared memory, so each barrier is asked ahead, behind
@@ -354,6 +347,18 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
   }
   if (!is_soft) {  // the others' ends: see below
     __syncthreads();
+    if (*(volatile int32_t*)&B.failed != 0) {
+      // A wait ran out somewhere: copies that nobody came to wait for land before the shared memory is used for anything else (bounded).
+      if (is_copy || is_copy_v) {
+        const int32_t keys = B.issued[0], values = B.issued[1], mine = is_copy ? keys : values;
+        for (int32_t i = max(0, mine - ring); i < mine; ++i) {
+          const int32_t u = is_copy ? Order::key(i) : v_use(i);
+          if (Order::may_be_on_its_way(u, ring, keys, values)) mbar_wait_timed(smem_u32(&B.full[u % ring]), (uint32_t)(u / ring & 1));
+        }
+        if (is_copy) mbar_wait_timed(smem_u32(&B.q_full), 0);
+      }
+      __syncthreads();
+    }
     if (s.parts > 1) cluster_sync(), cluster_sync();
     __syncthreads();
     if (is_mma) {
@@ -572,6 +577,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     tc_fence_after();
     __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
     const bool failed = *(volatile int32_t*)&B.failed != 0;
+    if (failed) __syncthreads();  // for the copies, see above
     const bool bad = B.bad && real && l_run != 0.f;
     const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32;  // of this warp
     auto extra = [&](uint32_t (&o)[32], int c) {
