@@ -18,6 +18,7 @@
 // rows to a key head) 132 us, 1.04 PFLOP/s, 0.55 of the measured bf16 rate.
 #include <stddef.h>
 
+#include "ring.h"
 #include "tiles.cuh"
 
 namespace okv {
@@ -565,9 +566,8 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   const int32_t bs = A.G.bs, spt = kTile / bs, tt = spt * bs;
   const uint32_t ring0 = smem_u32(rs);
 
-  // The uses of the ring are in the order in which the MMAs take them. With two S buffers, S of tile i + 1
-  // comes before O of tile i: K of tile i is use 2i - 1 (the first: 0), V use 2i + 2. With one, K is 2i, V 2i + 1.
-  auto v_use = [](int32_t i) { return kS == 2 ? 2 * i + 2 : 2 * i + 1; };
+  using Order = RingOrder<kS>;
+  auto v_use = [](int32_t i) { return Order::value(i); };
   auto uses = [](int32_t tiles_) { return kS == 2 ? 2 * tiles_ + 1 : 2 * tiles_; };
   auto full = [&](int32_t use) { return mbar_wait_timed(smem_u32(&B.full[use % ring]), (uint32_t)((use / ring) & 1)); };
   // ... by all lanes of a warp: what follows is by whole warps
@@ -681,13 +681,8 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
     if (lane == 0) {
       bool ok = true;
       while (next < uses(n) && ok) ok = fill();
-      if (!ok) {
-        fail(0);
-        // the copies still in flight land before the shared memory is given up (bounded)
-        for (int32_t use = issued > ring ? issued - ring : 0; use < issued; ++use) full(use);
-        if (draft && issued <= ring) full(0), full(v_use(0));
-      }
-      if (!ok || n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warp has seen it
+      if (!ok) fail(0);
+      if (n == 0) mbar_wait_timed(smem_u32(&B.q_full), 0);  // else the MMA warps wait for it
     }
   } else if (is_mma) {
     const bool one = lane == 0;
@@ -914,6 +909,21 @@ tree_mma_kernel(const TreeArgs A, const __grid_constant__ MmaMaps M, const Shape
   }
   __syncthreads();  // every product done: the ring and Q become the cluster's partials
   const bool failed = *(volatile int32_t*)&B.failed != 0;
+  if (failed) {
+    // A wait ran out somewhere: copies that nobody came to wait for land before the shared memory is used for anything else (bounded).
+    if (is_copy && lane == 0) {
+      // tiles whose keys, and whose values, were asked for: the drafted tokens' both, of the others those of the uses so far
+      int32_t keys = lead, values = lead;
+      while (keys < n && Order::key(keys) < issued) ++keys;
+      while (values < n && v_use(values) < issued) ++values;
+      for (int32_t i = 0; i < max(keys, values); ++i) {
+        if (i < keys && Order::may_be_on_its_way(Order::key(i), ring, keys, values)) full(Order::key(i));
+        if (i < values && Order::may_be_on_its_way(v_use(i), ring, keys, values)) full(v_use(i));
+      }
+      mbar_wait_timed(smem_u32(&B.q_full), 0);
+    }
+    __syncthreads();
+  }
   if (warp < NW * 4) {
     const int w = warp >> 2, row = tid & 127, wrow = w * gr + row, mrow = s.row0 + wrow;
     const bool real = row < gr && wrow < s.rows;
