@@ -419,7 +419,8 @@ OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, i
  * workspace, calls on different streams are independent, each can be captured, one launch each (up to two
  * for okv_attend_chunk_static with weight_out), EINVAL without a launch on what okv_create refuses, NULL or misaligned
  * pointers and a stream of another device. A copy or product that never completes is given up after about two seconds: the rows
- * of its group are then not written, or incomplete. A request whose length is negative, or past 2^31 - 1 with n_new more
+ * of its group then count as rows that see nothing, or nothing of a part of the slots, in out and lse as in weight_out; in the
+ * second launch the slots concerned draw nothing. A request whose length is negative, or past 2^31 - 1 with n_new more
  * tokens, counts as one without new tokens. */
 
 /* Attention of new tokens over the resident ones. Token t < counts[r] (device [n_requests] int32, clamped to

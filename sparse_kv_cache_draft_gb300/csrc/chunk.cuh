@@ -125,8 +125,6 @@ __device__ __forceinline__ List make_list(const ChunkArgs& A, const Span& s, int
 }
 
 // ---- a CTA's rows of the attention --------------------------------------------------------------------
-constexpr float kLn2 = 0.6931471805599453f;
-
 // Where a CTA's share is; the longest groups of a unit, its last rows, come first. What needs the lengths is filled in below, so
 // that they are on their way beside the slot table.
 __device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, int32_t group_rows) {
@@ -141,9 +139,6 @@ __device__ __forceinline__ Span make_span(const ChunkArgs& A, const Shape& P, in
   s.h = ua - s.r * A.G.Hkv;
   s.row0 = group * group_rows;
   return s;
-}
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
 }
 
 // Adds what the values that are not finite, of tokens in tiles that were masked, give to four outputs (dims c .. c + 3) of

@@ -578,6 +578,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
     const bool failed = *(volatile int32_t*)&B.failed != 0;
     if (failed) __syncthreads();  // for the copies, see above
+    const RowSums end = sums_at_end(failed, m_run, l_run);
+    m_run = end.m, l_run = end.l;
     const bool bad = B.bad && real && l_run != 0.f;
     const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32;  // of this warp
     auto extra = [&](uint32_t (&o)[32], int c) {
@@ -590,7 +592,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
         o[e + 3] = __float_as_uint(__uint_as_float(o[e + 3]) + x.w);
       }
     };
-    if (rows > 0 && s.parts == 1 && !failed) {
+    if (rows > 0 && s.parts == 1) {
       // through shared memory (in the place of the queries), to write whole lines: a warpgroup's by TMA as the queries came, or,
       // where some of its rows are not the request's, a warp's row by row
       constexpr int kPieces = D / 8, kXor = kPieces % 8 ? 3 : 7;  // pieces of eight rows on different banks
@@ -653,8 +655,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     } else if (rows > 0 && s.parts > 1) {
       float* ml = reinterpret_cast<float*>(qs);
       if (real) {
-        ml[wrow] = failed ? -INFINITY : m_run;
-        ml[NW * q_rows + wrow] = failed ? 0.f : l_run;
+        ml[wrow] = m_run;
+        ml[NW * q_rows + wrow] = l_run;
       }
       if (n > 0) {
 #pragma unroll 1

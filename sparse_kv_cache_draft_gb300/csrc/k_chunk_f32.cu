@@ -273,9 +273,12 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG, ST)) chunk_f32_k
     load(0, tid >> 6);
   }
   float* ks = ks0;
-  if (failed || !ok) {  // a row of a CTA that gave up has seen nothing
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+  if (failed || !ok) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const RowSums end = sums_at_end(true, m[i], l[i]);
+      m[i] = end.m, l[i] = end.l;
+    }
 #pragma unroll
     for (int n = 0; n < d / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   }

@@ -47,12 +47,12 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& A, const Site& s, int32
   return {(int32_t)from * A.G.g, (int32_t)t1 * A.G.g};
 }
 
-// The exponent's part of a row: p = 2^(score * scale + shift). Rows that see nothing have no weights.
+// The exponent's part of a row: p = 2^(score * scale + shift). Infinity for a row that draws nothing.
 __device__ __forceinline__ float shift_of(const ChunkArgs& A, const Site& s, int32_t m) {
-  if (m >= s.cnt * A.G.g) return -INFINITY;
+  if (m >= s.cnt * A.G.g) return INFINITY;
   const int32_t t = m / A.G.g, j = m - t * A.G.g;
   const float x = A.lse[((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j];
-  return x == -INFINITY ? x : -x * kLog2e;
+  return draws(x) ? -x * kLog2e : INFINITY;
 }
 
 // Slots that nothing is added to.
@@ -291,7 +291,7 @@ weigh_mma_kernel(const ChunkArgs A, const __grid_constant__ WeighMaps M, const i
       m += gr;
       lse_at += q_tok * A.G.Hq;
       const float next = i + 1 < n && m < m_end ? *lse_at : -INFINITY;  // on its way for a tile's time
-      uint64_t vis = lse != -INFINITY ? ~0ull : 0;
+      uint64_t vis = draws(lse) ? ~0ull : 0;
       if (masked && vis) {
         vis = 0;
 #pragma unroll 1
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs 
       if (i < end && row < gr && t < s.cnt)
         rows[u] = *reinterpret_cast<const float4*>((const float*)A.q + ((((int64_t)s.r * A.T + t) * A.G.Hq + s.h * g + m - t * g) * d + c * 4));
     }
-    if (tid < kF32Rows) row_shift = i < end && tid < gr ? shift_of(A, s, m0 + tid) : -INFINITY;
+    if (tid < kF32Rows) row_shift = i < end && tid < gr ? shift_of(A, s, m0 + tid) : INFINITY;
   };
   fetch(first);
   for (int32_t i = first; i < end; ++i) {
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs 
       for (int e = 0; e < 4; ++e) {
         const int row = 8 * n + 2 * ti + (e & 1);
         const Rows& v = mine[e >> 1];
-        if (m0 + row < v.lo || m0 + row >= v.hi || row >= gr) continue;
+        if (m0 + row < v.lo || m0 + row >= v.hi || row >= gr || shift[row] == INFINITY) continue;
         float x = sc[n][e];
         if (!is_finite(x)) {
           const float *y = ks + (warp * 16 + gi + 8 * (e >> 1)) * pitch, *z = qs + row * pitch;

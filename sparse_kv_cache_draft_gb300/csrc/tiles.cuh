@@ -9,11 +9,11 @@
 #include <utility>
 
 #include "okv_tree.h"
+#include "row_sums.h"
 #include "tc5.cuh"
 
 namespace okv {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 12;     // CTAs of a cluster; above 8 a kernel has to ask for it
 constexpr int kMaxSmem = 232448;  // bytes of shared memory a CTA may have
 
