@@ -436,8 +436,9 @@ OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, i
  * A token that a row does not see has no part in it, whatever its place holds (infinite and NaN among it); a slot
  * whose tokens are all behind the last new token counts as empty. Scores, maxima and sums are binary32; bf16 queries give weights that
  * are rounded to bf16 for their product with the values, binary32 operands enter the products with 22 of their 24 bits. NaN and
- * infinities go where the formula takes them (a weight below 2^-126 counts as zero). The same inputs give
- * the same bits. Rows from a request's count on are not written; out and lse may not overlap the inputs.
+ * infinities go where the formula takes them (a weight below 2^-126 counts as zero): a score of +infinity makes lse +infinity
+ * and the weight of its token NaN, and with it out. A row whose every score is -infinity counts as one that sees nothing. The same
+ * inputs give the same bits. Rows from a request's count on are not written; out and lse may not overlap the inputs.
  *
  * With weight_out (device [n_requests][kv_heads][slots] binary32; lse is then needed) also what each slot draws:
  *   weight_out[r][h][s] = weight[r][h][s] + sum of exp(q.k / sqrt(d) - lse) over the new tokens of r, the query heads

@@ -508,8 +508,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         if (__any_sync(0xffffffffu, top > m_run + 8.f) || i == 0) {
-          const float mn = fmaxf(m_run, top);  // of every row of the warp: the next vote is then far off
-          const float f = m_run == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m_run - mn);
+          const float mn = real ? larger_max(m_run, top) : m_run;  // of every row of the warp: the next vote is then far off
+          const float f = m_run == mn ? 1.f : ex2(m_run - mn);
           m_run = mn;
           l_run *= f;
           neg = m_run == -INFINITY ? 0.f : -m_run;
@@ -688,8 +688,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
         }
         for (int32_t i = 0; i < n; ++i) {
           float& at = drawn_m[i * q_rows + row];
-          // without a maximum the weights are zeros, or not numbers, as their sum then
-          at = l == 0.f ? 0.f : at == -INFINITY ? l * 0.f : ex2(at - m) / l;
+          // without a maximum the weights are zeros, or not numbers, as their sum then; an infinite sum leaves zero of finite weights,
+          // and no number of the infinite ones
+          at = l == 0.f ? 0.f : at == -INFINITY ? (l == l ? 0.f : l) : ex2(at - m) / l;
         }
       }
       asm volatile("bar.sync 9, 128;" ::: "memory");

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG, ST)) chunk_f32_k
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
+        const float mn = larger_max(m[i], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[i] - ref);
         m[i] = mn;
         float sum = 0.f;
 #pragma unroll

@@ -11,11 +11,16 @@
 
 namespace okv {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kMaxFinite = 3.402823466e38f;
 
 struct RowSums {
   float m, l;  // the largest score, in log2 units (-infinity: none), and the sum of 2^(score - m)
 };
+
+// A maximum that takes in another one: at most the largest finite number. A score of infinity then has an infinite weight and makes
+// the sum infinite, where the difference of two infinities would be no number, as that of a score that is none; against it every finite
+// score's weight is zero.
+OKV_SUMS_FN float larger_max(float m, float other) { return fminf(fmaxf(m, other), kMaxFinite); }
 
 // Of a block in which a wait ran out: what its rows have so far may be anything, so they count as rows that see nothing.
 OKV_SUMS_FN RowSums sums_at_end(bool gave_up, float m, float l) { return gave_up ? RowSums{-INFINITY, 0.f} : RowSums{m, l}; }
