@@ -444,7 +444,7 @@ OKV_API okv_status okv_attend_tree_static(int32_t n_requests, int32_t n_draft, i
  *   weight_out[r][h][s] = weight[r][h][s] + sum of exp(q.k / sqrt(d) - lse) over the new tokens of r, the query heads
  *                         of h and the tokens of slot s that they see
  * for every slot of every request. weight: the same shape, weight_out itself, or NULL for zeros. q_heads / kv_heads *
- * n_new and n_requests * kv_heads * n_new must be less than 2^31. */
+ * n_new must be less than 2^31 - 512, n_requests * kv_heads * n_new less than 2^31. */
 OKV_API okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new, int32_t q_heads, int32_t kv_heads,
                                            int32_t head_dim, int32_t block_size, int32_t slots, int32_t dtype,
                                            const void* pool, const int32_t* slot_block, const int32_t* lengths,

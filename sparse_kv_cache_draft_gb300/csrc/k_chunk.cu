@@ -810,7 +810,8 @@ extern "C" okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new,
   using namespace okv;
   Geom G{};
   if (!tree_geom(n_requests, q_heads, kv_heads, head_dim, block_size, slots, dtype, &G)) return OKV_EINVAL;
-  if (n_new <= 0 || (int64_t)n_requests * kv_heads * n_new > INT32_MAX || (int64_t)n_new * G.g > INT32_MAX) return OKV_EINVAL;
+  // rows of a unit are counted in 32 bits, those of the last group and of the one behind it, up to 256 each, among them
+  if (n_new <= 0 || (int64_t)n_requests * kv_heads * n_new > INT32_MAX || (int64_t)n_new * G.g > INT32_MAX - 512) return OKV_EINVAL;
   if (window < 0 || sinks < 0) return OKV_EINVAL;
   if (!pool || !slot_block || !lengths || !q || !out || (weight_out && !lse) || (weight && !weight_out)) return OKV_EINVAL;
   if (!aligned16(pool) || !aligned16(q) || !aligned16(out)) return OKV_EINVAL;
