@@ -88,6 +88,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Waits (bounded) for the copies that a warp, for values or for keys and the queries, started and that may be on their way still. Called where
+// a block gives up, and not inlined: one token of 128 requests under a window takes 112.5 us, with this code in the kernel's 113.6.
+template <int kS>
+__device__ __noinline__ void land_copies(uint32_t full, uint32_t q_full, int32_t keys, int32_t values, bool v, int32_t ring) {
+  using Order = RingOrder<kS>;
+  const int32_t mine = v ? values : keys;
+  for (int32_t i = max(0, mine - ring); i < mine; ++i) {
+    const int32_t u = v ? Order::value(i) : Order::key(i);
+    if (Order::may_be_on_its_way(u, ring, keys, values)) mbar_wait_timed(full + u % ring * 8, (uint32_t)(u / ring & 1));
+  }
+  if (!v) mbar_wait_timed(q_full, 0);
+}
+
 // Two warpgroups hold 128 scores to a thread, more registers than each thread of the block can have: the others, a whole
 // warpgroup (one warp idle), give up what they do not need. 2 x 216 + 72 is what 3 x 168 were at the launch.
 template <int NW>
@@ -348,15 +361,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
   if (!is_soft) {  // the others' ends: see below
     __syncthreads();
     if (*(volatile int32_t*)&B.failed != 0) {
-      // A wait ran out somewhere: copies that nobody came to wait for land before the shared memory is used for anything else (bounded).
-      if (is_copy || is_copy_v) {
-        const int32_t keys = B.issued[0], values = B.issued[1], mine = is_copy ? keys : values;
-        for (int32_t i = max(0, mine - ring); i < mine; ++i) {
-          const int32_t u = is_copy ? Order::key(i) : v_use(i);
-          if (Order::may_be_on_its_way(u, ring, keys, values)) mbar_wait_timed(smem_u32(&B.full[u % ring]), (uint32_t)(u / ring & 1));
-        }
-        if (is_copy) mbar_wait_timed(smem_u32(&B.q_full), 0);
-      }
+      // A wait ran out somewhere: copies that nobody came to wait for land before the shared memory is used for anything else.
+      if (is_copy || is_copy_v) land_copies<kS>(smem_u32(B.full), smem_u32(&B.q_full), B.issued[0], B.issued[1], is_copy_v, ring);
       __syncthreads();
     }
     if (s.parts > 1) cluster_sync(), cluster_sync();
@@ -577,9 +583,11 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
     tc_fence_after();
     __syncthreads();  // every product done: the ring and Q become the outputs' and the cluster's
     const bool failed = *(volatile int32_t*)&B.failed != 0;
-    if (failed) __syncthreads();  // for the copies, see above
-    const RowSums end = sums_at_end(failed, m_run, l_run);
-    m_run = end.m, l_run = end.l;
+    if (failed) {
+      __syncthreads();  // for the copies, see above
+      const RowSums end = sums_at_end(true, m_run, l_run);
+      m_run = end.m, l_run = end.l;
+    }
     const bool bad = B.bad && real && l_run != 0.f;
     const int32_t rows = min(gr, s.rows - w * gr) - (warp & 3) * 32;  // of this warp
     auto extra = [&](uint32_t (&o)[32], int c) {
