@@ -47,12 +47,13 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& A, const Site& s, int32
   return {(int32_t)from * A.G.g, (int32_t)t1 * A.G.g};
 }
 
-// The exponent's part of a row: p = 2^(score * scale + shift). Infinity for a row that draws nothing.
+// The exponent's part of a row: p = 2^(score * scale + shift). -infinity for a row that draws nothing, as for one with a score of infinity: every
+// finite score's weight is zero then.
 __device__ __forceinline__ float shift_of(const ChunkArgs& A, const Site& s, int32_t m) {
-  if (m >= s.cnt * A.G.g) return INFINITY;
+  if (m >= s.cnt * A.G.g) return -INFINITY;
   const int32_t t = m / A.G.g, j = m - t * A.G.g;
   const float x = A.lse[((int64_t)s.r * A.T + t) * A.G.Hq + s.h * A.G.g + j];
-  return draws(x) ? -x * kLog2e : INFINITY;
+  return draws(x) ? -x * kLog2e : -INFINITY;
 }
 
 // Slots that nothing is added to.
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs 
       if (i < end && row < gr && t < s.cnt)
         rows[u] = *reinterpret_cast<const float4*>((const float*)A.q + ((((int64_t)s.r * A.T + t) * A.G.Hq + s.h * g + m - t * g) * d + c * 4));
     }
-    if (tid < kF32Rows) row_shift = i < end && tid < gr ? shift_of(A, s, m0 + tid) : INFINITY;
+    if (tid < kF32Rows) row_shift = i < end && tid < gr ? shift_of(A, s, m0 + tid) : -INFINITY;
   };
   fetch(first);
   for (int32_t i = first; i < end; ++i) {
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kF32Threads) weigh_f32_kernel(const ChunkArgs 
       for (int e = 0; e < 4; ++e) {
         const int row = 8 * n + 2 * ti + (e & 1);
         const Rows& v = mine[e >> 1];
-        if (m0 + row < v.lo || m0 + row >= v.hi || row >= gr || shift[row] == INFINITY) continue;
+        if (m0 + row < v.lo || m0 + row >= v.hi || row >= gr) continue;
         float x = sc[n][e];
         if (!is_finite(x)) {
           const float *y = ks + (warp * 16 + gi + 8 * (e >> 1)) * pitch, *z = qs + row * pitch;
