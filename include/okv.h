@@ -459,7 +459,8 @@ OKV_API okv_status okv_attend_chunk_static(int32_t n_requests, int32_t n_new, in
  *   2. those of least weight (binary32; NaN above all), of equal ones by index, but not a block with one of the first
  *      `sinks` tokens, one of the last `recent` tokens, or the part-filled last block.
  * The taken slots, by index, get the placed blocks, ascending, and a weight of zero; the others stay as they are. A part-filled
- * last block that no slot holds is not brought back: its first tokens are gone. slot_block: device
+ * last block that no slot holds is not brought back: its first tokens are gone. Eviction knows no window: a block behind
+ * one keeps the weight that it drew, and may outlive a block that the next tokens see unless recent >= window. slot_block: device
  * [n_requests][kv_heads][slots] int32; weight: the same shape binary32; slot_block_out, weight_out: written whole, either the
  * input itself or not overlapping the inputs. block_size 1 to 64, slots 1 to 1024, n_requests * kv_heads * slots < 2^31;
  * sinks, recent >= 0. What the pool holds of an evicted block stays until it is written over. */

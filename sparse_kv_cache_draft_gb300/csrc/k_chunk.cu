@@ -8,10 +8,10 @@
 // few tiles of a group need a mask whatever the slots' order, and slots that no row sees are not read. Tiles are dealt
 // to the CTAs of a cluster where there are too few groups to fill the GPU, as for drafted trees.
 //
-// Measured (32 / 8 heads of 128 dims, bf16): 4 requests x 1024 tokens with 64 / 8 heads behind 31K 2.53 to 2.66 ms, 1.63 to 1.71
-// PFLOP/s, 0.84 to 0.88 of the measured rate; 2048 tokens behind 14K 350 us, 1.46 PFLOP/s (two rounds of 256 groups on 152 SMs);
-// one token for 128 requests over 2048 resident ones 162 us, 0.97 of a copy's rate, 186 with the slots' weights; one token of one
-// request 9.3 us.
+// Measured (32 / 8 heads of 128 dims, bf16): 4 requests x 1024 tokens with 64 / 8 heads behind 31K 2.58 to 2.80 ms, 1.55 to 1.68
+// PFLOP/s, 0.80 to 0.87 of the measured rate, by the GPU's power; 2048 tokens behind 14K 348 to 370 us, 1.39 to 1.48 PFLOP/s (two
+// rounds of 256 groups on 152 SMs); one token for 128 requests over 2048 resident ones 162 us, 0.97 of a copy's rate, 184 with the
+// slots' weights; one token of one request 9.4 us.
 #include <stddef.h>
 
 #include "chunk.cuh"
@@ -59,9 +59,11 @@ struct MmaBars {
 
 __host__ __device__ constexpr size_t mma_misc(int kb) { return sizeof(MmaBars) + ((size_t)kb * 2 + 15) / 16 * 16; }
 
-// Up to 128 rows the weights that slots draw are summed on the way: [entries][q_rows] sums of a row's weights over a slot's
-// tokens, against the maximum of then, [tiles][q_rows], both of this CTA's tiles; with the final maxima and sums they are
-// joined at the end. Where a slot is a multiple of eight columns of a tile, as the sums come by eight.
+// Up to 128 rows the weights that slots draw are summed on the way, where there is room: [entries][q_rows] sums of a row's weights over a
+// slot's tokens, against the maximum of then, [tiles][q_rows], both of this CTA's tiles; with the final maxima and sums they are
+// joined at the end. Where a slot is a multiple of eight columns of a tile, as the sums come by eight. At d 128, blocks of 16 and
+// four heads to a key head there is room for 1024 slots for two tokens, 524 for four, 240 for eight, 92 for 16 and 20 for 32; beyond,
+// a second launch reads the keys again (128 requests x 8 tokens: 209 us over 128 slots, 1079 over 256; without weights 167 and 308).
 __host__ __device__ constexpr size_t drawn_bytes(int tiles, int spt, int q_rows) { return (size_t)tiles * (spt + 1) * q_rows * 4; }
 
 struct ChunkMaps {
@@ -724,7 +726,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Ch
 
 // ---- launches ----------------------------------------------------------------------------------------------
 
-constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1};  // as for drafted trees
+// Those of the drafted trees. They were not fitted for these kernels: a start and end of the wide one are 4.6 of its tiles, not one.
+constexpr Costs kMmaCosts{5.5, 6, 1}, kMmaCostsWide{1, 6, 1};
 
 // Maps of 5 dims over lines and chunks: the pool as [slots][K, V][tokens], a box of one chunk of the tokens of spt slots
 // or of one; the queries and outputs as [tokens][KV heads][group], a box of q_tok tokens of a KV head.

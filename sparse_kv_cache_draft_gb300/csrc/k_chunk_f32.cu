@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(DV, RG, ST)) chunk_f32_k
 
 // ---- launches ----------------------------------------------------------------------------------------------
 
-constexpr Costs kF32Costs{2.8, 0.5, 1.3};  // as for drafted trees
+constexpr Costs kF32Costs{2.8, 0.5, 1.3};  // those of the drafted trees, where a CTA has one stage of tiles
 
 template <int DV, int RG, int ST>
 cudaError_t run_f32(const ChunkArgs& A, cudaStream_t s) {

@@ -5,7 +5,7 @@
 // weights in registers. The m-th smallest weight is found bit by bit over the weights' ordered images, from the highest bit in
 // which any two differ (sorting them would move every slot), and slots of that weight go by their index. Everything is
 // integer work on a few kilobytes: a call is a launch, two rounds of memory and the sums over the unit. Measured: 128 requests x 8
-// heads of 128 slots, a sixteenth of which need one, 3.3 us; 16 x 8 of 1024 slots for 63 blocks each 8.3 us.
+// heads of 128 slots, a sixteenth of which need one, 2.9 to 4.4 us (by the host's rate of calls); 16 x 8 of 1024 slots for 63 blocks each 8.3 us.
 #include "okv_tree.h"
 #include "tc5.cuh"
 
